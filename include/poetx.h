@@ -78,6 +78,10 @@ typedef enum {
 typedef enum { POETX_F32 = 0, POETX_BF16 = 1, POETX_I8 = 2 } poetx_dtype;
 typedef enum { POETX_FAST = 0, POETX_MEM = 1 } poetx_variant;
 typedef enum { POETX_CNP_FWD = 0, POETX_CNP_BWD = 1 } poetx_cnp_dir;
+/* activations of poetx_linear_*: p; max(p, 0); p Phi(p) (erf form); its tanh form
+   p/2 (1 + tanh(sqrt(2/pi) (p + 0.044715 p^3))); p / (1 + exp(-p))                        */
+typedef enum { POETX_ACT_NONE = 0, POETX_ACT_RELU = 1, POETX_ACT_GELU = 2, POETX_ACT_GELU_TANH = 3,
+               POETX_ACT_SILU = 4 } poetx_act;
 
 /* [host] description of one layer.  Pointers inside are device pointers. */
 typedef struct {
@@ -283,6 +287,110 @@ int poetx_fold(const poetx_layer *L /*[host]*/, void *w_out, void *ws, size_t *w
 int poetx_adam_step(int64_t n_params, void *theta, int32_t theta_dtype, const float *grad, float *m,
                     float *v, float lr, float beta1, float beta2, float eps, int64_t step, float gamma,
                     void *stream);
+
+/*
+ * Operators around the layer.  A training step of a language model runs each POET-X layer
+ * after a layer norm, next to dense linear layers (those that are not reparameterized, or
+ * whose phase has been folded into an ordinary weight by poetx_fold), and ends in the cross
+ * entropy of its vocabulary head.  The three pairs of calls below follow the conventions
+ * above (contiguous token-major buffers, 16-byte aligned, outputs overwritten, no
+ * synchronization, errors before any launch), with any sizes from 1 up to the stated ones.
+ * dtype is F32 or BF16 and holds for every buffer not stated otherwise.  Sums, statistics
+ * and products accumulate in float32; reductions run in a fixed order, so results are
+ * bitwise reproducible run to run on one device.  Infinities and NaN go through as the
+ * formulas say, except where a call states that a row takes no part.
+ */
+
+/*
+ * poetx_layernorm_forward -- layer norm of each row x[i][0..d):
+ *     mu = sum_c x_c / d,  r = (sum_c (x_c - mu)^2 / d + eps)^(-1/2),
+ *     y_c = (x_c - mu) r gamma_c + beta_c
+ * x, y: [n_rows][d]; gamma, beta: [d] in p_dtype (F32 or BF16), each may be NULL (1 and 0);
+ * mean, rstd: [n_rows] float32 outputs mu and r for the backward, each may be NULL.
+ * n_rows == 0 is a no-op.  Errors: NULL x or y, n_rows < 0, eps < 0 or not finite, bad
+ * dtype, misaligned pointer, y == x -> INVALID_ARG; d < 1 -> POETX_ERR_SHAPE; d > 16384 ->
+ * UNSUPPORTED.
+ */
+int poetx_layernorm_forward(int64_t n_rows, int64_t d, int32_t dtype, const void *x, const void *gamma,
+                            const void *beta, int32_t p_dtype, float eps, void *y, float *mean, float *rstd,
+                            void *stream);
+
+/*
+ * poetx_layernorm_backward -- from dy = dL/dy, with xh = (x - mu) r and g = dy gamma:
+ *     dx = dres + r (g - mean_c(g) - xh mean_c(g xh)),
+ *     dgamma = sum_rows dy xh,  dbeta = sum_rows dy
+ * mean, rstd: as the forward wrote them.  dres (nullable): [n_rows][d], the gradient that
+ * reaches x past the norm (a residual stream's), added in the same pass.  gamma: as in the
+ * forward (NULL: 1).  dgamma, dbeta: [d] float32, each may be NULL; with n_rows == 0 they are
+ * zeros.  Workspace: query with ws == NULL (the same dgamma and dbeta, by which it is none
+ * when both are NULL).  Errors: as the forward; NULL dy, mean, rstd or dx -> INVALID_ARG.
+ */
+int poetx_layernorm_backward(int64_t n_rows, int64_t d, int32_t dtype, const void *x, const void *dy,
+                             const void *gamma, int32_t p_dtype, const float *mean, const float *rstd,
+                             const void *dres, void *dx, float *dgamma, float *dbeta, void *ws, size_t *ws_bytes,
+                             void *stream);
+
+/*
+ * poetx_linear_forward -- dense linear layer with its epilogue, in one product:
+ *     p = x . w^T + bias,  y = act(p) + residual
+ * x: [n_tokens][d_in]; w: [d_out][d_in]; bias: [d_out] in bias_dtype (F32 or BF16), nullable;
+ * residual: [n_tokens][d_out], nullable; act: a poetx_act; y: [n_tokens][d_out]; saved_pre
+ * (nullable): output p [n_tokens][d_out], rounded to dtype, for the backward (y itself takes
+ * the unrounded p).  Any widths; bf16 widths that are not multiples of 8 are copied to padded
+ * rows in the workspace (not for n_tokens <= 16).  n_tokens == 0 is a no-op.  Workspace: query
+ * with ws == NULL (it may depend on the current device).  Errors: NULL x, w or y, n_tokens < 0,
+ * bad enum, misaligned pointer, an output that equals an input or another output ->
+ * INVALID_ARG; d_in or d_out < 1 -> POETX_ERR_SHAPE; d_in or d_out > 2^20, or more than 2^22
+ * tiles of 128 x 128 results -> UNSUPPORTED.
+ */
+int poetx_linear_forward(int64_t n_tokens, int64_t d_in, int64_t d_out, int32_t dtype, const void *x, const void *w,
+                         const void *bias, int32_t bias_dtype, const void *residual, int32_t act, void *y,
+                         void *saved_pre, void *ws, size_t *ws_bytes, void *stream);
+
+/*
+ * poetx_linear_backward -- from dy = dL/dy:
+ *     dp = dy act'(p),  dx = dp . w,  dw = dp^T . x,  dbias = sum_tokens dp
+ * (the residual's gradient is dy itself).  saved_pre: p as the forward saved it; ignored (may
+ * be NULL) with POETX_ACT_NONE.  dx: [n_tokens][d_in]; dw: [d_out][d_in] in dtype; dbias:
+ * [d_out] float32; each may be NULL (a frozen weight needs no dw), not all three.  With
+ * n_tokens == 0, dw and dbias are zeros.  For bf16 the products read dp rounded to bf16;
+ * dbias sums the unrounded dp.  relu's slope at 0 is 0.  x may be NULL without dw, w without
+ * dx.  Workspace: query with ws == NULL, with the same output pointers NULL or not.  Errors:
+ * as the forward.
+ */
+int poetx_linear_backward(int64_t n_tokens, int64_t d_in, int64_t d_out, int32_t dtype, const void *x, const void *w,
+                          const void *dy, const void *saved_pre, int32_t act, void *dx, void *dw, float *dbias,
+                          void *ws, size_t *ws_bytes, void *stream);
+
+/*
+ * poetx_xent_forward -- softmax cross entropy of a linear head with logits l = h . w^T, which
+ * are never stored:
+ *     lse_i = log sum_v exp l_iv,   loss_i = lse_i - l_{i, target_i}
+ * h: [n_tokens][d]; w: [vocab][d]; target: [n_tokens] int32; loss, lse: [n_tokens] float32.
+ * A token whose target lies outside [0, vocab) takes no part: its loss is 0 (lse is still
+ * written).  n_tokens == 0 is a no-op.  Workspace: query with ws == NULL: 8 bytes per token and
+ * 128 or 256 vocabulary entries; bf16 with d not a multiple of 8 adds padded copies of h and of
+ * one piece of w.  Errors: NULL buffer, n_tokens < 0, bad dtype, misaligned pointer ->
+ * INVALID_ARG; d or vocab < 1 -> POETX_ERR_SHAPE; d > 2^20, vocab > 2^31 - 1, or more than 2^22
+ * tiles of 128 x 128 logits -> UNSUPPORTED.
+ */
+int poetx_xent_forward(int64_t n_tokens, int64_t d, int64_t vocab, int32_t dtype, const void *h, const void *w,
+                       const int32_t *target, float *loss, float *lse, void *ws, size_t *ws_bytes, void *stream);
+
+/*
+ * poetx_xent_backward -- from dloss_i = dL/dloss_i (float32 [n_tokens]; 1/count for a mean)
+ * and the forward's lse, piece by piece of the vocabulary:
+ *     dl_iv = (exp(l_iv - lse_i) - [v = target_i]) dloss_i,  dh = dl . w,  dw = dl^T . h
+ * dh: [n_tokens][d], dw: [vocab][d], both in dtype, each may be NULL, not both.  A token whose
+ * target lies outside [0, vocab) gets dh = 0 and leaves dw alone, whatever its h, lse and dloss
+ * hold.  With n_tokens == 0, dw is zeros.  For bf16 the products read dl rounded to bf16.
+ * Workspace: query with ws == NULL, with the same outputs NULL or not: dl of one piece (at most
+ * 512 MB, or 2048 vocabulary entries where those take more), float32 sums of dh when there are
+ * several pieces, a copy of h for dw.  Errors: as poetx_xent_forward.
+ */
+int poetx_xent_backward(int64_t n_tokens, int64_t d, int64_t vocab, int32_t dtype, const void *h, const void *w,
+                        const int32_t *target, const float *lse, const float *dloss, void *dh, void *dw, void *ws,
+                        size_t *ws_bytes, void *stream);
 
 /* Human-readable name of a poetx_status code (static string). */
 const char *poetx_status_string(int status);

@@ -7,13 +7,16 @@ If the shared library is missing this module raises at import: there is no
 fallback path.
 
 Python names mirror the C entry points:
-    poetx_merge_perm, poetx_cnp, poetx_forward, poetx_backward
+    poetx_merge_perm, poetx_cnp, poetx_forward, poetx_backward,
+    poetx_layernorm_forward / _backward, poetx_linear_forward / _backward,
+    poetx_xent_forward / _backward (the operators around the layer)
 plus ``Layer`` (the poetx_layer descriptor) and the measurement hooks.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -31,6 +34,7 @@ POETX_ERR_UNSUPPORTED, POETX_ERR_WORKSPACE, POETX_ERR_HIP = -3, -4, -5
 POETX_F32, POETX_BF16, POETX_I8 = 0, 1, 2
 POETX_FAST, POETX_MEM = 0, 1
 POETX_CNP_FWD, POETX_CNP_BWD = 0, 1
+POETX_ACT_NONE, POETX_ACT_RELU, POETX_ACT_GELU, POETX_ACT_GELU_TANH, POETX_ACT_SILU = 0, 1, 2, 3, 4
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 
@@ -66,6 +70,15 @@ _lib.poetx_backward_adam.argtypes = [ctypes.POINTER(PoetxLayerC), _i64, _vp, _vp
 _lib.poetx_fold.argtypes = [ctypes.POINTER(PoetxLayerC), _vp, _vp, ctypes.POINTER(_sz), _vp]
 _lib.poetx_adam_step.argtypes = [_i64, _vp, _i32, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                  ctypes.c_float, _i64, ctypes.c_float, _vp]
+_szp = ctypes.POINTER(_sz)
+_lib.poetx_layernorm_forward.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _vp, _vp]
+_lib.poetx_layernorm_backward.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _szp, _vp]
+_lib.poetx_linear_forward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _szp,
+                                      _vp]
+_lib.poetx_linear_backward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_xent_forward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_xent_backward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp]
 _lib.poetx_status_string.argtypes = [ctypes.c_int]
 _lib.poetx_status_string.restype = ctypes.c_char_p
 _lib.poetx_version.restype = ctypes.c_char_p
@@ -73,12 +86,14 @@ _lib.poetx_prof_enable.argtypes = [_i32]
 _lib.poetx_prof_read.argtypes = [ctypes.c_char_p, _sz]
 _lib.poetx_prof_only.argtypes = [ctypes.c_char_p]
 for _f in ("poetx_merge_perm", "poetx_cnp", "poetx_cnp_noalloc", "poetx_forward", "poetx_backward", "poetx_backward_adam", "poetx_fold",
-           "poetx_adam_step",
+           "poetx_adam_step", "poetx_layernorm_forward", "poetx_layernorm_backward", "poetx_linear_forward",
+           "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward",
            "poetx_prof_enable", "poetx_prof_only", "poetx_prof_read"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("poetx_merge_perm", "poetx_cnp", "poetx_cnp_noalloc", "poetx_forward", "poetx_backward", "poetx_backward_adam", "poetx_fold",
-            "poetx_adam_step",
+            "poetx_adam_step", "poetx_layernorm_forward", "poetx_layernorm_backward", "poetx_linear_forward",
+            "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward",
             "poetx_status_string", "poetx_version", "poetx_prof_enable", "poetx_prof_only", "poetx_prof_read")
 
 
@@ -129,12 +144,16 @@ def _stream(dev: torch.device):
 # Scratch tensors keyed by (device, stream): each is allocated while its stream is the
 # current one and only ever used by calls on that stream, so the caching allocator's
 # stream ordering makes both the reuse between calls and the release of an outgrown
-# buffer safe.  Layers driven on different streams get different workspaces.
+# buffer safe.  Layers driven on different streams get different workspaces.  A call that is
+# being captured into a graph takes a workspace of its own from the graph's memory pool: it
+# lives as long as the graph, and no eager call or other graph shares it.
 _ws_cache: dict = {}
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
     key = (idx, torch.cuda.current_stream(idx).cuda_stream)
     t = _ws_cache.get(key)
     if t is None or t.numel() < nbytes:
@@ -406,6 +425,234 @@ def poetx_backward_adam(layer: Layer, x: torch.Tensor, dz: torch.Tensor, state: 
     out = dict(dx=dx)
     if dtheta_r is not None:
         out.update(dtheta_r=dtheta_r, dtheta_p=dtheta_p)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around the layer: layer norm, dense linear layer, vocabulary cross entropy.
+# The last axis of x (h) is the feature axis, the leading axes together are the tokens.
+# ---------------------------------------------------------------------------
+_FLOATS = (torch.float32, torch.bfloat16)
+_ACTS = {"none": POETX_ACT_NONE, "relu": POETX_ACT_RELU, "gelu": POETX_ACT_GELU, "gelu_tanh": POETX_ACT_GELU_TANH,
+         "silu": POETX_ACT_SILU}
+
+
+def _act(act) -> int:
+    if act in _ACTS:
+        return _ACTS[act]
+    if act in _ACTS.values():
+        return act
+    raise ValueError(f"act: {act!r}, expected one of {tuple(_ACTS)}")
+
+
+def _check_in(t: Optional[torch.Tensor], name: str, shape, dtypes, dev) -> None:
+    """An input or output buffer: its shape, dtype, contiguity and device."""
+    if t is None:
+        return
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _tokens(t: torch.Tensor, name: str):
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [..., features]")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+@functools.lru_cache(maxsize=1024)
+def _ws_query(fn: str, device: int, args: tuple) -> int:
+    """Workspace bytes of a call: what its size query (ws == NULL) answers on this device."""
+    nb = _sz(0)
+    _check(getattr(_lib, fn)(*args, None, ctypes.byref(nb), None), f"{fn}(size)")
+    return nb.value
+
+
+_SOME = 256  # a non-null pointer for size queries, which look only at which outputs are wanted
+
+
+def _run(fn: str, dev: torch.device, args: tuple, query: Optional[tuple]) -> None:
+    """The call on dev's current stream, with its workspace when `query` has its size query's
+    arguments.  The library launches on the current device, so that is made dev's."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(fn, dev, args, query)
+    st = _stream(dev)
+    if query is None:
+        _check(getattr(_lib, fn)(*args, st), fn)
+        return
+    ws = _workspace(dev, _ws_query(fn, dev.index, query))
+    nb = _sz(ws.numel())
+    _check(getattr(_lib, fn)(*args, _ptr(ws), ctypes.byref(nb), st), fn)
+
+
+def poetx_layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                            beta: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
+                            y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                            rstd: Optional[torch.Tensor] = None):
+    """Layer norm over the last axis.  Returns (y, mean, rstd): mean and rstd float32 [tokens],
+    for the backward.  gamma and beta: [d], both float32 or both bf16, each optional."""
+    n, d = _tokens(x, "x")
+    dev = x.device
+    _check_in(x, "x", x.shape, _FLOATS, dev)
+    p = next((t for t in (gamma, beta) if t is not None), None)
+    pd = (p.dtype,) if p is not None and p.dtype in _FLOATS else _FLOATS
+    _check_in(gamma, "gamma", (d,), pd, dev)
+    _check_in(beta, "beta", (d,), pd, dev)
+    y = torch.empty_like(x) if y is None else y
+    mean = torch.empty(n, dtype=torch.float32, device=dev) if mean is None else mean
+    rstd = torch.empty(n, dtype=torch.float32, device=dev) if rstd is None else rstd
+    _check_in(y, "y", x.shape, (x.dtype,), dev)
+    _check_in(mean, "mean", (n,), (torch.float32,), dev)
+    _check_in(rstd, "rstd", (n,), (torch.float32,), dev)
+    _run("poetx_layernorm_forward", dev,
+         (n, d, _dt(x), _ptr(x), _ptr(gamma), _ptr(beta), _dt(p) if p is not None else POETX_F32, eps, _ptr(y),
+          _ptr(mean), _ptr(rstd)), None)
+    return y, mean, rstd
+
+
+def poetx_layernorm_backward(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[torch.Tensor], mean: torch.Tensor,
+                             rstd: torch.Tensor, *, dres: Optional[torch.Tensor] = None,
+                             dx: Optional[torch.Tensor] = None, want_params: bool = True):
+    """Returns dict(dx[, dgamma, dbeta]); dgamma, dbeta float32 [d].  dres: the gradient that
+    reaches x past the norm, added to dx."""
+    n, d = _tokens(x, "x")
+    dev = x.device
+    _check_in(x, "x", x.shape, _FLOATS, dev)
+    _check_in(dy, "dy", x.shape, (x.dtype,), dev)
+    _check_in(dres, "dres", x.shape, (x.dtype,), dev)
+    _check_in(gamma, "gamma", (d,), _FLOATS, dev)
+    _check_in(mean, "mean", (n,), (torch.float32,), dev)
+    _check_in(rstd, "rstd", (n,), (torch.float32,), dev)
+    dx = torch.empty_like(x) if dx is None else dx
+    _check_in(dx, "dx", x.shape, (x.dtype,), dev)
+    dg = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
+    db = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
+    pd = _dt(gamma) if gamma is not None else POETX_F32
+    some = _SOME if want_params else None
+    _run("poetx_layernorm_backward", dev,
+         (n, d, _dt(x), _ptr(x), _ptr(dy), _ptr(gamma), pd, _ptr(mean), _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dg),
+          _ptr(db)),
+         (n, d, _dt(x), None, None, None, pd, None, None, None, None, some, some))
+    return dict(dx=dx, dgamma=dg, dbeta=db) if want_params else dict(dx=dx)
+
+
+def poetx_linear_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                         residual: Optional[torch.Tensor] = None, act="none", *, y: Optional[torch.Tensor] = None,
+                         save_pre: bool = False):
+    """act(x . w^T + bias) + residual.  Returns (y, pre): pre, what the activation took, for
+    the backward when save_pre is set, else None.  act: a name ("none", "relu", "gelu",
+    "gelu_tanh", "silu") or a POETX_ACT_* code."""
+    n, d_in = _tokens(x, "x")
+    dev = x.device
+    d_out = w.shape[0]
+    a = _act(act)
+    shape = x.shape[:-1] + (d_out,)
+    _check_in(x, "x", x.shape, _FLOATS, dev)
+    _check_in(w, "w", (d_out, d_in), (x.dtype,), dev)
+    _check_in(bias, "bias", (d_out,), _FLOATS, dev)
+    _check_in(residual, "residual", shape, (x.dtype,), dev)
+    y = torch.empty(shape, dtype=x.dtype, device=dev) if y is None else y
+    _check_in(y, "y", shape, (x.dtype,), dev)
+    pre = torch.empty(shape, dtype=x.dtype, device=dev) if save_pre else None
+    bd = _dt(bias) if bias is not None else POETX_F32
+    _run("poetx_linear_forward", dev,
+         (n, d_in, d_out, _dt(x), _ptr(x), _ptr(w), _ptr(bias), bd, _ptr(residual), a, _ptr(y), _ptr(pre)),
+         (n, d_in, d_out, _dt(x), None, None, None, bd, None, a, None, None))
+    return y, pre
+
+
+def poetx_linear_backward(x: Optional[torch.Tensor], w: Optional[torch.Tensor], dy: torch.Tensor,
+                          pre: Optional[torch.Tensor] = None, act="none", *, want_dx: bool = True,
+                          want_dw: bool = True, want_dbias: bool = True):
+    """Returns dict with those of dx, dw (x's dtype) and dbias (float32) that are wanted.  pre:
+    what poetx_linear_forward(save_pre=True) returned (not needed for act "none").  x is needed
+    for dw, w for dx."""
+    n, d_out = _tokens(dy, "dy")
+    dev = dy.device
+    a = _act(act)
+    if want_dx and w is None or want_dw and x is None:
+        raise ValueError("dx needs w, dw needs x")
+    if a != POETX_ACT_NONE and pre is None:
+        raise ValueError("pre is required for this activation")
+    ref = x if x is not None else w
+    d_in = ref.shape[-1] if ref is not None else 1
+    shape = dy.shape[:-1] + (d_in,)
+    _check_in(dy, "dy", dy.shape, _FLOATS, dev)
+    _check_in(x, "x", shape, (dy.dtype,), dev)
+    _check_in(w, "w", (d_out, d_in), (dy.dtype,), dev)
+    _check_in(pre, "pre", dy.shape, (dy.dtype,), dev)
+    out = {}
+    if want_dx:
+        out["dx"] = torch.empty(shape, dtype=dy.dtype, device=dev)
+    if want_dw:
+        out["dw"] = torch.empty((d_out, d_in), dtype=dy.dtype, device=dev)
+    if want_dbias:
+        out["dbias"] = torch.empty(d_out, dtype=torch.float32, device=dev)
+    if n == 0 and not (want_dw or want_dbias):
+        return out
+    ptrs = [_ptr(out.get(k)) for k in ("dx", "dw", "dbias")]
+    _run("poetx_linear_backward", dev,
+         (n, d_in, d_out, _dt(dy), _ptr(x), _ptr(w), _ptr(dy), _ptr(pre), a, *ptrs),
+         (n, d_in, d_out, _dt(dy), None, None, None, None, a, *(None if p is None else _SOME for p in ptrs)))
+    return out
+
+
+def poetx_xent_forward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, *,
+                       loss: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Softmax cross entropy of the logits h . w^T, which are not stored.  target: int32, one
+    per token; a target outside [0, vocab) marks a token that takes no part (loss 0).  Returns
+    (loss, lse), float32, one per token."""
+    n, d = _tokens(h, "h")
+    dev = h.device
+    vocab = w.shape[0]
+    lead = h.shape[:-1]
+    _check_in(h, "h", h.shape, _FLOATS, dev)
+    _check_in(w, "w", (vocab, d), (h.dtype,), dev)
+    _check_in(target, "target", lead, (torch.int32,), dev)
+    loss = torch.empty(lead, dtype=torch.float32, device=dev) if loss is None else loss
+    lse = torch.empty(lead, dtype=torch.float32, device=dev) if lse is None else lse
+    _check_in(loss, "loss", lead, (torch.float32,), dev)
+    _check_in(lse, "lse", lead, (torch.float32,), dev)
+    _run("poetx_xent_forward", dev,
+         (n, d, vocab, _dt(h), _ptr(h), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse)),
+         (n, d, vocab, _dt(h), None, None, None, None, None))
+    return loss, lse
+
+
+def poetx_xent_backward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                        dloss: torch.Tensor, *, want_dh: bool = True, want_dw: bool = True):
+    """Gradients of sum(dloss * loss): dict with those of dh and dw that are wanted, in h's
+    dtype.  lse: poetx_xent_forward's; dloss: float32, one per token (1 / count for a mean)."""
+    n, d = _tokens(h, "h")
+    dev = h.device
+    vocab = w.shape[0]
+    lead = h.shape[:-1]
+    if not (want_dh or want_dw):
+        raise ValueError("neither dh nor dw is wanted")
+    _check_in(h, "h", h.shape, _FLOATS, dev)
+    _check_in(w, "w", (vocab, d), (h.dtype,), dev)
+    _check_in(target, "target", lead, (torch.int32,), dev)
+    _check_in(lse, "lse", lead, (torch.float32,), dev)
+    _check_in(dloss, "dloss", lead, (torch.float32,), dev)
+    out = {}
+    if want_dh:
+        out["dh"] = torch.empty_like(h)
+    if want_dw:
+        out["dw"] = torch.empty_like(w)
+    if n == 0 and not want_dw:
+        return out
+    ptrs = [_ptr(out.get(k)) for k in ("dh", "dw")]
+    _run("poetx_xent_backward", dev,
+         (n, d, vocab, _dt(h), _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), *ptrs),
+         (n, d, vocab, _dt(h), None, None, None, None, None, *(None if p is None else _SOME for p in ptrs)))
     return out
 
 

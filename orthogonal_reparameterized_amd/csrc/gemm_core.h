@@ -1,0 +1,491 @@
+// Products C[m][n] = sum_k A(m, k) B(n, k) whose results go straight into an epilogue:
+// the dense linear layer's and the cross entropy's kernels.  Internal to libpoetx.
+//
+// bf16 operands run on v_mfma_f32_16x16x32_bf16, float32 ones on v_mfma_f32_16x16x4f32,
+// both with float32 accumulators.  An operand is k-contiguous (element (r, k) at
+// base + r ld + k) or k-major (base + k ld + r).
+//
+// What a kernel does with its tile is an epilogue type:
+//   kStats == false: put(m, n, v, nv) takes 8 (nv <= 8 valid) consecutive columns of row m;
+//     the accumulators pass through a wave's own piece of LDS so that a row's 64 columns
+//     leave as whole 128-byte lines.
+//   kStats == true: reduce() gets the whole tile's accumulators (row statistics).
+// kSplits says whether a product with this epilogue may be split over k.
+#pragma once
+
+#include "lds_tiles.h"
+#include "vec.h"
+
+namespace poetx {
+
+struct MmArgs {
+  int64_t M, N, K;
+  const void *A; int64_t lda;
+  const void *B; int64_t ldb;
+  int tiles_m, tiles_n;
+  int splits;   // k ranges; split s covers k in [s kc, (s+1) kc)
+  int64_t kc;   // a multiple of 64 when splits > 1
+};
+
+namespace {
+
+// Tile and split of a workgroup.  Workgroups go to the 8 XCDs round-robin; ids are dealt
+// so that each XCD gets one contiguous run of the tile order (any count), in which groups
+// of 4 m-tiles sweep n: the workgroups running together on an XCD share their panels in
+// its L2.
+struct MmTile { int tm, tn, split; };
+__device__ inline MmTile mm_tile(const MmArgs &a) {
+  const int T = a.tiles_m * a.tiles_n, tot = T * a.splits;
+  const int id = (int)blockIdx.x, x = id & 7, q = tot >> 3, r = tot & 7;
+  int L = x * q + (x < r ? x : r) + (id >> 3);
+  MmTile t;
+  t.split = L / T;
+  L -= t.split * T;
+  const int GM = a.tiles_m < 4 ? a.tiles_m : 4, per = GM * a.tiles_n;
+  const int grp = L / per, first = grp * GM, gm = a.tiles_m - first < GM ? a.tiles_m - first : GM, loc = L - grp * per;
+  // divisions run on the vector ALU: back to scalars, so that operand bases stay uniform
+  t.tm = __builtin_amdgcn_readfirstlane(first + loc % gm);
+  t.tn = __builtin_amdgcn_readfirstlane(loc / gm);
+  t.split = __builtin_amdgcn_readfirstlane(t.split);
+  return t;
+}
+
+// Global -> LDS loads of one operand's [R rows] x [64 k] stage.  k-contiguous: the base is
+// the tile's first row; chunks of 8 k past the range read as zero (their offset is past
+// the buffer), rows past the operand too.  k-major: the base moves with k.
+constexpr int kPast = 0x7ffffff0;  // beyond every buffer extent used here
+
+template <int R, int NW>
+struct StageKC {
+  static constexpr int INSTR = R / 8 / NW;
+  int voff[INSTR];
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ void init(const bf16_t *P, int64_t ld, int64_t row0, int64_t rows, int64_t kbeg) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int64_t left = rows - row0 < R ? rows - row0 : R;
+    rs = make_rsrc(P + row0 * ld, left * ld * 2);
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) {
+      const int row = (w * INSTR + i) * 8 + (l >> 3);
+      voff[i] = (int)((row * ld + kbeg) * 2) + (((l & 7) ^ kc_key<64>(row)) << 4);
+    }
+  }
+  // step t (64 k); left: k of the range from this step on
+  __device__ void issue(int t, int64_t left, bf16_t *tile, int i) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
+    int off = voff[i] + t * 128;
+    if (left < 64) {
+      const int row = (w * INSTR + i) * 8 + (l >> 3);
+      if ((((l & 7) ^ kc_key<64>(row)) << 3) >= left) off = kPast;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * INSTR + i) * 512), 16, off, 0, 0, 0);
+  }
+  __device__ void issue_all(int t, int64_t left, bf16_t *tile) const {
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) issue(t, left, tile, i);
+  }
+};
+
+template <int R, int NW>
+struct StageKM {
+  static constexpr int CH = R / 8, RPI = 64 / CH, INSTR = 64 / RPI / NW;
+  int voff[INSTR];
+  const bf16_t *base;
+  int64_t ld, cols;
+  __device__ void init(const bf16_t *P, int64_t ld_, int64_t col0, int64_t, int64_t kbeg) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    ld = ld_;
+    base = P + kbeg * ld;
+    cols = col0;
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) {
+      const int row = (w * INSTR + i) * RPI + l / CH;
+      voff[i] = (int)((row * ld + col0) * 2) + (((l % CH) ^ km_xor<R>(row)) << 4);
+    }
+  }
+  __device__ void issue(int t, int64_t left, bf16_t *tile, int i) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + (int64_t)t * 64 * ld, (left < 64 ? left : 64) * ld * 2);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * INSTR + i) * RPI * R), 16, voff[i], 0, 0, 0);
+  }
+  __device__ void issue_all(int t, int64_t left, bf16_t *tile) const {
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) issue(t, left, tile, i);
+  }
+};
+
+// The accumulators of a wave's WTM x WTN patch, handed to the epilogue as rows.  Fragment
+// (i, j): lane l holds row 16 i + l % 16, columns 16 j + 4 (l / 16) .. +3.  16 rows at a
+// time go through `st`, this wave's own 16 x (WTN + 4) floats.
+template <int FM, int FN, class Epi>
+__device__ inline void put_rows(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, float *st,
+                                const Epi &epi) {
+  constexpr int W = FN * 16, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
+  const int l = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) *(f32x4 *)(st + (l & 15) * LD + 16 * j + 4 * (l >> 4)) = acc[i][j];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < 16 / RPP; ++p) {
+      const int r = p * RPP + l / LPR, c = (l % LPR) * 8;
+      const f32x4 a = *(const f32x4 *)(st + r * LD + c), b = *(const f32x4 *)(st + r * LD + c + 4);
+      const int64_t m = m0 + 16 * i + r, n = n0 + c;
+      if (m < M && n < N) {
+        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        epi.put(m, n, v, N - n >= 8 ? 8 : (int)(N - n));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+}  // namespace
+
+// bf16 kernel: BM x BN tile over WGM x WGN waves, 64-deep k steps, two LDS stages filled by
+// direct global -> LDS loads, one barrier per step.
+template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, class Epi>
+__global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
+  constexpr int NW = WGM * WGN, BK = 64;
+  constexpr int WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 16, FN = WTN / 16;
+  constexpr int AE = BM * BK, BE = BN * BK;
+  extern __shared__ __align__(16) bf16_t smem[];
+
+  const MmTile tile = mm_tile(a);
+  const int64_t m0 = (int64_t)tile.tm * BM, n0 = (int64_t)tile.tn * BN;
+  const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
+  const int wave = threadIdx.x >> 6;
+  const int wm = (wave / WGN) * WTM, wn = (wave % WGN) * WTN;
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  using SA = typename std::conditional<AKM, StageKM<BM, NW>, StageKC<BM, NW>>::type;
+  using SB = typename std::conditional<BKM, StageKM<BN, NW>, StageKC<BN, NW>>::type;
+  SA sa;
+  SB sb;
+  sa.init((const bf16_t *)a.A, a.lda, m0, a.M, kbeg);
+  sb.init((const bf16_t *)a.B, a.ldb, n0, a.N, kbeg);
+  const int64_t span = kend - kbeg;
+  const int nk = (int)((span + BK - 1) / BK);
+  auto issue = [&](int t) {
+    sa.issue_all(t, span - (int64_t)t * BK, smem + (t & 1) * AE);
+    sb.issue_all(t, span - (int64_t)t * BK, smem + 2 * AE + (t & 1) * BE);
+  };
+  if (nk > 0) issue(0);
+  for (int t = 0; t < nk; ++t) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();  // stage t is in LDS for every wave; the other stage is no longer read
+    const bf16_t *ta = smem + (t & 1) * AE, *tb = smem + 2 * AE + (t & 1) * BE;
+    bf16x8 fa[2][FM], fb[2][FN];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        fa[h][i] = AKM ? frag_km<BM>(ta, wm + 16 * i, 32 * h) : frag_kc<BK>(ta, wm + 16 * i, 32 * h);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        fb[h][j] = BKM ? frag_km<BN>(tb, wn + 16 * j, 32 * h) : frag_kc<BK>(tb, wn + 16 * j, 32 * h);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (t + 1 < nk) issue(t + 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          // operands swapped: lane l then holds C[m = l % 16][n = 4 (l / 16) + 0..3]
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+  }
+  __syncthreads();  // every wave is done with the last stage: the epilogue reuses the LDS
+  if constexpr (Epi::kStats) {
+    epi.template reduce<BM, BN, WGM, WGN>(acc, m0, n0, a.M, a.N, tile.tn, (float *)smem);
+  } else {
+    put_rows<FM, FN>(acc, m0 + wm, n0 + wn, a.M, a.N, (float *)smem + wave * 16 * (WTN + 4), epi.at(tile.split));
+  }
+}
+
+// float32 kernel: 128 x 128 tile over 2 x 2 waves, 16-deep k steps.  Operands pass through
+// registers into k-major LDS rows (any alignment, any tail), two stages; an MFMA of 16 x 16
+// takes 4 k.
+template <bool AKM, bool BKM, class Epi>
+__global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
+  constexpr int BT = 128, BK = 16, LD = BT + 4, ST = BK * LD;
+  __shared__ __align__(16) float smem[4 * ST];
+  const MmTile tile = mm_tile(a);
+  const int64_t m0 = (int64_t)tile.tm * BT, n0 = (int64_t)tile.tn * BT;
+  const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
+  const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // four consecutive floats from p, the first nv in range
+  auto load4 = [](const float *p, int nv) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (nv >= 4) {
+      __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < nv) v[e] = p[e];
+    }
+    return v;
+  };
+  auto cl4 = [](int64_t left) { return left >= 4 ? 4 : left > 0 ? (int)left : 0; };
+  // thread's two 4-float pieces of an operand's 128 x 16 stage
+  auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int64_t k0, f32x4 (&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = tid + 256 * i;
+      if (km) {  // 32 pieces along the rows of one k
+        const int64_t k = k0 + (e >> 5), r = r0 + (e & 31) * 4;
+        v[i] = load4(P + k * ld + r, k < kend ? cl4(rows - r) : 0);
+      } else {   // 4 pieces along k of one row
+        const int64_t r = r0 + (e >> 2), k = k0 + (e & 3) * 4;
+        v[i] = load4(P + r * ld + k, r < rows ? cl4(kend - k) : 0);
+      }
+    }
+  };
+  auto stash = [&](float *st, bool km, const f32x4 (&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = tid + 256 * i;
+      if (km) {
+        *(f32x4 *)(st + (e >> 5) * LD + (e & 31) * 4) = v[i];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st[((e & 3) * 4 + q) * LD + (e >> 2)] = v[i][q];
+      }
+    }
+  };
+  const float *A = (const float *)a.A, *B = (const float *)a.B;
+  const int nk = (int)((kend - kbeg + BK - 1) / BK);
+  f32x4 va[2], vb[2];
+  if (nk > 0) {
+    fetch(A, a.lda, m0, a.M, AKM, kbeg, va);
+    fetch(B, a.ldb, n0, a.N, BKM, kbeg, vb);
+  }
+  for (int t = 0; t < nk; ++t) {
+    float *ta = smem + (t & 1) * 2 * ST, *tb = ta + ST;
+    stash(ta, AKM, va);
+    stash(tb, BKM, vb);
+    // one barrier per step: stage t-1 may still be read by a slower wave, stage t-2, whose
+    // LDS this step has just overwritten, may not (its readers passed the last barrier)
+    __syncthreads();
+    if (t + 1 < nk) {
+      const int64_t k1 = kbeg + (int64_t)(t + 1) * BK;
+      fetch(A, a.lda, m0, a.M, AKM, k1, va);
+      fetch(B, a.ldb, n0, a.N, BKM, k1, vb);
+    }
+#pragma unroll
+    for (int s = 0; s < BK / 4; ++s) {
+      float fa[4], fb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i] = ta[(4 * s + (l >> 4)) * LD + wm + 16 * i + (l & 15)];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[j] = tb[(4 * s + (l >> 4)) * LD + wn + 16 * j + (l & 15)];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  __syncthreads();
+  if constexpr (Epi::kStats) {
+    epi.template reduce<BT, BT, 2, 2>(acc, m0, n0, a.M, a.N, tile.tn, smem);
+  } else {
+    put_rows<4, 4>(acc, m0 + wm, n0 + wn, a.M, a.N, smem + wave * 16 * 68, epi.at(tile.split));
+  }
+}
+
+// Eight consecutive k of an operand row as an MFMA fragment, the first `left` in range.
+__device__ inline bf16x8 row_frag(const bf16_t *p, int64_t left) {
+  u32v4 u = {0u, 0u, 0u, 0u};
+  if (left >= 8) {
+    __builtin_memcpy(&u, p, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) u[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+  }
+  return __builtin_bit_cast(bf16x8, u);
+}
+
+// Few rows (M <= 16, bf16, both operands k-contiguous): bound by reading B once.  Each
+// workgroup takes 16 NG rows of B; its 8 waves are NG groups of 8 / NG, which share a
+// group's k range in 64-deep steps and are joined in LDS.  Operands go from memory into
+// fragments: lane l reads 16 bytes of row l % 16 at k = 8 (l / 16) of each 32-deep step.
+template <int NG, class Epi>
+__global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
+  constexpr int KW = 8 / NG, U = 4;  // U 32-deep steps in flight per wave
+  __shared__ __align__(16) float red[8 * 16 * 20];  // the parts (8 x 256), then the rows (8 x 320)
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int ng = wave / KW, kw = wave % KW;
+  const int64_t n0 = ((int64_t)blockIdx.x * NG + ng) * 16, n = n0 + (l & 15), m = l & 15;
+  const bf16_t *pb = (const bf16_t *)a.B + (n < a.N ? n : a.N - 1) * a.ldb;
+  const bf16_t *pa = (const bf16_t *)a.A + (m < a.M ? m : a.M - 1) * a.lda;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  const int64_t steps = cdiv(a.K, 32 * U);
+  for (int64_t t = kw; t < steps; t += KW) {
+    const int64_t k0 = t * 32 * U + 8 * (l >> 4);
+    bf16x8 fb[U], fa[U];
+    if ((t + 1) * 32 * U <= a.K) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) fb[u] = row_frag(pb + k0 + 32 * u, 8);
+#pragma unroll
+      for (int u = 0; u < U; ++u) fa[u] = row_frag(pa + k0 + 32 * u, 8);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        fb[u] = row_frag(pb + k0 + 32 * u, a.K - k0 - 32 * u);
+        fa[u] = row_frag(pa + k0 + 32 * u, a.K - k0 - 32 * u);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[u], fa[u], acc, 0, 0, 0);
+  }
+  // the k parts of a group, summed in wave order by its first wave
+  if constexpr (KW > 1) {
+    *(f32x4 *)(red + (wave * 64 + l) * 4) = acc;
+    __syncthreads();
+    if (kw == 0) {
+#pragma unroll
+      for (int w = 1; w < KW; ++w) acc += *(const f32x4 *)(red + ((wave + w) * 64 + l) * 4);
+    }
+    __syncthreads();
+  }
+  if (kw) return;
+  // lane l: row l % 16, columns 4 (l / 16) .. +3; pairs of lanes make 8 columns
+  float *st = red + wave * 16 * 20;
+  *(f32x4 *)(st + (l & 15) * 20 + 4 * (l >> 4)) = acc;
+  __builtin_amdgcn_wave_barrier();
+  const int r = l >> 1, c = (l & 1) * 8;
+  if (l < 32 && r < a.M && n0 + c < a.N) {
+    const f32x4 p = *(const f32x4 *)(st + r * 20 + c), q = *(const f32x4 *)(st + r * 20 + c + 4);
+    float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+    epi.put(r, n0 + c, v, a.N - n0 - c >= 8 ? 8 : (int)(a.N - n0 - c));
+  }
+}
+
+// Sum of the float32 partials of a split product, [splits][M][ld] in split order, into the
+// epilogue; one thread per 8 columns.
+template <class Epi>
+__global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, int64_t M, int64_t N, Epi epi) {
+  const int64_t cpr = cdiv(N, 8), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= M * cpr) return;
+  const int64_t m = i / cpr, n = (i % cpr) * 8;
+  const int nv = N - n >= 8 ? 8 : (int)(N - n);
+  float v[8];
+  load8(part + m * N + n, nv, v);
+  for (int s = 1; s < splits; ++s) {
+    float w[8];
+    load8(part + ((int64_t)s * M + m) * N + n, nv, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
+  }
+  epi.put(m, n, v, nv);
+}
+
+// Epilogue that only writes: C[m][n] in T, split s at C + s * stride.  Tag (every epilogue
+// names one, as Tag_) keeps the kernels of two source files apart.
+template <typename T, class Tag>
+struct StoreEpi {
+  static constexpr bool kStats = false, kSplits = true;
+  using Tag_ = Tag;
+  T *C; int64_t ld, stride;
+  __device__ StoreEpi at(int split) const { return StoreEpi{C + split * stride, ld, stride}; }
+  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
+};
+
+// ------------------------------------------------------------------ host side ----
+constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // a grid holds fewer than 2^32 threads
+
+// How a product is tiled: 256 x 256 or 128 x 128 tiles, and over how many k ranges.
+struct MmPlan {
+  int64_t bt = 128, splits = 1, kc = 0;
+  int64_t tiles_m = 0, tiles_n = 0;
+  size_t part_bytes = 0;  // workspace of a split product
+};
+
+struct MmDesc {
+  int64_t M = 0, N = 0, K = 0;
+  const void *A = nullptr; int64_t lda = 0;
+  const void *B = nullptr; int64_t ldb = 0;
+  const char *name = "mm";
+};
+
+inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true) {
+  MmPlan p;
+  if (M <= 0 || N <= 0) return p;  // nothing to launch
+  const int64_t cus = device_cus() > 0 ? device_cus() : 256;
+  const int64_t t256 = cdiv(M, 256) * cdiv(N, 256);
+  p.bt = dt == POETX_BF16 && 4 * t256 >= 3 * cus ? 256 : 128;
+  p.tiles_m = cdiv(M, p.bt);
+  p.tiles_n = cdiv(N, p.bt);
+  p.kc = K;
+  const int64_t tiles = p.tiles_m * p.tiles_n, slots = p.bt == 256 ? cus : 2 * cus;
+  // too few tiles to fill the GPU: split k, each range at least 256 (bf16) deep
+  if (may_split && tiles < slots) {
+    int64_t sp = slots / tiles;
+    const int64_t deep = K / (dt == POETX_BF16 ? 256 : 128);
+    if (sp > deep) sp = deep;
+    if (sp > 32) sp = 32;
+    if (sp >= 2) {
+      p.kc = cdiv(cdiv(K, sp), 64) * 64;
+      p.splits = cdiv(K, p.kc);
+      if (p.splits < 2) { p.splits = 1; p.kc = K; }
+      else p.part_bytes = (size_t)p.splits * M * N * 4;
+    }
+  }
+  return p;
+}
+
+template <int BT, bool AKM, bool BKM, class Epi>
+int mm_launch(const MmArgs &a, const char *name, const Epi &epi, hipStream_t s) {
+  constexpr int WGM = 2, WGN = BT == 256 ? 4 : 2, NT = 64 * WGM * WGN;
+  constexpr size_t lds = (size_t)2 * 2 * BT * 64 * 2;
+  auto kern = &k_mm<BT, BT, WGM, WGN, AKM, BKM, Epi>;
+  static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
+  POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
+  return launch_k(name, s, kern, dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(NT), lds, a, epi);
+}
+
+template <typename T, bool AKM, bool BKM, class Epi>
+int mm_run_as(const MmArgs &a, const MmPlan &p, const char *name, const Epi &epi, hipStream_t s) {
+  if constexpr (sizeof(T) == 4) {
+    return launch_k(name, s, k_mm_f32<AKM, BKM, Epi>, dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(256), 0,
+                    a, epi);
+  } else {
+    if (p.bt == 256) return mm_launch<256, AKM, BKM>(a, name, epi, s);
+    return mm_launch<128, AKM, BKM>(a, name, epi, s);
+  }
+}
+
+// The product of operands of type T (float or bf16_t) through its plan; `part` holds
+// p.part_bytes when the plan splits k.
+template <typename T, bool AKM, bool BKM, class Epi>
+int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStream_t s) {
+  if (d.M <= 0 || d.N <= 0) return POETX_OK;
+  const MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, (int)p.splits, p.kc};
+  if (p.tiles_m * p.tiles_n * p.splits > kMaxTiles) return POETX_ERR_UNSUPPORTED;
+  if (p.splits == 1) return mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s);
+  if constexpr (!Epi::kSplits) {
+    return POETX_ERR_UNSUPPORTED;  // planned without splits
+  } else {
+    POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, StoreEpi<float, typename Epi::Tag_>{part, d.N, d.M * d.N}, s)));
+    return launch_k("mm_join", s, k_mm_join<Epi>, dim3((unsigned)cdiv(d.M * cdiv(d.N, 8), 256)), dim3(256), 0,
+                    (const float *)part, (int)p.splits, d.M, d.N, epi);
+  }
+}
+
+}  // namespace poetx

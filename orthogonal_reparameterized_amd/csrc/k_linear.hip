@@ -1,0 +1,292 @@
+// Dense linear layer with its epilogue:
+//   forward   p = x W^T + bias,  y = act(p) + residual
+//   backward  dp = dy act'(p),  dx = dp W,  dW = dp^T x,  dbias = sum_tokens dp
+// The products run on the kernels of gemm_core.h; bias, activation, residual and the kept
+// pre-activation are part of the product's epilogue, on the float32 accumulators.
+#include "gemm_core.h"
+
+namespace poetx {
+
+struct LinTag {};
+
+// ------------------------------------------------------------- activations ----
+namespace {
+
+constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTanhC = 0.79788456080286536f, kTanhA = 0.044715f;  // sqrt(2 / pi)
+
+__device__ inline float act_value(float p, int act) {
+  switch (act) {
+    case POETX_ACT_RELU: return p < 0.f ? 0.f : p;  // a NaN stays NaN
+    case POETX_ACT_GELU: return 0.5f * p * (1.f + erff(p * kSqrtHalf));
+    case POETX_ACT_GELU_TANH: return 0.5f * p * (1.f + tanhf(kTanhC * (p + kTanhA * p * p * p)));
+    case POETX_ACT_SILU: return p / (1.f + expf(-p));
+    default: return p;
+  }
+}
+
+__device__ inline float act_slope(float p, int act) {
+  switch (act) {
+    case POETX_ACT_RELU: return p > 0.f ? 1.f : 0.f;
+    case POETX_ACT_GELU:
+      return 0.5f * (1.f + erff(p * kSqrtHalf)) + p * kInvSqrt2Pi * expf(-0.5f * p * p);
+    case POETX_ACT_GELU_TANH: {
+      // beyond |p| = 20 the slope is 0 or 1 to every float32 digit, while p^3 could overflow
+      const float q = fminf(fmaxf(p, -20.f), 20.f);
+      const float t = tanhf(kTanhC * (q + kTanhA * q * q * q));
+      return 0.5f * (1.f + t) + 0.5f * q * (1.f - t * t) * kTanhC * (1.f + 3.f * kTanhA * q * q);
+    }
+    case POETX_ACT_SILU: {
+      const float g = 1.f / (1.f + expf(-p));
+      return g * (1.f + p * (1.f - g));
+    }
+    default: return 1.f;
+  }
+}
+
+}  // namespace
+
+template <typename T>
+struct LinEpi {
+  static constexpr bool kStats = false, kSplits = true;
+  using Tag_ = LinTag;
+  T *y, *pre;
+  const T *res;
+  ParamVec bias;
+  int act;
+  int64_t ld;
+  __device__ const LinEpi &at(int) const { return *this; }
+  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const {
+    const int64_t o = m * ld + n;
+    if (bias.p) {
+      float b[8];
+      bias.load(n, nv, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += b[e];
+    }
+    if (pre) store8(pre + o, nv, v);
+    if (act != POETX_ACT_NONE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], act);
+    }
+    if (res) {
+      float r[8];
+      load8(res + o, nv, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+    store8(y + o, nv, v);
+  }
+};
+
+// ------------------------------------------------- dp and the bias gradient ----
+// dp = dy act'(p) in T, rows of ld_out >= cols elements (the rest zero), and its column
+// sums: a workgroup owns 512 columns of a run of rows, a wave one row at a time, 8 columns
+// per lane.  The sums take dp before it is rounded to T.  part: [gridDim.y][cols].
+template <typename T>
+__global__ __launch_bounds__(256) void k_act_grad(const T *dy, const T *pre, int act, int64_t rows, int64_t cols,
+                                                  T *dp, int64_t ld_out, float *part) {
+  __shared__ float red[4][512];
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int64_t c0 = (int64_t)blockIdx.x * 512, c = c0 + l * 8;
+  const int64_t left = cols - c;
+  const int nv = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  const int64_t per = cdiv(rows, (int64_t)gridDim.y), r0 = per * blockIdx.y, r1 = r0 + per < rows ? r0 + per : rows;
+  float sum[8] = {};
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    float v[8];
+    load8(dy + r * cols + c, nv, v);
+    if (act != POETX_ACT_NONE) {
+      float p[8];
+      load8(pre + r * cols + c, nv, p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < nv ? v[e] * act_slope(p[e], act) : 0.f;
+    }
+    // ld_out is a multiple of 8, so a partly valid group is stored whole, with its zeros
+    if (dp && nv) store8(dp + r * ld_out + c, ld_out == cols ? nv : 8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += v[e];
+  }
+  if (!part) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[wave][l * 8 + e] = sum[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256)
+    if (c0 + i < cols)
+      part[(int64_t)blockIdx.y * cols + c0 + i] = ((red[0][i] + red[1][i]) + red[2][i]) + red[3][i];
+}
+
+// out[c] = sum over the parts, in a fixed order: 64 columns per workgroup, 16 threads per
+// column each summing every 16th part.
+__global__ __launch_bounds__(1024) void k_sum_parts(const float *part, int64_t parts, int64_t cols, float *out) {
+  __shared__ float red[16][64];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + c;
+  float s = 0.f;
+  if (col < cols)
+    for (int64_t p = q; p < parts; p += 16) s += part[p * cols + col];
+  red[q][c] = s;
+  __syncthreads();
+  if (q || col >= cols) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) s += red[i][c];
+  out[col] = s;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_fill_zero(T *out, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) out[i] = 0;
+}
+
+// Rows copied to a stride of ld_out elements (a multiple of 8), zero past cols; rows whose
+// target lies outside [0, vocab) zero.
+template <typename T>
+__global__ __launch_bounds__(256) void k_pack_rows(const T *in, int64_t rows, int64_t cols, T *out, int64_t ld_out,
+                                                   const int32_t *target, int64_t vocab) {
+  const int64_t cpr = cdiv(ld_out, 8);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * cpr; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cpr, c = (i % cpr) * 8, left = cols - c;
+    float v[8] = {};
+    const bool keep = !target || (target[r] >= 0 && target[r] < vocab);
+    if (keep) load8(in + r * cols + c, left >= 8 ? 8 : left > 0 ? (int)left : 0, v);
+    store8(out + r * ld_out + c, ld_out - c >= 8 ? 8 : (int)(ld_out - c), v);
+  }
+}
+
+// Workgroups of 256 for `n` independent items, walked with the grid's stride.
+static dim3 stride_grid(int64_t n) {
+  const int64_t g = cdiv(n, 256);
+  return dim3((unsigned)(g < 65536 ? g : 65536));
+}
+
+int pack_rows(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
+              int64_t vocab, int dt, hipStream_t s) {
+  if (rows == 0) return POETX_OK;
+  const dim3 grid = stride_grid(rows * cdiv(ld_out, 8));
+  if (dt == POETX_F32)
+    return launch_k("pack_rows", s, k_pack_rows<float>, grid, dim3(256), 0, (const float *)in, rows, cols,
+                    (float *)out, ld_out, target, vocab);
+  return launch_k("pack_rows", s, k_pack_rows<bf16_t>, grid, dim3(256), 0, (const bf16_t *)in, rows, cols,
+                  (bf16_t *)out, ld_out, target, vocab);
+}
+
+int fill_zero(void *p, int64_t n, int dt, hipStream_t s) {
+  if (n == 0) return POETX_OK;
+  const dim3 grid = stride_grid(n);
+  if (dt == POETX_F32) return launch_k("fill_zero", s, k_fill_zero<float>, grid, dim3(256), 0, (float *)p, n);
+  return launch_k("fill_zero", s, k_fill_zero<bf16_t>, grid, dim3(256), 0, (bf16_t *)p, n);
+}
+
+// ------------------------------------------------------------------- host ----
+namespace {
+
+int64_t round8(int64_t v) { return (v + 7) & ~(int64_t)7; }
+
+// A bf16 operand whose rows are not a multiple of 16 bytes is copied to padded rows, which
+// the direct global -> LDS loads need; others (and float32 ones) are used as they are.
+struct Packed {
+  const void *p = nullptr;
+  int64_t ld = 0;
+};
+int packed(const void *in, int64_t rows, int64_t cols, int dt, Arena &ar, bool measure, hipStream_t s, Packed &o) {
+  o.p = in;
+  o.ld = cols;
+  if (dt == POETX_F32 || cols % 8 == 0) return POETX_OK;
+  o.ld = round8(cols);
+  void *q = ar.take((size_t)rows * o.ld * 2);
+  o.p = q;
+  return measure ? POETX_OK : pack_rows(in, rows, cols, q, o.ld, nullptr, 0, dt, s);
+}
+
+template <typename T>
+int fwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  const LinEpi<T> epi{(T *)d.y, (T *)d.pre, (const T *)d.residual, {d.bias, d.bias_bf16}, d.act, d.d_out};
+  MmDesc m;
+  m.M = d.n; m.N = d.d_out; m.K = d.d_in; m.name = "linear_fwd";
+  m.A = d.x; m.lda = d.d_in; m.B = d.w; m.ldb = d.d_in;
+  if constexpr (sizeof(T) == 2) {
+    if (d.n <= 16) {  // reading W bounds these: no LDS tiles, any alignment
+      if (measure) return POETX_OK;
+      MmArgs a{m.M, m.N, m.K, m.A, m.lda, m.B, m.ldb, 1, 1, 1, m.K};
+      const int64_t groups = cdiv(d.d_out, 16);
+      if (groups >= 1024)
+        return launch_k(m.name, s, k_mm_few<2, LinEpi<T>>, dim3((unsigned)cdiv(groups, 2)), dim3(512), 0, a, epi);
+      return launch_k(m.name, s, k_mm_few<1, LinEpi<T>>, dim3((unsigned)groups), dim3(512), 0, a, epi);
+    }
+  }
+  Packed x, w;
+  POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));
+  POETX_TRY(packed(d.w, d.d_out, d.d_in, d.dt, ar, measure, s, w));
+  m.A = x.p; m.lda = x.ld; m.B = w.p; m.ldb = w.ld;
+  if (d.dt == POETX_BF16) m.K = round8(d.d_in);  // the padding is zero
+  const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
+  float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
+  if (measure) return POETX_OK;
+  return mm_run<T, false, false>(m, p, part, epi, s);
+}
+
+// dx = dp W: dp k-contiguous, W k-major;  dW = dp^T x: both k-major
+template <typename T>
+int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  const bool b16 = d.dt == POETX_BF16;
+  const void *dp = d.dy;
+  int64_t ld = d.d_out;
+  const bool products = d.dx || d.dw;
+  const bool copy = products && (d.act != POETX_ACT_NONE || (b16 && d.d_out % 8));
+  T *dpw = nullptr;
+  if (copy) {
+    if (b16) ld = round8(d.d_out);
+    dpw = (T *)ar.take((size_t)d.n * ld * sizeof(T));
+    dp = dpw;
+  }
+  if (copy || d.dbias) {
+    const int64_t cb = cdiv(d.d_out, 512), cus = device_cus() > 0 ? device_cus() : 256;
+    int64_t parts = cdiv(4 * cus, cb);
+    if (parts > cdiv(d.n, 16)) parts = cdiv(d.n, 16);
+    if (parts > 1024) parts = 1024;
+    float *part = d.dbias ? (float *)ar.take((size_t)(parts > 0 ? parts : 1) * d.d_out * 4) : nullptr;
+    if (!measure) {
+      if (parts > 0)
+        POETX_TRY(launch_k("linear_act_grad", s, k_act_grad<T>, dim3((unsigned)cb, (unsigned)parts), dim3(256), 0,
+                           (const T *)d.dy, (const T *)d.saved_pre, d.act, d.n, d.d_out, dpw, ld, part));
+      if (d.dbias)
+        POETX_TRY(launch_k("linear_bias_grad", s, k_sum_parts, dim3((unsigned)cdiv(d.d_out, 64)), dim3(1024), 0,
+                           (const float *)part, parts, d.d_out, d.dbias));
+    }
+  }
+  if (d.dx) {
+    Packed w;
+    POETX_TRY(packed(d.w, d.d_out, d.d_in, d.dt, ar, measure, s, w));
+    MmDesc m;
+    m.M = d.n; m.N = d.d_in; m.K = d.d_out; m.name = "linear_dx";
+    m.A = dp; m.lda = ld; m.B = w.p; m.ldb = w.ld;
+    const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
+    float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
+    if (!measure) POETX_TRY((mm_run<T, false, true>(m, p, part, StoreEpi<T, LinTag>{(T *)d.dx, d.d_in, 0}, s)));
+  }
+  if (d.dw) {
+    if (d.n == 0) return measure ? POETX_OK : fill_zero(d.dw, d.d_out * d.d_in, d.dt, s);
+    Packed x;
+    POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));
+    MmDesc m;
+    m.M = d.d_out; m.N = d.d_in; m.K = d.n; m.name = "linear_dw";
+    m.A = dp; m.lda = ld; m.B = x.p; m.ldb = x.ld;
+    const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
+    float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
+    if (!measure) POETX_TRY((mm_run<T, true, true>(m, p, part, StoreEpi<T, LinTag>{(T *)d.dw, d.d_in, 0}, s)));
+  }
+  return POETX_OK;
+}
+
+}  // namespace
+
+int linear_forward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  if (d.n == 0) return POETX_OK;
+  return d.dt == POETX_F32 ? fwd_t<float>(d, ar, measure, s) : fwd_t<bf16_t>(d, ar, measure, s);
+}
+
+int linear_backward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  return d.dt == POETX_F32 ? bwd_t<float>(d, ar, measure, s) : bwd_t<bf16_t>(d, ar, measure, s);
+}
+
+}  // namespace poetx

@@ -1,0 +1,368 @@
+// Softmax cross entropy of a linear head, without keeping the logits l = h W^T:
+//   forward   lse_i = log sum_v exp l_iv,  loss_i = lse_i - l_i,t(i)
+//   backward  dl_iv = (exp(l_iv - lse_i) - [v = t(i)]) dloss_i,  dh = dl W,  dW = dl^T h
+// A row whose target lies outside the vocabulary takes no part: loss 0, dl 0.
+//
+// Forward: the product's epilogue reduces each row of a tile to its maximum and its sum of
+// exp(l - maximum), 8 bytes per row and 256 columns; k_xent_join joins them.  Backward: the
+// logits of a piece of the vocabulary are computed again and leave the epilogue as dl (bf16
+// for bf16 operands, the operand type of the two products that read it), then dh += dl W and
+// dW of the piece follow while dl is in the caches.  8 n d v flops in all, where keeping the
+// logits would take 6 n d v and n v values of memory.  Bound by the matrix cores for many
+// tokens and by reading W for few.
+#include "gemm_core.h"
+
+namespace poetx {
+
+struct XentTag {};
+
+namespace {
+// (max, sum of exp(l - max)) of two sets of logits.  An empty set has max = -inf, sum = 0.
+__device__ inline void join_stats(float &m, float &s, float m2, float s2) {
+  const float t = fmaxf(m, m2);
+  const float ref = fabsf(t) == INFINITY ? 0.f : t;
+  s = s * __expf(m - ref) + s2 * __expf(m2 - ref);
+  m = t;
+}
+__device__ inline float safe_ref(float m) { return fabsf(m) == INFINITY ? 0.f : m; }
+}  // namespace
+
+// part[tile][row] = (max, sum) over the tile's columns; at_target[row] = l of the target.
+struct XentStats {
+  static constexpr bool kStats = true, kSplits = false;
+  using Tag_ = XentTag;
+  float2 *part;
+  const int32_t *target;
+  float *at_target;
+  int64_t v0;     // first vocabulary entry of this launch
+  int tile0;      // first row of `part`
+  __device__ const XentStats &at(int) const { return *this; }
+
+  template <int BM, int BN, int WGM, int WGN, int FM, int FN>
+  __device__ void reduce(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, int tn,
+                         float *lds) const {
+    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
+    const int64_t nb = n0 + wn + 4 * (l >> 4);  // this lane's columns: nb + 16 j + e
+    float2 *st = (float2 *)lds;                 // [WGN][BM]
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = wm + 16 * i + (l & 15);
+      const int64_t m = m0 + r;
+      const int64_t t = m < M ? (int64_t)target[m] - v0 - nb : -1;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = nb + 16 * j + e < N ? acc[i][j][e] : -INFINITY;
+          if (t == 16 * j + e && nb + t < N) at_target[m] = v;
+          mx = fmaxf(mx, v);
+        }
+      const float ref = safe_ref(mx);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s += nb + 16 * j + e < N ? __expf(acc[i][j][e] - ref) : 0.f;
+#pragma unroll
+      for (int o = 16; o <= 32; o <<= 1) {
+        const float m2 = __shfl_xor(mx, o), s2 = __shfl_xor(s, o);
+        join_stats(mx, s, m2, s2);
+      }
+      if (l < 16) st[(wave % WGN) * BM + r] = make_float2(mx, s);
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < BM; r += 64 * WGM * WGN) {
+      if (m0 + r >= M) continue;
+      float2 p = st[r];
+#pragma unroll
+      for (int w = 1; w < WGN; ++w) join_stats(p.x, p.y, st[w * BM + r].x, st[w * BM + r].y);
+      part[(int64_t)(tile0 + tn) * M + m0 + r] = p;
+    }
+  }
+};
+
+// dl of a piece of the vocabulary, rows of ld elements (a multiple of 8 for bf16, zeros
+// past the piece).  Rounding dl to bf16 is the products' operand precision: relative 2^-9
+// per element, of independent sign.
+template <typename T>
+struct XentDl {
+  static constexpr bool kStats = false, kSplits = false;
+  using Tag_ = XentTag;
+  T *dl;
+  int64_t ld;
+  const int32_t *target;
+  const float *lse, *dloss;
+  int64_t v0, vocab;
+  __device__ const XentDl &at(int) const { return *this; }
+  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const {
+    const int64_t t = target[m];
+    const bool on = t >= 0 && t < vocab;
+    const float z = lse[m], g = dloss[m];
+    const int64_t q = t - v0 - n;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = __expf(v[e] - z) - (q == e ? 1.f : 0.f);
+      v[e] = on && e < nv ? p * g : 0.f;
+    }
+    store8(dl + m * ld + n, sizeof(T) == 2 ? 8 : nv, v);
+  }
+};
+
+// dh over the pieces: float32 sums in `sum` between the first and the last piece.
+template <typename T>
+struct XentDh {
+  static constexpr bool kStats = false, kSplits = true;
+  using Tag_ = XentTag;
+  float *sum;
+  T *dh;
+  int64_t ld;
+  int first, last;
+  __device__ const XentDh &at(int) const { return *this; }
+  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const {
+    const int64_t o = m * ld + n;
+    if (!first) {
+      float w[8];
+      load8(sum + o, nv, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += w[e];
+    }
+    if (last) store8(dh + o, nv, v);
+    else store8(sum + o, nv, v);
+  }
+};
+
+// Few tokens (n <= 16, bf16): every wave walks groups of 16 vocabulary rows, a whole k range
+// each, and keeps a running (max, sum) per lane (row l % 16, its 4 columns of each group);
+// one partial per workgroup.  Bound by reading W once.
+__global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
+  constexpr int U = 4;
+  __shared__ float2 st[8][16];
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int64_t m = l & 15;
+  const bf16_t *pa = (const bf16_t *)a.A + (m < a.M ? m : a.M - 1) * a.lda;
+  const int64_t t = m < a.M ? (int64_t)epi.target[m] : -1;
+  const int64_t groups = cdiv(a.N, 16);
+  float mx = -INFINITY, s = 0.f;
+  for (int64_t g = (int64_t)blockIdx.x * 8 + wave; g < groups; g += (int64_t)gridDim.x * 8) {
+    const int64_t n = g * 16 + (l & 15);
+    const bf16_t *pb = (const bf16_t *)a.B + (n < a.N ? n : a.N - 1) * a.ldb;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    int64_t k0 = 8 * (l >> 4);
+    int64_t k = 0;
+    for (; k + 32 * U <= a.K; k += 32 * U) {
+      bf16x8 fb[U], fa[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) fb[u] = row_frag(pb + k + k0 + 32 * u, 8);
+#pragma unroll
+      for (int u = 0; u < U; ++u) fa[u] = row_frag(pa + k + k0 + 32 * u, 8);
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[u], fa[u], acc, 0, 0, 0);
+    }
+    for (; k < a.K; k += 32) {
+      const bf16x8 fb = row_frag(pb + k + k0, a.K - k - k0), fa = row_frag(pa + k + k0, a.K - k - k0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa, acc, 0, 0, 0);
+    }
+    // lane l: row l % 16, columns n0 .. n0 + 3
+    const int64_t n0 = g * 16 + 4 * (l >> 4);
+    float m2 = -INFINITY, s2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n0 + e >= a.N) continue;
+      if (t == n0 + e) epi.at_target[m] = acc[e];
+      m2 = fmaxf(m2, acc[e]);
+    }
+    const float ref = safe_ref(m2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s2 += n0 + e < a.N ? __expf(acc[e] - ref) : 0.f;
+    join_stats(mx, s, m2, s2);
+  }
+#pragma unroll
+  for (int o = 16; o <= 32; o <<= 1) {
+    const float m2 = __shfl_xor(mx, o), s2 = __shfl_xor(s, o);
+    join_stats(mx, s, m2, s2);
+  }
+  if (l < 16) st[wave][l] = make_float2(mx, s);
+  __syncthreads();
+  if (threadIdx.x < a.M) {
+    float2 p = st[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) join_stats(p.x, p.y, st[w][threadIdx.x].x, st[w][threadIdx.x].y);
+    epi.part[(int64_t)blockIdx.x * a.M + threadIdx.x] = p;
+  }
+}
+
+// lse and loss from the partials [tiles][n]: 16 rows per workgroup, 16 threads per row.
+__global__ __launch_bounds__(256) void k_xent_join(const float2 *part, int64_t tiles, int64_t n, const int32_t *target,
+                                                   int64_t vocab, const float *at_target, float *loss, float *lse) {
+  __shared__ float2 red[16][16];
+  const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int64_t row = (int64_t)blockIdx.x * 16 + c;
+  float m = -INFINITY, s = 0.f;
+  if (row < n)
+    for (int64_t t = q; t < tiles; t += 16) {
+      const float2 p = part[t * n + row];
+      join_stats(m, s, p.x, p.y);
+    }
+  red[q][c] = make_float2(m, s);
+  __syncthreads();
+  if (q || row >= n) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) join_stats(m, s, red[i][c].x, red[i][c].y);
+  const float z = safe_ref(m) + logf(s);
+  lse[row] = z;
+  const int32_t t = target[row];
+  loss[row] = t >= 0 && t < vocab ? z - at_target[row] : 0.f;
+}
+
+namespace {
+
+int64_t round8(int64_t v) { return (v + 7) & ~(int64_t)7; }
+
+// Vocabulary entries per piece of the backward: dl of a piece takes at most 512 MB (more
+// only where 2048 entries already do), a multiple of 256 entries.
+int64_t piece_of(const XentDesc &d) {
+  const int64_t es = d.dt == POETX_F32 ? 4 : 2;
+  int64_t p = ((int64_t)512 << 20) / (d.n * es) & ~(int64_t)255;
+  if (p < 2048) p = 2048;
+  return p < d.v ? p : d.v;
+}
+
+// A bf16 operand whose rows are not a multiple of 16 bytes is read from padded copies: h
+// whole, W one piece at a time.
+bool pads(const XentDesc &d) { return d.dt == POETX_BF16 && d.d % 8; }
+
+struct Operands {
+  const void *h = nullptr;
+  int64_t ld = 0;
+  void *wp = nullptr;  // one padded piece of W
+};
+int operands(const XentDesc &d, int64_t piece, Arena &ar, bool measure, hipStream_t s, Operands &o) {
+  o.h = d.h;
+  o.ld = d.d;
+  if (!pads(d)) return POETX_OK;
+  o.ld = round8(d.d);
+  void *hp = ar.take((size_t)d.n * o.ld * 2);
+  o.wp = ar.take((size_t)piece * o.ld * 2);
+  o.h = hp;
+  return measure ? POETX_OK : pack_rows(d.h, d.n, d.d, hp, o.ld, nullptr, 0, d.dt, s);
+}
+int w_piece(const XentDesc &d, const Operands &o, int64_t v0, int64_t vc, hipStream_t s, const void **w) {
+  const int64_t es = d.dt == POETX_F32 ? 4 : 2;
+  *w = (const char *)d.w + v0 * d.d * es;
+  if (!o.wp) return POETX_OK;
+  POETX_TRY(pack_rows(*w, vc, d.d, o.wp, o.ld, nullptr, 0, d.dt, s));
+  *w = o.wp;
+  return POETX_OK;
+}
+
+MmDesc logits_desc(const XentDesc &d, const Operands &o, const void *w, int64_t vc, const char *name) {
+  MmDesc m;
+  m.M = d.n; m.N = vc; m.K = pads(d) ? o.ld : d.d; m.name = name;
+  m.A = o.h; m.lda = o.ld; m.B = w; m.ldb = o.ld;
+  return m;
+}
+
+template <typename T>
+int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  const int64_t piece = piece_of(d);
+  Operands o;
+  POETX_TRY(operands(d, piece, ar, measure, s, o));
+  // dW reads h with the rows that take no part as zeros: their dl is zero, but zero times an
+  // infinity or a NaN in such a row would not be
+  const void *hz = nullptr;
+  if (d.dw) {
+    hz = ar.take((size_t)d.n * o.ld * sizeof(T));
+    if (!measure) POETX_TRY(pack_rows(d.h, d.n, d.d, (void *)hz, o.ld, d.target, d.v, d.dt, s));
+  }
+  const int64_t ldl = sizeof(T) == 2 ? round8(piece) : piece;
+  T *dl = (T *)ar.take((size_t)d.n * ldl * sizeof(T));
+  float *sum = d.dh && piece < d.v ? (float *)ar.take((size_t)d.n * d.d * 4) : nullptr;
+  // partials of split products: of whole pieces and of the last one
+  size_t part_bytes = 0;
+  const int64_t last = d.v % piece ? d.v % piece : piece;
+  for (const int64_t vc : {piece, last}) {
+    const size_t a = d.dh ? mm_plan(d.n, d.d, vc, d.dt).part_bytes : 0;
+    const size_t b = d.dw ? mm_plan(vc, d.d, d.n, d.dt).part_bytes : 0;
+    part_bytes = a > part_bytes ? a : part_bytes;
+    part_bytes = b > part_bytes ? b : part_bytes;
+  }
+  float *part = part_bytes ? (float *)ar.take(part_bytes) : nullptr;
+  if (measure) return POETX_OK;
+  for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
+    const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
+    const void *w = nullptr;
+    POETX_TRY(w_piece(d, o, v0, vc, s, &w));
+    const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits");
+    POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt, false), nullptr,
+                                    XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, v0, d.v}, s)));
+    if (d.dh) {
+      MmDesc g;
+      g.M = d.n; g.N = d.d; g.K = vc; g.name = "xent_dh";
+      g.A = dl; g.lda = ldl; g.B = w; g.ldb = o.ld;
+      POETX_TRY((mm_run<T, false, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
+                                     XentDh<T>{sum, (T *)d.dh, d.d, v0 == 0, v0 + vc == d.v}, s)));
+    }
+    if (d.dw) {
+      MmDesc g;
+      g.M = vc; g.N = d.d; g.K = d.n; g.name = "xent_dw";
+      g.A = dl; g.lda = ldl; g.B = hz; g.ldb = o.ld;
+      POETX_TRY((mm_run<T, true, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
+                                    StoreEpi<T, XentTag>{(T *)d.dw + v0 * d.d, d.d, 0}, s)));
+    }
+  }
+  return POETX_OK;
+}
+
+template <typename T>
+int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  const int64_t cus = device_cus() > 0 ? device_cus() : 256;
+  float *at = (float *)ar.take((size_t)d.n * 4);
+  int64_t tiles = 0;
+  float2 *part = nullptr;
+  if (sizeof(T) == 2 && d.n <= 16) {
+    tiles = cdiv(d.v, 128) < 2 * cus ? cdiv(d.v, 128) : 2 * cus;
+    part = (float2 *)ar.take((size_t)tiles * d.n * 8);
+    if (measure) return POETX_OK;
+    const MmArgs a{d.n, d.v, d.d, d.h, d.d, d.w, d.d, 1, 1, 1, d.d};
+    POETX_TRY(launch_k("xent_few", s, k_xent_few, dim3((unsigned)tiles), dim3(512), 0, a,
+                       XentStats{part, d.target, at, 0, 0}));
+  } else {
+    const int64_t piece = pads(d) ? piece_of(d) : d.v;
+    Operands o;
+    POETX_TRY(operands(d, piece, ar, measure, s, o));
+    // partials: one row per n-tile of every piece (pieces are multiples of the tile width)
+    for (int64_t v0 = 0; v0 < d.v; v0 += piece)
+      tiles += mm_plan(d.n, d.v - v0 < piece ? d.v - v0 : piece, d.d, d.dt, false).tiles_n;
+    part = (float2 *)ar.take((size_t)tiles * d.n * 8);
+    if (measure) return POETX_OK;
+    int64_t t0 = 0;
+    for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
+      const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
+      const void *w = nullptr;
+      POETX_TRY(w_piece(d, o, v0, vc, s, &w));
+      const MmDesc m = logits_desc(d, o, w, vc, "xent_fwd");
+      const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt, false);
+      POETX_TRY((mm_run<T, false, false>(m, p, nullptr, XentStats{part, d.target, at, v0, (int)t0}, s)));
+      t0 += p.tiles_n;
+    }
+  }
+  return launch_k("xent_join", s, k_xent_join, dim3((unsigned)cdiv(d.n, 16)), dim3(256), 0, (const float2 *)part,
+                  tiles, d.n, d.target, d.v, (const float *)at, d.loss, d.lse);
+}
+
+}  // namespace
+
+int xent_forward(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  if (d.n == 0) return POETX_OK;
+  return d.dt == POETX_F32 ? fwd_t<float>(d, ar, measure, s) : fwd_t<bf16_t>(d, ar, measure, s);
+}
+
+int xent_backward(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  if (d.n == 0) return measure || !d.dw ? POETX_OK : fill_zero(d.dw, d.v * d.d, d.dt, s);
+  return d.dt == POETX_F32 ? bwd_t<float>(d, ar, measure, s) : bwd_t<bf16_t>(d, ar, measure, s);
+}
+
+}  // namespace poetx

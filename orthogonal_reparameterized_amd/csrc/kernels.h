@@ -201,4 +201,59 @@ int cnp_chain(const CnpChainArgs &a, hipStream_t s);
 bool cnp_bwd5_supported(int64_t b);
 int cnp_bwd5(const CnpChainArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// Layer norm (k_norm.hip): rows of d <= 16384 elements.
+// ---------------------------------------------------------------------------
+constexpr int64_t kNormMaxD = 16384;
+struct NormDesc {
+  int64_t n = 0, d = 0;
+  int dt = POETX_BF16, p_bf16 = 0;             // dtype of x, y, dy, dx, dres; of gamma and beta
+  const void *x = nullptr, *dy = nullptr, *dres = nullptr;
+  const void *gamma = nullptr, *beta = nullptr;
+  float eps = 0.f;
+  void *out = nullptr;                         // y, or dx
+  float *mean = nullptr, *rstd = nullptr;      // written forward (nullable), read backward
+};
+int norm_forward(const NormDesc &n, hipStream_t s);
+// partials of dgamma and dbeta, [parts][2][d] float32 (part null: neither is wanted)
+int64_t norm_bwd_parts(int64_t n, int64_t d);
+int norm_backward(const NormDesc &n, float *part, float *dgamma, float *dbeta, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Dense linear layer (k_linear.hip).  Operands and results contiguous, any widths.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;  // 32-bit offsets within a tile's rows
+struct LinDesc {
+  int64_t n = 0, d_in = 0, d_out = 0;
+  int dt = POETX_BF16, act = POETX_ACT_NONE, bias_bf16 = 0;
+  const void *x = nullptr, *w = nullptr, *bias = nullptr, *residual = nullptr;
+  void *y = nullptr, *pre = nullptr;           // forward results
+  const void *dy = nullptr, *saved_pre = nullptr;
+  void *dx = nullptr, *dw = nullptr;           // backward results, each nullable
+  float *dbias = nullptr;
+};
+// With measure == true only the workspace is carved (nothing is launched).
+int linear_forward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s);
+int linear_backward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s);
+// out[r][c] = in[r][c] for c < cols, 0 up to ld_out, for bf16 rows; with `target`, rows
+// whose target lies outside [0, vocab) become zero
+int pack_rows(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
+              int64_t vocab, int dt, hipStream_t s);
+int fill_zero(void *p, int64_t n, int dt, hipStream_t s);  // n elements
+
+// ---------------------------------------------------------------------------
+// Softmax cross entropy of a linear head (k_xent.hip), in pieces of the vocabulary.
+// ---------------------------------------------------------------------------
+struct XentDesc {
+  int64_t n = 0, d = 0, v = 0;
+  int dt = POETX_BF16;
+  const void *h = nullptr, *w = nullptr;
+  const int32_t *target = nullptr;
+  float *loss = nullptr, *lse = nullptr;       // forward results
+  const float *lse_in = nullptr, *dloss = nullptr;
+  void *dh = nullptr, *dw = nullptr;           // backward results, each nullable
+};
+int xent_forward(const XentDesc &d, Arena &ar, bool measure, hipStream_t s);
+int xent_backward(const XentDesc &d, Arena &ar, bool measure, hipStream_t s);
+
 }  // namespace poetx

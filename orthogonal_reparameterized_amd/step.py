@@ -133,3 +133,60 @@ class LayerStep:
                                      eps=eps, gamma=gamma, saved_x=self.saved_x, dx=self.dx,
                                      dtheta_r=self.dtheta_r if keep_dtheta else None,
                                      dtheta_p=self.dtheta_p if keep_dtheta else None)
+
+
+class BlockStep:
+    """One training step of a pre-norm block with a vocabulary head around a POET-X layer:
+
+        a = norm(x0),  z = POET-X(a),  u = act(z . w1^T + b1),  y = u . w2^T + b2 + x0,
+        h = norm(y),   loss_i = cross entropy of h_i . head^T at target_i
+
+    and the gradients of sum_i dloss_i loss_i.  ``layer`` is a LayerStep whose layer maps d to
+    d; the dense weights (w1 [f][d], w2 [d][f], head [vocab][d]) are in its activation dtype,
+    the vectors (norm gammas and betas, b1, b2) in float32 or bf16.  Marshalling only.
+    """
+
+    NAMES = ("gamma1", "beta1", "w1", "b1", "w2", "b2", "gamma2", "beta2", "head")
+
+    def __init__(self, layer: LayerStep, params: dict, act: str = "gelu", eps: float = 1e-5):
+        missing = [k for k in self.NAMES if k not in params]
+        if missing:
+            raise ValueError(f"params lacks {missing}")
+        if layer.wl.d_in != layer.wl.d_out:
+            raise ValueError("the block's layer maps its width to itself")
+        self.layer, self.p, self.act, self.eps = layer, params, act, eps
+
+    def forward(self, x0, target):
+        p, s = self.p, {"x0": x0, "target": target}
+        s["a"], s["mean1"], s["rstd1"] = B.poetx_layernorm_forward(x0, p["gamma1"], p["beta1"], self.eps)
+        self.layer.cnp()
+        s["z"], s["saved_b"] = B.poetx_forward(self.layer.layer, s["a"])
+        s["u"], s["pre"] = B.poetx_linear_forward(s["z"], p["w1"], p["b1"], None, self.act, save_pre=True)
+        s["y"], _ = B.poetx_linear_forward(s["u"], p["w2"], p["b2"], x0)
+        s["h"], s["mean2"], s["rstd2"] = B.poetx_layernorm_forward(s["y"], p["gamma2"], p["beta2"], self.eps)
+        s["loss"], s["lse"] = B.poetx_xent_forward(s["h"], p["head"], target)
+        return s
+
+    def backward(self, s, dloss):
+        """Gradients by name: the parameters', theta_r, theta_p and x0."""
+        p, g = self.p, {}
+        top = B.poetx_xent_backward(s["h"], p["head"], s["target"], s["lse"], dloss)
+        g["head"] = top["dw"]
+        n2 = B.poetx_layernorm_backward(s["y"], top["dh"], p["gamma2"], s["mean2"], s["rstd2"])
+        g["gamma2"], g["beta2"] = n2["dgamma"], n2["dbeta"]
+        dy = n2["dx"]
+        l2 = B.poetx_linear_backward(s["u"], p["w2"], dy)
+        g["w2"], g["b2"] = l2["dw"], l2["dbias"]
+        l1 = B.poetx_linear_backward(s["z"], p["w1"], l2["dx"], s["pre"], self.act)
+        g["w1"], g["b1"] = l1["dw"], l1["dbias"]
+        mid = B.poetx_backward(self.layer.layer, s["a"], l1["dx"], s["saved_b"])
+        g["theta_r"], g["theta_p"] = mid["dtheta_r"], mid["dtheta_p"]
+        # x0 reaches y through the residual as well: dy joins in the norm's backward
+        n1 = B.poetx_layernorm_backward(s["x0"], mid["dx"], p["gamma1"], s["mean1"], s["rstd1"], dres=dy)
+        g["gamma1"], g["beta1"], g["x0"] = n1["dgamma"], n1["dbeta"], n1["dx"]
+        return g
+
+    def step(self, x0, target, dloss):
+        """(loss per token, gradients by name)."""
+        s = self.forward(x0, target)
+        return s["loss"], self.backward(s, dloss)
