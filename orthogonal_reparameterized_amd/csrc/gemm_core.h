@@ -114,24 +114,33 @@ struct StageKM {
   }
 };
 
-// The accumulators of a wave's WTM x WTN patch, handed to the epilogue as rows.  Fragment
-// (i, j): lane l holds row 16 i + l % 16, columns 16 j + 4 (l / 16) .. +3.  16 rows at a
-// time go through `st`, this wave's own 16 x (WTN + 4) floats.
-template <int FM, int FN, class Epi>
-__device__ inline void put_rows(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, float *st,
+// Accumulator layout of one MFMA result with the operands swapped (B fragment first): lane l
+// holds row l % ROWS; element 4 q + e is column 8 q + 4 (l / ROWS) + e.
+template <class V> struct FragOf;
+template <> struct FragOf<f32x4> { static constexpr int ROWS = 16, QUADS = 1; };    // 16 x 16
+
+// The accumulators of a wave's patch (FM x FN results), handed to the epilogue as rows.  One
+// row of results at a time goes through `st`, this wave's own ROWS x (columns + 4) floats.
+template <int FM, int FN, class V, class Epi>
+__device__ inline void put_rows(const V (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, float *st,
                                 const Epi &epi) {
-  constexpr int W = FN * 16, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
+  constexpr int R = FragOf<V>::ROWS, Q = FragOf<V>::QUADS;
+  constexpr int W = FN * R, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
   const int l = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) *(f32x4 *)(st + (l & 15) * LD + 16 * j + 4 * (l >> 4)) = acc[i][j];
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        *(f32x4 *)(st + (l % R) * LD + R * j + 8 * q + 4 * (l / R)) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int p = 0; p < 16 / RPP; ++p) {
+    for (int p = 0; p < R / RPP; ++p) {
       const int r = p * RPP + l / LPR, c = (l % LPR) * 8;
       const f32x4 a = *(const f32x4 *)(st + r * LD + c), b = *(const f32x4 *)(st + r * LD + c + 4);
-      const int64_t m = m0 + 16 * i + r, n = n0 + c;
+      const int64_t m = m0 + R * i + r, n = n0 + c;
       if (m < M && n < N) {
         float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         epi.put(m, n, v, N - n >= 8 ? 8 : (int)(N - n));
@@ -207,6 +216,211 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
     epi.template reduce<BM, BN, WGM, WGN>(acc, m0, n0, a.M, a.N, tile.tn, (float *)smem);
   } else {
     put_rows<FM, FN>(acc, m0 + wm, n0 + wn, a.M, a.N, (float *)smem + wave * 16 * (WTN + 4), epi.at(tile.split));
+  }
+}
+
+// 256 x 256 tile, 8 waves (2 x 4, 128 x 64 each), 64-deep k steps: the large products.
+//
+// The tile's operands are kept in LDS as half tiles of 128 rows (A0, A1, B0, B1; 16 KB each),
+// two k steps of them.  A wave owns 64 rows of each A half and 32 columns of each B half, so a
+// k step is two phases of 32 MFMAs, one per A half:
+//
+//     phase   reads             loads                multiplies
+//       0     A0(t), B1(t)      A1(t+1), B0(t+2)     A0 B0, A0 B1
+//       1     A1(t), B0(t+1)    A0(t+2), B1(t+2)     A1 B0, A1 B1
+//
+// The waves form two groups of four (one wave of each per SIMD); group 1 runs one barrier
+// behind group 0, so while one group multiplies the other reads: the matrix cores of every
+// SIMD stay fed.  Every half tile is loaded three phases before it is read, into LDS that was
+// last read in the phase before.  A phase ends its reading part by waiting for its own LDS
+// reads and for all but its 8 newest loads (two phases'), so after the barrier the halves that
+// the next phase reads have landed for all waves, and those just read may be overwritten.
+// Loads past the k range read zeros.
+template <int HALF_ROWS, bool KM>
+struct Half;
+
+// rows of a half tile: local row r of half h is tile row (r / RUN) 2 RUN + h RUN + r % RUN
+// (RUN = 64 for A, 32 for B), so that a wave's rows of both halves are consecutive
+template <int RUN>
+struct Half<RUN, false> {
+  int voff[2], step;
+  int64_t span;
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ void init(const bf16_t *P, int64_t ld, int64_t row0, int64_t rows, int64_t kbeg, int64_t span_) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int64_t left = rows - row0 < 256 ? rows - row0 : 256;
+    rs = make_rsrc(P + row0 * ld, left * ld * 2);
+    step = (int)(RUN * ld * 2);
+    span = span_;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (w * 2 + i) * 8 + (l >> 3), row = (r / RUN) * 2 * RUN + r % RUN;
+      voff[i] = (int)((row * ld + kbeg) * 2) + (((l & 7) ^ kc_key<64>(r)) << 4);
+    }
+  }
+  __device__ void issue(int t, int h, bf16_t *tile) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
+    const int64_t left = span - (int64_t)t * 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int off = voff[i] + t * 128 + h * step;
+      if (left < 64) {
+        const int r = (w * 2 + i) * 8 + (l >> 3);
+        if ((((l & 7) ^ kc_key<64>(r)) << 3) >= left) off = kPast;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * 2 + i) * 512), 16, off, 0, 0, 0);
+    }
+  }
+  __device__ static bf16x8 frag(const bf16_t *tile, int r0, int ks) { return frag_kc<64>(tile, r0, ks); }
+};
+
+template <int RUN>
+struct Half<RUN, true> {
+  int voff[2];
+  const bf16_t *base;
+  int64_t ld, span;
+  __device__ void init(const bf16_t *P, int64_t ld_, int64_t col0, int64_t, int64_t kbeg, int64_t span_) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    ld = ld_;
+    span = span_;
+    base = P + kbeg * ld;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = (w * 2 + i) * 4 + (l >> 4), c = ((l & 15) ^ km_xor<128>(row)) * 8;
+      voff[i] = (int)((row * ld + col0 + (c / RUN) * 2 * RUN + c % RUN) * 2);
+    }
+  }
+  __device__ void issue(int t, int h, bf16_t *tile) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t left = span - (int64_t)t * 64;
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(base + (int64_t)t * 64 * ld, (left < 0 ? 0 : left < 64 ? left : 64) * ld * 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * 2 + i) * 512), 16, voff[i] + h * RUN * 2, 0,
+                                               0, 0);
+  }
+  __device__ static bf16x8 frag(const bf16_t *tile, int r0, int ks) { return frag_km<128>(tile, r0, ks); }
+};
+
+namespace {
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ inline void wait_vm_lds() {
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (((N >> 4) & 3) << 14));
+}
+// a barrier that nothing is moved across and that waits for no memory operation by itself
+__device__ inline void phase_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+}  // namespace
+
+template <bool AKM, bool BKM, class Epi>
+__global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
+  constexpr int HE = 128 * 64, FM = 8, FN = 4;  // elements of a half tile; 16 x 16 results per wave
+  extern __shared__ __align__(16) bf16_t smem[];  // [A0 A1 B0 B1][2 steps]
+  const MmTile tile = mm_tile(a);
+  const int64_t m0 = (int64_t)tile.tm * 256, n0 = (int64_t)tile.tn * 256;
+  const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wr = wave >> 2, wc = wave & 3;
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  using HA = Half<64, AKM>;
+  using HB = Half<32, BKM>;
+  HA ha;
+  HB hb;
+  ha.init((const bf16_t *)a.A, a.lda, m0, a.M, kbeg, kend - kbeg);
+  hb.init((const bf16_t *)a.B, a.ldb, n0, a.N, kbeg, kend - kbeg);
+  const int nk = (int)((kend - kbeg + 63) / 64);
+  // all of A's halves within 64 KB of one base, and all of B's: the reach of a DS offset
+  auto sA = [&](int s, int h) { return smem + (2 * h + s) * HE; };
+  auto sB = [&](int s, int h) { return smem + (4 + 2 * h + s) * HE; };
+
+  bf16x8 fa[2][4], fb0[2][2][2], fb1[2][2];  // [32-deep half of the step][fragment]; fb0 by step parity
+  auto read_a = [&](const bf16_t *t) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[q][i] = HA::frag(t, wr * 64 + 16 * i, 32 * q);
+  };
+  auto read_b = [&](const bf16_t *t, bf16x8 (&f)[2][2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) f[q][j] = HB::frag(t, wc * 32 + 16 * j, 32 * q);
+  };
+  // phase P of k step t, whose halves are in LDS buffer S = t % 2
+  auto phase = [&](auto pc, auto sc, int t) {
+    constexpr int P = decltype(pc)::value, S = decltype(sc)::value;
+    read_a(sA(S, P));
+    if constexpr (P == 0) {
+      read_b(sB(S, 1), fb1);
+      ha.issue(t + 1, 1, sA(S ^ 1, 1));
+      hb.issue(t + 2, 0, sB(S, 0));
+    } else {
+      read_b(sB(S ^ 1, 0), fb0[S ^ 1]);
+      ha.issue(t + 2, 0, sA(S, 0));
+      hb.issue(t + 2, 1, sB(S, 1));
+    }
+    wait_vm_lds<8>();
+    phase_barrier();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          // operands swapped: lane l then holds C[m = l % 16][n = 4 (l / 16) + 0..3]
+          acc[4 * P + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(j < 2 ? fb0[S][q][j] : fb1[q][j - 2], fa[q][i],
+                                                                      acc[4 * P + i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    phase_barrier();
+  };
+  using I0_ = std::integral_constant<int, 0>;
+  using I1_ = std::integral_constant<int, 1>;
+  auto step = [&](auto sc, int t) {
+    phase(I0_{}, sc, t);
+    phase(I1_{}, sc, t);
+  };
+
+  // what the phases before the first would have loaded, in their order
+  hb.issue(0, 0, sB(0, 0));
+  ha.issue(0, 0, sA(0, 0));
+  hb.issue(0, 1, sB(0, 1));
+  ha.issue(0, 1, sA(0, 1));
+  hb.issue(1, 0, sB(1, 0));
+  ha.issue(1, 0, sA(1, 0));
+  hb.issue(1, 1, sB(1, 1));
+  wait_vmcnt<8>();  // B0(0), A0(0), B1(0) have landed
+  phase_barrier();
+  read_b(sB(0, 0), fb0[0]);
+  wait_vm_lds<8>();
+  phase_barrier();          // B0(0) is read: phase 0 loads into it
+  if (wr) phase_barrier();  // group 1 runs one barrier behind
+  int t = 0;
+  for (; t + 1 < nk; t += 2) {
+    step(I0_{}, t);
+    step(I1_{}, t + 1);
+  }
+  if (t < nk) step(I0_{}, t);
+  if (!wr) phase_barrier();
+  __builtin_amdgcn_s_waitcnt(0);  // the loads past the range have written their zeros
+  __syncthreads();                // the epilogue reuses the LDS
+  if constexpr (Epi::kStats) {
+    epi.template reduce<256, 256, 2, 4>(acc, m0, n0, a.M, a.N, tile.tn, (float *)smem);
+  } else {
+    put_rows<FM, FN>(acc, m0 + wr * 128, n0 + wc * 64, a.M, a.N, (float *)smem + wave * 16 * 68, epi.at(tile.split));
   }
 }
 
@@ -450,14 +664,21 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
   return p;
 }
 
-template <int BT, bool AKM, bool BKM, class Epi>
-int mm_launch(const MmArgs &a, const char *name, const Epi &epi, hipStream_t s) {
-  constexpr int WGM = 2, WGN = BT == 256 ? 4 : 2, NT = 64 * WGM * WGN;
-  constexpr size_t lds = (size_t)2 * 2 * BT * 64 * 2;
-  auto kern = &k_mm<BT, BT, WGM, WGN, AKM, BKM, Epi>;
-  static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
+template <bool AKM, bool BKM, class Epi>
+int mm_launch(const MmArgs &a, int64_t bt, const char *name, const Epi &epi, hipStream_t s) {
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n * a.splits));
+  if (bt == 256) {
+    constexpr size_t lds = (size_t)2 * 4 * 128 * 64 * 2;
+    auto kern = &k_mm8<AKM, BKM, Epi>;
+    static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
+    POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
+    return launch_k(name, s, kern, grid, dim3(512), lds, a, epi);
+  }
+  constexpr size_t lds = (size_t)2 * 2 * 128 * 64 * 2;
+  auto kern = &k_mm<128, 128, 2, 2, AKM, BKM, Epi>;
+  static std::atomic<uint64_t> attr{0};
   POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
-  return launch_k(name, s, kern, dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(NT), lds, a, epi);
+  return launch_k(name, s, kern, grid, dim3(256), lds, a, epi);
 }
 
 template <typename T, bool AKM, bool BKM, class Epi>
@@ -466,8 +687,7 @@ int mm_run_as(const MmArgs &a, const MmPlan &p, const char *name, const Epi &epi
     return launch_k(name, s, k_mm_f32<AKM, BKM, Epi>, dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(256), 0,
                     a, epi);
   } else {
-    if (p.bt == 256) return mm_launch<256, AKM, BKM>(a, name, epi, s);
-    return mm_launch<128, AKM, BKM>(a, name, epi, s);
+    return mm_launch<AKM, BKM>(a, p.bt, name, epi, s);
   }
 }
 

@@ -38,40 +38,47 @@ struct XentStats {
   int tile0;      // first row of `part`
   __device__ const XentStats &at(int) const { return *this; }
 
-  template <int BM, int BN, int WGM, int WGN, int FM, int FN>
-  __device__ void reduce(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, int tn,
+  template <int BM, int BN, int WGM, int WGN, int FM, int FN, class V>
+  __device__ void reduce(const V (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, int tn,
                          float *lds) const {
+    constexpr int R = FragOf<V>::ROWS, Q = FragOf<V>::QUADS;
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
-    const int64_t nb = n0 + wn + 4 * (l >> 4);  // this lane's columns: nb + 16 j + e
-    float2 *st = (float2 *)lds;                 // [WGN][BM]
+    const int64_t nb = n0 + wn + 4 * (l / R);  // this lane's columns: nb + R j + 8 q + e
+    const int left = N - nb < 65536 ? (int)(N - nb) : 65536;
+    float2 *st = (float2 *)lds;                // [WGN][BM]
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int r = wm + 16 * i + (l & 15);
+      const int r = wm + R * i + l % R;
       const int64_t m = m0 + r;
-      const int64_t t = m < M ? (int64_t)target[m] - v0 - nb : -1;
+      const int64_t tt = m < M ? (int64_t)target[m] - v0 - nb : -1;
+      const int t = tt >= 0 && tt < left && tt < 65536 ? (int)tt : -1;
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = nb + 16 * j + e < N ? acc[i][j][e] : -INFINITY;
-          if (t == 16 * j + e && nb + t < N) at_target[m] = v;
-          mx = fmaxf(mx, v);
-        }
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = R * j + 8 * q + e;
+            const float v = c < left ? acc[i][j][4 * q + e] : -INFINITY;
+            if (t == c) at_target[m] = v;
+            mx = fmaxf(mx, v);
+          }
       const float ref = safe_ref(mx);
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s += nb + 16 * j + e < N ? __expf(acc[i][j][e] - ref) : 0.f;
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int o = 16; o <= 32; o <<= 1) {
+          for (int e = 0; e < 4; ++e) s += R * j + 8 * q + e < left ? __expf(acc[i][j][4 * q + e] - ref) : 0.f;
+#pragma unroll
+      for (int o = R; o <= 32; o <<= 1) {
         const float m2 = __shfl_xor(mx, o), s2 = __shfl_xor(s, o);
         join_stats(mx, s, m2, s2);
       }
-      if (l < 16) st[(wave % WGN) * BM + r] = make_float2(mx, s);
+      if (l < R) st[(wave % WGN) * BM + r] = make_float2(mx, s);
     }
     __syncthreads();
     for (int r = threadIdx.x; r < BM; r += 64 * WGM * WGN) {
