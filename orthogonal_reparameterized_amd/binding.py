@@ -137,8 +137,13 @@ def _ptr(t: Optional[torch.Tensor], align: int = 16):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(idx: int) -> int:
+    """The current HIP stream of device idx, without building a torch Stream object (2 us)."""
+    return torch._C._cuda_getCurrentRawStream(idx)
+
+
 def _stream(dev: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(dev.index if dev.index is not None else torch.cuda.current_device()))
 
 
 # Scratch tensors keyed by (device, stream): each is allocated while its stream is the
@@ -154,7 +159,7 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
-    key = (idx, torch.cuda.current_stream(idx).cuda_stream)
+    key = (idx, _raw_stream(idx))
     t = _ws_cache.get(key)
     if t is None or t.numel() < nbytes:
         with torch.cuda.device(idx):
@@ -433,6 +438,7 @@ def poetx_backward_adam(layer: Layer, x: torch.Tensor, dz: torch.Tensor, state: 
 # The last axis of x (h) is the feature axis, the leading axes together are the tokens.
 # ---------------------------------------------------------------------------
 _FLOATS = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
 _ACTS = {"none": POETX_ACT_NONE, "relu": POETX_ACT_RELU, "gelu": POETX_ACT_GELU, "gelu_tanh": POETX_ACT_GELU_TANH,
          "silu": POETX_ACT_SILU}
 
@@ -445,18 +451,32 @@ def _act(act) -> int:
     raise ValueError(f"act: {act!r}, expected one of {tuple(_ACTS)}")
 
 
-def _check_in(t: Optional[torch.Tensor], name: str, shape, dtypes, dev) -> None:
-    """An input or output buffer: its shape, dtype, contiguity and device."""
+def _buf(t: Optional[torch.Tensor], name: str, shape, dtypes, dev) -> Optional[int]:
+    """The address of an input or output buffer (None for None), once its shape, dtype, layout,
+    device and alignment are what the library expects."""
     if t is None:
-        return
+        return None
+    if t.dtype in dtypes and t.shape == shape and t.device == dev and t.is_contiguous():
+        p = t.data_ptr()
+        if not p & 15:
+            return p
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
+    """(tensor, address) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _buf(t, name, shape, (dtype,), dev)
 
 
 def _tokens(t: torch.Tensor, name: str):
@@ -476,21 +496,23 @@ def _ws_query(fn: str, device: int, args: tuple) -> int:
 _SOME = 256  # a non-null pointer for size queries, which look only at which outputs are wanted
 
 
-def _run(fn: str, dev: torch.device, args: tuple, query: Optional[tuple]) -> None:
+def _run(fn, dev: torch.device, args: tuple, query: Optional[tuple] = None) -> None:
     """The call on dev's current stream, with its workspace when `query` has its size query's
     arguments.  The library launches on the current device, so that is made dev's."""
     if dev.type != "cuda":
         raise ValueError("tensors must be on the GPU")
-    if torch.cuda.current_device() != dev.index:
+    idx = dev.index
+    if torch.cuda.current_device() != idx:
         with torch.cuda.device(dev):
             return _run(fn, dev, args, query)
-    st = _stream(dev)
+    st = _raw_stream(idx)
     if query is None:
-        _check(getattr(_lib, fn)(*args, st), fn)
-        return
-    ws = _workspace(dev, _ws_query(fn, dev.index, query))
-    nb = _sz(ws.numel())
-    _check(getattr(_lib, fn)(*args, _ptr(ws), ctypes.byref(nb), st), fn)
+        code = fn(*args, st)
+    else:
+        ws = _workspace(dev, _ws_query(fn.__name__, idx, query))
+        code = fn(*args, ws.data_ptr(), ctypes.byref(_sz(ws.numel())), st)
+    if code != POETX_OK:
+        _check(code, fn.__name__)
 
 
 def poetx_layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
@@ -501,20 +523,15 @@ def poetx_layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = Non
     for the backward.  gamma and beta: [d], both float32 or both bf16, each optional."""
     n, d = _tokens(x, "x")
     dev = x.device
-    _check_in(x, "x", x.shape, _FLOATS, dev)
-    p = next((t for t in (gamma, beta) if t is not None), None)
+    px = _buf(x, "x", x.shape, _FLOATS, dev)
+    p = gamma if gamma is not None else beta
     pd = (p.dtype,) if p is not None and p.dtype in _FLOATS else _FLOATS
-    _check_in(gamma, "gamma", (d,), pd, dev)
-    _check_in(beta, "beta", (d,), pd, dev)
-    y = torch.empty_like(x) if y is None else y
-    mean = torch.empty(n, dtype=torch.float32, device=dev) if mean is None else mean
-    rstd = torch.empty(n, dtype=torch.float32, device=dev) if rstd is None else rstd
-    _check_in(y, "y", x.shape, (x.dtype,), dev)
-    _check_in(mean, "mean", (n,), (torch.float32,), dev)
-    _check_in(rstd, "rstd", (n,), (torch.float32,), dev)
-    _run("poetx_layernorm_forward", dev,
-         (n, d, _dt(x), _ptr(x), _ptr(gamma), _ptr(beta), _dt(p) if p is not None else POETX_F32, eps, _ptr(y),
-          _ptr(mean), _ptr(rstd)), None)
+    pg, pb = _buf(gamma, "gamma", (d,), pd, dev), _buf(beta, "beta", (d,), pd, dev)
+    y, py = _out(y, "y", x.shape, x.dtype, dev)
+    mean, pm = _out(mean, "mean", (n,), torch.float32, dev)
+    rstd, pr = _out(rstd, "rstd", (n,), torch.float32, dev)
+    _run(_lib.poetx_layernorm_forward, dev,
+         (n, d, _DT[x.dtype], px, pg, pb, _DT[p.dtype] if p is not None else POETX_F32, eps, py, pm, pr))
     return y, mean, rstd
 
 
@@ -524,24 +541,21 @@ def poetx_layernorm_backward(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[
     """Returns dict(dx[, dgamma, dbeta]); dgamma, dbeta float32 [d].  dres: the gradient that
     reaches x past the norm, added to dx."""
     n, d = _tokens(x, "x")
-    dev = x.device
-    _check_in(x, "x", x.shape, _FLOATS, dev)
-    _check_in(dy, "dy", x.shape, (x.dtype,), dev)
-    _check_in(dres, "dres", x.shape, (x.dtype,), dev)
-    _check_in(gamma, "gamma", (d,), _FLOATS, dev)
-    _check_in(mean, "mean", (n,), (torch.float32,), dev)
-    _check_in(rstd, "rstd", (n,), (torch.float32,), dev)
-    dx = torch.empty_like(x) if dx is None else dx
-    _check_in(dx, "dx", x.shape, (x.dtype,), dev)
-    dg = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
-    db = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
-    pd = _dt(gamma) if gamma is not None else POETX_F32
-    some = _SOME if want_params else None
-    _run("poetx_layernorm_backward", dev,
-         (n, d, _dt(x), _ptr(x), _ptr(dy), _ptr(gamma), pd, _ptr(mean), _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dg),
-          _ptr(db)),
-         (n, d, _dt(x), None, None, None, pd, None, None, None, None, some, some))
-    return dict(dx=dx, dgamma=dg, dbeta=db) if want_params else dict(dx=dx)
+    dev, shape, dt = x.device, x.shape, (x.dtype,)
+    px = _buf(x, "x", shape, _FLOATS, dev)
+    ins = (_buf(dy, "dy", shape, dt, dev), _buf(gamma, "gamma", (d,), _FLOATS, dev))
+    stats = (_buf(mean, "mean", (n,), _F32, dev), _buf(rstd, "rstd", (n,), _F32, dev),
+             _buf(dres, "dres", shape, dt, dev))
+    dx, pdx = _out(dx, "dx", shape, x.dtype, dev)
+    pd, code = _DT[gamma.dtype] if gamma is not None else POETX_F32, _DT[x.dtype]
+    out, some, params = dict(dx=dx), None, (None, None)
+    if want_params:
+        out["dgamma"] = torch.empty(d, dtype=torch.float32, device=dev)
+        out["dbeta"] = torch.empty(d, dtype=torch.float32, device=dev)
+        some, params = _SOME, (out["dgamma"].data_ptr(), out["dbeta"].data_ptr())
+    _run(_lib.poetx_layernorm_backward, dev, (n, d, code, px, *ins, pd, *stats, pdx, *params),
+         (n, d, code, None, None, None, pd, None, None, None, None, some, some))
+    return out
 
 
 def poetx_linear_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -551,21 +565,19 @@ def poetx_linear_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.
     the backward when save_pre is set, else None.  act: a name ("none", "relu", "gelu",
     "gelu_tanh", "silu") or a POETX_ACT_* code."""
     n, d_in = _tokens(x, "x")
-    dev = x.device
+    dev, dt = x.device, (x.dtype,)
     d_out = w.shape[0]
     a = _act(act)
     shape = x.shape[:-1] + (d_out,)
-    _check_in(x, "x", x.shape, _FLOATS, dev)
-    _check_in(w, "w", (d_out, d_in), (x.dtype,), dev)
-    _check_in(bias, "bias", (d_out,), _FLOATS, dev)
-    _check_in(residual, "residual", shape, (x.dtype,), dev)
-    y = torch.empty(shape, dtype=x.dtype, device=dev) if y is None else y
-    _check_in(y, "y", shape, (x.dtype,), dev)
+    ins = (_buf(x, "x", x.shape, _FLOATS, dev), _buf(w, "w", (d_out, d_in), dt, dev),
+           _buf(bias, "bias", (d_out,), _FLOATS, dev))
+    pr = _buf(residual, "residual", shape, dt, dev)
+    y, py = _out(y, "y", shape, x.dtype, dev)
     pre = torch.empty(shape, dtype=x.dtype, device=dev) if save_pre else None
-    bd = _dt(bias) if bias is not None else POETX_F32
-    _run("poetx_linear_forward", dev,
-         (n, d_in, d_out, _dt(x), _ptr(x), _ptr(w), _ptr(bias), bd, _ptr(residual), a, _ptr(y), _ptr(pre)),
-         (n, d_in, d_out, _dt(x), None, None, None, bd, None, a, None, None))
+    bd, code = _DT[bias.dtype] if bias is not None else POETX_F32, _DT[x.dtype]
+    _run(_lib.poetx_linear_forward, dev,
+         (n, d_in, d_out, code, *ins, bd, pr, a, py, pre.data_ptr() if save_pre else None),
+         (n, d_in, d_out, code, None, None, None, bd, None, a, None, None))
     return y, pre
 
 
@@ -576,7 +588,7 @@ def poetx_linear_backward(x: Optional[torch.Tensor], w: Optional[torch.Tensor], 
     what poetx_linear_forward(save_pre=True) returned (not needed for act "none").  x is needed
     for dw, w for dx."""
     n, d_out = _tokens(dy, "dy")
-    dev = dy.device
+    dev, dt = dy.device, (dy.dtype,)
     a = _act(act)
     if want_dx and w is None or want_dw and x is None:
         raise ValueError("dx needs w, dw needs x")
@@ -585,23 +597,20 @@ def poetx_linear_backward(x: Optional[torch.Tensor], w: Optional[torch.Tensor], 
     ref = x if x is not None else w
     d_in = ref.shape[-1] if ref is not None else 1
     shape = dy.shape[:-1] + (d_in,)
-    _check_in(dy, "dy", dy.shape, _FLOATS, dev)
-    _check_in(x, "x", shape, (dy.dtype,), dev)
-    _check_in(w, "w", (d_out, d_in), (dy.dtype,), dev)
-    _check_in(pre, "pre", dy.shape, (dy.dtype,), dev)
-    out = {}
-    if want_dx:
-        out["dx"] = torch.empty(shape, dtype=dy.dtype, device=dev)
-    if want_dw:
-        out["dw"] = torch.empty((d_out, d_in), dtype=dy.dtype, device=dev)
-    if want_dbias:
-        out["dbias"] = torch.empty(d_out, dtype=torch.float32, device=dev)
+    pdy = _buf(dy, "dy", dy.shape, _FLOATS, dev)
+    ins = (_buf(x, "x", shape, dt, dev), _buf(w, "w", (d_out, d_in), dt, dev), pdy,
+           _buf(pre, "pre", dy.shape, dt, dev))
+    out, ptrs = {}, []
+    for name, want, size, dtype in (("dx", want_dx, shape, dy.dtype), ("dw", want_dw, (d_out, d_in), dy.dtype),
+                                    ("dbias", want_dbias, (d_out,), torch.float32)):
+        if want:
+            out[name] = torch.empty(size, dtype=dtype, device=dev)
+        ptrs.append(out[name].data_ptr() if want else None)
     if n == 0 and not (want_dw or want_dbias):
         return out
-    ptrs = [_ptr(out.get(k)) for k in ("dx", "dw", "dbias")]
-    _run("poetx_linear_backward", dev,
-         (n, d_in, d_out, _dt(dy), _ptr(x), _ptr(w), _ptr(dy), _ptr(pre), a, *ptrs),
-         (n, d_in, d_out, _dt(dy), None, None, None, None, a, *(None if p is None else _SOME for p in ptrs)))
+    code = _DT[dy.dtype]
+    _run(_lib.poetx_linear_backward, dev, (n, d_in, d_out, code, *ins, a, *ptrs),
+         (n, d_in, d_out, code, None, None, None, None, a, *(None if p is None else _SOME for p in ptrs)))
     return out
 
 
@@ -614,16 +623,13 @@ def poetx_xent_forward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, *
     dev = h.device
     vocab = w.shape[0]
     lead = h.shape[:-1]
-    _check_in(h, "h", h.shape, _FLOATS, dev)
-    _check_in(w, "w", (vocab, d), (h.dtype,), dev)
-    _check_in(target, "target", lead, (torch.int32,), dev)
-    loss = torch.empty(lead, dtype=torch.float32, device=dev) if loss is None else loss
-    lse = torch.empty(lead, dtype=torch.float32, device=dev) if lse is None else lse
-    _check_in(loss, "loss", lead, (torch.float32,), dev)
-    _check_in(lse, "lse", lead, (torch.float32,), dev)
-    _run("poetx_xent_forward", dev,
-         (n, d, vocab, _dt(h), _ptr(h), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse)),
-         (n, d, vocab, _dt(h), None, None, None, None, None))
+    ins = (_buf(h, "h", h.shape, _FLOATS, dev), _buf(w, "w", (vocab, d), (h.dtype,), dev),
+           _buf(target, "target", lead, (torch.int32,), dev))
+    loss, pl = _out(loss, "loss", lead, torch.float32, dev)
+    lse, pz = _out(lse, "lse", lead, torch.float32, dev)
+    code = _DT[h.dtype]
+    _run(_lib.poetx_xent_forward, dev, (n, d, vocab, code, *ins, pl, pz),
+         (n, d, vocab, code, None, None, None, None, None))
     return loss, lse
 
 
@@ -637,11 +643,9 @@ def poetx_xent_backward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, 
     lead = h.shape[:-1]
     if not (want_dh or want_dw):
         raise ValueError("neither dh nor dw is wanted")
-    _check_in(h, "h", h.shape, _FLOATS, dev)
-    _check_in(w, "w", (vocab, d), (h.dtype,), dev)
-    _check_in(target, "target", lead, (torch.int32,), dev)
-    _check_in(lse, "lse", lead, (torch.float32,), dev)
-    _check_in(dloss, "dloss", lead, (torch.float32,), dev)
+    ins = (_buf(h, "h", h.shape, _FLOATS, dev), _buf(w, "w", (vocab, d), (h.dtype,), dev),
+           _buf(target, "target", lead, (torch.int32,), dev), _buf(lse, "lse", lead, _F32, dev),
+           _buf(dloss, "dloss", lead, _F32, dev))
     out = {}
     if want_dh:
         out["dh"] = torch.empty_like(h)
@@ -649,10 +653,11 @@ def poetx_xent_backward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, 
         out["dw"] = torch.empty_like(w)
     if n == 0 and not want_dw:
         return out
-    ptrs = [_ptr(out.get(k)) for k in ("dh", "dw")]
-    _run("poetx_xent_backward", dev,
-         (n, d, vocab, _dt(h), _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), *ptrs),
-         (n, d, vocab, _dt(h), None, None, None, None, None, *(None if p is None else _SOME for p in ptrs)))
+    code = _DT[h.dtype]
+    _run(_lib.poetx_xent_backward, dev,
+         (n, d, vocab, code, *ins, out["dh"].data_ptr() if want_dh else None,
+          out["dw"].data_ptr() if want_dw else None),
+         (n, d, vocab, code, None, None, None, None, None, _SOME if want_dh else None, _SOME if want_dw else None))
     return out
 
 
