@@ -424,23 +424,25 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   }
 }
 
-// float32 kernel: 128 x 128 tile over 2 x 2 waves, 16-deep k steps.  Operands pass through
-// registers into k-major LDS rows (any alignment, any tail), two stages; an MFMA of 16 x 16
-// takes 4 k.
-template <bool AKM, bool BKM, class Epi>
+// float32 kernel: BT x BT tile (128 or 64) over 2 x 2 waves, BK-deep k steps.  Operands pass
+// through registers into k-major LDS rows (any alignment, any tail), two stages; an MFMA of
+// 16 x 16 takes 4 k.  Bound by the float32 matrix rate (157 TFLOP/s): a step's 8 BK / 4 ..
+// 32 BK / 4 MFMAs of 32 cycles cover its LDS reads many times over.
+template <int BT, int BK, bool AKM, bool BKM, class Epi>
 __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
-  constexpr int BT = 128, BK = 16, LD = BT + 4, ST = BK * LD;
+  constexpr int LD = BT + 4, ST = BK * LD, WT = BT / 2, F = WT / 16;
+  constexpr int PC = BT * BK / 4 / 256;  // 4-float pieces per thread and operand stage
   __shared__ __align__(16) float smem[4 * ST];
   const MmTile tile = mm_tile(a);
   const int64_t m0 = (int64_t)tile.tm * BT, n0 = (int64_t)tile.tn * BT;
   const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
   const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x4 acc[4][4];
+  const int wm = (wave >> 1) * WT, wn = (wave & 1) * WT;
+  f32x4 acc[F][F];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // four consecutive floats from p, the first nv in range
   auto load4 = [](const float *p, int nv) {
@@ -455,35 +457,35 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
     return v;
   };
   auto cl4 = [](int64_t left) { return left >= 4 ? 4 : left > 0 ? (int)left : 0; };
-  // thread's two 4-float pieces of an operand's 128 x 16 stage
-  auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int64_t k0, f32x4 (&v)[2]) {
+  // thread's pieces of an operand's BT x BK stage
+  auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int64_t k0, f32x4 (&v)[PC]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < PC; ++i) {
       const int e = tid + 256 * i;
-      if (km) {  // 32 pieces along the rows of one k
-        const int64_t k = k0 + (e >> 5), r = r0 + (e & 31) * 4;
+      if (km) {  // BT / 4 pieces along the rows of one k
+        const int64_t k = k0 + e / (BT / 4), r = r0 + e % (BT / 4) * 4;
         v[i] = load4(P + k * ld + r, k < kend ? cl4(rows - r) : 0);
-      } else {   // 4 pieces along k of one row
-        const int64_t r = r0 + (e >> 2), k = k0 + (e & 3) * 4;
+      } else {   // BK / 4 pieces along k of one row
+        const int64_t r = r0 + e / (BK / 4), k = k0 + e % (BK / 4) * 4;
         v[i] = load4(P + r * ld + k, r < rows ? cl4(kend - k) : 0);
       }
     }
   };
-  auto stash = [&](float *st, bool km, const f32x4 (&v)[2]) {
+  auto stash = [&](float *st, bool km, const f32x4 (&v)[PC]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < PC; ++i) {
       const int e = tid + 256 * i;
       if (km) {
-        *(f32x4 *)(st + (e >> 5) * LD + (e & 31) * 4) = v[i];
+        *(f32x4 *)(st + e / (BT / 4) * LD + e % (BT / 4) * 4) = v[i];
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) st[((e & 3) * 4 + q) * LD + (e >> 2)] = v[i][q];
+        for (int q = 0; q < 4; ++q) st[(e % (BK / 4) * 4 + q) * LD + e / (BK / 4)] = v[i][q];
       }
     }
   };
   const float *A = (const float *)a.A, *B = (const float *)a.B;
   const int nk = (int)((kend - kbeg + BK - 1) / BK);
-  f32x4 va[2], vb[2];
+  f32x4 va[PC], vb[PC];
   if (nk > 0) {
     fetch(A, a.lda, m0, a.M, AKM, kbeg, va);
     fetch(B, a.ldb, n0, a.N, BKM, kbeg, vb);
@@ -502,15 +504,15 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
     }
 #pragma unroll
     for (int s = 0; s < BK / 4; ++s) {
-      float fa[4], fb[4];
+      float fa[F], fb[F];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i] = ta[(4 * s + (l >> 4)) * LD + wm + 16 * i + (l & 15)];
+      for (int i = 0; i < F; ++i) fa[i] = ta[(4 * s + (l >> 4)) * LD + wm + 16 * i + (l & 15)];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = tb[(4 * s + (l >> 4)) * LD + wn + 16 * j + (l & 15)];
+      for (int j = 0; j < F; ++j) fb[j] = tb[(4 * s + (l >> 4)) * LD + wn + 16 * j + (l & 15)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < F; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
@@ -518,7 +520,7 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
   if constexpr (Epi::kStats) {
     epi.template reduce<BT, BT, 2, 2>(acc, m0, n0, a.M, a.N, tile.tn, smem);
   } else {
-    put_rows<4, 4>(acc, m0 + wm, n0 + wn, a.M, a.N, smem + wave * 16 * 68, epi.at(tile.split));
+    put_rows<F, F>(acc, m0 + wm, n0 + wn, a.M, a.N, smem + wave * 16 * (WT + 4), epi.at(tile.split));
   }
 }
 
@@ -601,6 +603,7 @@ __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, 
   const int nv = N - n >= 8 ? 8 : (int)(N - n);
   float v[8];
   load8(part + m * N + n, nv, v);
+#pragma unroll 4
   for (int s = 1; s < splits; ++s) {
     float w[8];
     load8(part + ((int64_t)s * M + m) * N + n, nv, w);
@@ -624,9 +627,9 @@ struct StoreEpi {
 // ------------------------------------------------------------------ host side ----
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // a grid holds fewer than 2^32 threads
 
-// How a product is tiled: 256 x 256 or 128 x 128 tiles, and over how many k ranges.
+// How a product is tiled (bt x bt results per workgroup), and over how many k ranges.
 struct MmPlan {
-  int64_t bt = 128, splits = 1, kc = 0;
+  int64_t bt = 64, splits = 1, kc = 0;
   int64_t tiles_m = 0, tiles_n = 0;
   size_t part_bytes = 0;  // workspace of a split product
 };
@@ -638,17 +641,27 @@ struct MmDesc {
   const char *name = "mm";
 };
 
+// bf16: 256 x 256 tiles (one workgroup per CU) where they fill three quarters of the GPU, else
+// 128 x 128 (two per CU).  float32: 128 x 128 (two per CU) where they fill the GPU twice, else
+// 64 x 64 (four per CU), which cut small results finer and overlap their load latencies.
 inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true) {
   MmPlan p;
   if (M <= 0 || N <= 0) return p;  // nothing to launch
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
-  const int64_t t256 = cdiv(M, 256) * cdiv(N, 256);
-  p.bt = dt == POETX_BF16 && 4 * t256 >= 3 * cus ? 256 : 128;
+  auto tiles_of = [&](int64_t t) { return cdiv(M, t) * cdiv(N, t); };
+  int64_t slots;
+  if (dt == POETX_BF16) {
+    p.bt = 4 * tiles_of(256) >= 3 * cus ? 256 : 128;
+    slots = p.bt == 256 ? cus : 2 * cus;
+  } else {
+    p.bt = tiles_of(128) >= 2 * cus ? 128 : 64;
+    slots = p.bt == 128 ? 2 * cus : 4 * cus;
+  }
   p.tiles_m = cdiv(M, p.bt);
   p.tiles_n = cdiv(N, p.bt);
   p.kc = K;
-  const int64_t tiles = p.tiles_m * p.tiles_n, slots = p.bt == 256 ? cus : 2 * cus;
-  // too few tiles to fill the GPU: split k, each range at least 256 (bf16) deep
+  const int64_t tiles = p.tiles_m * p.tiles_n;
+  // too few tiles to fill the GPU: split k, each range at least 256 (float32: 128) deep
   if (may_split && tiles < slots) {
     int64_t sp = slots / tiles;
     const int64_t deep = K / (dt == POETX_BF16 ? 256 : 128);
@@ -684,8 +697,9 @@ int mm_launch(const MmArgs &a, int64_t bt, const char *name, const Epi &epi, hip
 template <typename T, bool AKM, bool BKM, class Epi>
 int mm_run_as(const MmArgs &a, const MmPlan &p, const char *name, const Epi &epi, hipStream_t s) {
   if constexpr (sizeof(T) == 4) {
-    return launch_k(name, s, k_mm_f32<AKM, BKM, Epi>, dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(256), 0,
-                    a, epi);
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n * a.splits));
+    if (p.bt == 128) return launch_k(name, s, k_mm_f32<128, 16, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
+    return launch_k(name, s, k_mm_f32<64, 32, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
   } else {
     return mm_launch<AKM, BKM>(a, p.bt, name, epi, s);
   }

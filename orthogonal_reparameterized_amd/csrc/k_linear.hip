@@ -242,7 +242,7 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   if (copy || d.dbias) {
     const int64_t cb = cdiv(d.d_out, 512), cus = device_cus() > 0 ? device_cus() : 256;
     int64_t parts = cdiv(4 * cus, cb);
-    if (parts > cdiv(d.n, 16)) parts = cdiv(d.n, 16);
+    if (parts > cdiv(d.n, 4)) parts = cdiv(d.n, 4);  // a row per wave at least
     if (parts > 1024) parts = 1024;
     float *part = d.dbias ? (float *)ar.take((size_t)(parts > 0 ? parts : 1) * d.d_out * 4) : nullptr;
     if (!measure) {

@@ -126,17 +126,37 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_norm_bwd(NormArgs a) 
     for (int e = 0; e < 8; ++e) { ga[c][e] = 1.f; dg[c][e] = db[c][e] = 0.f; }
     if (nv && a.gamma.p) a.gamma.load(col, nv, ga[c]);
   }
-  int parity = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / THR; row < a.n; row += (int64_t)gridDim.x * RPB) {
-    const T *x = (const T *)a.x + row * a.d, *dy = (const T *)a.dy + row * a.d;
-    const float mu = a.mean[row], r = a.rstd[row];
-    float xh[CH][8], g[CH][8], s[2] = {0.f, 0.f};
+  // the next row's loads are in flight while this row is reduced (not with two chunks in each
+  // of 1024 threads, whose 128 registers do not hold them)
+  constexpr bool AHEAD = THR < 1024 || CH == 1;
+  Raw8<T> rx[CH], ry[CH], rr[CH];
+  float mu_n = 0.f, r_n = 0.f;
+  auto fetch = [&](int64_t row) {
+    mu_n = a.mean[row];
+    r_n = a.rstd[row];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int64_t col = (int64_t)(c * THR + t) * 8;
       const int nv = clamp8(a.d - col);
-      load8(x + col, nv, xh[c]);
-      load8(dy + col, nv, g[c]);
+      load_raw((const T *)a.x + row * a.d + col, nv, rx[c]);
+      load_raw((const T *)a.dy + row * a.d + col, nv, ry[c]);
+      if (a.dres) load_raw((const T *)a.dres + row * a.d + col, nv, rr[c]);
+    }
+  };
+  int parity = 0;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / THR;
+  if (AHEAD && row < a.n) fetch(row);
+  for (; row < a.n; row += step) {
+    if (!AHEAD) fetch(row);
+    const float mu = mu_n, r = r_n;
+    float xh[CH][8], g[CH][8], q[CH][8], s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int nv = clamp8(a.d - (int64_t)(c * THR + t) * 8);
+      widen(rx[c], xh[c]);
+      widen(ry[c], g[c]);
+      if (a.dres) widen(rr[c], q[c]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         xh[c][e] = e < nv ? (xh[c][e] - mu) * r : 0.f;
@@ -147,25 +167,21 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_norm_bwd(NormArgs a) 
         s[1] += g[c][e] * xh[c][e];
       }
     }
+    if (AHEAD && row + step < a.n) fetch(row + step);
     row_sum<THR, 2>(s, red, parity);
     parity ^= 1;
     const float m1 = s[0] / a.fd, m2 = s[1] / a.fd;
     T *dx = (T *)a.out + row * a.d;
-    const T *dr = (const T *)a.dres + (a.dres ? row * a.d : 0);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int64_t col = (int64_t)(c * THR + t) * 8;
-      const int nv = clamp8(a.d - col);
       float o[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = r * (g[c][e] - m1 - xh[c][e] * m2);
-      if (a.dres) {
-        float q[8];
-        load8(dr + col, nv, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += q[e];
+      for (int e = 0; e < 8; ++e) {
+        o[e] = r * (g[c][e] - m1 - xh[c][e] * m2);
+        if (a.dres) o[e] += q[c][e];
       }
-      store8(dx + col, nv, o);
+      store8(dx + col, clamp8(a.d - col), o);
     }
   }
   if (!a.part) return;
@@ -200,23 +216,42 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_norm_bwd(NormArgs a) 
   }
 }
 
-// dgamma, dbeta = the sums over the workgroups' partials [parts][2 d]: 64 columns per
-// workgroup, 16 threads per column each summing every 16th partial, joined in order.
+// dgamma, dbeta = the sums over the workgroups' partials [parts][2 d], in a fixed order: 32
+// columns per workgroup, 128 threads per 4 columns each summing every 128th partial, joined
+// pairwise.
 __global__ __launch_bounds__(1024) void k_norm_params(const float *part, int64_t parts, int64_t d, float *dgamma,
                                                       float *dbeta) {
-  __shared__ float red[16][64];
-  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + c;
-  float s = 0.f;
-  if (col < 2 * d)
-    for (int64_t p = q; p < parts; p += 16) s += part[p * 2 * d + col];
-  red[q][c] = s;
-  __syncthreads();
-  if (q || col >= 2 * d) return;
+  __shared__ f32v4 red[128][8];
+  const int c = threadIdx.x & 7, q = threadIdx.x >> 3;
+  const int64_t col = (int64_t)blockIdx.x * 32 + c * 4, left = 2 * d - col;
+  f32v4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t p = q; p < parts; p += 128) {
+    const float *src = part + p * 2 * d + col;
+    if (left >= 4) {
+      f32v4 v;
+      __builtin_memcpy(&v, src, 16);
+      s += v;
+    } else {
 #pragma unroll
-  for (int i = 1; i < 16; ++i) s += red[i][c];
-  float *out = col < d ? dgamma : dbeta;
-  if (out) out[col < d ? col : col - d] = s;
+      for (int e = 0; e < 4; ++e) s[e] += e < left ? src[e] : 0.f;
+    }
+  }
+  red[q][c] = s;
+#pragma unroll
+  for (int o = 64; o; o >>= 1) {
+    __syncthreads();
+    if (q < o) {
+      s += red[q + o][c];
+      red[q][c] = s;
+    }
+  }
+  if (q) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= left) break;
+    float *out = col + e < d ? dgamma : dbeta;
+    if (out) out[col + e < d ? col + e : col + e - d] = s[e];
+  }
 }
 
 namespace {
@@ -232,21 +267,19 @@ int run_bwd(const NormArgs &a, int64_t blocks, hipStream_t s) {
   return launch_k("layernorm_bwd", s, k_norm_bwd<T, THR, CH>, dim3((unsigned)blocks), dim3(BLK), 0, a);
 }
 
-// Rows per workgroup of the kernels below (a wave per row up to 1024 columns).
-int64_t rows_per_block(int64_t d) { return d <= 1024 ? 4 : 1; }
-int64_t threads_per_block(int64_t d) { return d <= 4096 ? 256 : 1024; }
-
-// Workgroups that walk the n rows: at most as many as the GPU holds `per_cu` rounds of
-// 1024 threads per CU for.
-int64_t norm_blocks(int64_t n, int64_t d, int per_cu) {
+// Workgroups that walk the n rows (a wave per row up to 1024 columns).  Forward: 8 of 256
+// threads (2 of 1024) per CU.  Backward: 2 (1) per CU, which with a row in flight ahead keep
+// as much memory traffic going while they leave fewer partial sums to write and join.
+int64_t norm_blocks(int64_t n, int64_t d, bool bwd) {
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
-  const int64_t most = cus * per_cu * (1024 / threads_per_block(d)), need = cdiv(n, rows_per_block(d));
+  const int64_t most = cus * (bwd ? (d <= 4096 ? 2 : 1) : (d <= 4096 ? 8 : 2));
+  const int64_t need = cdiv(n, d <= 1024 ? 4 : 1);
   return need < most ? need : most;
 }
 
 template <typename T>
 int fwd_t(const NormArgs &a, hipStream_t s) {
-  const int64_t g = norm_blocks(a.n, a.d, 2);
+  const int64_t g = norm_blocks(a.n, a.d, false);
   if (a.d <= 512) return run_fwd<T, 64, 1>(a, g, s);
   if (a.d <= 1024) return run_fwd<T, 64, 2>(a, g, s);
   if (a.d <= 2048) return run_fwd<T, 256, 1>(a, g, s);
@@ -266,7 +299,7 @@ int bwd_t(const NormArgs &a, int64_t g, hipStream_t s) {
 
 }  // namespace
 
-int64_t norm_bwd_parts(int64_t n, int64_t d) { return norm_blocks(n, d, 1); }
+int64_t norm_bwd_parts(int64_t n, int64_t d) { return norm_blocks(n, d, true); }
 
 int norm_forward(const NormDesc &n, hipStream_t s) {
   if (n.n == 0) return POETX_OK;
@@ -284,7 +317,7 @@ int norm_backward(const NormDesc &n, float *part, float *dgamma, float *dbeta, h
   }
   if (!dgamma && !dbeta) return POETX_OK;
   // no rows: no partials, and the sums over nothing are zero
-  return launch_k("layernorm_params", s, k_norm_params, dim3((unsigned)cdiv(2 * n.d, 64)), dim3(1024), 0,
+  return launch_k("layernorm_params", s, k_norm_params, dim3((unsigned)cdiv(2 * n.d, 32)), dim3(1024), 0,
                   (const float *)part, n.n > 0 ? g : (int64_t)0, n.d, dgamma, dbeta);
 }
 

@@ -71,6 +71,34 @@ __device__ inline void store8(float *p, int nv, const float (&v)[8]) {
   }
 }
 
+// Eight elements as they lie in memory, so that a load can stay in flight before it is widened.
+template <typename T> struct Raw8 { u32v4 u[sizeof(T) / 2]; };
+template <typename T>
+__device__ inline void load_raw(const T *p, int nv, Raw8<T> &r) {
+  if (nv >= 8) {
+    __builtin_memcpy(&r, p, sizeof(r));
+  } else {
+    float v[8];
+    load8(p, nv, v);
+    if constexpr (sizeof(T) == 2) {
+      r.u[0] = u32v4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.u[e >> 2][e & 3] = __float_as_uint(v[e]);
+    }
+  }
+}
+template <typename T>
+__device__ inline void widen(const Raw8<T> &r, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (sizeof(T) == 2)
+      v[e] = __uint_as_float(e & 1 ? r.u[0][e >> 1] & 0xffff0000u : r.u[0][e >> 1] << 16);
+    else
+      v[e] = __uint_as_float(r.u[e >> 2][e & 3]);
+  }
+}
+
 // A parameter vector (gamma, beta, bias) stored as float32 or bf16.
 struct ParamVec {
   const void *p;
