@@ -424,13 +424,16 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   }
 }
 
-// float32 kernel: BT x BT tile (128 or 64) over 2 x 2 waves, BK-deep k steps.  Operands pass
-// through registers into k-major LDS rows (any alignment, any tail), two stages; an MFMA of
-// 16 x 16 takes 4 k.  Bound by the float32 matrix rate (157 TFLOP/s): a step's 8 BK / 4 ..
-// 32 BK / 4 MFMAs of 32 cycles cover its LDS reads many times over.
+// float32 kernel: BT x BT tile (128 or 64) over 2 x 2 waves, BK-deep k steps (16 or 32), two
+// LDS stages, operands through registers (any alignment, any tail).  An MFMA of 16 x 16 takes
+// four k; the four of one 16-deep block take k = 4 g + s (lane group g, MFMA s) instead of
+// 4 s + g, so that a k-contiguous operand is read 16 bytes (its lane's four MFMAs) at a time
+// from rows as they lie in memory, chunks XORed as in the bf16 tiles, and a k-major one, in
+// rows of BT + 4 floats, meets four different 16-bank groups.  Bound by the float32 matrix
+// rate (157 TFLOP/s).
 template <int BT, int BK, bool AKM, bool BKM, class Epi>
 __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
-  constexpr int LD = BT + 4, ST = BK * LD, WT = BT / 2, F = WT / 16;
+    constexpr int LD = BT + 4, ST = BK * LD, WT = BT / 2, F = WT / 16;  // a stage of either layout fits ST
   constexpr int PC = BT * BK / 4 / 256;  // 4-float pieces per thread and operand stage
   __shared__ __align__(16) float smem[4 * ST];
   const MmTile tile = mm_tile(a);
@@ -444,31 +447,32 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // four consecutive floats from p, the first nv in range
-  auto load4 = [](const float *p, int nv) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (nv >= 4) {
-      __builtin_memcpy(&v, p, 16);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < nv) v[e] = p[e];
-    }
-    return v;
-  };
-  auto cl4 = [](int64_t left) { return left >= 4 ? 4 : left > 0 ? (int)left : 0; };
-  // thread's pieces of an operand's BT x BK stage
-  auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int64_t k0, f32x4 (&v)[PC]) {
+  // Global loads go through a buffer that ends with the operand's valid rows, so what lies past
+  // them reads as zero.  k-contiguous: the base is the tile's first row and only a last step
+  // that is not whole needs its elements past k cleared; k-major: the base moves with k.
+  const int64_t span = kend - kbeg;
+  auto offsets = [&](int64_t ld, bool km, int (&off)[PC]) {
 #pragma unroll
     for (int i = 0; i < PC; ++i) {
       const int e = tid + 256 * i;
-      if (km) {  // BT / 4 pieces along the rows of one k
-        const int64_t k = k0 + e / (BT / 4), r = r0 + e % (BT / 4) * 4;
-        v[i] = load4(P + k * ld + r, k < kend ? cl4(rows - r) : 0);
-      } else {   // BK / 4 pieces along k of one row
-        const int64_t r = r0 + e / (BK / 4), k = k0 + e % (BK / 4) * 4;
-        v[i] = load4(P + r * ld + k, r < rows ? cl4(kend - k) : 0);
-      }
+      off[i] = km ? (int)((e / (BT / 4) * ld + e % (BT / 4) * 4) * 4) : (int)((e / (BK / 4) * ld + e % (BK / 4) * 4) * 4);
+    }
+  };
+  auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int t, const int (&off)[PC],
+                   f32x4 (&v)[PC]) {
+    const int64_t left = span - (int64_t)t * BK;
+    const int64_t nr = rows - r0 < BT ? rows - r0 : BT;
+    const __amdgpu_buffer_rsrc_t rs =
+        km ? make_rsrc(P + (kbeg + (int64_t)t * BK) * ld + r0, ((left < BK ? left : BK) * ld - r0) * 4)
+           : make_rsrc(P + r0 * ld + kbeg + (int64_t)t * BK, (nr * ld - kbeg - (int64_t)t * BK) * 4);
+#pragma unroll
+    for (int i = 0; i < PC; ++i) v[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off[i], 0, 0));
+    if (!km && left < BK) {
+#pragma unroll
+      for (int i = 0; i < PC; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if ((tid + 256 * i) % (BK / 4) * 4 + q >= left) v[i][q] = 0.f;
     }
   };
   auto stash = [&](float *st, bool km, const f32x4 (&v)[PC]) {
@@ -478,17 +482,20 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
       if (km) {
         *(f32x4 *)(st + e / (BT / 4) * LD + e % (BT / 4) * 4) = v[i];
       } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) st[(e % (BK / 4) * 4 + q) * LD + e / (BK / 4)] = v[i][q];
+        const int r = e / (BK / 4), c = e % (BK / 4);
+        *(f32x4 *)(st + r * BK + (c ^ kc_key<2 * BK>(r)) * 4) = v[i];
       }
     }
   };
   const float *A = (const float *)a.A, *B = (const float *)a.B;
-  const int nk = (int)((kend - kbeg + BK - 1) / BK);
+  const int nk = (int)((span + BK - 1) / BK);
   f32x4 va[PC], vb[PC];
+  int oa[PC], ob[PC];
+  offsets(a.lda, AKM, oa);
+  offsets(a.ldb, BKM, ob);
   if (nk > 0) {
-    fetch(A, a.lda, m0, a.M, AKM, kbeg, va);
-    fetch(B, a.ldb, n0, a.N, BKM, kbeg, vb);
+    fetch(A, a.lda, m0, a.M, AKM, 0, oa, va);
+    fetch(B, a.ldb, n0, a.N, BKM, 0, ob, vb);
   }
   for (int t = 0; t < nk; ++t) {
     float *ta = smem + (t & 1) * 2 * ST, *tb = ta + ST;
@@ -498,22 +505,32 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
     // LDS this step has just overwritten, may not (its readers passed the last barrier)
     __syncthreads();
     if (t + 1 < nk) {
-      const int64_t k1 = kbeg + (int64_t)(t + 1) * BK;
-      fetch(A, a.lda, m0, a.M, AKM, k1, va);
-      fetch(B, a.ldb, n0, a.N, BKM, k1, vb);
+      fetch(A, a.lda, m0, a.M, AKM, t + 1, oa, va);
+      fetch(B, a.ldb, n0, a.N, BKM, t + 1, ob, vb);
     }
+    // the four MFMAs' elements of 16 rows from r0 in 16-deep block h
+    auto frag = [&](const float *st, bool km, int r0, int h) {
+      const int r = r0 + (l & 15), g = l >> 4;
+      if (!km) return *(const f32x4 *)(st + r * BK + ((4 * h + g) ^ kc_key<2 * BK>(r)) * 4);
+      f32x4 v;
 #pragma unroll
-    for (int s = 0; s < BK / 4; ++s) {
-      float fa[F], fb[F];
+      for (int s = 0; s < 4; ++s) v[s] = st[(16 * h + 4 * g + s) * LD + r];
+      return v;
+    };
 #pragma unroll
-      for (int i = 0; i < F; ++i) fa[i] = ta[(4 * s + (l >> 4)) * LD + wm + 16 * i + (l & 15)];
+    for (int h = 0; h < BK / 16; ++h) {
+      f32x4 fa[F], fb[F];
 #pragma unroll
-      for (int j = 0; j < F; ++j) fb[j] = tb[(4 * s + (l >> 4)) * LD + wn + 16 * j + (l & 15)];
+      for (int i = 0; i < F; ++i) fa[i] = frag(ta, AKM, wm + 16 * i, h);
 #pragma unroll
-      for (int i = 0; i < F; ++i)
+      for (int j = 0; j < F; ++j) fb[j] = frag(tb, BKM, wn + 16 * j, h);
 #pragma unroll
-        for (int j = 0; j < F; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][s], fa[i][s], acc[i][j], 0, 0, 0);
     }
   }
   __syncthreads();
