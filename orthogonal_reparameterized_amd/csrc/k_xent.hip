@@ -141,36 +141,46 @@ struct XentDh {
   }
 };
 
-// Few tokens (n <= 16, bf16): every wave walks groups of 16 vocabulary rows, a whole k range
-// each, and keeps a running (max, sum) per lane (row l % 16, its 4 columns of each group);
-// one partial per workgroup.  Bound by reading W once.
+// Few tokens (n <= 16, bf16): bound by reading W once.  Every wave walks groups of 16
+// vocabulary rows, takes each group's whole k (the next 256 k in flight while these multiply)
+// and keeps a running (max, sum) per lane (row l % 16, its 4 columns of each group); one
+// partial per workgroup.  8 tokens, d = 4096, 131072 rows: 214 us, 5.0 TB/s, the rate of a
+// large copy (242 us without the loads ahead; 228-240 us with a group's k shared by 4 or 8
+// waves; 222 us with half or twice the workgroups).
 __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
-  constexpr int U = 4;
+  constexpr int U = 8;  // 32-deep steps per turn
   __shared__ float2 st[8][16];
   const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int64_t m = l & 15;
-  const bf16_t *pa = (const bf16_t *)a.A + (m < a.M ? m : a.M - 1) * a.lda;
+  const bf16_t *pa = (const bf16_t *)a.A + (m < a.M ? m : a.M - 1) * a.lda + 8 * (l >> 4);
   const int64_t t = m < a.M ? (int64_t)epi.target[m] : -1;
-  const int64_t groups = cdiv(a.N, 16);
+  const int64_t groups = cdiv(a.N, 16), whole = a.K / (32 * U);  // whole turns of k
   float mx = -INFINITY, s = 0.f;
   for (int64_t g = (int64_t)blockIdx.x * 8 + wave; g < groups; g += (int64_t)gridDim.x * 8) {
     const int64_t n = g * 16 + (l & 15);
-    const bf16_t *pb = (const bf16_t *)a.B + (n < a.N ? n : a.N - 1) * a.ldb;
+    const bf16_t *pb = (const bf16_t *)a.B + (n < a.N ? n : a.N - 1) * a.ldb + 8 * (l >> 4);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    int64_t k0 = 8 * (l >> 4);
-    int64_t k = 0;
-    for (; k + 32 * U <= a.K; k += 32 * U) {
-      bf16x8 fb[U], fa[U];
+    bf16x8 fb[2][U], fa[2][U];
+    auto load = [&](int64_t q, bf16x8 (&b_)[U], bf16x8 (&a_)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) fb[u] = row_frag(pb + k + k0 + 32 * u, 8);
+      for (int u = 0; u < U; ++u) b_[u] = row_frag(pb + (q * U + u) * 32, 8);
 #pragma unroll
-      for (int u = 0; u < U; ++u) fa[u] = row_frag(pa + k + k0 + 32 * u, 8);
+      for (int u = 0; u < U; ++u) a_[u] = row_frag(pa + (q * U + u) * 32, 8);
+    };
+    auto mul = [&](const bf16x8 (&b_)[U], const bf16x8 (&a_)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[u], fa[u], acc, 0, 0, 0);
+      for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b_[u], a_[u], acc, 0, 0, 0);
+    };
+    if (whole > 0) load(0, fb[0], fa[0]);
+    for (int64_t q = 0; q < whole; q += 2) {
+      if (q + 1 < whole) load(q + 1, fb[1], fa[1]);
+      mul(fb[0], fa[0]);
+      if (q + 2 < whole) load(q + 2, fb[0], fa[0]);
+      if (q + 1 < whole) mul(fb[1], fa[1]);
     }
-    for (; k < a.K; k += 32) {
-      const bf16x8 fb = row_frag(pb + k + k0, a.K - k - k0), fa = row_frag(pa + k + k0, a.K - k - k0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa, acc, 0, 0, 0);
+    for (int64_t k = whole * 32 * U; k < a.K; k += 32) {  // the rest, 32 at a time
+      const int64_t left = a.K - k - 8 * (l >> 4);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(row_frag(pb + k, left), row_frag(pa + k, left), acc, 0, 0, 0);
     }
     // lane l: row l % 16, columns n0 .. n0 + 3
     const int64_t n0 = g * 16 + 4 * (l >> 4);
@@ -201,23 +211,31 @@ __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
   }
 }
 
-// lse and loss from the partials [tiles][n]: 16 rows per workgroup, 16 threads per row.
+// lse and loss from the partials [tiles][n]: C rows per workgroup of 256, 256 / C threads per
+// row (16 rows read whole 128-byte lines; few rows take all threads each).
+template <int C>
 __global__ __launch_bounds__(256) void k_xent_join(const float2 *part, int64_t tiles, int64_t n, const int32_t *target,
                                                    int64_t vocab, const float *at_target, float *loss, float *lse) {
-  __shared__ float2 red[16][16];
-  const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
-  const int64_t row = (int64_t)blockIdx.x * 16 + c;
+  constexpr int Q = 256 / C;
+  __shared__ float2 red[Q][C];
+  const int c = threadIdx.x % C, q = threadIdx.x / C;
+  const int64_t row = (int64_t)blockIdx.x * C + c;
   float m = -INFINITY, s = 0.f;
   if (row < n)
-    for (int64_t t = q; t < tiles; t += 16) {
+    for (int64_t t = q; t < tiles; t += Q) {
       const float2 p = part[t * n + row];
       join_stats(m, s, p.x, p.y);
     }
   red[q][c] = make_float2(m, s);
-  __syncthreads();
-  if (q || row >= n) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) join_stats(m, s, red[i][c].x, red[i][c].y);
+  for (int o = Q / 2; o; o >>= 1) {
+    __syncthreads();
+    if (q < o) {
+      join_stats(m, s, red[q + o][c].x, red[q + o][c].y);
+      red[q][c] = make_float2(m, s);
+    }
+  }
+  if (q || row >= n) return;
   const float z = safe_ref(m) + logf(s);
   lse[row] = z;
   const int32_t t = target[row];
@@ -330,7 +348,7 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   int64_t tiles = 0;
   float2 *part = nullptr;
   if (sizeof(T) == 2 && d.n <= 16) {
-    tiles = cdiv(d.v, 128) < 2 * cus ? cdiv(d.v, 128) : 2 * cus;
+    tiles = cdiv(d.v, 128) < 2 * cus ? cdiv(d.v, 128) : 2 * cus;  // workgroups
     part = (float2 *)ar.take((size_t)tiles * d.n * 8);
     if (measure) return POETX_OK;
     const MmArgs a{d.n, d.v, d.d, d.h, d.d, d.w, d.d, 1, 1, 1, d.d};
@@ -356,7 +374,10 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
       t0 += p.tiles_n;
     }
   }
-  return launch_k("xent_join", s, k_xent_join, dim3((unsigned)cdiv(d.n, 16)), dim3(256), 0, (const float2 *)part,
+  if (d.n <= 256)
+    return launch_k("xent_join", s, k_xent_join<1>, dim3((unsigned)d.n), dim3(256), 0, (const float2 *)part, tiles,
+                    d.n, d.target, d.v, (const float *)at, d.loss, d.lse);
+  return launch_k("xent_join", s, k_xent_join<16>, dim3((unsigned)cdiv(d.n, 16)), dim3(256), 0, (const float2 *)part,
                   tiles, d.n, d.target, d.v, (const float *)at, d.loss, d.lse);
 }
 
