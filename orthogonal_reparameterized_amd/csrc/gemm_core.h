@@ -6,9 +6,11 @@
 // base + r ld + k) or k-major (base + k ld + r).
 //
 // What a kernel does with its tile is an epilogue type:
-//   kStats == false: put(m, n, v, nv) takes 8 (nv <= 8 valid) consecutive columns of row m;
+//   kStats == false: put(c, m, n, v, nv) takes 8 (nv <= 8 valid) consecutive columns of row m;
 //     the accumulators pass through a wave's own piece of LDS so that a row's 64 columns
-//     leave as whole 128-byte lines.
+//     leave as whole 128-byte lines.  c = cols(n, nv, rows): what a lane keeps for its 8
+//     columns over all its rows.  kRows > 0: floats per row that stage(m0, M, i) supplies; the
+//     kernel puts them into LDS for the tile's rows first (`rows` points at row m0's).
 //   kStats == true: reduce() gets the whole tile's accumulators (row statistics).
 // kSplits says whether a product with this epilogue may be split over k.
 #pragma once
@@ -123,10 +125,13 @@ template <> struct FragOf<f32x4> { static constexpr int ROWS = 16, QUADS = 1; };
 // row of results at a time goes through `st`, this wave's own ROWS x (columns + 4) floats.
 template <int FM, int FN, class V, class Epi>
 __device__ inline void put_rows(const V (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, float *st,
-                                const Epi &epi) {
+                                const Epi &epi, const float *rows = nullptr) {
   constexpr int R = FragOf<V>::ROWS, Q = FragOf<V>::QUADS;
   constexpr int W = FN * R, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
-  const int l = threadIdx.x & 63;
+  const int l = threadIdx.x & 63, c = (l % LPR) * 8;
+  const int64_t n = n0 + c;
+  const int nv = N - n >= 8 ? 8 : N - n > 0 ? (int)(N - n) : 0;
+  const auto ctx = epi.cols(n, nv, rows);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -138,15 +143,35 @@ __device__ inline void put_rows(const V (&acc)[FM][FN], int64_t m0, int64_t n0, 
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int p = 0; p < R / RPP; ++p) {
-      const int r = p * RPP + l / LPR, c = (l % LPR) * 8;
+      const int r = p * RPP + l / LPR;
       const f32x4 a = *(const f32x4 *)(st + r * LD + c), b = *(const f32x4 *)(st + r * LD + c + 4);
-      const int64_t m = m0 + R * i + r, n = n0 + c;
-      if (m < M && n < N) {
+      const int64_t m = m0 + R * i + r;
+      if (m < M && nv) {
         float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        epi.put(m, n, v, N - n >= 8 ? 8 : (int)(N - n));
+        epi.put(ctx, m, n, v, nv);
       }
     }
     __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// The epilogue of a kernel's BM x BN tile; lds: free, at least 16 (columns + 4) floats per wave
+// and kRows BM floats more.
+template <int BM, int BN, int WGM, int WGN, int FM, int FN, class V, class Epi>
+__device__ inline void finish(const V (&acc)[FM][FN], const MmArgs &a, const MmTile &tile, float *lds, const Epi &epi) {
+  constexpr int R = FragOf<V>::ROWS, WTM = BM / WGM, WTN = BN / WGN;
+  const int64_t m0 = (int64_t)tile.tm * BM, n0 = (int64_t)tile.tn * BN;
+  if constexpr (Epi::kStats) {
+    epi.template reduce<BM, BN, WGM, WGN>(acc, m0, n0, a.M, a.N, tile.tn, lds);
+  } else {
+    const int wave = threadIdx.x >> 6, wm = (wave / WGN) * WTM, wn = (wave % WGN) * WTN;
+    float *rows = lds + WGM * WGN * R * (WTN + 4);
+    if constexpr (Epi::kRows > 0) {
+      for (int i = threadIdx.x; i < BM * Epi::kRows; i += 64 * WGM * WGN) rows[i] = epi.stage(m0, a.M, i);
+      __syncthreads();
+    }
+    put_rows<FM, FN>(acc, m0 + wm, n0 + wn, a.M, a.N, lds + wave * R * (WTN + 4), epi.at(tile.split),
+                     rows + wm * Epi::kRows - (m0 + wm) * Epi::kRows);
   }
 }
 
@@ -212,11 +237,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
   }
   __syncthreads();  // every wave is done with the last stage: the epilogue reuses the LDS
-  if constexpr (Epi::kStats) {
-    epi.template reduce<BM, BN, WGM, WGN>(acc, m0, n0, a.M, a.N, tile.tn, (float *)smem);
-  } else {
-    put_rows<FM, FN>(acc, m0 + wm, n0 + wn, a.M, a.N, (float *)smem + wave * 16 * (WTN + 4), epi.at(tile.split));
-  }
+  finish<BM, BN, WGM, WGN>(acc, a, tile, (float *)smem, epi);
 }
 
 // 256 x 256 tile, 8 waves (2 x 4, 128 x 64 each), 64-deep k steps: the large products.
@@ -417,11 +438,7 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   if (!wr) phase_barrier();
   __builtin_amdgcn_s_waitcnt(0);  // the loads past the range have written their zeros
   __syncthreads();                // the epilogue reuses the LDS
-  if constexpr (Epi::kStats) {
-    epi.template reduce<256, 256, 2, 4>(acc, m0, n0, a.M, a.N, tile.tn, (float *)smem);
-  } else {
-    put_rows<FM, FN>(acc, m0 + wr * 128, n0 + wc * 64, a.M, a.N, (float *)smem + wave * 16 * 68, epi.at(tile.split));
-  }
+  finish<256, 256, 2, 4>(acc, a, tile, (float *)smem, epi);
 }
 
 // float32 kernel: BT x BT tile (128 or 64) over 2 x 2 waves, BK-deep k steps (16 or 32), two
@@ -534,11 +551,7 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
     }
   }
   __syncthreads();
-  if constexpr (Epi::kStats) {
-    epi.template reduce<BT, BT, 2, 2>(acc, m0, n0, a.M, a.N, tile.tn, smem);
-  } else {
-    put_rows<F, F>(acc, m0 + wm, n0 + wn, a.M, a.N, smem + wave * 16 * (WT + 4), epi.at(tile.split));
-  }
+  finish<BT, BT, 2, 2>(acc, a, tile, smem, epi);
 }
 
 // Eight consecutive k of an operand row as an MFMA fragment, the first `left` in range.
@@ -606,7 +619,8 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
   if (l < 32 && r < a.M && n0 + c < a.N) {
     const f32x4 p = *(const f32x4 *)(st + r * 20 + c), q = *(const f32x4 *)(st + r * 20 + c + 4);
     float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
-    epi.put(r, n0 + c, v, a.N - n0 - c >= 8 ? 8 : (int)(a.N - n0 - c));
+    const int nv = a.N - n0 - c >= 8 ? 8 : (int)(a.N - n0 - c);
+    epi.put(epi.cols(n0 + c, nv, nullptr), r, n0 + c, v, nv);
   }
 }
 
@@ -627,7 +641,7 @@ __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, 
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += w[e];
   }
-  epi.put(m, n, v, nv);
+  epi.put(epi.cols(n, nv, nullptr), m, n, v, nv);
 }
 
 // Epilogue that only writes: C[m][n] in T, split s at C + s * stride.  Tag (every epilogue
@@ -635,10 +649,13 @@ __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, 
 template <typename T, class Tag>
 struct StoreEpi {
   static constexpr bool kStats = false, kSplits = true;
+  static constexpr int kRows = 0;
   using Tag_ = Tag;
+  struct Cols {};
   T *C; int64_t ld, stride;
+  __device__ Cols cols(int64_t, int, const float *) const { return {}; }
   __device__ StoreEpi at(int split) const { return StoreEpi{C + split * stride, ld, stride}; }
-  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
+  __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
 };
 
 // ------------------------------------------------------------------ host side ----

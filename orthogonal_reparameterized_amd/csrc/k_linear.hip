@@ -12,15 +12,34 @@ struct LinTag {};
 // ------------------------------------------------------------- activations ----
 namespace {
 
-constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhC = 0.79788456080286536f, kTanhA = 0.044715f;  // sqrt(2 / pi)
+
+// The activations run on every result of a product's epilogue, where the matrix cores wait for
+// them: one hardware exp and one reciprocal each (both to about 1 ulp), not the library's erf
+// and tanh (whose epilogue took 31 us of a 130 us round of 256 x 256 tiles, k = 4096).
+
+__device__ inline float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+
+// Phi(p) = erfc(-p / sqrt 2) / 2 by Abramowitz and Stegun's formula 7.1.26 (erf to 1.5e-7):
+// erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0; e: exp(-p^2 / 2).
+__device__ inline float normal_cdf(float p, float e) {
+  const float x = fabsf(p) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  q *= 0.5f * t * e;
+  return p < 0.f ? q : 1.f - q;
+}
 
 __device__ inline float act_value(float p, int act) {
   switch (act) {
     case POETX_ACT_RELU: return p < 0.f ? 0.f : p;  // a NaN stays NaN
-    case POETX_ACT_GELU: return 0.5f * p * (1.f + erff(p * kSqrtHalf));
-    case POETX_ACT_GELU_TANH: return 0.5f * p * (1.f + tanhf(kTanhC * (p + kTanhA * p * p * p)));
-    case POETX_ACT_SILU: return p / (1.f + expf(-p));
+    case POETX_ACT_GELU: return p * normal_cdf(p, __expf(-0.5f * p * p));
+    // (1 + tanh u) / 2 = sigmoid(2 u)
+    case POETX_ACT_GELU_TANH: return p * sigmoid(2.f * kTanhC * (p + kTanhA * p * p * p));
+    case POETX_ACT_SILU: return p * sigmoid(p);
     default: return p;
   }
 }
@@ -28,16 +47,19 @@ __device__ inline float act_value(float p, int act) {
 __device__ inline float act_slope(float p, int act) {
   switch (act) {
     case POETX_ACT_RELU: return p > 0.f ? 1.f : 0.f;
-    case POETX_ACT_GELU:
-      return 0.5f * (1.f + erff(p * kSqrtHalf)) + p * kInvSqrt2Pi * expf(-0.5f * p * p);
+    case POETX_ACT_GELU: {
+      const float e = __expf(-0.5f * p * p);
+      return normal_cdf(p, e) + p * kInvSqrt2Pi * e;
+    }
     case POETX_ACT_GELU_TANH: {
-      // beyond |p| = 20 the slope is 0 or 1 to every float32 digit, while p^3 could overflow
+      // beyond |p| = 20 the slope is 0 or 1 to every float32 digit, while p^3 could overflow;
+      // with g = sigmoid(2 u): d(p g) = g + p g (1 - g) 2 u'
       const float q = fminf(fmaxf(p, -20.f), 20.f);
-      const float t = tanhf(kTanhC * (q + kTanhA * q * q * q));
-      return 0.5f * (1.f + t) + 0.5f * q * (1.f - t * t) * kTanhC * (1.f + 3.f * kTanhA * q * q);
+      const float g = sigmoid(2.f * kTanhC * (q + kTanhA * q * q * q));
+      return g + q * g * (1.f - g) * 2.f * kTanhC * (1.f + 3.f * kTanhA * q * q);
     }
     case POETX_ACT_SILU: {
-      const float g = 1.f / (1.f + expf(-p));
+      const float g = sigmoid(p);
       return g * (1.f + p * (1.f - g));
     }
     default: return 1.f;
@@ -49,21 +71,24 @@ __device__ inline float act_slope(float p, int act) {
 template <typename T>
 struct LinEpi {
   static constexpr bool kStats = false, kSplits = true;
+  static constexpr int kRows = 0;
   using Tag_ = LinTag;
+  struct Cols { float b[8]; };
   T *y, *pre;
   const T *res;
   ParamVec bias;
   int act;
   int64_t ld;
   __device__ const LinEpi &at(int) const { return *this; }
-  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const {
+  __device__ Cols cols(int64_t n, int nv, const float *) const {
+    Cols c = {};
+    if (bias.p && nv) bias.load(n, nv, c.b);
+    return c;
+  }
+  __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
     const int64_t o = m * ld + n;
-    if (bias.p) {
-      float b[8];
-      bias.load(n, nv, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += b[e];
-    }
+    for (int e = 0; e < 8; ++e) v[e] += c.b[e];
     if (pre) store8(pre + o, nv, v);
     if (act != POETX_ACT_NONE) {
 #pragma unroll

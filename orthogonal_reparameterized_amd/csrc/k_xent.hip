@@ -97,22 +97,34 @@ struct XentStats {
 template <typename T>
 struct XentDl {
   static constexpr bool kStats = false, kSplits = false;
+  static constexpr int kRows = 3;
   using Tag_ = XentTag;
+  struct Cols { const float *rows; };
   T *dl;
   int64_t ld;
   const int32_t *target;
   const float *lse, *dloss;
   int64_t v0, vocab;
   __device__ const XentDl &at(int) const { return *this; }
-  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const {
-    const int64_t t = target[m];
-    const bool on = t >= 0 && t < vocab;
-    const float z = lse[m], g = dloss[m];
+  __device__ Cols cols(int64_t, int, const float *rows) const { return {rows}; }
+  // lse, dloss and the target of each row of the tile; a row that takes no part has target -1
+  __device__ float stage(int64_t m0, int64_t M, int i) const {
+    const int64_t m = m0 + i / 3;
+    if (m >= M) return 0.f;
+    if (i % 3 == 0) return lse[m];
+    if (i % 3 == 1) return dloss[m];
+    const int32_t t = target[m];
+    return __int_as_float(t >= 0 && t < vocab ? t : -1);
+  }
+  __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
+    const float *r = c.rows + m * 3;
+    const float z = r[0], g = r[1];
+    const int t = __float_as_int(r[2]);
     const int64_t q = t - v0 - n;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = __expf(v[e] - z) - (q == e ? 1.f : 0.f);
-      v[e] = on && e < nv ? p * g : 0.f;
+      v[e] = t >= 0 && e < nv ? p * g : 0.f;
     }
     store8(dl + m * ld + n, sizeof(T) == 2 ? 8 : nv, v);
   }
@@ -122,13 +134,16 @@ struct XentDl {
 template <typename T>
 struct XentDh {
   static constexpr bool kStats = false, kSplits = true;
+  static constexpr int kRows = 0;
   using Tag_ = XentTag;
+  struct Cols {};
   float *sum;
   T *dh;
   int64_t ld;
   int first, last;
   __device__ const XentDh &at(int) const { return *this; }
-  __device__ void put(int64_t m, int64_t n, float (&v)[8], int nv) const {
+  __device__ Cols cols(int64_t, int, const float *) const { return {}; }
+  __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const {
     const int64_t o = m * ld + n;
     if (!first) {
       float w[8];
