@@ -279,16 +279,15 @@ struct Half<RUN, false> {
       voff[i] = (int)((row * ld + kbeg) * 2) + (((l & 7) ^ kc_key<64>(r)) << 4);
     }
   }
+  // branch-free: a lane whose k lies past the range takes an offset past the buffer
   __device__ void issue(int t, int h, bf16_t *tile) const {
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
-    const int64_t left = span - (int64_t)t * 64;
+    const int64_t left64 = span - (int64_t)t * 64;
+    const int left = left64 < 64 ? (int)left64 : 64;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      int off = voff[i] + t * 128 + h * step;
-      if (left < 64) {
-        const int r = (w * 2 + i) * 8 + (l >> 3);
-        if ((((l & 7) ^ kc_key<64>(r)) << 3) >= left) off = kPast;
-      }
+      const int r = (w * 2 + i) * 8 + (l >> 3);
+      const int off = (((l & 7) ^ kc_key<64>(r)) << 3) < left ? voff[i] + t * 128 + h * step : kPast;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * 2 + i) * 512), 16, off, 0, 0, 0);
     }
   }
@@ -340,7 +339,9 @@ __device__ inline void phase_barrier() {
 }
 }  // namespace
 
-template <bool AKM, bool BKM, class Epi>
+// FLIP: the results leave as C^T, rows n and columns m: the roles of the operands (128 rows of
+// A and 64 of B per wave) are then the caller's choice.
+template <bool AKM, bool BKM, bool FLIP, class Epi>
 __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   constexpr int HE = 128 * 64, FM = 8, FN = 4;  // elements of a half tile; 16 x 16 results per wave
   extern __shared__ __align__(16) bf16_t smem[];  // [A0 A1 B0 B1][2 steps]
@@ -402,9 +403,12 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          // operands swapped: lane l then holds C[m = l % 16][n = 4 (l / 16) + 0..3]
-          acc[4 * P + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(j < 2 ? fb0[S][q][j] : fb1[q][j - 2], fa[q][i],
-                                                                      acc[4 * P + i][j], 0, 0, 0);
+        {
+          // operands swapped (B first): lane l then holds C[m = l % 16][n = 4 (l / 16) + 0..3]
+          const bf16x8 b = j < 2 ? fb0[S][q][j] : fb1[q][j - 2];
+          acc[4 * P + i][j] = FLIP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[q][i], b, acc[4 * P + i][j], 0, 0, 0)
+                                   : __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, fa[q][i], acc[4 * P + i][j], 0, 0, 0);
+        }
     __builtin_amdgcn_s_setprio(0);
     phase_barrier();
   };
@@ -438,7 +442,16 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   if (!wr) phase_barrier();
   __builtin_amdgcn_s_waitcnt(0);  // the loads past the range have written their zeros
   __syncthreads();                // the epilogue reuses the LDS
-  finish<256, 256, 2, 4>(acc, a, tile, (float *)smem, epi);
+  if constexpr (FLIP) {
+    f32x4 tr[FN][FM];  // the same registers, rows and columns exchanged
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) tr[j][i] = acc[i][j];
+    put_rows<FN, FM>(tr, n0 + wc * 64, m0 + wr * 128, a.N, a.M, (float *)smem + wave * 16 * 132, epi);
+  } else {
+    finish<256, 256, 2, 4>(acc, a, tile, (float *)smem, epi);
+  }
 }
 
 // float32 kernel: BT x BT tile (128 or 64) over 2 x 2 waves, BK-deep k steps (16 or 32), two
@@ -720,7 +733,7 @@ int mm_launch(const MmArgs &a, int64_t bt, const char *name, const Epi &epi, hip
   const dim3 grid((unsigned)(a.tiles_m * a.tiles_n * a.splits));
   if (bt == 256) {
     constexpr size_t lds = (size_t)2 * 4 * 128 * 64 * 2;
-    auto kern = &k_mm8<AKM, BKM, Epi>;
+    auto kern = &k_mm8<AKM, BKM, false, Epi>;
     static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
     POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
     return launch_k(name, s, kern, grid, dim3(512), lds, a, epi);
@@ -758,6 +771,28 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
     return launch_k("mm_join", s, k_mm_join<Epi>, dim3((unsigned)cdiv(d.M * cdiv(d.N, 8), 256)), dim3(256), 0,
                     (const float *)part, (int)p.splits, d.M, d.N, epi);
   }
+}
+
+// dW = D^T X (D [K][M] and X [K][N], both k-major) for bf16: the kernels read a k-major operand
+// with twice the LDS instructions of a k-contiguous one.  Where a transposed copy of X costs
+// less than that (one pass over X, against a product M times as large), X^T takes the kernel's
+// 128-row role k-contiguous and D its 64-row role.  M, N, K = 65536, 4096, 4096: 1790 us as it
+// lies, 1560 us so; below about M = 8192 the copy eats the gain (8192 tokens, 4096 x 4096: 208 us,
+// of which it would take 27).
+inline bool dw_flips(int64_t M, int64_t N, int64_t K, int dt) {
+  return dt == POETX_BF16 && M >= 8192 && mm_plan(N, M, K, dt).bt == 256 && mm_plan(N, M, K, dt).splits == 1;
+}
+// XT: [N][ldt], ldt a multiple of 8, zeros past K
+template <class Epi>
+int mm_run_flipped(const MmDesc &d, const Epi &epi, hipStream_t s) {
+  const MmPlan p = mm_plan(d.M, d.N, d.K, POETX_BF16);
+  const MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, 1, d.K};
+  if (p.tiles_m * p.tiles_n > kMaxTiles) return POETX_ERR_UNSUPPORTED;
+  constexpr size_t lds = (size_t)2 * 4 * 128 * 64 * 2;
+  auto kern = &k_mm8<false, true, true, Epi>;
+  static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
+  POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
+  return launch_k(d.name, s, kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), lds, a, epi);
 }
 
 }  // namespace poetx

@@ -178,6 +178,44 @@ __global__ __launch_bounds__(256) void k_pack_rows(const T *in, int64_t rows, in
   }
 }
 
+// The same, transposed, through 64 x 64 tiles of LDS.
+__global__ __launch_bounds__(256) void k_pack_rows_t(const bf16_t *in, int64_t rows, int64_t cols, bf16_t *out,
+                                                     int64_t ld_out, const int32_t *target, int64_t vocab,
+                                                     int64_t tiles_r, int64_t tiles) {
+  __shared__ bf16_t t[64][66];
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t r0 = tile % tiles_r * 64, c0 = tile / tiles_r * 64;
+    __syncthreads();  // the tile before has been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = threadIdx.x + 256 * i, r = e >> 3, c = (e & 7) * 8;
+      const int64_t row = r0 + r, left = cols - c0 - c;
+      u32v4 u = {0u, 0u, 0u, 0u};
+      if (row < rows && (!target || (target[row] >= 0 && target[row] < vocab))) {
+        if (left >= 8) {
+          __builtin_memcpy(&u, in + row * cols + c0 + c, 16);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < left) u[k >> 1] |= (uint32_t)in[row * cols + c0 + c + k] << (16 * (k & 1));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *(uint32_t *)&t[r][c + 2 * k] = u[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = threadIdx.x + 256 * i, c = e >> 3, r = (e & 7) * 8;
+      if (c0 + c >= cols || r0 + r >= ld_out) continue;
+      u32v4 u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = (uint32_t)t[r + 2 * k][c] | (uint32_t)t[r + 2 * k + 1][c] << 16;
+      __builtin_memcpy(out + (c0 + c) * ld_out + r0 + r, &u, 16);
+    }
+  }
+}
+
 // Workgroups of 256 for `n` independent items, walked with the grid's stride.
 static dim3 stride_grid(int64_t n) {
   const int64_t g = cdiv(n, 256);
@@ -193,6 +231,14 @@ int pack_rows(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_
                     (float *)out, ld_out, target, vocab);
   return launch_k("pack_rows", s, k_pack_rows<bf16_t>, grid, dim3(256), 0, (const bf16_t *)in, rows, cols,
                   (bf16_t *)out, ld_out, target, vocab);
+}
+
+int pack_rows_t(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
+                int64_t vocab, hipStream_t s) {
+  if (rows == 0) return POETX_OK;
+  const int64_t tr = cdiv(ld_out, 64), tiles = tr * cdiv(cols, 64);
+  return launch_k("pack_rows_t", s, k_pack_rows_t, dim3((unsigned)(tiles < 65536 ? tiles : 65536)), dim3(256), 0,
+                  (const bf16_t *)in, rows, cols, (bf16_t *)out, ld_out, target, vocab, tr, tiles);
 }
 
 int fill_zero(void *p, int64_t n, int dt, hipStream_t s) {
@@ -291,6 +337,18 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   }
   if (d.dw) {
     if (d.n == 0) return measure ? POETX_OK : fill_zero(d.dw, d.d_out * d.d_in, d.dt, s);
+    if constexpr (sizeof(T) == 2) {
+      if (dw_flips(d.d_out, d.d_in, d.n, d.dt)) {
+        const int64_t ldt = round8(d.n);
+        void *xt = ar.take((size_t)d.d_in * ldt * 2);
+        if (measure) return POETX_OK;
+        POETX_TRY(pack_rows_t(d.x, d.n, d.d_in, xt, ldt, nullptr, 0, s));
+        MmDesc m;
+        m.M = d.d_in; m.N = d.d_out; m.K = d.n; m.name = "linear_dw";
+        m.A = xt; m.lda = ldt; m.B = dp; m.ldb = ld;
+        return mm_run_flipped(m, StoreEpi<T, LinTag>{(T *)d.dw, d.d_in, 0}, s);
+      }
+    }
     Packed x;
     POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));
     MmDesc m;

@@ -311,21 +311,27 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   Operands o;
   POETX_TRY(operands(d, piece, ar, measure, s, o));
   // dW reads h with the rows that take no part as zeros: their dl is zero, but zero times an
-  // infinity or a NaN in such a row would not be
-  const void *hz = nullptr;
+  // infinity or a NaN in such a row would not be.  The copy is transposed where the product's
+  // kernel gains by it.
+  const int64_t last = d.v % piece ? d.v % piece : piece;
+  const bool flip = sizeof(T) == 2 && d.dw && dw_flips(piece, d.d, d.n, d.dt) && dw_flips(last, d.d, d.n, d.dt);
+  const int64_t ldt = round8(d.n);
+  void *hz = nullptr;
   if (d.dw) {
-    hz = ar.take((size_t)d.n * o.ld * sizeof(T));
-    if (!measure) POETX_TRY(pack_rows(d.h, d.n, d.d, (void *)hz, o.ld, d.target, d.v, d.dt, s));
+    hz = ar.take((flip ? (size_t)d.d * ldt : (size_t)d.n * o.ld) * sizeof(T));
+    if (!measure) {
+      if (flip) POETX_TRY(pack_rows_t(d.h, d.n, d.d, hz, ldt, d.target, d.v, s));
+      else POETX_TRY(pack_rows(d.h, d.n, d.d, hz, o.ld, d.target, d.v, d.dt, s));
+    }
   }
   const int64_t ldl = sizeof(T) == 2 ? round8(piece) : piece;
   T *dl = (T *)ar.take((size_t)d.n * ldl * sizeof(T));
   float *sum = d.dh && piece < d.v ? (float *)ar.take((size_t)d.n * d.d * 4) : nullptr;
   // partials of split products: of whole pieces and of the last one
   size_t part_bytes = 0;
-  const int64_t last = d.v % piece ? d.v % piece : piece;
   for (const int64_t vc : {piece, last}) {
     const size_t a = d.dh ? mm_plan(d.n, d.d, vc, d.dt).part_bytes : 0;
-    const size_t b = d.dw ? mm_plan(vc, d.d, d.n, d.dt).part_bytes : 0;
+    const size_t b = d.dw && !flip ? mm_plan(vc, d.d, d.n, d.dt).part_bytes : 0;
     part_bytes = a > part_bytes ? a : part_bytes;
     part_bytes = b > part_bytes ? b : part_bytes;
   }
@@ -345,7 +351,15 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
       POETX_TRY((mm_run<T, false, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
                                      XentDh<T>{sum, (T *)d.dh, d.d, v0 == 0, v0 + vc == d.v}, s)));
     }
-    if (d.dw) {
+    if constexpr (sizeof(T) == 2) {
+      if (flip) {
+        MmDesc g;
+        g.M = d.d; g.N = vc; g.K = d.n; g.name = "xent_dw";
+        g.A = hz; g.lda = ldt; g.B = dl; g.ldb = ldl;
+        POETX_TRY(mm_run_flipped(g, StoreEpi<T, XentTag>{(T *)d.dw + v0 * d.d, d.d, 0}, s));
+      }
+    }
+    if (d.dw && !flip) {
       MmDesc g;
       g.M = vc; g.N = d.d; g.K = d.n; g.name = "xent_dw";
       g.A = dl; g.lda = ldl; g.B = hz; g.ldb = o.ld;

@@ -239,6 +239,10 @@ int linear_backward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s);
 // whose target lies outside [0, vocab) become zero
 int pack_rows(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
               int64_t vocab, int dt, hipStream_t s);
+// out[c][r] = in[r][c] (bf16 [rows][cols] -> [cols][ld_out], ld_out >= rows a multiple of 8, zero
+// past rows); `target` as above
+int pack_rows_t(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
+                int64_t vocab, hipStream_t s);
 int fill_zero(void *p, int64_t n, int dt, hipStream_t s);  // n elements
 
 // ---------------------------------------------------------------------------

@@ -234,6 +234,13 @@ def test_linear_many_tiles(B, n, i, o):
     check_linear_bwd(B, n, i, o, BF16, "silu")
 
 
+@pytest.mark.parametrize("n,i,o", [(203, 1100, 12300), (64, 1288, 12301)])
+def test_linear_wide_weight_gradient(B, n, i, o):
+    """Weight gradients with many rows, whose product takes a transposed copy of x."""
+    check_linear_bwd(B, n, i, o, BF16, "gelu")
+    check_linear_bwd(B, n, i, o, BF16, "none")
+
+
 def test_linear_outputs_not_wanted_and_no_tokens(B):
     x, w = linear_case(60, 50, 72, 40, BF16)
     dy = rand(62, 50, 40, dtype=BF16)
@@ -330,6 +337,7 @@ def test_xent(B, n, d, v, dtype):
 
 def test_xent_large_tiles(B):
     check_xent(B, 3400, 136, 3333, BF16)
+    check_xent(B, 131, 1004, 12500, BF16)  # dW by way of a transposed copy of h
 
 
 def test_xent_every_row_masked_and_no_rows(B):
