@@ -27,6 +27,11 @@ struct MmArgs {
   int tiles_m, tiles_n;
   int splits;   // k ranges; split s covers k in [s kc, (s+1) kc)
   int64_t kc;   // a multiple of 64 when splits > 1
+  // k_mm8: tiles at or past `full` (in tile order) are each shared by tail_splits workgroups,
+  // k ranges of tail_kc; their float32 tiles go to tail_part[tile - full][range] (256 x 256)
+  int full = 0x7fffffff, tail_splits = 1;
+  int64_t tail_kc = 0;
+  float *tail_part = nullptr;
 };
 
 namespace {
@@ -35,20 +40,31 @@ namespace {
 // so that each XCD gets one contiguous run of the tile order (any count), in which groups
 // of 4 m-tiles sweep n: the workgroups running together on an XCD share their panels in
 // its L2.
-struct MmTile { int tm, tn, split; };
-__device__ inline MmTile mm_tile(const MmArgs &a) {
-  const int T = a.tiles_m * a.tiles_n, tot = T * a.splits;
-  const int id = (int)blockIdx.x, x = id & 7, q = tot >> 3, r = tot & 7;
-  int L = x * q + (x < r ? x : r) + (id >> 3);
-  MmTile t;
-  t.split = L / T;
-  L -= t.split * T;
+struct MmTile { int tm, tn, split, tail; };  // tail: index of a shared tile, or -1
+__device__ inline void tile_at(const MmArgs &a, int L, int &tm, int &tn) {
   const int GM = a.tiles_m < 4 ? a.tiles_m : 4, per = GM * a.tiles_n;
   const int grp = L / per, first = grp * GM, gm = a.tiles_m - first < GM ? a.tiles_m - first : GM, loc = L - grp * per;
   // divisions run on the vector ALU: back to scalars, so that operand bases stay uniform
-  t.tm = __builtin_amdgcn_readfirstlane(first + loc % gm);
-  t.tn = __builtin_amdgcn_readfirstlane(loc / gm);
-  t.split = __builtin_amdgcn_readfirstlane(t.split);
+  tm = __builtin_amdgcn_readfirstlane(first + loc % gm);
+  tn = __builtin_amdgcn_readfirstlane(loc / gm);
+}
+__device__ inline MmTile mm_tile(const MmArgs &a) {
+  const int T = a.tiles_m * a.tiles_n, id = (int)blockIdx.x;
+  MmTile t;
+  int L;
+  if (id >= a.full) {
+    const int u = (id - a.full) / a.tail_splits;
+    t.tail = __builtin_amdgcn_readfirstlane(u);
+    t.split = __builtin_amdgcn_readfirstlane(id - a.full - u * a.tail_splits);
+    L = a.full + u;
+  } else {
+    const int tot = a.full < T ? a.full : T * a.splits, x = id & 7, q = tot >> 3, r = tot & 7;
+    L = x * q + (x < r ? x : r) + (id >> 3);
+    t.tail = -1;
+    t.split = __builtin_amdgcn_readfirstlane(L / T);
+    L -= t.split * T;
+  }
+  tile_at(a, L, t.tm, t.tn);
   return t;
 }
 
@@ -176,6 +192,20 @@ __device__ inline void finish(const V (&acc)[FM][FN], const MmArgs &a, const MmT
 }
 
 }  // namespace
+
+// Epilogue that only writes: C[m][n] in T, split s at C + s * stride.  Tag (every epilogue
+// names one, as Tag_) keeps the kernels of two source files apart.
+template <typename T, class Tag>
+struct StoreEpi {
+  static constexpr bool kStats = false, kSplits = true;
+  static constexpr int kRows = 0;
+  using Tag_ = Tag;
+  struct Cols {};
+  T *C; int64_t ld, stride;
+  __device__ Cols cols(int64_t, int, const float *) const { return {}; }
+  __device__ StoreEpi at(int split) const { return StoreEpi{C + split * stride, ld, stride}; }
+  __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
+};
 
 // bf16 kernel: BM x BN tile over WGM x WGN waves, 64-deep k steps, two LDS stages filled by
 // direct global -> LDS loads, one barrier per step.
@@ -347,7 +377,8 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   extern __shared__ __align__(16) bf16_t smem[];  // [A0 A1 B0 B1][2 steps]
   const MmTile tile = mm_tile(a);
   const int64_t m0 = (int64_t)tile.tm * 256, n0 = (int64_t)tile.tn * 256;
-  const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
+  const int64_t kc = tile.tail >= 0 ? a.tail_kc : a.splits > 1 ? a.kc : a.K;
+  const int64_t kbeg = tile.split * kc, kend = kbeg + kc < a.K ? kbeg + kc : a.K;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wr = wave >> 2, wc = wave & 3;
 
@@ -442,6 +473,14 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   if (!wr) phase_barrier();
   __builtin_amdgcn_s_waitcnt(0);  // the loads past the range have written their zeros
   __syncthreads();                // the epilogue reuses the LDS
+  if constexpr (Epi::kSplits) {
+    if (tile.tail >= 0) {
+      float *part = a.tail_part + ((int64_t)tile.tail * a.tail_splits + tile.split) * 65536;
+      put_rows<FM, FN>(acc, wr * 128, wc * 64, 256, 256, (float *)smem + wave * 16 * 68,
+                       StoreEpi<float, typename Epi::Tag_>{part, 256, 0});
+      return;
+    }
+  }
   if constexpr (FLIP) {
     f32x4 tr[FN][FM];  // the same registers, rows and columns exchanged
 #pragma unroll
@@ -657,19 +696,27 @@ __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, 
   epi.put(epi.cols(n, nv, nullptr), m, n, v, nv);
 }
 
-// Epilogue that only writes: C[m][n] in T, split s at C + s * stride.  Tag (every epilogue
-// names one, as Tag_) keeps the kernels of two source files apart.
-template <typename T, class Tag>
-struct StoreEpi {
-  static constexpr bool kStats = false, kSplits = true;
-  static constexpr int kRows = 0;
-  using Tag_ = Tag;
-  struct Cols {};
-  T *C; int64_t ld, stride;
-  __device__ Cols cols(int64_t, int, const float *) const { return {}; }
-  __device__ StoreEpi at(int split) const { return StoreEpi{C + split * stride, ld, stride}; }
-  __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
-};
+// The same for the shared tiles of k_mm8: 32 workgroups per tile, one thread per 8 columns.
+template <class Epi>
+__global__ __launch_bounds__(256) void k_mm_tail(MmArgs a, Epi epi) {
+  const int tail = blockIdx.x / 32, i = (int)(blockIdx.x % 32) * 256 + threadIdx.x;
+  int tm, tn;
+  tile_at(a, a.full + tail, tm, tn);
+  const int64_t m = (int64_t)tm * 256 + i / 32, n = (int64_t)tn * 256 + i % 32 * 8;
+  if (m >= a.M || n >= a.N) return;
+  const float *p = a.tail_part + (int64_t)tail * a.tail_splits * 65536 + i * 8;
+  float v[8];
+  load8(p, 8, v);
+#pragma unroll 2
+  for (int s = 1; s < a.tail_splits; ++s) {
+    float w[8];
+    load8(p + (int64_t)s * 65536, 8, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
+  }
+  const int nv = a.N - n >= 8 ? 8 : (int)(a.N - n);
+  epi.put(epi.cols(n, nv, nullptr), m, n, v, nv);
+}
 
 // ------------------------------------------------------------------ host side ----
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // a grid holds fewer than 2^32 threads
@@ -678,6 +725,7 @@ constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // a grid holds fewer than 2^32
 struct MmPlan {
   int64_t bt = 64, splits = 1, kc = 0;
   int64_t tiles_m = 0, tiles_n = 0;
+  int64_t full = 0, tail_splits = 1, tail_kc = 0;  // 256 x 256 tiles from `full` on share their k
   size_t part_bytes = 0;  // workspace of a split product
 };
 
@@ -725,12 +773,30 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
       else p.part_bytes = (size_t)p.splits * M * N * 4;
     }
   }
+  // 256 x 256 tiles past the last whole round of one per CU: where at most half the CUs would
+  // have one, its k is shared by as many as fill the round.  Kept where the round's time (a CU
+  // does 5.6 TFLOP/s) shrinks by more than the partials' write, read and join (4.5 TB/s, 6 us).
+  p.full = tiles;
+  const int64_t left = tiles % cus;
+  if (may_split && p.bt == 256 && tiles > cus && left && 2 * left <= cus) {
+    int64_t sp = cus / left;
+    if (sp > K / 256) sp = K / 256;
+    if (sp > 8) sp = 8;
+    const double round_us = (double)K * 131072 / 5.6e6, parts_us = (double)left * sp * 524288 / 4.5e6 + 6;
+    if (sp >= 2 && round_us * (sp - 1) / sp > 1.2 * parts_us) {
+      p.full = tiles - left;
+      p.tail_kc = cdiv(cdiv(K, sp), 64) * 64;
+      p.tail_splits = cdiv(K, p.tail_kc);
+      p.part_bytes = (size_t)left * p.tail_splits * 65536 * 4;
+    }
+  }
   return p;
 }
 
 template <bool AKM, bool BKM, class Epi>
 int mm_launch(const MmArgs &a, int64_t bt, const char *name, const Epi &epi, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n * a.splits));
+  const int tiles = a.tiles_m * a.tiles_n;
+  const dim3 grid((unsigned)(a.full < tiles ? a.full + (tiles - a.full) * a.tail_splits : tiles * a.splits));
   if (bt == 256) {
     constexpr size_t lds = (size_t)2 * 4 * 128 * 64 * 2;
     auto kern = &k_mm8<AKM, BKM, false, Epi>;
@@ -761,8 +827,16 @@ int mm_run_as(const MmArgs &a, const MmPlan &p, const char *name, const Epi &epi
 template <typename T, bool AKM, bool BKM, class Epi>
 int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStream_t s) {
   if (d.M <= 0 || d.N <= 0) return POETX_OK;
-  const MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, (int)p.splits, p.kc};
-  if (p.tiles_m * p.tiles_n * p.splits > kMaxTiles) return POETX_ERR_UNSUPPORTED;
+  MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, (int)p.splits, p.kc};
+  const int64_t tiles = p.tiles_m * p.tiles_n;
+  if (tiles * p.splits > kMaxTiles) return POETX_ERR_UNSUPPORTED;
+  if constexpr (Epi::kSplits && sizeof(T) == 2) {
+    if (p.full < tiles) {
+      a.full = (int)p.full; a.tail_splits = (int)p.tail_splits; a.tail_kc = p.tail_kc; a.tail_part = part;
+      POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s)));
+      return launch_k("mm_tail", s, k_mm_tail<Epi>, dim3((unsigned)((tiles - p.full) * 32)), dim3(256), 0, a, epi);
+    }
+  }
   if (p.splits == 1) return mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s);
   if constexpr (!Epi::kSplits) {
     return POETX_ERR_UNSUPPORTED;  // planned without splits
@@ -780,12 +854,13 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
 // lies, 1560 us so; below about M = 8192 the copy eats the gain (8192 tokens, 4096 x 4096: 208 us,
 // of which it would take 27).
 inline bool dw_flips(int64_t M, int64_t N, int64_t K, int dt) {
-  return dt == POETX_BF16 && M >= 8192 && mm_plan(N, M, K, dt).bt == 256 && mm_plan(N, M, K, dt).splits == 1;
+  const MmPlan p = mm_plan(N, M, K, dt, false);
+  return dt == POETX_BF16 && M >= 8192 && p.bt == 256;
 }
 // XT: [N][ldt], ldt a multiple of 8, zeros past K
 template <class Epi>
 int mm_run_flipped(const MmDesc &d, const Epi &epi, hipStream_t s) {
-  const MmPlan p = mm_plan(d.M, d.N, d.K, POETX_BF16);
+  const MmPlan p = mm_plan(d.M, d.N, d.K, POETX_BF16, false);
   const MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, 1, d.K};
   if (p.tiles_m * p.tiles_n > kMaxTiles) return POETX_ERR_UNSUPPORTED;
   constexpr size_t lds = (size_t)2 * 4 * 128 * 64 * 2;

@@ -234,6 +234,23 @@ def test_linear_many_tiles(B, n, i, o):
     check_linear_bwd(B, n, i, o, BF16, "silu")
 
 
+@pytest.mark.parametrize("n,i,o", [(4100, 4097, 4352), (2100, 8300, 8448)])
+def test_linear_shared_last_round(B, n, i, o):
+    """More tiles than CUs by a few: the tiles of the last round share their k."""
+    x = (torch.randn(n, i, generator=torch.Generator("cuda").manual_seed(1), device="cuda")).to(BF16)
+    w = (torch.randn(o, i, generator=torch.Generator("cuda").manual_seed(2), device="cuda") * i ** -0.5).to(BF16)
+    dy = torch.randn(n, o, generator=torch.Generator("cuda").manual_seed(3), device="cuda").to(BF16)
+    y, pre = B.poetx_linear_forward(x, w, act="gelu", save_pre=True)
+    p = x.double() @ w.double().t()
+    # roundings of the results alone: at most u(bf16) each, u / sqrt(3) in the mean square
+    assert off(pre, p.cpu()) <= U[BF16] and off(y, torch.nn.functional.gelu(p).cpu()) <= U[BF16]
+    within(pre[-3:], p[-3:].cpu(), U[BF16] * p[-3:].abs().cpu() + acc(i) * (x[-3:].double().abs() @ w.double().abs().t()).cpu(),
+           "last rows")
+    g = B.poetx_linear_backward(x, w, dy)
+    assert off(g["dx"], (dy.double() @ w.double()).cpu()) <= U[BF16]
+    assert off(g["dw"], (dy.double().t().contiguous() @ x.double()).cpu()) <= U[BF16]
+
+
 @pytest.mark.parametrize("n,i,o", [(203, 1100, 12300), (64, 1288, 12301)])
 def test_linear_wide_weight_gradient(B, n, i, o):
     """Weight gradients with many rows, whose product takes a transposed copy of x."""
