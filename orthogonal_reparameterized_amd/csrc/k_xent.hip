@@ -92,8 +92,10 @@ struct XentStats {
 };
 
 // dl of a piece of the vocabulary, rows of ld elements (a multiple of 8 for bf16, zeros
-// past the piece).  Rounding dl to bf16 is the products' operand precision: relative 2^-9
-// per element, of independent sign.
+// past the piece).  Rounding dl to bf16 is the products' operand precision.  So that the errors
+// are independent from row to row, bf16 rows carry dloss_i / G with G the largest |dloss| (the
+// products' epilogues multiply by G): rounded as they are, the rows of a mean, whose dl at the
+// target is nearly -dloss_i = -1 / count for all of them, would share one rounding error.
 template <typename T>
 struct XentDl {
   static constexpr bool kStats = false, kSplits = false;
@@ -103,7 +105,7 @@ struct XentDl {
   T *dl;
   int64_t ld;
   const int32_t *target;
-  const float *lse, *dloss;
+  const float *lse, *dloss, *scale;  // scale: G, or null for 1
   int64_t v0, vocab;
   __device__ const XentDl &at(int) const { return *this; }
   __device__ Cols cols(int64_t, int, const float *rows) const { return {rows}; }
@@ -112,7 +114,7 @@ struct XentDl {
     const int64_t m = m0 + i / 3;
     if (m >= M) return 0.f;
     if (i % 3 == 0) return lse[m];
-    if (i % 3 == 1) return dloss[m];
+    if (i % 3 == 1) return scale ? dloss[m] / *scale : dloss[m];
     const int32_t t = target[m];
     return __int_as_float(t >= 0 && t < vocab ? t : -1);
   }
@@ -136,14 +138,15 @@ struct XentDh {
   static constexpr bool kStats = false, kSplits = true;
   static constexpr int kRows = 0;
   using Tag_ = XentTag;
-  struct Cols {};
+  struct Cols { float g; };
   float *sum;
   T *dh;
+  const float *scale;
   int64_t ld;
   int first, last;
   __device__ const XentDh &at(int) const { return *this; }
-  __device__ Cols cols(int64_t, int, const float *) const { return {}; }
-  __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const {
+  __device__ Cols cols(int64_t, int, const float *) const { return {scale ? *scale : 1.f}; }
+  __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
     const int64_t o = m * ld + n;
     if (!first) {
       float w[8];
@@ -151,10 +154,55 @@ struct XentDh {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += w[e];
     }
-    if (last) store8(dh + o, nv, v);
-    else store8(sum + o, nv, v);
+    if (last) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= c.g;
+      store8(dh + o, nv, v);
+    } else {
+      store8(sum + o, nv, v);
+    }
   }
 };
+
+// dW of a piece.
+template <typename T>
+struct XentDw {
+  static constexpr bool kStats = false, kSplits = true;
+  static constexpr int kRows = 0;
+  using Tag_ = XentTag;
+  struct Cols { float g; };
+  T *dw;
+  const float *scale;
+  int64_t ld;
+  __device__ const XentDw &at(int) const { return *this; }
+  __device__ Cols cols(int64_t, int, const float *) const { return {scale ? *scale : 1.f}; }
+  __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= c.g;
+    store8(dw + m * ld + n, nv, v);
+  }
+};
+
+// G: the largest |dloss| of the tokens that take part, 1 where that is 0 or not finite.
+__global__ __launch_bounds__(1024) void k_xent_scale(const float *dloss, const int32_t *target, int64_t n, int64_t vocab,
+                                                     float *scale) {
+  __shared__ float red[16];
+  float g = 0.f;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < n; i += 1024) {
+    const int32_t t = target[i];
+    const float a = fabsf(dloss[i]);
+    if (t >= 0 && t < vocab && a > g && a < INFINITY) g = a;
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) g = fmaxf(g, __shfl_xor(g, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = g;
+  __syncthreads();
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) g = fmaxf(g, red[w]);
+  *scale = g > 0.f ? g : 1.f;
+}
 
 // Few tokens (n <= 16, bf16): bound by reading W once.  Every wave walks groups of 16
 // vocabulary rows, takes each group's whole k (the next 256 k in flight while these multiply)
@@ -324,6 +372,9 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
       else POETX_TRY(pack_rows(d.h, d.n, d.d, hz, o.ld, d.target, d.v, d.dt, s));
     }
   }
+  float *scale = sizeof(T) == 2 ? (float *)ar.take(4) : nullptr;
+  if (scale && !measure)
+    POETX_TRY(launch_k("xent_scale", s, k_xent_scale, dim3(1), dim3(1024), 0, d.dloss, d.target, d.n, d.v, scale));
   const int64_t ldl = sizeof(T) == 2 ? round8(piece) : piece;
   T *dl = (T *)ar.take((size_t)d.n * ldl * sizeof(T));
   float *sum = d.dh && piece < d.v ? (float *)ar.take((size_t)d.n * d.d * 4) : nullptr;
@@ -343,20 +394,20 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     POETX_TRY(w_piece(d, o, v0, vc, s, &w));
     const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits");
     POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt, false), nullptr,
-                                    XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, v0, d.v}, s)));
+                                    XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, scale, v0, d.v}, s)));
     if (d.dh) {
       MmDesc g;
       g.M = d.n; g.N = d.d; g.K = vc; g.name = "xent_dh";
       g.A = dl; g.lda = ldl; g.B = w; g.ldb = o.ld;
       POETX_TRY((mm_run<T, false, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
-                                     XentDh<T>{sum, (T *)d.dh, d.d, v0 == 0, v0 + vc == d.v}, s)));
+                                     XentDh<T>{sum, (T *)d.dh, scale, d.d, v0 == 0, v0 + vc == d.v}, s)));
     }
     if constexpr (sizeof(T) == 2) {
       if (flip) {
         MmDesc g;
         g.M = d.d; g.N = vc; g.K = d.n; g.name = "xent_dw";
         g.A = hz; g.lda = ldt; g.B = dl; g.ldb = ldl;
-        POETX_TRY(mm_run_flipped(g, StoreEpi<T, XentTag>{(T *)d.dw + v0 * d.d, d.d, 0}, s));
+        POETX_TRY(mm_run_flipped(g, XentDw<T>{(T *)d.dw + v0 * d.d, scale, d.d}, s));
       }
     }
     if (d.dw && !flip) {
@@ -364,7 +415,7 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
       g.M = vc; g.N = d.d; g.K = d.n; g.name = "xent_dw";
       g.A = dl; g.lda = ldl; g.B = hz; g.ldb = o.ld;
       POETX_TRY((mm_run<T, true, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
-                                    StoreEpi<T, XentTag>{(T *)d.dw + v0 * d.d, d.d, 0}, s)));
+                                    XentDw<T>{(T *)d.dw + v0 * d.d, scale, d.d}, s)));
     }
   }
   return POETX_OK;

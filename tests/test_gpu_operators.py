@@ -357,6 +357,25 @@ def test_xent_large_tiles(B):
     check_xent(B, 131, 1004, 12500, BF16)  # dW by way of a transposed copy of h
 
 
+def test_xent_mean_keeps_its_digits(B):
+    """The rows of a mean share one dloss, and their dl at the target is nearly -dloss for all of
+    them: its rounding to bf16 must not become one common error of the gradients.  The dloss
+    here would be off by 0.98 u(bf16), u = 2^-8.  Independent roundings of dl and of the results
+    are 0.43 u each in the mean square (u / 2^e(x) / sqrt(3) over a uniform log x), 0.61 u
+    together."""
+    n, d, v = 700, 256, 6000
+    h, w, t, _ = xent_case(160, n, d, v, BF16)
+    dl = torch.full((n,), 2.0 ** -12 * (1 + 0.98 * 2.0 ** -8))
+    loss, lse = B.poetx_xent_forward(dev(h), dev(w), dev(t))
+    g = B.poetx_xent_backward(dev(h), dev(w), dev(t), lse, dev(dl))
+    on = (t >= 0) & (t < v)
+    p = torch.softmax(h.double() @ w.double().t(), 1)
+    p[torch.arange(n), t.long().clamp(0, v - 1)] -= 1
+    p = p * torch.where(on, dl.double(), torch.zeros(n, dtype=torch.float64))[:, None]
+    assert off(g["dh"], p @ w.double()) <= 0.7 * U[BF16]
+    assert off(g["dw"], p.t() @ h.double()) <= 0.7 * U[BF16]
+
+
 def test_xent_every_row_masked_and_no_rows(B):
     h, w, t, dl = xent_case(130, 40, 64, 500, BF16)
     t[:] = -1
