@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -151,8 +152,18 @@ def _stream(dev: torch.device):
 # stream ordering makes both the reuse between calls and the release of an outgrown
 # buffer safe.  Layers driven on different streams get different workspaces.  A call that is
 # being captured into a graph takes a workspace of its own from the graph's memory pool: it
-# lives as long as the graph, and no eager call or other graph shares it.
-_ws_cache: dict = {}
+# lives as long as the graph, and no eager call or other graph shares it.  Each thread has its
+# own workspaces: a call launches several kernels, and another thread's may come between them
+# on the same stream.
+_ws_local = threading.local()
+
+
+def _ws_cache() -> dict:
+    try:
+        return _ws_local.cache
+    except AttributeError:
+        _ws_local.cache = {}
+        return _ws_local.cache
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
@@ -160,16 +171,18 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
     key = (idx, _raw_stream(idx))
-    t = _ws_cache.get(key)
+    cache = _ws_cache()
+    t = cache.get(key)
     if t is None or t.numel() < nbytes:
         with torch.cuda.device(idx):
             t = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
-        _ws_cache[key] = t
+        cache[key] = t
     return t
 
 
 def release_workspace():
-    _ws_cache.clear()
+    """Drop the calling thread's cached workspaces."""
+    _ws_cache().clear()
 
 
 # --------------------------------------------------------------------------

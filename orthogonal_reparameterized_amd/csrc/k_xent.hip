@@ -315,6 +315,7 @@ int64_t piece_of(const XentDesc &d) {
   const int64_t es = d.dt == POETX_F32 ? 4 : 2;
   int64_t p = ((int64_t)512 << 20) / (d.n * es) & ~(int64_t)255;
   if (p < 2048) p = 2048;
+  if (p > kMaxWidth) p = kMaxWidth;  // a row stride of the products that read dl
   return p < d.v ? p : d.v;
 }
 

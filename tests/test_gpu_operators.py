@@ -523,6 +523,33 @@ def test_captured_and_replayed(B, n):
                 assert torch.equal(p, q), rep
 
 
+def test_two_threads_on_one_stream(B):
+    """Calls of two threads whose kernels interleave on one stream keep their own workspaces."""
+    import threading
+    sets = [chain_inputs(260, 333, BF16), chain_inputs(270, 210, BF16, v=5003)]
+    want = [[r.clone() for r in run_all(B, *a)] for a in sets]
+    bad = []
+
+    def work(k):
+        for _ in range(25):
+            got = run_all(B, *sets[k])
+            torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(p, q) for p, q in zip(want[k], got)):
+                bad.append(k)
+
+    ts = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
+
+
+def test_xent_wide_pieces(B):
+    """Few tokens over more than 2^20 vocabulary entries: pieces of 2^20."""
+    check_xent(B, 18, 16, (1 << 20) + 777, BF16, seed=280)
+
+
 def test_block_step(B):
     """The operators with the POET-X layer between them, as a training step: loss and every
     gradient against float64 (autograd through the definitions, the layer's G from the oracle)."""
