@@ -138,9 +138,8 @@ def _ptr(t: Optional[torch.Tensor], align: int = 16):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _raw_stream(idx: int) -> int:
-    """The current HIP stream of device idx, without building a torch Stream object (2 us)."""
-    return torch._C._cuda_getCurrentRawStream(idx)
+# the current HIP stream of a device by its index, without building a torch Stream object (2 us)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream(dev: torch.device):
@@ -156,6 +155,7 @@ def _stream(dev: torch.device):
 # own workspaces: a call launches several kernels, and another thread's may come between them
 # on the same stream.
 _ws_local = threading.local()
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _ws_cache() -> dict:
@@ -168,7 +168,7 @@ def _ws_cache() -> dict:
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
     key = (idx, _raw_stream(idx))
     cache = _ws_cache()
@@ -499,31 +499,33 @@ def _tokens(t: torch.Tensor, name: str):
 
 
 @functools.lru_cache(maxsize=1024)
-def _ws_query(fn: str, device: int, args: tuple) -> int:
-    """Workspace bytes of a call: what its size query (ws == NULL) answers on this device."""
+def _ws_query(fn: str, idx: int, args: tuple) -> int:
+    """Workspace bytes of a call: what its size query (ws == NULL) answers on device idx, which
+    is the current one."""
     nb = _sz(0)
     _check(getattr(_lib, fn)(*args, None, ctypes.byref(nb), None), f"{fn}(size)")
     return nb.value
 
 
 _SOME = 256  # a non-null pointer for size queries, which look only at which outputs are wanted
+_current_device = torch.cuda.current_device
+_byref = ctypes.byref
 
 
 def _run(fn, dev: torch.device, args: tuple, query: Optional[tuple] = None) -> None:
     """The call on dev's current stream, with its workspace when `query` has its size query's
     arguments.  The library launches on the current device, so that is made dev's."""
+    idx = dev.index
     if dev.type != "cuda":
         raise ValueError("tensors must be on the GPU")
-    idx = dev.index
-    if torch.cuda.current_device() != idx:
+    if _current_device() != idx:
         with torch.cuda.device(dev):
             return _run(fn, dev, args, query)
-    st = _raw_stream(idx)
     if query is None:
-        code = fn(*args, st)
+        code = fn(*args, _raw_stream(idx))
     else:
         ws = _workspace(dev, _ws_query(fn.__name__, idx, query))
-        code = fn(*args, ws.data_ptr(), ctypes.byref(_sz(ws.numel())), st)
+        code = fn(*args, ws.data_ptr(), _byref(_sz(ws.numel())), _raw_stream(idx))
     if code != POETX_OK:
         _check(code, fn.__name__)
 

@@ -680,9 +680,10 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
 // epilogue; one thread per 8 columns.
 template <class Epi>
 __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, int64_t M, int64_t N, Epi epi) {
-  const int64_t cpr = cdiv(N, 8), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  // (a split product has fewer than 2^32 results)
+  const uint32_t cpr = (uint32_t)cdiv(N, 8), i = blockIdx.x * 256 + threadIdx.x;
   if (i >= M * cpr) return;
-  const int64_t m = i / cpr, n = (i % cpr) * 8;
+  const int64_t m = i / cpr, n = (int64_t)(i - (uint32_t)m * cpr) * 8;
   const int nv = N - n >= 8 ? 8 : (int)(N - n);
   float v[8];
   load8(part + m * N + n, nv, v);

@@ -33,36 +33,61 @@ __device__ inline float normal_cdf(float p, float e) {
   return p < 0.f ? q : 1.f - q;
 }
 
-__device__ inline float act_value(float p, int act) {
+// v = act(v); one branch for the eight
+__device__ inline void act_values(float (&v)[8], int act) {
   switch (act) {
-    case POETX_ACT_RELU: return p < 0.f ? 0.f : p;  // a NaN stays NaN
-    case POETX_ACT_GELU: return p * normal_cdf(p, __expf(-0.5f * p * p));
-    // (1 + tanh u) / 2 = sigmoid(2 u)
-    case POETX_ACT_GELU_TANH: return p * sigmoid(2.f * kTanhC * (p + kTanhA * p * p * p));
-    case POETX_ACT_SILU: return p * sigmoid(p);
-    default: return p;
+    case POETX_ACT_RELU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] < 0.f ? 0.f : v[e];  // a NaN stays NaN
+      break;
+    case POETX_ACT_GELU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= normal_cdf(v[e], __expf(-0.5f * v[e] * v[e]));
+      break;
+    case POETX_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2 u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= sigmoid(2.f * kTanhC * (v[e] + kTanhA * v[e] * v[e] * v[e]));
+      break;
+    case POETX_ACT_SILU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= sigmoid(v[e]);
+      break;
+    default: break;
   }
 }
 
-__device__ inline float act_slope(float p, int act) {
+// v *= act'(p)
+__device__ inline void act_slopes(float (&v)[8], const float (&p)[8], int act) {
   switch (act) {
-    case POETX_ACT_RELU: return p > 0.f ? 1.f : 0.f;
-    case POETX_ACT_GELU: {
-      const float e = __expf(-0.5f * p * p);
-      return normal_cdf(p, e) + p * kInvSqrt2Pi * e;
-    }
-    case POETX_ACT_GELU_TANH: {
+    case POETX_ACT_RELU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = p[e] > 0.f ? v[e] : v[e] * 0.f;  // 0 at 0; NaN and infinities of v stay
+      break;
+    case POETX_ACT_GELU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = __expf(-0.5f * p[e] * p[e]);
+        v[e] *= normal_cdf(p[e], d) + p[e] * kInvSqrt2Pi * d;
+      }
+      break;
+    case POETX_ACT_GELU_TANH:
       // beyond |p| = 20 the slope is 0 or 1 to every float32 digit, while p^3 could overflow;
       // with g = sigmoid(2 u): d(p g) = g + p g (1 - g) 2 u'
-      const float q = fminf(fmaxf(p, -20.f), 20.f);
-      const float g = sigmoid(2.f * kTanhC * (q + kTanhA * q * q * q));
-      return g + q * g * (1.f - g) * 2.f * kTanhC * (1.f + 3.f * kTanhA * q * q);
-    }
-    case POETX_ACT_SILU: {
-      const float g = sigmoid(p);
-      return g * (1.f + p * (1.f - g));
-    }
-    default: return 1.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float q = p[e] < -20.f ? -20.f : p[e] > 20.f ? 20.f : p[e];
+        const float g = sigmoid(2.f * kTanhC * (q + kTanhA * q * q * q));
+        v[e] *= g + q * g * (1.f - g) * 2.f * kTanhC * (1.f + 3.f * kTanhA * q * q);
+      }
+      break;
+    case POETX_ACT_SILU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = sigmoid(p[e]);
+        v[e] *= g * (1.f + p[e] * (1.f - g));
+      }
+      break;
+    default: break;
   }
 }
 
@@ -90,10 +115,7 @@ struct LinEpi {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += c.b[e];
     if (pre) store8(pre + o, nv, v);
-    if (act != POETX_ACT_NONE) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], act);
-    }
+    act_values(v, act);
     if (res) {
       float r[8];
       load8(res + o, nv, r);
@@ -124,8 +146,7 @@ __global__ __launch_bounds__(256) void k_act_grad(const T *dy, const T *pre, int
     if (act != POETX_ACT_NONE) {
       float p[8];
       load8(pre + r * cols + c, nv, p);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < nv ? v[e] * act_slope(p[e], act) : 0.f;
+      act_slopes(v, p, act);  // past nv: zero times a finite slope
     }
     // ld_out is a multiple of 8, so a partly valid group is stored whole, with its zeros
     if (dp && nv) store8(dp + r * ld_out + c, ld_out == cols ? nv : 8, v);
@@ -168,9 +189,11 @@ __global__ __launch_bounds__(256) void k_fill_zero(T *out, int64_t n) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_pack_rows(const T *in, int64_t rows, int64_t cols, T *out, int64_t ld_out,
                                                    const int32_t *target, int64_t vocab) {
-  const int64_t cpr = cdiv(ld_out, 8);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * cpr; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cpr, c = (i % cpr) * 8, left = cols - c;
+  const int64_t cpr = cdiv(ld_out, 8), total = rows * cpr;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    // a 32-bit division where it reaches (a 64-bit one is a long sequence)
+    const int64_t r = total <= 0xffffffff ? (int64_t)((uint32_t)i / (uint32_t)cpr) : i / cpr;
+    const int64_t c = (i - r * cpr) * 8, left = cols - c;
     float v[8] = {};
     const bool keep = !target || (target[r] >= 0 && target[r] < vocab);
     if (keep) load8(in + r * cols + c, left >= 8 ? 8 : left > 0 ? (int)left : 0, v);
@@ -315,14 +338,16 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
     int64_t parts = cdiv(4 * cus, cb);
     if (parts > cdiv(d.n, 4)) parts = cdiv(d.n, 4);  // a row per wave at least
     if (parts > 1024) parts = 1024;
-    float *part = d.dbias ? (float *)ar.take((size_t)(parts > 0 ? parts : 1) * d.d_out * 4) : nullptr;
+    if (d.n <= 32) parts = 1;  // the column sums of few rows are whole at once: one launch less
+    const bool join = d.dbias && (parts != 1 || d.n == 0);
+    float *part = join ? (float *)ar.take((size_t)(parts > 0 ? parts : 1) * d.d_out * 4) : d.dbias;
     if (!measure) {
-      if (parts > 0)
+      if (d.n > 0)
         POETX_TRY(launch_k("linear_act_grad", s, k_act_grad<T>, dim3((unsigned)cb, (unsigned)parts), dim3(256), 0,
                            (const T *)d.dy, (const T *)d.saved_pre, d.act, d.n, d.d_out, dpw, ld, part));
-      if (d.dbias)
+      if (join)
         POETX_TRY(launch_k("linear_bias_grad", s, k_sum_parts, dim3((unsigned)cdiv(d.d_out, 64)), dim3(1024), 0,
-                           (const float *)part, parts, d.d_out, d.dbias));
+                           (const float *)part, d.n > 0 ? parts : (int64_t)0, d.d_out, d.dbias));
     }
   }
   if (d.dx) {
