@@ -484,18 +484,20 @@ def _buf(t: Optional[torch.Tensor], name: str, shape, dtypes, dev) -> Optional[i
     raise ValueError(f"{name} must be 16-byte aligned")
 
 
-def _out(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
-    """(tensor, address) of an output: the caller's, checked, or a new one."""
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, ref: torch.Tensor):
+    """(tensor, address) of an output on ref's device: the caller's, checked, or a new one
+    (new_empty and empty_like take half the time of torch.empty with a device)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty_like(ref) if shape is None else ref.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
-    return t, _buf(t, name, shape, (dtype,), dev)
+    return t, _buf(t, name, ref.shape if shape is None else shape, (dtype,), ref.device)
 
 
 def _tokens(t: torch.Tensor, name: str):
-    if t.dim() < 1 or t.shape[-1] < 1:
+    d = t.shape[-1] if t.dim() else 0
+    if d < 1:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [..., features]")
-    return t.numel() // t.shape[-1], t.shape[-1]
+    return t.numel() // d, d
 
 
 @functools.lru_cache(maxsize=1024)
@@ -542,9 +544,9 @@ def poetx_layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = Non
     p = gamma if gamma is not None else beta
     pd = (p.dtype,) if p is not None and p.dtype in _FLOATS else _FLOATS
     pg, pb = _buf(gamma, "gamma", (d,), pd, dev), _buf(beta, "beta", (d,), pd, dev)
-    y, py = _out(y, "y", x.shape, x.dtype, dev)
-    mean, pm = _out(mean, "mean", (n,), torch.float32, dev)
-    rstd, pr = _out(rstd, "rstd", (n,), torch.float32, dev)
+    y, py = _out(y, "y", None, x.dtype, x)
+    mean, pm = _out(mean, "mean", (n,), torch.float32, x)
+    rstd, pr = _out(rstd, "rstd", (n,), torch.float32, x)
     _run(_lib.poetx_layernorm_forward, dev,
          (n, d, _DT[x.dtype], px, pg, pb, _DT[p.dtype] if p is not None else POETX_F32, eps, py, pm, pr))
     return y, mean, rstd
@@ -561,12 +563,11 @@ def poetx_layernorm_backward(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[
     ins = (_buf(dy, "dy", shape, dt, dev), _buf(gamma, "gamma", (d,), _FLOATS, dev))
     stats = (_buf(mean, "mean", (n,), _F32, dev), _buf(rstd, "rstd", (n,), _F32, dev),
              _buf(dres, "dres", shape, dt, dev))
-    dx, pdx = _out(dx, "dx", shape, x.dtype, dev)
+    dx, pdx = _out(dx, "dx", None, x.dtype, x)
     pd, code = _DT[gamma.dtype] if gamma is not None else POETX_F32, _DT[x.dtype]
     out, some, params = dict(dx=dx), None, (None, None)
     if want_params:
-        out["dgamma"] = torch.empty(d, dtype=torch.float32, device=dev)
-        out["dbeta"] = torch.empty(d, dtype=torch.float32, device=dev)
+        out["dgamma"], out["dbeta"] = x.new_empty(d, dtype=torch.float32), x.new_empty(d, dtype=torch.float32)
         some, params = _SOME, (out["dgamma"].data_ptr(), out["dbeta"].data_ptr())
     _run(_lib.poetx_layernorm_backward, dev, (n, d, code, px, *ins, pd, *stats, pdx, *params),
          (n, d, code, None, None, None, pd, None, None, None, None, some, some))
@@ -587,8 +588,8 @@ def poetx_linear_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.
     ins = (_buf(x, "x", x.shape, _FLOATS, dev), _buf(w, "w", (d_out, d_in), dt, dev),
            _buf(bias, "bias", (d_out,), _FLOATS, dev))
     pr = _buf(residual, "residual", shape, dt, dev)
-    y, py = _out(y, "y", shape, x.dtype, dev)
-    pre = torch.empty(shape, dtype=x.dtype, device=dev) if save_pre else None
+    y, py = _out(y, "y", shape, x.dtype, x)
+    pre = torch.empty_like(y) if save_pre else None
     bd, code = _DT[bias.dtype] if bias is not None else POETX_F32, _DT[x.dtype]
     _run(_lib.poetx_linear_forward, dev,
          (n, d_in, d_out, code, *ins, bd, pr, a, py, pre.data_ptr() if save_pre else None),
@@ -619,7 +620,7 @@ def poetx_linear_backward(x: Optional[torch.Tensor], w: Optional[torch.Tensor], 
     for name, want, size, dtype in (("dx", want_dx, shape, dy.dtype), ("dw", want_dw, (d_out, d_in), dy.dtype),
                                     ("dbias", want_dbias, (d_out,), torch.float32)):
         if want:
-            out[name] = torch.empty(size, dtype=dtype, device=dev)
+            out[name] = dy.new_empty(size, dtype=dtype)
         ptrs.append(out[name].data_ptr() if want else None)
     if n == 0 and not (want_dw or want_dbias):
         return out
@@ -640,8 +641,8 @@ def poetx_xent_forward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, *
     lead = h.shape[:-1]
     ins = (_buf(h, "h", h.shape, _FLOATS, dev), _buf(w, "w", (vocab, d), (h.dtype,), dev),
            _buf(target, "target", lead, (torch.int32,), dev))
-    loss, pl = _out(loss, "loss", lead, torch.float32, dev)
-    lse, pz = _out(lse, "lse", lead, torch.float32, dev)
+    loss, pl = _out(loss, "loss", lead, torch.float32, h)
+    lse, pz = _out(lse, "lse", lead, torch.float32, h)
     code = _DT[h.dtype]
     _run(_lib.poetx_xent_forward, dev, (n, d, vocab, code, *ins, pl, pz),
          (n, d, vocab, code, None, None, None, None, None))
