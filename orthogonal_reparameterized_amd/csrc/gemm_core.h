@@ -207,8 +207,10 @@ struct StoreEpi {
   __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
 };
 
-// bf16 kernel: BM x BN tile over WGM x WGN waves, 64-deep k steps, two LDS stages filled by
-// direct global -> LDS loads, one barrier per step.
+// bf16 kernel of the smaller products: 128 x 128 tile over 2 x 2 waves (64 x 64 each), 64-deep k
+// steps, two LDS stages filled by direct global -> LDS loads, one barrier per step, two
+// workgroups per CU that fill each other's waits.  2048^3: 27-30 us, 0.6 PFLOP/s (the vendor
+// library 21-27 us); a handful of tokens or columns is bound by the load latency of its k range.
 template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, class Epi>
 __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
   constexpr int NW = WGM * WGN, BK = 64;
@@ -287,6 +289,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
 // reads and for all but its 8 newest loads (two phases'), so after the barrier the halves that
 // the next phase reads have landed for all waves, and those just read may be overwritten.
 // Loads past the k range read zeros.
+//
+// What bounds it: the chip's power.  At 8192^3 the matrix cores are busy 0.83 of the time at a
+// clock of 1.74 GHz (the vendor library: 0.88 at 1.78); 1.47 PFLOP/s with both operands
+// k-contiguous, 1.40 with a k-major B, 1.34 with both k-major (those issue two 8-byte
+// transposing LDS reads per fragment instead of one of 16 bytes; library 1.63).  One phase of 16
+// MFMAs per pair of halves instead of one of 32 per A half: 1.40, 1.30 and 1.25.  32 x 32 x 16
+// MFMAs in the same schedule were 2 to 6 % slower, four waves of 128 x 128 30 % (the compiler
+// moves accumulators between register files).
 template <int HALF_ROWS, bool KM>
 struct Half;
 
@@ -619,7 +629,8 @@ __device__ inline bf16x8 row_frag(const bf16_t *p, int64_t left) {
   return __builtin_bit_cast(bf16x8, u);
 }
 
-// Few rows (M <= 16, bf16, both operands k-contiguous): bound by reading B once.  Each
+// Few rows (M <= 16, bf16, both operands k-contiguous): bound by reading B once (one token,
+// 13824 x 5120: 26.7 us, 5.3 TB/s).  Each
 // workgroup takes 16 NG rows of B; its 8 waves are NG groups of 8 / NG, which share a
 // group's k range in 64-deep steps and are joined in LDS.  Operands go from memory into
 // fragments: lane l reads 16 bytes of row l % 16 at k = 8 (l / 16) of each 32-deep step.

@@ -7,6 +7,10 @@
 // Both directions read each row once: it stays in registers (chunks of 8 elements per
 // thread) between the statistics and the result, so the variance is the two-pass one.
 // All sums are float32.  Bound by HBM: 2 n d elements forward, 3 (4 with dres) backward.
+// 8192 x 4096 bf16: forward 25.7 us (5.2 TB/s, a large copy's rate), backward with dres 44.5 us
+// and 4.4 us to join its partials (268 MB of operands at 5.5 TB/s; without the row in flight
+// ahead and with 4 workgroups per CU it was 84 and 17 us).  A wave per row up to 1024 columns,
+// 256 threads up to 4096, 1024 above: the shortest reduction whose chunks fit the registers.
 #include "kernels.h"
 #include "vec.h"
 

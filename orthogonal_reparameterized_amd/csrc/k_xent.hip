@@ -9,7 +9,8 @@
 // for bf16 operands, the operand type of the two products that read it), then dh += dl W and
 // dW of the piece follow while dl is in the caches.  8 n d v flops in all, where keeping the
 // logits would take 6 n d v and n v values of memory.  Bound by the matrix cores for many
-// tokens and by reading W for few.
+// tokens (4096 x 4096 x 65536: forward 1.52, dl 1.59, dh 1.54, dW 1.71 ms, 1.29 to 1.45 PFLOP/s)
+// and by reading W for few.
 #include "gemm_core.h"
 
 namespace poetx {
