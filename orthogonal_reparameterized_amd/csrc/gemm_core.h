@@ -11,8 +11,8 @@
 //     leave as whole 128-byte lines.  c = cols(n, nv, rows): what a lane keeps for its 8
 //     columns over all its rows.  kRows > 0: floats per row that stage(m0, M, i) supplies; the
 //     kernel puts them into LDS for the tile's rows first (`rows` points at row m0's).
-//   kStats == true: reduce() gets the whole tile's accumulators (row statistics).
-// kSplits says whether a product with this epilogue may be split over k.
+//   kStats == true: reduce() gets the whole tile's accumulators (row statistics).  A product
+//     split over k leaves its partials to the caller then (no epilogue runs).
 #pragma once
 
 #include "lds_tiles.h"
@@ -197,7 +197,7 @@ __device__ inline void finish(const V (&acc)[FM][FN], const MmArgs &a, const MmT
 // names one, as Tag_) keeps the kernels of two source files apart.
 template <typename T, class Tag>
 struct StoreEpi {
-  static constexpr bool kStats = false, kSplits = true;
+  static constexpr bool kStats = false;
   static constexpr int kRows = 0;
   using Tag_ = Tag;
   struct Cols {};
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   if (!wr) phase_barrier();
   __builtin_amdgcn_s_waitcnt(0);  // the loads past the range have written their zeros
   __syncthreads();                // the epilogue reuses the LDS
-  if constexpr (Epi::kSplits) {
+  if constexpr (!Epi::kStats) {
     if (tile.tail >= 0) {
       float *part = a.tail_part + ((int64_t)tile.tail * a.tail_splits + tile.split) * 65536;
       put_rows<FM, FN>(acc, wr * 128, wc * 64, 256, 256, (float *)smem + wave * 16 * 68,
@@ -687,7 +687,7 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
   }
 }
 
-// Sum of the float32 partials of a split product, [splits][M][ld] in split order, into the
+// Sum of the float32 partials of a split product, [splits][M][N] in split order, into the
 // epilogue; one thread per 8 columns.
 template <class Epi>
 __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, int64_t M, int64_t N, Epi epi) {
@@ -751,7 +751,7 @@ struct MmDesc {
 // bf16: 256 x 256 tiles (one workgroup per CU) where they fill three quarters of the GPU, else
 // 128 x 128 (two per CU).  float32: 128 x 128 (two per CU) where they fill the GPU twice, else
 // 64 x 64 (four per CU), which cut small results finer and overlap their load latencies.
-inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true) {
+inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true) {
   MmPlan p;
   if (M <= 0 || N <= 0) return p;  // nothing to launch
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
@@ -790,7 +790,7 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
   // does 5.6 TFLOP/s) shrinks by more than the partials' write, read and join (4.5 TB/s, 6 us).
   p.full = tiles;
   const int64_t left = tiles % cus;
-  if (may_split && p.bt == 256 && tiles > cus && left && 2 * left <= cus) {
+  if (may_split && may_share && p.bt == 256 && tiles > cus && left && 2 * left <= cus) {
     int64_t sp = cus / left;
     if (sp > K / 256) sp = K / 256;
     if (sp > 8) sp = 8;
@@ -842,7 +842,7 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
   MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, (int)p.splits, p.kc};
   const int64_t tiles = p.tiles_m * p.tiles_n;
   if (tiles * p.splits > kMaxTiles) return POETX_ERR_UNSUPPORTED;
-  if constexpr (Epi::kSplits && sizeof(T) == 2) {
+  if constexpr (!Epi::kStats && sizeof(T) == 2) {
     if (p.full < tiles) {
       a.full = (int)p.full; a.tail_splits = (int)p.tail_splits; a.tail_kc = p.tail_kc; a.tail_part = part;
       POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s)));
@@ -850,10 +850,10 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
     }
   }
   if (p.splits == 1) return mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s);
-  if constexpr (!Epi::kSplits) {
-    return POETX_ERR_UNSUPPORTED;  // planned without splits
+  POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, StoreEpi<float, typename Epi::Tag_>{part, d.N, d.M * d.N}, s)));
+  if constexpr (Epi::kStats) {
+    return POETX_OK;
   } else {
-    POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, StoreEpi<float, typename Epi::Tag_>{part, d.N, d.M * d.N}, s)));
     return launch_k("mm_join", s, k_mm_join<Epi>, dim3((unsigned)cdiv(d.M * cdiv(d.N, 8), 256)), dim3(256), 0,
                     (const float *)part, (int)p.splits, d.M, d.N, epi);
   }

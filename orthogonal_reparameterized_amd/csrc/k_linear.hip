@@ -96,7 +96,7 @@ __device__ inline void act_slopes(float (&v)[8], const float (&p)[8], int act) {
 
 template <typename T>
 struct LinEpi {
-  static constexpr bool kStats = false, kSplits = true;
+  static constexpr bool kStats = false;
   static constexpr int kRows = 0;
   using Tag_ = LinTag;
   struct Cols { float b[8]; };

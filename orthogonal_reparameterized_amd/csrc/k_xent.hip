@@ -4,7 +4,9 @@
 // A row whose target lies outside the vocabulary takes no part: loss 0, dl 0.
 //
 // Forward: the product's epilogue reduces each row of a tile to its maximum and its sum of
-// exp(l - maximum), 8 bytes per row and 256 columns; k_xent_join joins them.  Backward: the
+// exp(l - maximum), 8 bytes per row and 256 columns; k_xent_join joins them.  (A product of so
+// few tiles that it is split over k passes its partial sums, at most 2^23 floats at a time,
+// through the workspace first.)  Backward: the
 // logits of a piece of the vocabulary are computed again and leave the epilogue as dl (bf16
 // for bf16 operands, the operand type of the two products that read it), then dh += dl W and
 // dW of the piece follow while dl is in the caches.  8 n d v flops in all, where keeping the
@@ -30,7 +32,7 @@ __device__ inline float safe_ref(float m) { return fabsf(m) == INFINITY ? 0.f : 
 
 // part[tile][row] = (max, sum) over the tile's columns; at_target[row] = l of the target.
 struct XentStats {
-  static constexpr bool kStats = true, kSplits = false;
+  static constexpr bool kStats = true;
   using Tag_ = XentTag;
   float2 *part;
   const int32_t *target;
@@ -99,7 +101,7 @@ struct XentStats {
 // target is nearly -dloss_i = -1 / count for all of them, would share one rounding error.
 template <typename T>
 struct XentDl {
-  static constexpr bool kStats = false, kSplits = false;
+  static constexpr bool kStats = false;
   static constexpr int kRows = 3;
   using Tag_ = XentTag;
   struct Cols { const float *rows; };
@@ -120,9 +122,10 @@ struct XentDl {
     return __int_as_float(t >= 0 && t < vocab ? t : -1);
   }
   __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
+    // from the tile's staged rows, or (where partials are joined) from memory
     const float *r = c.rows + m * 3;
-    const float z = r[0], g = r[1];
-    const int t = __float_as_int(r[2]);
+    const float z = c.rows ? r[0] : stage(m, m + 1, 0), g = c.rows ? r[1] : stage(m, m + 1, 1);
+    const int t = __float_as_int(c.rows ? r[2] : stage(m, m + 1, 2));
     const int64_t q = t - v0 - n;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -136,7 +139,7 @@ struct XentDl {
 // dh over the pieces: float32 sums in `sum` between the first and the last piece.
 template <typename T>
 struct XentDh {
-  static constexpr bool kStats = false, kSplits = true;
+  static constexpr bool kStats = false;
   static constexpr int kRows = 0;
   using Tag_ = XentTag;
   struct Cols { float g; };
@@ -168,7 +171,7 @@ struct XentDh {
 // dW of a piece.
 template <typename T>
 struct XentDw {
-  static constexpr bool kStats = false, kSplits = true;
+  static constexpr bool kStats = false;
   static constexpr int kRows = 0;
   using Tag_ = XentTag;
   struct Cols { float g; };
@@ -203,6 +206,43 @@ __global__ __launch_bounds__(1024) void k_xent_scale(const float *dloss, const i
 #pragma unroll
   for (int w = 1; w < 16; ++w) g = fmaxf(g, red[w]);
   *scale = g > 0.f ? g : 1.f;
+}
+
+// Row statistics of a split product: its partials [splits][n][v] summed in split order, a wave
+// per row and 256 columns.
+__global__ __launch_bounds__(256) void k_xent_parts(const float *src, int splits, int64_t n, int64_t v, XentStats epi) {
+  const int l = threadIdx.x & 63;
+  const int64_t m = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6), c = (int64_t)blockIdx.x * 256 + l * 4, left = v - c;
+  if (m >= n) return;
+  f32v4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < splits; ++k) {
+    const float *p = src + ((int64_t)k * n + m) * v + c;
+    if (left >= 4) {
+      f32v4 w;
+      __builtin_memcpy(&w, p, 16);
+      s += w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += e < left ? p[e] : 0.f;
+    }
+  }
+  const int64_t t = (int64_t)epi.target[m] - epi.v0 - c;
+  float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= left) continue;
+    if (t == e) epi.at_target[m] = s[e];
+    mx = fmaxf(mx, s[e]);
+  }
+  const float ref = safe_ref(mx);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum += e < left ? __expf(s[e] - ref) : 0.f;
+#pragma unroll
+  for (int o = 1; o <= 32; o <<= 1) {
+    const float m2 = __shfl_xor(mx, o), s2 = __shfl_xor(sum, o);
+    join_stats(mx, sum, m2, s2);
+  }
+  if (l == 0) epi.part[(int64_t)(epi.tile0 + (int)blockIdx.x) * n + m] = make_float2(mx, sum);
 }
 
 // Few tokens (n <= 16, bf16): bound by reading W once.  Every wave walks groups of 16
@@ -382,7 +422,10 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   float *sum = d.dh && piece < d.v ? (float *)ar.take((size_t)d.n * d.d * 4) : nullptr;
   // partials of split products: of whole pieces and of the last one
   size_t part_bytes = 0;
+  const int64_t kd = pads(d) ? o.ld : d.d;
   for (const int64_t vc : {piece, last}) {
+    const size_t l = mm_plan(d.n, vc, kd, d.dt).part_bytes;
+    part_bytes = l > part_bytes ? l : part_bytes;
     const size_t a = d.dh ? mm_plan(d.n, d.d, vc, d.dt).part_bytes : 0;
     const size_t b = d.dw && !flip ? mm_plan(vc, d.d, d.n, d.dt).part_bytes : 0;
     part_bytes = a > part_bytes ? a : part_bytes;
@@ -395,7 +438,7 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     const void *w = nullptr;
     POETX_TRY(w_piece(d, o, v0, vc, s, &w));
     const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits");
-    POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt, false), nullptr,
+    POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt), part,
                                     XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, scale, v0, d.v}, s)));
     if (d.dh) {
       MmDesc g;
@@ -440,10 +483,18 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     const int64_t piece = pads(d) ? piece_of(d) : d.v;
     Operands o;
     POETX_TRY(operands(d, piece, ar, measure, s, o));
-    // partials: one row per n-tile of every piece (pieces are multiples of the tile width)
-    for (int64_t v0 = 0; v0 < d.v; v0 += piece)
-      tiles += mm_plan(d.n, d.v - v0 < piece ? d.v - v0 : piece, d.d, d.dt, false).tiles_n;
+    // one row of statistics per n-tile of every piece (pieces are multiples of the tile width;
+    // 256 columns where the product is split over k)
+    const int64_t kd = pads(d) ? o.ld : d.d;
+    size_t split_bytes = 0;
+    for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
+      const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
+      const MmPlan p = mm_plan(d.n, vc, kd, d.dt, true, false);
+      tiles += p.splits > 1 ? cdiv(vc, 256) : p.tiles_n;
+      split_bytes = p.part_bytes > split_bytes ? p.part_bytes : split_bytes;
+    }
     part = (float2 *)ar.take((size_t)tiles * d.n * 8);
+    float *split = split_bytes ? (float *)ar.take(split_bytes) : nullptr;
     if (measure) return POETX_OK;
     int64_t t0 = 0;
     for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
@@ -451,9 +502,13 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
       const void *w = nullptr;
       POETX_TRY(w_piece(d, o, v0, vc, s, &w));
       const MmDesc m = logits_desc(d, o, w, vc, "xent_fwd");
-      const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt, false);
-      POETX_TRY((mm_run<T, false, false>(m, p, nullptr, XentStats{part, d.target, at, v0, (int)t0}, s)));
-      t0 += p.tiles_n;
+      const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt, true, false);
+      const XentStats epi{part, d.target, at, v0, (int)t0};
+      POETX_TRY((mm_run<T, false, false>(m, p, split, epi, s)));
+      if (p.splits > 1)
+        POETX_TRY(launch_k("xent_parts", s, k_xent_parts, dim3((unsigned)cdiv(vc, 256), (unsigned)cdiv(d.n, 4)),
+                           dim3(256), 0, (const float *)split, (int)p.splits, d.n, vc, epi));
+      t0 += p.splits > 1 ? cdiv(vc, 256) : p.tiles_n;
     }
   }
   if (d.n <= 256)

@@ -343,7 +343,8 @@ def check_xent(B, n, d, v, dtype, ignored=0.2, seed=100):
 
 
 XENT_SHAPES = [(1, 64, 1000), (1, 1, 1), (3, 5, 2), (8, 4096, 3001), (16, 77, 20001), (15, 520, 128), (17, 64, 257),
-               (64, 100, 5003), (301, 520, 1007), (130, 1000, 2049), (1025, 256, 4104)]
+               (64, 100, 5003), (301, 520, 1007), (130, 1000, 2049), (1025, 256, 4104), (28, 3330, 1301),
+              (70, 2500, 513), (19, 5000, 7)]
 
 
 @pytest.mark.parametrize("n,d,v", XENT_SHAPES)
