@@ -512,7 +512,7 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
 // rate (157 TFLOP/s).
 template <int BT, int BK, bool AKM, bool BKM, class Epi>
 __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
-    constexpr int LD = BT + 4, ST = BK * LD, WT = BT / 2, F = WT / 16;  // a stage of either layout fits ST
+  constexpr int LD = BT + 4, ST = BK * LD, WT = BT / 2, F = WT / 16;  // a stage of either layout fits ST
   constexpr int PC = BT * BK / 4 / 256;  // 4-float pieces per thread and operand stage
   __shared__ __align__(16) float smem[4 * ST];
   const MmTile tile = mm_tile(a);
@@ -864,12 +864,13 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
 // less than that (one pass over X, against a product M times as large), X^T takes the kernel's
 // 128-row role k-contiguous and D its 64-row role.  M, N, K = 65536, 4096, 4096: 1790 us as it
 // lies, 1560 us so; below about M = 8192 the copy eats the gain (8192 tokens, 4096 x 4096: 208 us,
-// of which it would take 27).
+// of which it would take 27).  K is a row stride of the copy: not past the widths whose offsets
+// within a tile's rows fit 32 bits.
 inline bool dw_flips(int64_t M, int64_t N, int64_t K, int dt) {
   const MmPlan p = mm_plan(N, M, K, dt, false);
-  return dt == POETX_BF16 && M >= 8192 && p.bt == 256;
+  return dt == POETX_BF16 && M >= 8192 && K <= kMaxWidth && p.bt == 256;
 }
-// XT: [N][ldt], ldt a multiple of 8, zeros past K
+// C^T of the product: A is X^T, [M][lda] with lda a multiple of 8 and zeros past K, B is D
 template <class Epi>
 int mm_run_flipped(const MmDesc &d, const Epi &epi, hipStream_t s) {
   const MmPlan p = mm_plan(d.M, d.N, d.K, POETX_BF16, false);

@@ -132,6 +132,17 @@ def test_workspace_queries(B):
     assert bwd < (600 << 20) + n * d * 8
 
 
+def test_weight_gradient_of_very_many_tokens_makes_no_transposed_copy(B):
+    """The transposed copy of x has the tokens as its row stride, and a tile's 256 rows of it
+    are reached by 32-bit offsets: 2^20 tokens at most."""
+    d_in, d_out = 4096, 8192
+    args = (d_in, d_out, 1, None, None, None, None, 0, None, A, None)
+    f = B.raw.poetx_linear_backward
+    assert query(f, 1 << 20, *args) >= d_in * 2 << 20
+    for n in ((1 << 20) + 1, 1 << 22, (1 << 23) - 8):
+        assert query(f, n, *args) < d_in * 2 * n
+
+
 def test_binding_refusals(B):
     """The binding refuses shapes, dtypes and layouts before it touches a device."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
