@@ -62,7 +62,7 @@ __device__ inline void act_slopes(float (&v)[8], const float (&p)[8], int act) {
   switch (act) {
     case POETX_ACT_RELU:
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = p[e] > 0.f ? v[e] : v[e] * 0.f;  // 0 at 0; NaN and infinities of v stay
+      for (int e = 0; e < 8; ++e) v[e] *= p[e] > 0.f ? 1.f : p[e] <= 0.f ? 0.f : p[e];  // 0 at 0; a NaN stays NaN
       break;
     case POETX_ACT_GELU:
 #pragma unroll

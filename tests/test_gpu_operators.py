@@ -631,3 +631,42 @@ def test_gradients_against_differences(B):
         # loss_of is off by about 2^-22 of the total (24 float32 losses): 2^-22 total / eps; the
         # third derivative's term is eps^2 / 6 of order the gradient's own scale
         assert abs(diff - want) <= 2.0 ** -22 * abs(total) / eps + 50 * eps ** 2 * abs(want) / 6, (k, diff, want)
+
+
+def test_linear_relu_slope_of_nan(B):
+    """A NaN that went into relu comes out of its slope; infinities of dy at a slope of 0 are
+    NaN as in the formula's product, and nothing spreads to other tokens."""
+    x, w = linear_case(310, 4, 16, 24, BF16)
+    dy, pre = rand(312, 4, 24, dtype=BF16), rand(313, 4, 24, dtype=BF16)
+    pre[1, 3], pre[2, 5], dy[2, 5] = float("nan"), -1.0, float("inf")
+    got = B.poetx_linear_backward(dev(x), dev(w), dev(dy), dev(pre), "relu")
+    assert torch.isnan(got["dx"][1:3]).all() and torch.isfinite(got["dx"][[0, 3]]).all()
+    assert sorted(torch.nonzero(torch.isnan(got["dbias"]))[:, 0].tolist()) == [3, 5]
+
+
+def test_more_than_2_31_elements(B):
+    """Results and operands whose offsets pass 32 bits: the last rows are right."""
+    n, i, o = 33000, 8, 65600
+    g = torch.Generator(device="cuda").manual_seed(320)
+    x = torch.randn(n, i, generator=g, device="cuda").to(BF16)
+    w = torch.randn(o, i, generator=g, device="cuda").to(BF16)
+    y, _ = B.poetx_linear_forward(x, w)
+    assert y.numel() > 1 << 31
+    xd, wd = x.double(), w.double()
+    ref, mag = xd[-3:] @ wd.t(), xd[-3:].abs() @ wd.abs().t()
+    within(y[-3:], ref.cpu(), (U[BF16] * ref.abs() + 1.01 * acc(i) * mag).cpu(), "y")
+    got = B.poetx_linear_backward(x, w, y)
+    r, c = y[-3:].double(), y[:, -3:].double()
+    for name, at, ref, mag, k in (("dx", got["dx"][-3:], r @ wd, r.abs() @ wd.abs(), o),
+                                  ("dw", got["dw"][-3:], c.t() @ xd, c.abs().t() @ xd.abs(), n)):
+        within(at, ref.cpu(), (U[BF16] * ref.abs() + 1.02 * acc(k) * mag).cpu(), name)
+    within(got["dbias"][-3:], c.sum(0).cpu(), (acc(n) * c.abs().sum(0)).cpu(), "dbias")
+    del got, y
+    n, d = 140000, 16384
+    x = torch.randn(n, d, generator=g, device="cuda", dtype=BF16)
+    y, mean, rstd = B.poetx_layernorm_forward(x)
+    dx = B.poetx_layernorm_backward(x, y, None, mean, rstd, want_params=False)["dx"]
+    tail = x[-3:].clone()
+    y3, mean3, rstd3 = B.poetx_layernorm_forward(tail)
+    assert torch.equal(y[-3:], y3) and torch.equal(mean[-3:], mean3) and torch.equal(rstd[-3:], rstd3)
+    assert torch.equal(dx[-3:], B.poetx_layernorm_backward(tail, y3, None, mean3, rstd3)["dx"])
