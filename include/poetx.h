@@ -370,7 +370,7 @@ int poetx_linear_backward(int64_t n_tokens, int64_t d_in, int64_t d_out, int32_t
  * A token whose target lies outside [0, vocab) takes no part: its loss is 0 (lse is still
  * written).  n_tokens == 0 is a no-op.  Workspace: query with ws == NULL: 8 bytes per token and
  * 64 to 256 vocabulary entries; products too small to fill the GPU are split over d and add
- * their partial sums (at most 32 MB); bf16 with d not a multiple of 8 adds padded copies of h
+ * their partial sums (at most 64 MB); bf16 with d not a multiple of 8 adds padded copies of h
  * and of one piece of w.  Errors: NULL buffer, n_tokens < 0, bad dtype, misaligned pointer ->
  * INVALID_ARG; d or vocab < 1 -> POETX_ERR_SHAPE; d > 2^20, vocab > 2^31 - 1, or more than 2^22
  * tiles of 128 x 128 logits -> UNSUPPORTED.

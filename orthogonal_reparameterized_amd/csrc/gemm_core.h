@@ -748,35 +748,58 @@ struct MmDesc {
   const char *name = "mm";
 };
 
+// float32: the kernels are bound by the matrix cores, so a CU's time is that of the tiles dealt to
+// it: w = ceil(workgroups / CUs) of them, a 32-deep step of a 64 x 64 tile taking 0.55 us (0.83
+// where the CU has one workgroup, which waits for its loads), a 16-deep one of 128 x 128 1.03 us.
+// 128 x 128 tiles are taken where that comes out lower, which asks for enough of them to spread
+// evenly (4096^3: 974-1114 us against 1078; 3000^3, 2.2 tiles per CU: 573 against 457).  Of the 64 x
+// 64 ones, k is split where that spreads the work better by more than the partials' write, read
+// and join (6 us, 5 TB/s) and a tenth of the time: 896 x 2573 x 3056, 2.2 tiles per CU, 166 us
+// whole, 132 in 4 ranges; 64 x 4096 x 4096 105 and 33; 1024^3 stays whole, 29 against 34.
+constexpr size_t kMaxPart = (size_t)64 << 20;
+inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_split, MmPlan &p) {
+  const int64_t t64 = cdiv(M, 64) * cdiv(N, 64), t128 = cdiv(M, 128) * cdiv(N, 128);
+  auto cost = [&](int64_t kc, int64_t sp) {
+    const int64_t w = cdiv(t64 * sp, cus);
+    return (double)cdiv(kc, 32) * (w == 1 ? 0.83 : 0.55 * w) + (sp > 1 ? 6 + (double)sp * M * N * 4 / 5e6 : 0);
+  };
+  const double whole = cost(K, 1);
+  if (t128 >= 2 * cus && (double)cdiv(K, 16) * 1.03 * cdiv(t128, cus) < whole) {
+    p.bt = 128;
+    return;
+  }
+  if (!may_split || t64 >= 8 * cus) return;
+  double best = 0.9 * whole;
+  for (int64_t want = 2; want <= 32 && want <= K / 128; ++want) {
+    const int64_t kc = cdiv(cdiv(K, want), 64) * 64, sp = cdiv(K, kc);
+    const size_t bytes = (size_t)sp * M * N * 4;
+    if (sp < 2 || bytes > kMaxPart || cost(kc, sp) >= best) continue;
+    best = cost(kc, sp);
+    p.kc = kc;
+    p.splits = sp;
+    p.part_bytes = bytes;
+  }
+}
+
 // bf16: 256 x 256 tiles (one workgroup per CU) where they fill three quarters of the GPU, else
-// 128 x 128 (two per CU).  float32: 128 x 128 (two per CU) where they fill the GPU twice, else
-// 64 x 64 (four per CU), which cut small results finer and overlap their load latencies.
+// 128 x 128 (two per CU).
 inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true) {
   MmPlan p;
   if (M <= 0 || N <= 0) return p;  // nothing to launch
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
-  auto tiles_of = [&](int64_t t) { return cdiv(M, t) * cdiv(N, t); };
-  int64_t slots;
-  if (dt == POETX_BF16) {
-    p.bt = 4 * tiles_of(256) >= 3 * cus ? 256 : 128;
-    slots = p.bt == 256 ? cus : 2 * cus;
-  } else {
-    p.bt = tiles_of(128) >= 2 * cus ? 128 : 64;
-    slots = p.bt == 128 ? 2 * cus : 4 * cus;
-  }
+  p.kc = K;
+  if (dt == POETX_BF16) p.bt = 4 * cdiv(M, 256) * cdiv(N, 256) >= 3 * cus ? 256 : 128;
+  else plan_f32(M, N, K, cus, may_split, p);
   p.tiles_m = cdiv(M, p.bt);
   p.tiles_n = cdiv(N, p.bt);
-  p.kc = K;
-  const int64_t tiles = p.tiles_m * p.tiles_n;
-  // Too few tiles to fill the GPU: split k, each range at least 256 (float32: 128) deep.  The
-  // partials' join costs about 5 us, so a product with tiles for a quarter of the CUs and no
-  // more than 32 steps of 64 (float32: 24 of 32) stays whole: 1024 x 2048 x 2048 24.5 -> 22.3 us,
-  // 1024^3 20 -> 14 us, while 64 x 4096 x 4096 takes 18 us split and 45 us whole.
-  const bool whole = 4 * tiles >= cus && K <= (dt == POETX_BF16 ? 32 * 64 : 24 * 32);
-  if (may_split && tiles < slots && !whole) {
+  const int64_t tiles = p.tiles_m * p.tiles_n, slots = p.bt == 256 ? cus : 2 * cus;
+  // Too few bf16 tiles to fill the GPU: split k, each range at least 256 deep.  The partials'
+  // join costs about 5 us, so a product with tiles for a quarter of the CUs and no more than 32
+  // steps of 64 stays whole: 1024 x 2048 x 2048 24.5 -> 22.3 us, 1024^3 20 -> 14 us, while 64 x 4096
+  // x 4096 takes 18 us split and 45 us whole.
+  if (may_split && dt == POETX_BF16 && tiles < slots && !(4 * tiles >= cus && K <= 32 * 64)) {
     int64_t sp = slots / tiles;
-    const int64_t deep = K / (dt == POETX_BF16 ? 256 : 128);
-    if (sp > deep) sp = deep;
+    if (sp > K / 256) sp = K / 256;
     if (sp > 32) sp = 32;
     if (sp >= 2) {
       p.kc = cdiv(cdiv(K, sp), 64) * 64;

@@ -5,7 +5,7 @@
 //
 // Forward: the product's epilogue reduces each row of a tile to its maximum and its sum of
 // exp(l - maximum), 8 bytes per row and 256 columns; k_xent_join joins them.  (A product of so
-// few tiles that it is split over k passes its partial sums, at most 2^23 floats at a time,
+// few tiles that it is split over k passes its partial sums, at most 2^24 floats at a time,
 // through the workspace first.)  Backward: the
 // logits of a piece of the vocabulary are computed again and leave the epilogue as dl (bf16
 // for bf16 operands, the operand type of the two products that read it), then dh += dl W and
