@@ -616,52 +616,70 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
   finish<BT, BT, 2, 2>(acc, a, tile, smem, epi);
 }
 
-// Eight consecutive k of an operand row as an MFMA fragment, the first `left` in range.
-__device__ inline bf16x8 row_frag(const bf16_t *p, int64_t left) {
+// 16 bytes of an operand row as an MFMA fragment (8 bf16 or 4 floats), the first `left` in range.
+template <typename T> struct RowFrag;
+template <> struct RowFrag<bf16_t> { using V = bf16x8; static constexpr int E = 8; };
+template <> struct RowFrag<float> { using V = f32x4; static constexpr int E = 4; };
+template <typename T>
+__device__ inline typename RowFrag<T>::V row_frag(const T *p, int64_t left) {
+  constexpr int E = RowFrag<T>::E, PER = E / 4;
   u32v4 u = {0u, 0u, 0u, 0u};
-  if (left >= 8) {
+  if (left >= E) {
     __builtin_memcpy(&u, p, 16);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) u[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    for (int e = 0; e < E; ++e)
+      if (e < left) {
+        if constexpr (PER == 2) u[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        else u[e] = __float_as_uint(p[e]);
+      }
   }
-  return __builtin_bit_cast(bf16x8, u);
+  return __builtin_bit_cast(typename RowFrag<T>::V, u);
+}
+// acc += the fragments' product over their four lane groups' k: 32 (one MFMA) or 16 (four, the
+// s-th over element s of every group); operands swapped as everywhere
+__device__ inline f32x4 mul_frag(bf16x8 b, bf16x8 a, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, acc, 0, 0, 0);
+}
+__device__ inline f32x4 mul_frag(f32x4 b, f32x4 a, f32x4 acc) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(b[s], a[s], acc, 0, 0, 0);
+  return acc;
 }
 
-// Few rows (M <= 16, bf16, both operands k-contiguous): bound by reading B once (one token,
-// 13824 x 5120: 26.7 us, 5.3 TB/s).  Each
+// Few rows (M <= 16, both operands k-contiguous): bound by reading B once (one token, 13824 x
+// 5120 bf16: 26.7 us, 5.3 TB/s).  Each
 // workgroup takes 16 NG rows of B; its 8 waves are NG groups of 8 / NG, which share a
-// group's k range in 64-deep steps and are joined in LDS.  Operands go from memory into
-// fragments: lane l reads 16 bytes of row l % 16 at k = 8 (l / 16) of each 32-deep step.
-template <int NG, class Epi>
+// group's k range in turns of U fragments and are joined in LDS.  Operands go from memory into
+// fragments: lane l reads 16 bytes of row l % 16 in its quarter (l / 16) of each fragment's k.
+template <typename T, int NG, class Epi>
 __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
-  constexpr int KW = 8 / NG, U = 4;  // U 32-deep steps in flight per wave
+  constexpr int KW = 8 / NG, U = 4, E = RowFrag<T>::E, D = 4 * E;  // U fragments of D k in flight per wave
   __shared__ __align__(16) float red[8 * 16 * 20];  // the parts (8 x 256), then the rows (8 x 320)
   const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int ng = wave / KW, kw = wave % KW;
   const int64_t n0 = ((int64_t)blockIdx.x * NG + ng) * 16, n = n0 + (l & 15), m = l & 15;
-  const bf16_t *pb = (const bf16_t *)a.B + (n < a.N ? n : a.N - 1) * a.ldb;
-  const bf16_t *pa = (const bf16_t *)a.A + (m < a.M ? m : a.M - 1) * a.lda;
+  const T *pb = (const T *)a.B + (n < a.N ? n : a.N - 1) * a.ldb;
+  const T *pa = (const T *)a.A + (m < a.M ? m : a.M - 1) * a.lda;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const int64_t steps = cdiv(a.K, 32 * U);
+  const int64_t steps = cdiv(a.K, D * U);
   for (int64_t t = kw; t < steps; t += KW) {
-    const int64_t k0 = t * 32 * U + 8 * (l >> 4);
-    bf16x8 fb[U], fa[U];
-    if ((t + 1) * 32 * U <= a.K) {
+    const int64_t k0 = t * D * U + E * (l >> 4);
+    typename RowFrag<T>::V fb[U], fa[U];
+    if ((t + 1) * D * U <= a.K) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) fb[u] = row_frag(pb + k0 + 32 * u, 8);
+      for (int u = 0; u < U; ++u) fb[u] = row_frag(pb + k0 + D * u, E);
 #pragma unroll
-      for (int u = 0; u < U; ++u) fa[u] = row_frag(pa + k0 + 32 * u, 8);
+      for (int u = 0; u < U; ++u) fa[u] = row_frag(pa + k0 + D * u, E);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        fb[u] = row_frag(pb + k0 + 32 * u, a.K - k0 - 32 * u);
-        fa[u] = row_frag(pa + k0 + 32 * u, a.K - k0 - 32 * u);
+        fb[u] = row_frag(pb + k0 + D * u, a.K - k0 - D * u);
+        fa[u] = row_frag(pa + k0 + D * u, a.K - k0 - D * u);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[u], fa[u], acc, 0, 0, 0);
+    for (int u = 0; u < U; ++u) acc = mul_frag(fb[u], fa[u], acc);
   }
   // the k parts of a group, summed in wave order by its first wave
   if constexpr (KW > 1) {

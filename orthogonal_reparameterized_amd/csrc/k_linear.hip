@@ -301,15 +301,13 @@ int fwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   MmDesc m;
   m.M = d.n; m.N = d.d_out; m.K = d.d_in; m.name = "linear_fwd";
   m.A = d.x; m.lda = d.d_in; m.B = d.w; m.ldb = d.d_in;
-  if constexpr (sizeof(T) == 2) {
-    if (d.n <= 16) {  // reading W bounds these: no LDS tiles, any alignment
-      if (measure) return POETX_OK;
-      MmArgs a{m.M, m.N, m.K, m.A, m.lda, m.B, m.ldb, 1, 1, 1, m.K};
-      const int64_t groups = cdiv(d.d_out, 16);
-      if (groups >= 1024)
-        return launch_k(m.name, s, k_mm_few<2, LinEpi<T>>, dim3((unsigned)cdiv(groups, 2)), dim3(512), 0, a, epi);
-      return launch_k(m.name, s, k_mm_few<1, LinEpi<T>>, dim3((unsigned)groups), dim3(512), 0, a, epi);
-    }
+  if (d.n <= 16) {  // reading W bounds these: no LDS tiles, any alignment
+    if (measure) return POETX_OK;
+    MmArgs a{m.M, m.N, m.K, m.A, m.lda, m.B, m.ldb, 1, 1, 1, m.K};
+    const int64_t groups = cdiv(d.d_out, 16);
+    if (groups >= 1024)
+      return launch_k(m.name, s, k_mm_few<T, 2, LinEpi<T>>, dim3((unsigned)cdiv(groups, 2)), dim3(512), 0, a, epi);
+    return launch_k(m.name, s, k_mm_few<T, 1, LinEpi<T>>, dim3((unsigned)groups), dim3(512), 0, a, epi);
   }
   Packed x, w;
   POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));

@@ -245,47 +245,52 @@ __global__ __launch_bounds__(256) void k_xent_parts(const float *src, int splits
   if (l == 0) epi.part[(int64_t)(epi.tile0 + (int)blockIdx.x) * n + m] = make_float2(mx, sum);
 }
 
-// Few tokens (n <= 16, bf16): bound by reading W once.  Every wave walks groups of 16
-// vocabulary rows, takes each group's whole k (the next 256 k in flight while these multiply)
-// and keeps a running (max, sum) per lane (row l % 16, its 4 columns of each group); one
-// partial per workgroup.  8 tokens, d = 4096, 131072 rows: 214 us, 5.0 TB/s, the rate of a
-// large copy (242 us without the loads ahead; 228-240 us with a group's k shared by 4 or 8
-// waves; 222 us with half or twice the workgroups).
+// Few tokens (n <= 16): bound by reading W once.  KW waves share a group of 16 vocabulary rows:
+// each takes every KW-th turn of the group's k (the next U fragments in flight while these
+// multiply) and keeps (max, sum) per lane (row l % 16, its 4 columns of the group); one partial per
+// workgroup.  KW = 1 walks groups and keeps a running (max, sum): 8 tokens, d = 4096, 131072 rows,
+// bf16: 199 us, 5.4 TB/s, the rate of a large copy (242 us without the loads ahead; 222 us with
+// half or twice the workgroups).
+template <typename T, int KW>
 __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
-  constexpr int U = 8;  // 32-deep steps per turn
+  constexpr int NG = 8 / KW, U = 8, E = RowFrag<T>::E, D = 4 * E;  // fragments of D k per turn
+  using V = typename RowFrag<T>::V;
   __shared__ float2 st[8][16];
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, kw = wave % KW;
   const int64_t m = l & 15;
-  const bf16_t *pa = (const bf16_t *)a.A + (m < a.M ? m : a.M - 1) * a.lda + 8 * (l >> 4);
+  const T *pa = (const T *)a.A + (m < a.M ? m : a.M - 1) * a.lda + E * (l >> 4);
   const int64_t t = m < a.M ? (int64_t)epi.target[m] : -1;
-  const int64_t groups = cdiv(a.N, 16), whole = a.K / (32 * U);  // whole turns of k
+  const int64_t groups = cdiv(a.N, 16), whole = a.K / (D * U);  // whole turns of k
   float mx = -INFINITY, s = 0.f;
-  for (int64_t g = (int64_t)blockIdx.x * 8 + wave; g < groups; g += (int64_t)gridDim.x * 8) {
+  auto dot = [&](int64_t g) {
     const int64_t n = g * 16 + (l & 15);
-    const bf16_t *pb = (const bf16_t *)a.B + (n < a.N ? n : a.N - 1) * a.ldb + 8 * (l >> 4);
+    const T *pb = (const T *)a.B + (n < a.N ? n : a.N - 1) * a.ldb + E * (l >> 4);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    bf16x8 fb[2][U], fa[2][U];
-    auto load = [&](int64_t q, bf16x8 (&b_)[U], bf16x8 (&a_)[U]) {
+    V fb[2][U], fa[2][U];
+    auto load = [&](int64_t q, V (&b_)[U], V (&a_)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) b_[u] = row_frag(pb + (q * U + u) * 32, 8);
+      for (int u = 0; u < U; ++u) b_[u] = row_frag(pb + (q * U + u) * D, E);
 #pragma unroll
-      for (int u = 0; u < U; ++u) a_[u] = row_frag(pa + (q * U + u) * 32, 8);
+      for (int u = 0; u < U; ++u) a_[u] = row_frag(pa + (q * U + u) * D, E);
     };
-    auto mul = [&](const bf16x8 (&b_)[U], const bf16x8 (&a_)[U]) {
+    auto mul = [&](const V (&b_)[U], const V (&a_)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b_[u], a_[u], acc, 0, 0, 0);
+      for (int u = 0; u < U; ++u) acc = mul_frag(b_[u], a_[u], acc);
     };
-    if (whole > 0) load(0, fb[0], fa[0]);
-    for (int64_t q = 0; q < whole; q += 2) {
-      if (q + 1 < whole) load(q + 1, fb[1], fa[1]);
+    if (kw < whole) load(kw, fb[0], fa[0]);
+    for (int64_t q = kw; q < whole; q += 2 * KW) {
+      if (q + KW < whole) load(q + KW, fb[1], fa[1]);
       mul(fb[0], fa[0]);
-      if (q + 2 < whole) load(q + 2, fb[0], fa[0]);
-      if (q + 1 < whole) mul(fb[1], fa[1]);
+      if (q + 2 * KW < whole) load(q + 2 * KW, fb[0], fa[0]);
+      if (q + KW < whole) mul(fb[1], fa[1]);
     }
-    for (int64_t k = whole * 32 * U; k < a.K; k += 32) {  // the rest, 32 at a time
-      const int64_t left = a.K - k - 8 * (l >> 4);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(row_frag(pb + k, left), row_frag(pa + k, left), acc, 0, 0, 0);
+    for (int64_t k = (whole * U + kw) * D; k < a.K; k += KW * D) {  // the rest, a fragment at a time
+      const int64_t left = a.K - k - E * (l >> 4);
+      acc = mul_frag(row_frag(pb + k, left), row_frag(pa + k, left), acc);
     }
+    return acc;
+  };
+  auto stats = [&](int64_t g, f32x4 acc) {
     // lane l: row l % 16, columns n0 .. n0 + 3
     const int64_t n0 = g * 16 + 4 * (l >> 4);
     float m2 = -INFINITY, s2 = 0.f;
@@ -299,6 +304,20 @@ __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) s2 += n0 + e < a.N ? __expf(acc[e] - ref) : 0.f;
     join_stats(mx, s, m2, s2);
+  };
+  const int64_t g0 = (int64_t)blockIdx.x * NG + wave / KW;
+  if constexpr (KW == 1) {
+    for (int64_t g = g0; g < groups; g += (int64_t)gridDim.x * NG) stats(g, dot(g));
+  } else {  // one group each; the parts of its k, summed in wave order by its first wave
+    __shared__ f32x4 red[8][64];
+    f32x4 acc = dot(g0);
+    red[wave][l] = acc;
+    __syncthreads();
+    if (kw == 0 && g0 < groups) {
+#pragma unroll
+      for (int w = 1; w < KW; ++w) acc += red[wave + w][l];
+      stats(g0, acc);
+    }
   }
 #pragma unroll
   for (int o = 16; o <= 32; o <<= 1) {
@@ -472,13 +491,23 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   float *at = (float *)ar.take((size_t)d.n * 4);
   int64_t tiles = 0;
   float2 *part = nullptr;
-  if (sizeof(T) == 2 && d.n <= 16) {
-    tiles = cdiv(d.v, 128) < 2 * cus ? cdiv(d.v, 128) : 2 * cus;  // workgroups
+  if (d.n <= 16) {
+    const int64_t groups = cdiv(d.v, 16);
+    // Waves that share a group's k: all eight while that makes at most two workgroups per CU,
+    // two while a wave per group would load the CUs unevenly.  With 1, 2 and 8: 1734 rows of 3200
+    // float32 64, 35 and 15 us; 12000 of 4096 93, 51 and 51; 42114 of 4608 248, 190 and 197;
+    // 131072 of 4096 396, 411 and 480.
+    const int64_t share = groups <= 2 * cus ? 8 : groups <= 12 * cus ? 2 : 1;
+    tiles = cdiv(groups * share, 8);  // workgroups
+    if (share == 1 && tiles > 2 * cus) tiles = 2 * cus;
     part = (float2 *)ar.take((size_t)tiles * d.n * 8);
     if (measure) return POETX_OK;
     const MmArgs a{d.n, d.v, d.d, d.h, d.d, d.w, d.d, 1, 1, 1, d.d};
-    POETX_TRY(launch_k("xent_few", s, k_xent_few, dim3((unsigned)tiles), dim3(512), 0, a,
-                       XentStats{part, d.target, at, 0, 0}));
+    const XentStats epi{part, d.target, at, 0, 0};
+    const dim3 grid((unsigned)tiles), block(512);
+    POETX_TRY(share == 8   ? launch_k("xent_few", s, k_xent_few<T, 8>, grid, block, 0, a, epi)
+              : share == 2 ? launch_k("xent_few", s, k_xent_few<T, 2>, grid, block, 0, a, epi)
+                           : launch_k("xent_few", s, k_xent_few<T, 1>, grid, block, 0, a, epi));
   } else {
     const int64_t piece = pads(d) ? piece_of(d) : d.v;
     Operands o;

@@ -670,3 +670,11 @@ def test_more_than_2_31_elements(B):
     y3, mean3, rstd3 = B.poetx_layernorm_forward(tail)
     assert torch.equal(y[-3:], y3) and torch.equal(mean[-3:], mean3) and torch.equal(rstd[-3:], rstd3)
     assert torch.equal(dx[-3:], B.poetx_layernorm_backward(tail, y3, None, mean3, rstd3)["dx"])
+
+
+@pytest.mark.parametrize("n,d,v", [(16, 1029, 8200), (5, 600, 50000), (2, 3333, 40), (1, 40, 8192)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_xent_few_tokens(B, n, d, v, dtype):
+    """Few tokens over vocabularies of each way to share a group's k, with tails of k that end
+    inside a turn of the waves."""
+    check_xent(B, n, d, v, dtype, seed=330)
