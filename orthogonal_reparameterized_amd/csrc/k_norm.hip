@@ -5,12 +5,17 @@
 //             dx = dres + r (g - mean_c(g) - xh mean_c(g xh)),
 //             dgamma = sum_rows dy xh,  dbeta = sum_rows dy
 // Both directions read each row once: it stays in registers (chunks of 8 elements per
-// thread) between the statistics and the result, so the variance is the two-pass one.
+// thread) between the statistics and the result, so the variance is the two-pass one.  (Above
+// 12288 columns the backward reads it twice.)
 // All sums are float32.  Bound by HBM: 2 n d elements forward, 3 (4 with dres) backward.
 // 8192 x 4096 bf16: forward 25.7 us (5.2 TB/s, a large copy's rate), backward with dres 44.5 us
 // and 4.4 us to join its partials (268 MB of operands at 5.5 TB/s; without the row in flight
 // ahead and with 4 workgroups per CU it was 84 and 17 us).  A wave per row up to 1024 columns,
-// 256 threads up to 4096, 1024 above: the shortest reduction whose chunks fit the registers.
+// 256 threads up to 6144, 512 (the forward's last 4096 columns: 1024) above: few threads with up to
+// three chunks each leave room for more rows on a CU than many threads with one (8192 rows of 5120
+// bf16, forward and backward: 256 x 3 chunks 29 and 48 us, 512 x 2 34 and 67, 1024 x 1 43 and 65; of
+// 12288: 512 x 3 77 and 112, 1024 x 2 111 and 349; float32 gains less, 75 and 113 us at 6144 against 79
+// and 118).
 #include "kernels.h"
 #include "vec.h"
 
@@ -130,60 +135,79 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_norm_bwd(NormArgs a) 
     for (int e = 0; e < 8; ++e) { ga[c][e] = 1.f; dg[c][e] = db[c][e] = 0.f; }
     if (nv && a.gamma.p) a.gamma.load(col, nv, ga[c]);
   }
-  // the next row's loads are in flight while this row is reduced (not with two chunks in each
-  // of 1024 threads, whose 128 registers do not hold them)
-  constexpr bool AHEAD = THR < 1024 || CH == 1;
-  Raw8<T> rx[CH], ry[CH], rr[CH];
+  // The next row's loads are in flight while this row is reduced.  With four chunks the registers
+  // do not hold that: LEAN loads the row once for its sums and again (from L2) for its results (8192
+  // rows of 16384 bf16 224 us; with all of it in registers, which spills, 419, with the row kept as
+  // it lies in memory 466).
+  constexpr bool LEAN = CH == 4;
+  constexpr int KEEP = LEAN ? 1 : CH;
+  Raw8<T> rx[KEEP], ry[KEEP], rr[KEEP];
   float mu_n = 0.f, r_n = 0.f;
+  auto fetch_chunk = [&](int64_t row, int c, int k) {
+    const int64_t col = (int64_t)(c * THR + t) * 8;
+    const int nv = clamp8(a.d - col);
+    load_raw((const T *)a.x + row * a.d + col, nv, rx[k]);
+    load_raw((const T *)a.dy + row * a.d + col, nv, ry[k]);
+    if (a.dres) load_raw((const T *)a.dres + row * a.d + col, nv, rr[k]);
+  };
   auto fetch = [&](int64_t row) {
     mu_n = a.mean[row];
     r_n = a.rstd[row];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int64_t col = (int64_t)(c * THR + t) * 8;
-      const int nv = clamp8(a.d - col);
-      load_raw((const T *)a.x + row * a.d + col, nv, rx[c]);
-      load_raw((const T *)a.dy + row * a.d + col, nv, ry[c]);
-      if (a.dres) load_raw((const T *)a.dres + row * a.d + col, nv, rr[c]);
-    }
+    for (int c = 0; c < CH && !LEAN; ++c) fetch_chunk(row, c, c);
   };
   int parity = 0;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / THR;
-  if (AHEAD && row < a.n) fetch(row);
+  if (!LEAN && row < a.n) fetch(row);
   for (; row < a.n; row += step) {
-    if (!AHEAD) fetch(row);
+    if (LEAN) fetch(row);
     const float mu = mu_n, r = r_n;
-    float xh[CH][8], g[CH][8], q[CH][8], s[2] = {0.f, 0.f};
+    float xh[KEEP][8], g[KEEP][8], q[KEEP][8], s[2] = {0.f, 0.f};
+    auto expand = [&](int c, float (&xh_)[8], float (&g_)[8], float (&q_)[8]) {
+      const int nv = clamp8(a.d - (int64_t)(c * THR + t) * 8);
+      const int k = LEAN ? 0 : c;
+      widen(rx[k], xh_);
+      widen(ry[k], g_);
+      if (a.dres) widen(rr[k], q_);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xh_[e] = e < nv ? (xh_[e] - mu) * r : 0.f;
+    };
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int nv = clamp8(a.d - (int64_t)(c * THR + t) * 8);
-      widen(rx[c], xh[c]);
-      widen(ry[c], g[c]);
-      if (a.dres) widen(rr[c], q[c]);
+      const int k = LEAN ? 0 : c;
+      if (LEAN) fetch_chunk(row, c, k);
+      expand(c, xh[k], g[k], q[k]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[c][e] = e < nv ? (xh[c][e] - mu) * r : 0.f;
-        dg[c][e] += g[c][e] * xh[c][e];
-        db[c][e] += g[c][e];
-        g[c][e] *= ga[c][e];
-        s[0] += g[c][e];
-        s[1] += g[c][e] * xh[c][e];
+        dg[c][e] += g[k][e] * xh[k][e];
+        db[c][e] += g[k][e];
+        g[k][e] *= ga[c][e];
+        s[0] += g[k][e];
+        s[1] += g[k][e] * xh[k][e];
       }
     }
-    if (AHEAD && row + step < a.n) fetch(row + step);
+    if (!LEAN && row + step < a.n) fetch(row + step);
     row_sum<THR, 2>(s, red, parity);
+    if (LEAN) asm volatile("" ::: "memory");  // the second pass loads again
     parity ^= 1;
     const float m1 = s[0] / a.fd, m2 = s[1] / a.fd;
     T *dx = (T *)a.out + row * a.d;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      const int k = LEAN ? 0 : c;
+      if constexpr (LEAN) {
+        fetch_chunk(row, c, k);
+        expand(c, xh[k], g[k], q[k]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[k][e] *= ga[c][e];
+      }
       const int64_t col = (int64_t)(c * THR + t) * 8;
       float o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[e] = r * (g[c][e] - m1 - xh[c][e] * m2);
-        if (a.dres) o[e] += q[c][e];
+        o[e] = r * (g[k][e] - m1 - xh[k][e] * m2);
+        if (a.dres) o[e] += q[k][e];
       }
       store8(dx + col, clamp8(a.d - col), o);
     }
@@ -271,12 +295,12 @@ int run_bwd(const NormArgs &a, int64_t blocks, hipStream_t s) {
   return launch_k("layernorm_bwd", s, k_norm_bwd<T, THR, CH>, dim3((unsigned)blocks), dim3(BLK), 0, a);
 }
 
-// Workgroups that walk the n rows (a wave per row up to 1024 columns).  Forward: 8 of 256
-// threads (2 of 1024) per CU.  Backward: 2 (1) per CU, which with a row in flight ahead keep
+// Workgroups that walk the n rows (a wave per row up to 1024 columns).  Forward: 8 per CU (2 above
+// 8192 columns).  Backward: 2 (1 above 6144 columns) per CU, which with a row in flight ahead keep
 // as much memory traffic going while they leave fewer partial sums to write and join.
 int64_t norm_blocks(int64_t n, int64_t d, bool bwd) {
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
-  const int64_t most = cus * (bwd ? (d <= 4096 ? 2 : 1) : (d <= 4096 ? 8 : 2));
+  const int64_t most = cus * (bwd ? (d <= 6144 ? 2 : 1) : (d <= 8192 ? 8 : 2));
   const int64_t need = cdiv(n, d <= 1024 ? 4 : 1);
   return need < most ? need : most;
 }
@@ -288,7 +312,9 @@ int fwd_t(const NormArgs &a, hipStream_t s) {
   if (a.d <= 1024) return run_fwd<T, 64, 2>(a, g, s);
   if (a.d <= 2048) return run_fwd<T, 256, 1>(a, g, s);
   if (a.d <= 4096) return run_fwd<T, 256, 2>(a, g, s);
-  if (a.d <= 8192) return run_fwd<T, 1024, 1>(a, g, s);
+  if (a.d <= 6144) return run_fwd<T, 256, 3>(a, g, s);
+  if (a.d <= 8192) return run_fwd<T, 512, 2>(a, g, s);
+  if (a.d <= 12288) return run_fwd<T, 512, 3>(a, g, s);
   return run_fwd<T, 1024, 2>(a, g, s);
 }
 template <typename T>
@@ -297,8 +323,10 @@ int bwd_t(const NormArgs &a, int64_t g, hipStream_t s) {
   if (a.d <= 1024) return run_bwd<T, 64, 2>(a, g, s);
   if (a.d <= 2048) return run_bwd<T, 256, 1>(a, g, s);
   if (a.d <= 4096) return run_bwd<T, 256, 2>(a, g, s);
-  if (a.d <= 8192) return run_bwd<T, 1024, 1>(a, g, s);
-  return run_bwd<T, 1024, 2>(a, g, s);
+  if (a.d <= 6144) return run_bwd<T, 256, 3>(a, g, s);
+  if (a.d <= 8192) return run_bwd<T, 512, 2>(a, g, s);
+  if (a.d <= 12288) return run_bwd<T, 512, 3>(a, g, s);
+  return run_bwd<T, 512, 4>(a, g, s);
 }
 
 }  // namespace

@@ -678,3 +678,10 @@ def test_xent_few_tokens(B, n, d, v, dtype):
     """Few tokens over vocabularies of each way to share a group's k, with tails of k that end
     inside a turn of the waves."""
     check_xent(B, n, d, v, dtype, seed=330)
+
+
+@pytest.mark.parametrize("n,d", [(600, 5121), (530, 6144), (270, 6150), (300, 12288), (280, 12289), (3, 15000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_layernorm_wide_rows(B, n, d, dtype):
+    """Each way to spread a wide row over threads, with more rows than workgroups."""
+    test_layernorm(B, n, d, dtype, F32)
