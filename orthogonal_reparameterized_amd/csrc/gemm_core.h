@@ -617,15 +617,28 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
 }
 
 // 16 bytes of an operand row as an MFMA fragment (8 bf16 or 4 floats), the first `left` in range.
+// ODD: the rows are an odd number of bf16 apart.  A 16-byte load off its 4-byte alignment takes
+// three times as long (14 tokens, 100793 rows of 641: 98 us, of 642: 40), so every load starts at
+// the element before where the address is odd, the last element is loaded by itself, and the
+// words are shifted into place.  (An odd address is never the operand's first.)
 template <typename T> struct RowFrag;
 template <> struct RowFrag<bf16_t> { using V = bf16x8; static constexpr int E = 8; };
 template <> struct RowFrag<float> { using V = f32x4; static constexpr int E = 4; };
-template <typename T>
+template <bool ODD, typename T>
 __device__ inline typename RowFrag<T>::V row_frag(const T *p, int64_t left) {
   constexpr int E = RowFrag<T>::E, PER = E / 4;
   u32v4 u = {0u, 0u, 0u, 0u};
   if (left >= E) {
-    __builtin_memcpy(&u, p, 16);
+    if constexpr (ODD) {
+      const uint32_t sh = (uint32_t)((uintptr_t)p & 2) * 8;
+      u32v4 w;
+      __builtin_memcpy(&w, p - (sh ? 1 : 0), 16);
+      const uint32_t last = p[E - 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_alignbit(i < 3 ? w[i < 3 ? i + 1 : 3] : last, w[i], sh);
+    } else {
+      __builtin_memcpy(&u, p, 16);
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -652,7 +665,7 @@ __device__ inline f32x4 mul_frag(f32x4 b, f32x4 a, f32x4 acc) {
 // workgroup takes 16 NG rows of B; its 8 waves are NG groups of 8 / NG, which share a
 // group's k range in turns of U fragments and are joined in LDS.  Operands go from memory into
 // fragments: lane l reads 16 bytes of row l % 16 in its quarter (l / 16) of each fragment's k.
-template <typename T, int NG, class Epi>
+template <typename T, int NG, bool ODD, class Epi>
 __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
   constexpr int KW = 8 / NG, U = 4, E = RowFrag<T>::E, D = 4 * E;  // U fragments of D k in flight per wave
   __shared__ __align__(16) float red[8 * 16 * 20];  // the parts (8 x 256), then the rows (8 x 320)
@@ -668,14 +681,14 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
     typename RowFrag<T>::V fb[U], fa[U];
     if ((t + 1) * D * U <= a.K) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) fb[u] = row_frag(pb + k0 + D * u, E);
+      for (int u = 0; u < U; ++u) fb[u] = row_frag<ODD>(pb + k0 + D * u, E);
 #pragma unroll
-      for (int u = 0; u < U; ++u) fa[u] = row_frag(pa + k0 + D * u, E);
+      for (int u = 0; u < U; ++u) fa[u] = row_frag<ODD>(pa + k0 + D * u, E);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        fb[u] = row_frag(pb + k0 + D * u, a.K - k0 - D * u);
-        fa[u] = row_frag(pa + k0 + D * u, a.K - k0 - D * u);
+        fb[u] = row_frag<ODD>(pb + k0 + D * u, a.K - k0 - D * u);
+        fa[u] = row_frag<ODD>(pa + k0 + D * u, a.K - k0 - D * u);
       }
     }
 #pragma unroll

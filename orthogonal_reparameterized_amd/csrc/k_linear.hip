@@ -304,10 +304,11 @@ int fwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   if (d.n <= 16) {  // reading W bounds these: no LDS tiles, any alignment
     if (measure) return POETX_OK;
     MmArgs a{m.M, m.N, m.K, m.A, m.lda, m.B, m.ldb, 1, 1, 1, m.K};
-    const int64_t groups = cdiv(d.d_out, 16);
-    if (groups >= 1024)
-      return launch_k(m.name, s, k_mm_few<T, 2, LinEpi<T>>, dim3((unsigned)cdiv(groups, 2)), dim3(512), 0, a, epi);
-    return launch_k(m.name, s, k_mm_few<T, 1, LinEpi<T>>, dim3((unsigned)groups), dim3(512), 0, a, epi);
+    const int64_t groups = cdiv(d.d_out, 16), two = groups >= 1024;
+    constexpr bool B16 = sizeof(T) == 2;
+    auto kern = two ? k_mm_few<T, 2, false, LinEpi<T>> : k_mm_few<T, 1, false, LinEpi<T>>;
+    if (B16 && d.d_in % 2) kern = two ? k_mm_few<T, 2, B16, LinEpi<T>> : k_mm_few<T, 1, B16, LinEpi<T>>;
+    return launch_k(m.name, s, kern, dim3((unsigned)(two ? cdiv(groups, 2) : groups)), dim3(512), 0, a, epi);
   }
   Packed x, w;
   POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));

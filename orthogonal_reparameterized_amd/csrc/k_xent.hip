@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256) void k_xent_parts(const float *src, int splits
 // workgroup.  KW = 1 walks groups and keeps a running (max, sum): 8 tokens, d = 4096, 131072 rows,
 // bf16: 199 us, 5.4 TB/s, the rate of a large copy (242 us without the loads ahead; 222 us with
 // half or twice the workgroups).
-template <typename T, int KW>
+template <typename T, int KW, bool ODD>
 __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
   constexpr int NG = 8 / KW, U = 8, E = RowFrag<T>::E, D = 4 * E;  // fragments of D k per turn
   using V = typename RowFrag<T>::V;
@@ -269,9 +269,9 @@ __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
     V fb[2][U], fa[2][U];
     auto load = [&](int64_t q, V (&b_)[U], V (&a_)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) b_[u] = row_frag(pb + (q * U + u) * D, E);
+      for (int u = 0; u < U; ++u) b_[u] = row_frag<ODD>(pb + (q * U + u) * D, E);
 #pragma unroll
-      for (int u = 0; u < U; ++u) a_[u] = row_frag(pa + (q * U + u) * D, E);
+      for (int u = 0; u < U; ++u) a_[u] = row_frag<ODD>(pa + (q * U + u) * D, E);
     };
     auto mul = [&](const V (&b_)[U], const V (&a_)[U]) {
 #pragma unroll
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
     }
     for (int64_t k = (whole * U + kw) * D; k < a.K; k += KW * D) {  // the rest, a fragment at a time
       const int64_t left = a.K - k - E * (l >> 4);
-      acc = mul_frag(row_frag(pb + k, left), row_frag(pa + k, left), acc);
+      acc = mul_frag(row_frag<ODD>(pb + k, left), row_frag<ODD>(pa + k, left), acc);
     }
     return acc;
   };
@@ -503,11 +503,14 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     part = (float2 *)ar.take((size_t)tiles * d.n * 8);
     if (measure) return POETX_OK;
     const MmArgs a{d.n, d.v, d.d, d.h, d.d, d.w, d.d, 1, 1, 1, d.d};
-    const XentStats epi{part, d.target, at, 0, 0};
-    const dim3 grid((unsigned)tiles), block(512);
-    POETX_TRY(share == 8   ? launch_k("xent_few", s, k_xent_few<T, 8>, grid, block, 0, a, epi)
-              : share == 2 ? launch_k("xent_few", s, k_xent_few<T, 2>, grid, block, 0, a, epi)
-                           : launch_k("xent_few", s, k_xent_few<T, 1>, grid, block, 0, a, epi));
+    constexpr bool B16 = sizeof(T) == 2;
+    auto kern = share == 8   ? k_xent_few<T, 8, false>
+                : share == 2 ? k_xent_few<T, 2, false>
+                             : k_xent_few<T, 1, false>;
+    if (B16 && d.d % 2)
+      kern = share == 8 ? k_xent_few<T, 8, B16> : share == 2 ? k_xent_few<T, 2, B16> : k_xent_few<T, 1, B16>;
+    POETX_TRY(launch_k("xent_few", s, kern, dim3((unsigned)tiles), dim3(512), 0, a,
+                       XentStats{part, d.target, at, 0, 0}));
   } else {
     const int64_t piece = pads(d) ? piece_of(d) : d.v;
     Operands o;
