@@ -812,15 +812,26 @@ inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_spli
   }
 }
 
-// bf16: 256 x 256 tiles (one workgroup per CU) where they fill three quarters of the GPU, else
-// 128 x 128 (two per CU).
+// bf16: 256 x 256 tiles (one workgroup per CU), or 128 x 128 (two per CU) for smaller products.  The
+// larger are taken
+//   - where they fill three quarters of the GPU,
+//   - where 128 x 128 ones would begin a second round, from 512 deep (3000^3 102 -> 62 us, 8192 x
+//     1032 x 4096 105 -> 86, 2560 x 4096 x 512 equal; x 256 18 -> 19),
+//   - where k can be split over the GPU into ranges of 2304 at least (1024 x 1024 x 65536 175 -> 129 us,
+//     768 x 3000 x 16384 80 -> 77; 2048 x 2048 x 8192, ranges of 2048, equal; x 6144 58 -> 58).
 inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true) {
   MmPlan p;
   if (M <= 0 || N <= 0) return p;  // nothing to launch
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
   p.kc = K;
-  if (dt == POETX_BF16) p.bt = 4 * cdiv(M, 256) * cdiv(N, 256) >= 3 * cus ? 256 : 128;
-  else plan_f32(M, N, K, cus, may_split, p);
+  if (dt == POETX_F32) {
+    plan_f32(M, N, K, cus, may_split, p);
+  } else {
+    const int64_t t256 = cdiv(M, 256) * cdiv(N, 256), ranges = cus / t256 < 32 ? cus / t256 : 32;
+    const bool rounds = cdiv(M, 128) * cdiv(N, 128) > 2 * cus && K >= 512;
+    const bool deep = may_split && ranges >= 2 && K >= 2304 * ranges;
+    p.bt = 4 * t256 >= 3 * cus || rounds || deep ? 256 : 128;
+  }
   p.tiles_m = cdiv(M, p.bt);
   p.tiles_n = cdiv(N, p.bt);
   const int64_t tiles = p.tiles_m * p.tiles_n, slots = p.bt == 256 ? cus : 2 * cus;

@@ -685,3 +685,13 @@ def test_xent_few_tokens(B, n, d, v, dtype):
 def test_layernorm_wide_rows(B, n, d, dtype):
     """Each way to spread a wide row over threads, with more rows than workgroups."""
     test_layernorm(B, n, d, dtype, F32)
+
+
+@pytest.mark.parametrize("n,i,o", [(1500, 4700, 5300), (7001, 2200, 2000), (600, 7001, 6008)])
+def test_linear_large_tiles_over_ranges_of_k(B, n, i, o):
+    """Products whose 256 x 256 tiles are split over k, and ones with tiles for half the GPU."""
+    test_linear_shared_last_round(B, n, i, o)
+
+
+def test_xent_large_tiles_over_ranges_of_k(B):
+    check_xent(B, 1300, 4700, 4400, BF16, seed=340)
