@@ -812,11 +812,13 @@ inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_spli
   }
 }
 
-// bf16: 256 x 256 tiles (one workgroup per CU), or 128 x 128 (two per CU) for smaller products.  The
-// larger are taken
-//   - where they fill three quarters of the GPU,
-//   - where 128 x 128 ones would begin a second round, from 512 deep (3000^3 102 -> 62 us, 8192 x
-//     1032 x 4096 105 -> 86, 2560 x 4096 x 512 equal; x 256 18 -> 19),
+// bf16: 256 x 256 tiles (one workgroup per CU), or 128 x 128 (two per CU, one of which multiplies
+// while the other loads its first step or stores) for smaller products.  The larger are taken from
+// 384 deep
+//   - where they fill three quarters of the GPU (8192 x 4096 x 1024 with GELU 95 -> 81 us, x 512 63 ->
+//     61; not x 128, 42 -> 43, nor 1102 x 40000 x 256, 67 -> 90),
+//   - where 128 x 128 ones would begin a second round (3000^3 102 -> 62 us, 8192 x 1032 x 4096 105 ->
+//     86, 2560 x 4096 x 512 equal),
 //   - where k can be split over the GPU into ranges of 2304 at least (1024 x 1024 x 65536 175 -> 129 us,
 //     768 x 3000 x 16384 80 -> 77; 2048 x 2048 x 8192, ranges of 2048, equal; x 6144 58 -> 58).
 inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true) {
@@ -828,9 +830,9 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
     plan_f32(M, N, K, cus, may_split, p);
   } else {
     const int64_t t256 = cdiv(M, 256) * cdiv(N, 256), ranges = cus / t256 < 32 ? cus / t256 : 32;
-    const bool rounds = cdiv(M, 128) * cdiv(N, 128) > 2 * cus && K >= 512;
+    const bool many = 4 * t256 >= 3 * cus || cdiv(M, 128) * cdiv(N, 128) > 2 * cus;
     const bool deep = may_split && ranges >= 2 && K >= 2304 * ranges;
-    p.bt = 4 * t256 >= 3 * cus || rounds || deep ? 256 : 128;
+    p.bt = (many && K >= 384) || deep ? 256 : 128;
   }
   p.tiles_m = cdiv(M, p.bt);
   p.tiles_n = cdiv(N, p.bt);

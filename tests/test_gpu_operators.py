@@ -695,3 +695,9 @@ def test_linear_large_tiles_over_ranges_of_k(B, n, i, o):
 
 def test_xent_large_tiles_over_ranges_of_k(B):
     check_xent(B, 1300, 4700, 4400, BF16, seed=340)
+
+
+def test_wide_weight_gradients_of_more_tokens(B):
+    """Weight gradients by way of a transposed copy, with a tail of the tokens."""
+    check_linear_bwd(B, 413, 1100, 12300, BF16, "silu")
+    check_xent(B, 421, 1004, 12500, BF16, seed=350)
