@@ -820,7 +820,9 @@ inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_spli
 //   - where 128 x 128 ones would begin a second round (3000^3 102 -> 62 us, 8192 x 1032 x 4096 105 ->
 //     86, 2560 x 4096 x 512 equal),
 //   - where k can be split over the GPU into ranges of 2304 at least (1024 x 1024 x 65536 175 -> 129 us,
-//     768 x 3000 x 16384 80 -> 77; 2048 x 2048 x 8192, ranges of 2048, equal; x 6144 58 -> 58).
+//     768 x 3000 x 16384 80 -> 77; 2048 x 2048 x 8192, ranges of 2048, equal), or of 1792 where 128 x
+//     128 ones load the CUs unevenly (weights not in the caches: 190 x 17792 x 5384 128 -> 76 us, 512 x
+//     14336 x 4096 77 -> 66; ranges of 1024, 384 x 16000 x 2048, 40 -> 43).
 inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true) {
   MmPlan p;
   if (M <= 0 || N <= 0) return p;  // nothing to launch
@@ -830,8 +832,9 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
     plan_f32(M, N, K, cus, may_split, p);
   } else {
     const int64_t t256 = cdiv(M, 256) * cdiv(N, 256), ranges = cus / t256 < 32 ? cus / t256 : 32;
-    const bool many = 4 * t256 >= 3 * cus || cdiv(M, 128) * cdiv(N, 128) > 2 * cus;
-    const bool deep = may_split && ranges >= 2 && K >= 2304 * ranges;
+    const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
+    const bool many = 4 * t256 >= 3 * cus || t128 > 2 * cus;
+    const bool deep = may_split && ranges >= 2 && K >= (t128 > cus ? 1792 : 2304) * ranges;
     p.bt = (many && K >= 384) || deep ? 256 : 128;
   }
   p.tiles_m = cdiv(M, p.bt);
