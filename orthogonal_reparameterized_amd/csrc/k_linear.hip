@@ -18,7 +18,7 @@ constexpr float kTanhC = 0.79788456080286536f, kTanhA = 0.044715f;  // sqrt(2 / 
 // The activations run on every result of a product's epilogue, where the matrix cores wait for
 // them: one hardware exp and one reciprocal each (both to about 1 ulp), not the library's erf
 // and tanh (whose epilogue took 31 us of a 130 us round of 256 x 256 tiles, k = 4096; 8192
-// tokens, 4096 -> 14336 with GELU and the kept pre-activation: 904 us then, 743 us now).
+// tokens, 4096 -> 14336 with GELU and the kept pre-activation: 904 us then, 733 us now).
 
 __device__ inline float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
 
