@@ -762,7 +762,10 @@ __global__ __launch_bounds__(256) void k_mm_tail(MmArgs a, Epi epi) {
 }
 
 // ------------------------------------------------------------------ host side ----
-constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // a grid holds fewer than 2^32 threads
+// A grid holds fewer than 2^32 threads: 2^24 - 1 workgroups of 256.  (The callers admit 2^22 tiles of
+// 128 x 128; those of 256 x 256, of 512 threads, are no more, and 64 x 64 ones are taken where they
+// are less than 3.75 times as many.)
+constexpr int64_t kMaxTiles = ((int64_t)1 << 24) - 1;
 
 // How a product is tiled (bt x bt results per workgroup), and over how many k ranges.
 struct MmPlan {

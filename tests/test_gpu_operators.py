@@ -701,3 +701,17 @@ def test_wide_weight_gradients_of_more_tokens(B):
     """Weight gradients by way of a transposed copy, with a tail of the tokens."""
     check_linear_bwd(B, 413, 1100, 12300, BF16, "silu")
     check_xent(B, 421, 1004, 12500, BF16, seed=350)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_as_many_tokens_as_there_are_tiles_for(B, dtype):
+    """2^21 + 1 tiles of 128 tokens with one result each: in float32 twice as many tiles of 64."""
+    n, d = (1 << 28) + 1, 20
+    x = torch.zeros(n, d, dtype=dtype, device="cuda")
+    x[:, 3] = torch.arange(n, device="cuda", dtype=torch.int32).remainder_(251).to(dtype)
+    w = torch.zeros(1, d, dtype=dtype, device="cuda")
+    w[0, 3] = 2.0
+    y, _ = B.poetx_linear_forward(x, w)
+    assert torch.equal(y[:, 0], x[:, 3] * 2)  # exact in both types
+    dx = B.poetx_linear_backward(None, w, y, want_dw=False, want_dbias=False)["dx"]
+    assert torch.equal(dx[:, 3], y[:, 0] * 2) and not dx[:, 4].any()
