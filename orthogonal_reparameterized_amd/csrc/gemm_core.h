@@ -48,8 +48,8 @@ __device__ inline void tile_at(const MmArgs &a, int L, int &tm, int &tn) {
   tm = __builtin_amdgcn_readfirstlane(first + loc % gm);
   tn = __builtin_amdgcn_readfirstlane(loc / gm);
 }
-__device__ inline MmTile mm_tile(const MmArgs &a) {
-  const int T = a.tiles_m * a.tiles_n, id = (int)blockIdx.x;
+__device__ inline MmTile mm_tile(const MmArgs &a, int id) {
+  const int T = a.tiles_m * a.tiles_n;
   MmTile t;
   int L;
   if (id >= a.full) {
@@ -212,13 +212,12 @@ struct StoreEpi {
 // workgroups per CU that fill each other's waits.  2048^3: 27-30 us, 0.6 PFLOP/s (the vendor
 // library 21-27 us); a handful of tokens or columns is bound by the load latency of its k range.
 template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, class Epi>
-__global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
+__device__ inline void mm_body(const MmArgs &a, const Epi &epi, int id, bf16_t *smem) {
   constexpr int NW = WGM * WGN, BK = 64;
   constexpr int WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 16, FN = WTN / 16;
   constexpr int AE = BM * BK, BE = BN * BK;
-  extern __shared__ __align__(16) bf16_t smem[];
 
-  const MmTile tile = mm_tile(a);
+  const MmTile tile = mm_tile(a, id);
   const int64_t m0 = (int64_t)tile.tm * BM, n0 = (int64_t)tile.tn * BN;
   const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
   const int wave = threadIdx.x >> 6;
@@ -270,6 +269,11 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
   }
   __syncthreads();  // every wave is done with the last stage: the epilogue reuses the LDS
   finish<BM, BN, WGM, WGN>(acc, a, tile, (float *)smem, epi);
+}
+template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, class Epi>
+__global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
+  extern __shared__ __align__(16) bf16_t smem[];
+  mm_body<BM, BN, WGM, WGN, AKM, BKM>(a, epi, blockIdx.x, smem);
 }
 
 // 256 x 256 tile, 8 waves (2 x 4, 128 x 64 each), 64-deep k steps: the large products.
@@ -385,7 +389,7 @@ template <bool AKM, bool BKM, bool FLIP, class Epi>
 __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
   constexpr int HE = 128 * 64, FM = 8, FN = 4;  // elements of a half tile; 16 x 16 results per wave
   extern __shared__ __align__(16) bf16_t smem[];  // [A0 A1 B0 B1][2 steps]
-  const MmTile tile = mm_tile(a);
+  const MmTile tile = mm_tile(a, blockIdx.x);
   const int64_t m0 = (int64_t)tile.tm * 256, n0 = (int64_t)tile.tn * 256;
   const int64_t kc = tile.tail >= 0 ? a.tail_kc : a.splits > 1 ? a.kc : a.K;
   const int64_t kbeg = tile.split * kc, kend = kbeg + kc < a.K ? kbeg + kc : a.K;
@@ -510,12 +514,12 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
 // from rows as they lie in memory, chunks XORed as in the bf16 tiles, and a k-major one, in
 // rows of BT + 4 floats, meets four different 16-bank groups.  Bound by the float32 matrix
 // rate (157 TFLOP/s).
+constexpr int f32_lds(int bt, int bk) { return 4 * bk * (bt + 4); }  // floats
 template <int BT, int BK, bool AKM, bool BKM, class Epi>
-__global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
+__device__ inline void mm_f32_body(const MmArgs &a, const Epi &epi, int id, float *smem) {
   constexpr int LD = BT + 4, ST = BK * LD, WT = BT / 2, F = WT / 16;  // a stage of either layout fits ST
   constexpr int PC = BT * BK / 4 / 256;  // 4-float pieces per thread and operand stage
-  __shared__ __align__(16) float smem[4 * ST];
-  const MmTile tile = mm_tile(a);
+  const MmTile tile = mm_tile(a, id);
   const int64_t m0 = (int64_t)tile.tm * BT, n0 = (int64_t)tile.tn * BT;
   const int64_t kbeg = tile.split * a.kc, kend = a.splits > 1 && kbeg + a.kc < a.K ? kbeg + a.kc : a.K;
   const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
@@ -614,6 +618,46 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
   }
   __syncthreads();
   finish<BT, BT, 2, 2>(acc, a, tile, smem, epi);
+}
+template <int BT, int BK, bool AKM, bool BKM, class Epi>
+__global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
+  __shared__ __align__(16) float smem[f32_lds(BT, BK)];
+  mm_f32_body<BT, BK, AKM, BKM>(a, epi, blockIdx.x, smem);
+}
+
+// An epilogue whose product may be split over k: partials where `part` is set.
+template <class Epi>
+struct MaybePart {
+  static constexpr bool kStats = false;
+  static constexpr int kRows = 0;
+  using Tag_ = typename Epi::Tag_;
+  using Cols = typename Epi::Cols;
+  Epi epi;
+  float *part; int64_t N, stride;
+  __device__ MaybePart at(int split) const { return MaybePart{epi, part ? part + split * stride : nullptr, N, stride}; }
+  __device__ Cols cols(int64_t n, int nv, const float *rows) const { return epi.cols(n, nv, rows); }
+  __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
+    if (part) store8(part + m * N + n, nv, v);
+    else epi.put(c, m, n, v, nv);
+  }
+};
+
+// The two products of a backward pass, D W (W k-major) and D^T X (both k-major), in one launch:
+// small ones fill the GPU together and wait for one launch and one fill instead of two.
+// 513 x 1001 x 777 float32: PAIRUS.  The first has workgroups [0, ga), ga a multiple of 8 so that
+// both deal their tiles to the XCDs alike.
+template <typename T, class EA, class EB>
+__global__ __launch_bounds__(256) void k_mm_pair(MmArgs a, EA ea, MmArgs b, EB eb, int ga) {
+  extern __shared__ __align__(16) bf16_t smem[];
+  const int id = (int)blockIdx.x;
+  if (id < ga) {
+    if (id >= a.tiles_m * a.tiles_n * a.splits) return;
+    if constexpr (sizeof(T) == 4) mm_f32_body<64, 32, false, true>(a, ea, id, (float *)smem);
+    else mm_body<128, 128, 2, 2, false, true>(a, ea, id, smem);
+  } else {
+    if constexpr (sizeof(T) == 4) mm_f32_body<64, 32, true, true>(b, eb, id - ga, (float *)smem);
+    else mm_body<128, 128, 2, 2, true, true>(b, eb, id - ga, smem);
+  }
 }
 
 // 16 bytes of an operand row as an MFMA fragment (8 bf16 or 4 floats), the first `left` in range.
@@ -721,9 +765,9 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
 // Sum of the float32 partials of a split product, [splits][M][N] in split order, into the
 // epilogue; one thread per 8 columns.
 template <class Epi>
-__global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, int64_t M, int64_t N, Epi epi) {
+__device__ inline void join_body(const float *part, int splits, int64_t M, int64_t N, const Epi &epi, uint32_t id) {
   // (a split product has fewer than 2^32 results)
-  const uint32_t cpr = (uint32_t)cdiv(N, 8), i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t cpr = (uint32_t)cdiv(N, 8), i = id * 256 + threadIdx.x;
   if (i >= M * cpr) return;
   const int64_t m = i / cpr, n = (int64_t)(i - (uint32_t)m * cpr) * 8;
   const int nv = N - n >= 8 ? 8 : (int)(N - n);
@@ -737,6 +781,18 @@ __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, 
     for (int e = 0; e < 8; ++e) v[e] += w[e];
   }
   epi.put(epi.cols(n, nv, nullptr), m, n, v, nv);
+}
+template <class Epi>
+__global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, int64_t M, int64_t N, Epi epi) {
+  join_body(part, splits, M, N, epi, blockIdx.x);
+}
+// both products of a pair; the first has workgroups [0, ja)
+template <class EA, class EB>
+__global__ __launch_bounds__(256) void k_mm_join_pair(const float *pa, int sa, int64_t Ma, int64_t Na, EA ea,
+                                                      const float *pb, int sb, int64_t Mb, int64_t Nb, EB eb,
+                                                      uint32_t ja) {
+  if (blockIdx.x < ja) join_body(pa, sa, Ma, Na, ea, blockIdx.x);
+  else join_body(pb, sb, Mb, Nb, eb, blockIdx.x - ja);
 }
 
 // The same for the shared tiles of k_mm8: 32 workgroups per tile, one thread per 8 columns.
@@ -791,7 +847,7 @@ struct MmDesc {
 // and join (6 us, 5 TB/s) and a tenth of the time: 896 x 2573 x 3056, 2.2 tiles per CU, 166 us
 // whole, 132 in 4 ranges; 64 x 4096 x 4096 105 and 33; 1024^3 stays whole, 29 against 34.
 constexpr size_t kMaxPart = (size_t)64 << 20;
-inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_split, MmPlan &p) {
+inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, int halves, bool may_split, MmPlan &p) {
   const int64_t t64 = cdiv(M, 64) * cdiv(N, 64), t128 = cdiv(M, 128) * cdiv(N, 128);
   auto cost = [&](int64_t kc, int64_t sp) {
     const int64_t w = cdiv(t64 * sp, cus);
@@ -803,7 +859,8 @@ inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_spli
     return;
   }
   if (!may_split || t64 >= 8 * cus) return;
-  double best = 0.9 * whole;
+  cus /= halves;
+  double best = 0.9 * cost(K, 1);
   for (int64_t want = 2; want <= 32 && want <= K / 128; ++want) {
     const int64_t kc = cdiv(cdiv(K, want), 64) * 64, sp = cdiv(K, kc);
     const size_t bytes = (size_t)sp * M * N * 4;
@@ -826,13 +883,14 @@ inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, bool may_spli
 //     768 x 3000 x 16384 80 -> 77; 2048 x 2048 x 8192, ranges of 2048, equal), or of 1792 where 128 x
 //     128 ones load the CUs unevenly (weights not in the caches: 190 x 17792 x 5384 128 -> 76 us, 512 x
 //     14336 x 4096 77 -> 66; ranges of 1024, 384 x 16000 x 2048, 40 -> 43).
-inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true) {
+inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true,
+                      int halves = 1) {
   MmPlan p;
   if (M <= 0 || N <= 0) return p;  // nothing to launch
   const int64_t cus = device_cus() > 0 ? device_cus() : 256;
   p.kc = K;
   if (dt == POETX_F32) {
-    plan_f32(M, N, K, cus, may_split, p);
+    plan_f32(M, N, K, cus, halves, may_split, p);
   } else {
     const int64_t t256 = cdiv(M, 256) * cdiv(N, 256), ranges = cus / t256 < 32 ? cus / t256 : 32;
     const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
@@ -842,12 +900,12 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
   }
   p.tiles_m = cdiv(M, p.bt);
   p.tiles_n = cdiv(N, p.bt);
-  const int64_t tiles = p.tiles_m * p.tiles_n, slots = p.bt == 256 ? cus : 2 * cus;
+  const int64_t tiles = p.tiles_m * p.tiles_n, slots = (p.bt == 256 ? cus : 2 * cus) / halves;
   // Too few bf16 tiles to fill the GPU: split k, each range at least 256 deep.  The partials'
   // join costs about 5 us, so a product with tiles for a quarter of the CUs and no more than 32
   // steps of 64 stays whole: 1024 x 2048 x 2048 24.5 -> 22.3 us, 1024^3 20 -> 14 us, while 64 x 4096
   // x 4096 takes 18 us split and 45 us whole.
-  if (may_split && dt == POETX_BF16 && tiles < slots && !(4 * tiles >= cus && K <= 32 * 64)) {
+  if (may_split && dt == POETX_BF16 && tiles < slots && !(4 * halves * tiles >= cus && K <= 32 * 64)) {
     int64_t sp = slots / tiles;
     if (sp > K / 256) sp = K / 256;
     if (sp > 32) sp = 32;
@@ -930,6 +988,60 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
     return launch_k("mm_join", s, k_mm_join<Epi>, dim3((unsigned)cdiv(d.M * cdiv(d.N, 8), 256)), dim3(256), 0,
                     (const float *)part, (int)p.splits, d.M, d.N, epi);
   }
+}
+
+// Plans of a backward pass's two products (D W, D^T X; one that is not wanted has no rows), and
+// whether they run as a pair: both on the smaller tiles, and not slower so by the steps that their
+// workgroups take (0.94 us for 64 deep in bf16, float32 as in plan_f32; a join 6 us, a launch 5).
+// 7808 tokens, 768 -> 2816 bf16, where the pair would leave one product's k unsplit: 121 us apart, 137
+// as a pair; 2112 tokens, 248 -> 9984 81 and 66; 145 tokens, 1807 -> 606 float32 34 and 30.
+struct MmTwo {
+  MmPlan a, b;
+  bool pair = false;
+};
+inline MmTwo mm_two(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64_t Kb, int dt) {
+  MmTwo t;
+  t.a = mm_plan(Ma, Na, Ka, dt);
+  t.b = mm_plan(Mb, Nb, Kb, dt);
+  const bool b16 = dt == POETX_BF16;
+  const int64_t bt = b16 ? 128 : 64, cus = device_cus() > 0 ? device_cus() : 256;
+  if (t.a.bt != bt || t.b.bt != bt || t.a.tiles_m == 0 || t.b.tiles_m == 0) return t;
+  const MmPlan a = mm_plan(Ma, Na, Ka, dt, true, true, 2), b = mm_plan(Mb, Nb, Kb, dt, true, true, 2);
+  auto wgs = [](const MmPlan &p) { return p.tiles_m * p.tiles_n * p.splits; };
+  auto steps = [&](const MmPlan &p) { return cdiv(p.kc, b16 ? 64 : 32); };
+  auto alone = [&](const MmPlan &p) {
+    const int64_t w = cdiv(wgs(p), b16 ? 2 * cus : cus);
+    return steps(p) * (b16 ? 0.94 * w : w == 1 ? 0.83 : 0.55 * w) + (p.splits > 1 ? 6 : 0);
+  };
+  const double longest = (b16 ? 0.94 : 0.83) * (steps(a) > steps(b) ? steps(a) : steps(b));
+  const double shared = 1.1 * (b16 ? 0.47 : 0.55) * ((double)wgs(a) * steps(a) + (double)wgs(b) * steps(b)) / cus;
+  const double both = (longest > shared ? longest : shared) + (a.splits > 1 || b.splits > 1 ? 6 : 0);
+  if (both > alone(t.a) + alone(t.b) + 5) return t;
+  t.a = a;
+  t.b = b;
+  t.pair = true;
+  return t;
+}
+// The pair of mm_run<T, false, true>(da, ..) and mm_run<T, true, true>(db, ..); plans with halves = 2.
+template <typename T, class EA, class EB>
+int mm_run_pair(const char *name, const MmDesc &da, const MmPlan &pa, float *part_a, const EA &ea, const MmDesc &db,
+                const MmPlan &pb, float *part_b, const EB &eb, hipStream_t s) {
+  const int64_t na = pa.tiles_m * pa.tiles_n * pa.splits, nb = pb.tiles_m * pb.tiles_n * pb.splits, ga = cdiv(na, 8) * 8;
+  if (ga + nb > kMaxTiles) return POETX_ERR_UNSUPPORTED;
+  const MmArgs a{da.M, da.N, da.K, da.A, da.lda, da.B, da.ldb, (int)pa.tiles_m, (int)pa.tiles_n, (int)pa.splits, pa.kc};
+  const MmArgs b{db.M, db.N, db.K, db.A, db.lda, db.B, db.ldb, (int)pb.tiles_m, (int)pb.tiles_n, (int)pb.splits, pb.kc};
+  const bool sa = pa.splits > 1, sb = pb.splits > 1;
+  constexpr size_t lds = sizeof(T) == 4 ? f32_lds(64, 32) * 4 : (size_t)2 * 2 * 128 * 64 * 2;
+  auto kern = &k_mm_pair<T, MaybePart<EA>, MaybePart<EB>>;
+  static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
+  POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
+  POETX_TRY(launch_k(name, s, kern, dim3((unsigned)(ga + nb)), dim3(256), lds, a,
+                     MaybePart<EA>{ea, sa ? part_a : nullptr, da.N, da.M * da.N}, b,
+                     MaybePart<EB>{eb, sb ? part_b : nullptr, db.N, db.M * db.N}, (int)ga));
+  if (!sa && !sb) return POETX_OK;
+  const unsigned ja = sa ? (unsigned)cdiv(da.M * cdiv(da.N, 8), 256) : 0, jb = sb ? (unsigned)cdiv(db.M * cdiv(db.N, 8), 256) : 0;
+  return launch_k("mm_join", s, k_mm_join_pair<EA, EB>, dim3(ja + jb), dim3(256), 0, (const float *)part_a,
+                  (int)pa.splits, da.M, da.N, ea, (const float *)part_b, (int)pb.splits, db.M, db.N, eb, (uint32_t)ja);
 }
 
 // dW = D^T X (D [K][M] and X [K][N], both k-major) for bf16: the kernels read a k-major operand

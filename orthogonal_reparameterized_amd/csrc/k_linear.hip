@@ -352,38 +352,41 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
                            (const float *)part, d.n > 0 ? parts : (int64_t)0, d.d_out, d.dbias));
     }
   }
+  if (d.n == 0) return measure || !d.dw ? POETX_OK : fill_zero(d.dw, d.d_out * d.d_in, d.dt, s);
+  const StoreEpi<T, LinTag> ex{(T *)d.dx, d.d_in, 0}, ew{(T *)d.dw, d.d_in, 0};
+  MmDesc mx, mw;
+  Packed w, x;
   if (d.dx) {
-    Packed w;
     POETX_TRY(packed(d.w, d.d_out, d.d_in, d.dt, ar, measure, s, w));
-    MmDesc m;
-    m.M = d.n; m.N = d.d_in; m.K = d.d_out; m.name = "linear_dx";
-    m.A = dp; m.lda = ld; m.B = w.p; m.ldb = w.ld;
-    const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
-    float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
-    if (!measure) POETX_TRY((mm_run<T, false, true>(m, p, part, StoreEpi<T, LinTag>{(T *)d.dx, d.d_in, 0}, s)));
+    mx.M = d.n; mx.N = d.d_in; mx.K = d.d_out; mx.name = "linear_dx";
+    mx.A = dp; mx.lda = ld; mx.B = w.p; mx.ldb = w.ld;
   }
-  if (d.dw) {
-    if (d.n == 0) return measure ? POETX_OK : fill_zero(d.dw, d.d_out * d.d_in, d.dt, s);
-    if constexpr (sizeof(T) == 2) {
-      if (dw_flips(d.d_out, d.d_in, d.n, d.dt)) {
-        const int64_t ldt = round8(d.n);
-        void *xt = ar.take((size_t)d.d_in * ldt * 2);
-        if (measure) return POETX_OK;
-        POETX_TRY(pack_rows_t(d.x, d.n, d.d_in, xt, ldt, nullptr, 0, s));
-        MmDesc m;
-        m.M = d.d_in; m.N = d.d_out; m.K = d.n; m.name = "linear_dw";
-        m.A = xt; m.lda = ldt; m.B = dp; m.ldb = ld;
-        return mm_run_flipped(m, StoreEpi<T, LinTag>{(T *)d.dw, d.d_in, 0}, s);
-      }
-    }
-    Packed x;
+  const bool flip = b16 && d.dw && dw_flips(d.d_out, d.d_in, d.n, d.dt);
+  if (d.dw && !flip) {
     POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));
-    MmDesc m;
-    m.M = d.d_out; m.N = d.d_in; m.K = d.n; m.name = "linear_dw";
-    m.A = dp; m.lda = ld; m.B = x.p; m.ldb = x.ld;
-    const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
-    float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
-    if (!measure) POETX_TRY((mm_run<T, true, true>(m, p, part, StoreEpi<T, LinTag>{(T *)d.dw, d.d_in, 0}, s)));
+    mw.M = d.d_out; mw.N = d.d_in; mw.K = d.n; mw.name = "linear_dw";
+    mw.A = dp; mw.lda = ld; mw.B = x.p; mw.ldb = x.ld;
+  }
+  const MmTwo two = mm_two(mx.M, mx.N, mx.K, mw.M, mw.N, mw.K, d.dt);
+  const MmPlan &px = two.a, &pw = two.b;
+  float *part_x = px.part_bytes ? (float *)ar.take(px.part_bytes) : nullptr;
+  float *part_w = pw.part_bytes ? (float *)ar.take(pw.part_bytes) : nullptr;
+  if (two.pair) return measure ? POETX_OK : mm_run_pair<T>("linear_dx_dw", mx, px, part_x, ex, mw, pw, part_w, ew, s);
+  if (!measure) {
+    POETX_TRY((mm_run<T, false, true>(mx, px, part_x, ex, s)));
+    POETX_TRY((mm_run<T, true, true>(mw, pw, part_w, ew, s)));
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (flip) {
+      const int64_t ldt = round8(d.n);
+      void *xt = ar.take((size_t)d.d_in * ldt * 2);
+      if (measure) return POETX_OK;
+      POETX_TRY(pack_rows_t(d.x, d.n, d.d_in, xt, ldt, nullptr, 0, s));
+      MmDesc m;
+      m.M = d.d_in; m.N = d.d_out; m.K = d.n; m.name = "linear_dw";
+      m.A = xt; m.lda = ldt; m.B = dp; m.ldb = ld;
+      return mm_run_flipped(m, ew, s);
+    }
   }
   return POETX_OK;
 }

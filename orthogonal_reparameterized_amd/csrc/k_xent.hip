@@ -414,6 +414,11 @@ MmDesc logits_desc(const XentDesc &d, const Operands &o, const void *w, int64_t 
   return m;
 }
 
+// dh and dW of a piece of vc entries; `flip`: dW goes its own way
+MmTwo products(const XentDesc &d, int64_t vc, bool flip) {
+  return mm_two(d.dh ? d.n : 0, d.d, vc, d.dw && !flip ? vc : 0, d.d, d.n, d.dt);
+}
+
 template <typename T>
 int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const int64_t piece = piece_of(d);
@@ -440,17 +445,17 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   T *dl = (T *)ar.take((size_t)d.n * ldl * sizeof(T));
   float *sum = d.dh && piece < d.v ? (float *)ar.take((size_t)d.n * d.d * 4) : nullptr;
   // partials of split products: of whole pieces and of the last one
-  size_t part_bytes = 0;
+  size_t part_bytes = 0, part_w_bytes = 0;
   const int64_t kd = pads(d) ? o.ld : d.d;
   for (const int64_t vc : {piece, last}) {
     const size_t l = mm_plan(d.n, vc, kd, d.dt).part_bytes;
     part_bytes = l > part_bytes ? l : part_bytes;
-    const size_t a = d.dh ? mm_plan(d.n, d.d, vc, d.dt).part_bytes : 0;
-    const size_t b = d.dw && !flip ? mm_plan(vc, d.d, d.n, d.dt).part_bytes : 0;
-    part_bytes = a > part_bytes ? a : part_bytes;
-    part_bytes = b > part_bytes ? b : part_bytes;
+    const MmTwo q = products(d, vc, flip);
+    part_bytes = q.a.part_bytes > part_bytes ? q.a.part_bytes : part_bytes;
+    part_w_bytes = q.b.part_bytes > part_w_bytes ? q.b.part_bytes : part_w_bytes;
   }
   float *part = part_bytes ? (float *)ar.take(part_bytes) : nullptr;
+  float *part_w = part_w_bytes ? (float *)ar.take(part_w_bytes) : nullptr;
   if (measure) return POETX_OK;
   for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
     const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
@@ -459,28 +464,28 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits");
     POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt), part,
                                     XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, scale, v0, d.v}, s)));
-    if (d.dh) {
-      MmDesc g;
-      g.M = d.n; g.N = d.d; g.K = vc; g.name = "xent_dh";
-      g.A = dl; g.lda = ldl; g.B = w; g.ldb = o.ld;
-      POETX_TRY((mm_run<T, false, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
-                                     XentDh<T>{sum, (T *)d.dh, scale, d.d, v0 == 0, v0 + vc == d.v}, s)));
+    const MmTwo q = products(d, vc, flip);
+    const XentDh<T> eh{sum, (T *)d.dh, scale, d.d, v0 == 0, v0 + vc == d.v};
+    const XentDw<T> ew{d.dw ? (T *)d.dw + v0 * d.d : nullptr, scale, d.d};
+    MmDesc gh, gw;
+    gh.M = d.n; gh.N = d.d; gh.K = vc; gh.name = "xent_dh";
+    gh.A = dl; gh.lda = ldl; gh.B = w; gh.ldb = o.ld;
+    gw.M = vc; gw.N = d.d; gw.K = d.n; gw.name = "xent_dw";
+    gw.A = dl; gw.lda = ldl; gw.B = hz; gw.ldb = o.ld;
+    if (q.pair) {
+      POETX_TRY(mm_run_pair<T>("xent_dh_dw", gh, q.a, part, eh, gw, q.b, part_w, ew, s));
+      continue;
     }
+    if (d.dh) POETX_TRY((mm_run<T, false, true>(gh, q.a, part, eh, s)));
     if constexpr (sizeof(T) == 2) {
       if (flip) {
         MmDesc g;
         g.M = d.d; g.N = vc; g.K = d.n; g.name = "xent_dw";
         g.A = hz; g.lda = ldt; g.B = dl; g.ldb = ldl;
-        POETX_TRY(mm_run_flipped(g, XentDw<T>{(T *)d.dw + v0 * d.d, scale, d.d}, s));
+        POETX_TRY(mm_run_flipped(g, ew, s));
       }
     }
-    if (d.dw && !flip) {
-      MmDesc g;
-      g.M = vc; g.N = d.d; g.K = d.n; g.name = "xent_dw";
-      g.A = dl; g.lda = ldl; g.B = hz; g.ldb = o.ld;
-      POETX_TRY((mm_run<T, true, true>(g, mm_plan(g.M, g.N, g.K, d.dt), part,
-                                    XentDw<T>{(T *)d.dw + v0 * d.d, scale, d.d}, s)));
-    }
+    if (d.dw && !flip) POETX_TRY((mm_run<T, true, true>(gw, q.b, part_w, ew, s)));
   }
   return POETX_OK;
 }
