@@ -642,18 +642,43 @@ struct MaybePart {
   }
 };
 
+// out[c] = sum over the parts [parts][cols], in a fixed order: C columns per workgroup, 16 threads
+// per column each summing every 16th part.
+struct SumArgs {
+  const float *part = nullptr;
+  int64_t parts = 0, cols = 0;
+  float *out = nullptr;
+};
+template <int C>
+__device__ inline void sum_parts_body(const SumArgs &a, int64_t id, float *red) {
+  const int c = threadIdx.x % C, q = threadIdx.x / C;
+  const int64_t col = id * C + c;
+  float s = 0.f;
+  if (col < a.cols)
+    for (int64_t p = q; p < a.parts; p += 16) s += a.part[p * a.cols + col];
+  red[q * C + c] = s;
+  __syncthreads();
+  if (q || col >= a.cols) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) s += red[i * C + c];
+  a.out[col] = s;
+}
+
 // The two products of a backward pass, D W (W k-major) and D^T X (both k-major), in one launch:
 // small ones fill the GPU together and wait for one launch and one fill instead of two.
 // 513 x 1001 x 777 float32: PAIRUS.  The first has workgroups [0, ga), ga a multiple of 8 so that
 // both deal their tiles to the XCDs alike.
 template <typename T, class EA, class EB>
-__global__ __launch_bounds__(256) void k_mm_pair(MmArgs a, EA ea, MmArgs b, EB eb, int ga) {
+__global__ __launch_bounds__(256) void k_mm_pair(MmArgs a, EA ea, MmArgs b, EB eb, SumArgs sum, int ga,
+                                                 int gb) {
   extern __shared__ __align__(16) bf16_t smem[];
   const int id = (int)blockIdx.x;
   if (id < ga) {
     if (id >= a.tiles_m * a.tiles_n * a.splits) return;
     if constexpr (sizeof(T) == 4) mm_f32_body<64, 32, false, true>(a, ea, id, (float *)smem);
     else mm_body<128, 128, 2, 2, false, true>(a, ea, id, smem);
+  } else if (id >= gb) {
+    sum_parts_body<16>(sum, id - gb, (float *)smem);
   } else {
     if constexpr (sizeof(T) == 4) mm_f32_body<64, 32, true, true>(b, eb, id - ga, (float *)smem);
     else mm_body<128, 128, 2, 2, true, true>(b, eb, id - ga, smem);
@@ -1025,9 +1050,10 @@ inline MmTwo mm_two(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, 
 // The pair of mm_run<T, false, true>(da, ..) and mm_run<T, true, true>(db, ..); plans with halves = 2.
 template <typename T, class EA, class EB>
 int mm_run_pair(const char *name, const MmDesc &da, const MmPlan &pa, float *part_a, const EA &ea, const MmDesc &db,
-                const MmPlan &pb, float *part_b, const EB &eb, hipStream_t s) {
+                const MmPlan &pb, float *part_b, const EB &eb, const SumArgs &sum, hipStream_t s) {
   const int64_t na = pa.tiles_m * pa.tiles_n * pa.splits, nb = pb.tiles_m * pb.tiles_n * pb.splits, ga = cdiv(na, 8) * 8;
-  if (ga + nb > kMaxTiles) return POETX_ERR_UNSUPPORTED;
+  const int64_t ns = cdiv(sum.cols, 16);
+  if (ga + nb + ns > kMaxTiles) return POETX_ERR_UNSUPPORTED;
   const MmArgs a{da.M, da.N, da.K, da.A, da.lda, da.B, da.ldb, (int)pa.tiles_m, (int)pa.tiles_n, (int)pa.splits, pa.kc};
   const MmArgs b{db.M, db.N, db.K, db.A, db.lda, db.B, db.ldb, (int)pb.tiles_m, (int)pb.tiles_n, (int)pb.splits, pb.kc};
   const bool sa = pa.splits > 1, sb = pb.splits > 1;
@@ -1035,9 +1061,9 @@ int mm_run_pair(const char *name, const MmDesc &da, const MmPlan &pa, float *par
   auto kern = &k_mm_pair<T, MaybePart<EA>, MaybePart<EB>>;
   static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
   POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
-  POETX_TRY(launch_k(name, s, kern, dim3((unsigned)(ga + nb)), dim3(256), lds, a,
+  POETX_TRY(launch_k(name, s, kern, dim3((unsigned)(ga + nb + ns)), dim3(256), lds, a,
                      MaybePart<EA>{ea, sa ? part_a : nullptr, da.N, da.M * da.N}, b,
-                     MaybePart<EB>{eb, sb ? part_b : nullptr, db.N, db.M * db.N}, (int)ga));
+                     MaybePart<EB>{eb, sb ? part_b : nullptr, db.N, db.M * db.N}, sum, (int)ga, (int)(ga + nb)));
   if (!sa && !sb) return POETX_OK;
   const unsigned ja = sa ? (unsigned)cdiv(da.M * cdiv(da.N, 8), 256) : 0, jb = sb ? (unsigned)cdiv(db.M * cdiv(db.N, 8), 256) : 0;
   return launch_k("mm_join", s, k_mm_join_pair<EA, EB>, dim3(ja + jb), dim3(256), 0, (const float *)part_a,

@@ -165,21 +165,9 @@ __global__ __launch_bounds__(256) void k_act_grad(const T *dy, const T *pre, int
       part[(int64_t)blockIdx.y * cols + c0 + i] = ((red[0][i] + red[1][i]) + red[2][i]) + red[3][i];
 }
 
-// out[c] = sum over the parts, in a fixed order: 64 columns per workgroup, 16 threads per
-// column each summing every 16th part.
-__global__ __launch_bounds__(1024) void k_sum_parts(const float *part, int64_t parts, int64_t cols, float *out) {
-  __shared__ float red[16][64];
-  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + c;
-  float s = 0.f;
-  if (col < cols)
-    for (int64_t p = q; p < parts; p += 16) s += part[p * cols + col];
-  red[q][c] = s;
-  __syncthreads();
-  if (q || col >= cols) return;
-#pragma unroll
-  for (int i = 1; i < 16; ++i) s += red[i][c];
-  out[col] = s;
+__global__ __launch_bounds__(1024) void k_sum_parts(SumArgs a) {
+  __shared__ float red[16 * 64];
+  sum_parts_body<64>(a, blockIdx.x, red);
 }
 
 template <typename T>
@@ -335,6 +323,7 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
     dpw = (T *)ar.take((size_t)d.n * ld * sizeof(T));
     dp = dpw;
   }
+  SumArgs sum;  // the bias gradient's partials
   if (copy || d.dbias) {
     const int64_t cb = cdiv(d.d_out, 512), cus = device_cus() > 0 ? device_cus() : 256;
     int64_t parts = cdiv(4 * cus, cb);
@@ -343,16 +332,19 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
     if (d.n <= 32) parts = 1;  // the column sums of few rows are whole at once: one launch less
     const bool join = d.dbias && (parts != 1 || d.n == 0);
     float *part = join ? (float *)ar.take((size_t)(parts > 0 ? parts : 1) * d.d_out * 4) : d.dbias;
-    if (!measure) {
-      if (d.n > 0)
-        POETX_TRY(launch_k("linear_act_grad", s, k_act_grad<T>, dim3((unsigned)cb, (unsigned)parts), dim3(256), 0,
-                           (const T *)d.dy, (const T *)d.saved_pre, d.act, d.n, d.d_out, dpw, ld, part));
-      if (join)
-        POETX_TRY(launch_k("linear_bias_grad", s, k_sum_parts, dim3((unsigned)cdiv(d.d_out, 64)), dim3(1024), 0,
-                           (const float *)part, d.n > 0 ? parts : (int64_t)0, d.d_out, d.dbias));
-    }
+    if (!measure && d.n > 0)
+      POETX_TRY(launch_k("linear_act_grad", s, k_act_grad<T>, dim3((unsigned)cb, (unsigned)parts), dim3(256), 0,
+                         (const T *)d.dy, (const T *)d.saved_pre, d.act, d.n, d.d_out, dpw, ld, part));
+    if (join) sum = {part, d.n > 0 ? parts : (int64_t)0, d.d_out, d.dbias};
   }
-  if (d.n == 0) return measure || !d.dw ? POETX_OK : fill_zero(d.dw, d.d_out * d.d_in, d.dt, s);
+  auto run_sum = [&] {
+    if (measure || !sum.out) return (int)POETX_OK;
+    return launch_k("linear_bias_grad", s, k_sum_parts, dim3((unsigned)cdiv(d.d_out, 64)), dim3(1024), 0, sum);
+  };
+  if (d.n == 0) {
+    POETX_TRY(run_sum());
+    return measure || !d.dw ? POETX_OK : fill_zero(d.dw, d.d_out * d.d_in, d.dt, s);
+  }
   const StoreEpi<T, LinTag> ex{(T *)d.dx, d.d_in, 0}, ew{(T *)d.dw, d.d_in, 0};
   MmDesc mx, mw;
   Packed w, x;
@@ -371,7 +363,9 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const MmPlan &px = two.a, &pw = two.b;
   float *part_x = px.part_bytes ? (float *)ar.take(px.part_bytes) : nullptr;
   float *part_w = pw.part_bytes ? (float *)ar.take(pw.part_bytes) : nullptr;
-  if (two.pair) return measure ? POETX_OK : mm_run_pair<T>("linear_dx_dw", mx, px, part_x, ex, mw, pw, part_w, ew, s);
+  if (two.pair)
+    return measure ? POETX_OK : mm_run_pair<T>("linear_dx_dw", mx, px, part_x, ex, mw, pw, part_w, ew, sum, s);
+  POETX_TRY(run_sum());
   if (!measure) {
     POETX_TRY((mm_run<T, false, true>(mx, px, part_x, ex, s)));
     POETX_TRY((mm_run<T, true, true>(mw, pw, part_w, ew, s)));

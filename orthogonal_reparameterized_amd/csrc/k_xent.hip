@@ -473,7 +473,7 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     gw.M = vc; gw.N = d.d; gw.K = d.n; gw.name = "xent_dw";
     gw.A = dl; gw.lda = ldl; gw.B = hz; gw.ldb = o.ld;
     if (q.pair) {
-      POETX_TRY(mm_run_pair<T>("xent_dh_dw", gh, q.a, part, eh, gw, q.b, part_w, ew, s));
+      POETX_TRY(mm_run_pair<T>("xent_dh_dw", gh, q.a, part, eh, gw, q.b, part_w, ew, {}, s));
       continue;
     }
     if (d.dh) POETX_TRY((mm_run<T, false, true>(gh, q.a, part, eh, s)));
