@@ -175,20 +175,26 @@ __global__ __launch_bounds__(256) void k_fill_zero(T *out, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) out[i] = 0;
 }
 
-// Rows copied to a stride of ld_out elements (a multiple of 8), zero past cols; rows whose
-// target lies outside [0, vocab) zero.
+// The copies of a list; job k has workgroups [end[k - 1], end[k]).  Rows are walked with that range's
+// stride.
+struct PackArgs {
+  PackJob j[3];
+  int end[3];
+};
 template <typename T>
-__global__ __launch_bounds__(256) void k_pack_rows(const T *in, int64_t rows, int64_t cols, T *out, int64_t ld_out,
-                                                   const int32_t *target, int64_t vocab) {
-  const int64_t cpr = cdiv(ld_out, 8), total = rows * cpr;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void k_pack_rows(PackArgs a) {
+  const int id = (int)blockIdx.x, k = id < a.end[0] ? 0 : id < a.end[1] ? 1 : 2;
+  const int begin = k == 0 ? 0 : k == 1 ? a.end[0] : a.end[1], groups = (k == 0 ? a.end[0] : k == 1 ? a.end[1] : a.end[2]) - begin;
+  const PackJob p = k == 0 ? a.j[0] : k == 1 ? a.j[1] : a.j[2];
+  const int64_t cpr = cdiv(p.ld_out, 8), total = p.rows * cpr;
+  for (int64_t i = (int64_t)(id - begin) * 256 + threadIdx.x; i < total; i += (int64_t)groups * 256) {
     // a 32-bit division where it reaches (a 64-bit one is a long sequence)
     const int64_t r = total <= 0xffffffff ? (int64_t)((uint32_t)i / (uint32_t)cpr) : i / cpr;
-    const int64_t c = (i - r * cpr) * 8, left = cols - c;
+    const int64_t c = (i - r * cpr) * 8, left = p.cols - c;
     float v[8] = {};
-    const bool keep = !target || (target[r] >= 0 && target[r] < vocab);
-    if (keep) load8(in + r * cols + c, left >= 8 ? 8 : left > 0 ? (int)left : 0, v);
-    store8(out + r * ld_out + c, ld_out - c >= 8 ? 8 : (int)(ld_out - c), v);
+    const bool keep = !p.target || (p.target[r] >= 0 && p.target[r] < p.vocab);
+    if (keep) load8((const T *)p.in + r * p.cols + c, left >= 8 ? 8 : left > 0 ? (int)left : 0, v);
+    store8((T *)p.out + r * p.ld_out + c, p.ld_out - c >= 8 ? 8 : (int)(p.ld_out - c), v);
   }
 }
 
@@ -236,15 +242,20 @@ static dim3 stride_grid(int64_t n) {
   return dim3((unsigned)(g < 65536 ? g : 65536));
 }
 
-int pack_rows(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
-              int64_t vocab, int dt, hipStream_t s) {
-  if (rows == 0) return POETX_OK;
-  const dim3 grid = stride_grid(rows * cdiv(ld_out, 8));
-  if (dt == POETX_F32)
-    return launch_k("pack_rows", s, k_pack_rows<float>, grid, dim3(256), 0, (const float *)in, rows, cols,
-                    (float *)out, ld_out, target, vocab);
-  return launch_k("pack_rows", s, k_pack_rows<bf16_t>, grid, dim3(256), 0, (const bf16_t *)in, rows, cols,
-                  (bf16_t *)out, ld_out, target, vocab);
+int pack_rows(PackList &l, int dt, hipStream_t s) {
+  if (l.n == 0) return POETX_OK;
+  PackArgs a = {};
+  int end = 0;
+  for (int k = 0; k < 3; ++k) {
+    if (k < l.n) {
+      a.j[k] = l.j[k];
+      end += (int)stride_grid(l.j[k].rows * cdiv(l.j[k].ld_out, 8)).x;
+    }
+    a.end[k] = end;
+  }
+  l.n = 0;
+  if (dt == POETX_F32) return launch_k("pack_rows", s, k_pack_rows<float>, dim3((unsigned)end), dim3(256), 0, a);
+  return launch_k("pack_rows", s, k_pack_rows<bf16_t>, dim3((unsigned)end), dim3(256), 0, a);
 }
 
 int pack_rows_t(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
@@ -273,14 +284,14 @@ struct Packed {
   const void *p = nullptr;
   int64_t ld = 0;
 };
-int packed(const void *in, int64_t rows, int64_t cols, int dt, Arena &ar, bool measure, hipStream_t s, Packed &o) {
-  o.p = in;
-  o.ld = cols;
-  if (dt == POETX_F32 || cols % 8 == 0) return POETX_OK;
+Packed packed(const void *in, int64_t rows, int64_t cols, int dt, Arena &ar, PackList &l) {
+  Packed o{in, cols};
+  if (dt == POETX_F32 || cols % 8 == 0) return o;
   o.ld = round8(cols);
   void *q = ar.take((size_t)rows * o.ld * 2);
   o.p = q;
-  return measure ? POETX_OK : pack_rows(in, rows, cols, q, o.ld, nullptr, 0, dt, s);
+  l.add({in, rows, cols, q, o.ld, nullptr, 0});
+  return o;
 }
 
 template <typename T>
@@ -298,14 +309,14 @@ int fwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
     if (B16 && d.d_in % 2) kern = two ? k_mm_few<T, 2, B16, LinEpi<T>> : k_mm_few<T, 1, B16, LinEpi<T>>;
     return launch_k(m.name, s, kern, dim3((unsigned)(two ? cdiv(groups, 2) : groups)), dim3(512), 0, a, epi);
   }
-  Packed x, w;
-  POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));
-  POETX_TRY(packed(d.w, d.d_out, d.d_in, d.dt, ar, measure, s, w));
+  PackList l;
+  const Packed x = packed(d.x, d.n, d.d_in, d.dt, ar, l), w = packed(d.w, d.d_out, d.d_in, d.dt, ar, l);
   m.A = x.p; m.lda = x.ld; m.B = w.p; m.ldb = w.ld;
   if (d.dt == POETX_BF16) m.K = round8(d.d_in);  // the padding is zero
   const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
   float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
   if (measure) return POETX_OK;
+  POETX_TRY(pack_rows(l, d.dt, s));
   return mm_run<T, false, false>(m, p, part, epi, s);
 }
 
@@ -347,15 +358,15 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   }
   const StoreEpi<T, LinTag> ex{(T *)d.dx, d.d_in, 0}, ew{(T *)d.dw, d.d_in, 0};
   MmDesc mx, mw;
-  Packed w, x;
+  PackList l;
   if (d.dx) {
-    POETX_TRY(packed(d.w, d.d_out, d.d_in, d.dt, ar, measure, s, w));
+    const Packed w = packed(d.w, d.d_out, d.d_in, d.dt, ar, l);
     mx.M = d.n; mx.N = d.d_in; mx.K = d.d_out; mx.name = "linear_dx";
     mx.A = dp; mx.lda = ld; mx.B = w.p; mx.ldb = w.ld;
   }
   const bool flip = b16 && d.dw && dw_flips(d.d_out, d.d_in, d.n, d.dt);
   if (d.dw && !flip) {
-    POETX_TRY(packed(d.x, d.n, d.d_in, d.dt, ar, measure, s, x));
+    const Packed x = packed(d.x, d.n, d.d_in, d.dt, ar, l);
     mw.M = d.d_out; mw.N = d.d_in; mw.K = d.n; mw.name = "linear_dw";
     mw.A = dp; mw.lda = ld; mw.B = x.p; mw.ldb = x.ld;
   }
@@ -363,6 +374,7 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const MmPlan &px = two.a, &pw = two.b;
   float *part_x = px.part_bytes ? (float *)ar.take(px.part_bytes) : nullptr;
   float *part_w = pw.part_bytes ? (float *)ar.take(pw.part_bytes) : nullptr;
+  if (!measure) POETX_TRY(pack_rows(l, d.dt, s));
   if (two.pair)
     return measure ? POETX_OK : mm_run_pair<T>("linear_dx_dw", mx, px, part_x, ex, mw, pw, part_w, ew, sum, s);
   POETX_TRY(run_sum());

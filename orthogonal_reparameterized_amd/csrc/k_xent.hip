@@ -388,23 +388,25 @@ struct Operands {
   int64_t ld = 0;
   void *wp = nullptr;  // one padded piece of W
 };
-int operands(const XentDesc &d, int64_t piece, Arena &ar, bool measure, hipStream_t s, Operands &o) {
-  o.h = d.h;
-  o.ld = d.d;
-  if (!pads(d)) return POETX_OK;
+Operands operands(const XentDesc &d, int64_t piece, Arena &ar, PackList &l) {
+  Operands o{d.h, d.d, nullptr};
+  if (!pads(d)) return o;
   o.ld = round8(d.d);
   void *hp = ar.take((size_t)d.n * o.ld * 2);
   o.wp = ar.take((size_t)piece * o.ld * 2);
   o.h = hp;
-  return measure ? POETX_OK : pack_rows(d.h, d.n, d.d, hp, o.ld, nullptr, 0, d.dt, s);
+  l.add({d.h, d.n, d.d, hp, o.ld, nullptr, 0});
+  return o;
 }
-int w_piece(const XentDesc &d, const Operands &o, int64_t v0, int64_t vc, hipStream_t s, const void **w) {
+// The piece of W from v0 on, after the copies still to be made (h's, before the first piece).
+int w_piece(const XentDesc &d, const Operands &o, int64_t v0, int64_t vc, PackList &l, hipStream_t s, const void **w) {
   const int64_t es = d.dt == POETX_F32 ? 4 : 2;
   *w = (const char *)d.w + v0 * d.d * es;
-  if (!o.wp) return POETX_OK;
-  POETX_TRY(pack_rows(*w, vc, d.d, o.wp, o.ld, nullptr, 0, d.dt, s));
-  *w = o.wp;
-  return POETX_OK;
+  if (o.wp) {
+    l.add({*w, vc, d.d, o.wp, o.ld, nullptr, 0});
+    *w = o.wp;
+  }
+  return pack_rows(l, d.dt, s);
 }
 
 MmDesc logits_desc(const XentDesc &d, const Operands &o, const void *w, int64_t vc, const char *name) {
@@ -422,8 +424,8 @@ MmTwo products(const XentDesc &d, int64_t vc, bool flip) {
 template <typename T>
 int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const int64_t piece = piece_of(d);
-  Operands o;
-  POETX_TRY(operands(d, piece, ar, measure, s, o));
+  PackList l;
+  const Operands o = operands(d, piece, ar, l);
   // dW reads h with the rows that take no part as zeros: their dl is zero, but zero times an
   // infinity or a NaN in such a row would not be.  The copy is transposed where the product's
   // kernel gains by it.
@@ -433,10 +435,8 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   void *hz = nullptr;
   if (d.dw) {
     hz = ar.take((flip ? (size_t)d.d * ldt : (size_t)d.n * o.ld) * sizeof(T));
-    if (!measure) {
-      if (flip) POETX_TRY(pack_rows_t(d.h, d.n, d.d, hz, ldt, d.target, d.v, s));
-      else POETX_TRY(pack_rows(d.h, d.n, d.d, hz, o.ld, d.target, d.v, d.dt, s));
-    }
+    if (!flip) l.add({d.h, d.n, d.d, hz, o.ld, d.target, d.v});
+    else if (!measure) POETX_TRY(pack_rows_t(d.h, d.n, d.d, hz, ldt, d.target, d.v, s));
   }
   float *scale = sizeof(T) == 2 ? (float *)ar.take(4) : nullptr;
   if (scale && !measure)
@@ -460,7 +460,7 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
     const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
     const void *w = nullptr;
-    POETX_TRY(w_piece(d, o, v0, vc, s, &w));
+    POETX_TRY(w_piece(d, o, v0, vc, l, s, &w));
     const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits");
     POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt), part,
                                     XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, scale, v0, d.v}, s)));
@@ -518,8 +518,8 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
                        XentStats{part, d.target, at, 0, 0}));
   } else {
     const int64_t piece = pads(d) ? piece_of(d) : d.v;
-    Operands o;
-    POETX_TRY(operands(d, piece, ar, measure, s, o));
+    PackList l;
+    const Operands o = operands(d, piece, ar, l);
     // one row of statistics per n-tile of every piece (pieces are multiples of the tile width;
     // 256 columns where the product is split over k)
     const int64_t kd = pads(d) ? o.ld : d.d;
@@ -537,7 +537,7 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     for (int64_t v0 = 0; v0 < d.v; v0 += piece) {
       const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
       const void *w = nullptr;
-      POETX_TRY(w_piece(d, o, v0, vc, s, &w));
+      POETX_TRY(w_piece(d, o, v0, vc, l, s, &w));
       const MmDesc m = logits_desc(d, o, w, vc, "xent_fwd");
       const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt, true, false);
       const XentStats epi{part, d.target, at, v0, (int)t0};

@@ -235,10 +235,23 @@ struct LinDesc {
 // With measure == true only the workspace is carved (nothing is launched).
 int linear_forward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s);
 int linear_backward(const LinDesc &d, Arena &ar, bool measure, hipStream_t s);
-// out[r][c] = in[r][c] for c < cols, 0 up to ld_out, for bf16 rows; with `target`, rows
-// whose target lies outside [0, vocab) become zero
-int pack_rows(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
-              int64_t vocab, int dt, hipStream_t s);
+// Copies of rows: out[r][c] = in[r][c] for c < cols, 0 up to ld_out (for bf16 a multiple of 8); with
+// `target`, rows whose target lies outside [0, vocab) become zero.  pack_rows makes those of a list
+// in one launch and empties it.
+struct PackJob {
+  const void *in;
+  int64_t rows, cols;
+  void *out;
+  int64_t ld_out;
+  const int32_t *target;
+  int64_t vocab;
+};
+struct PackList {
+  PackJob j[3];
+  int n = 0;
+  void add(const PackJob &p) { if (p.rows > 0) j[n++] = p; }
+};
+int pack_rows(PackList &l, int dt, hipStream_t s);
 // out[c][r] = in[r][c] (bf16 [rows][cols] -> [cols][ld_out], ld_out >= rows a multiple of 8, zero
 // past rows); `target` as above
 int pack_rows_t(const void *in, int64_t rows, int64_t cols, void *out, int64_t ld_out, const int32_t *target,
