@@ -1041,7 +1041,7 @@ inline MmTwo mm_two(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, 
   const double longest = (b16 ? 0.94 : 0.83) * (steps(a) > steps(b) ? steps(a) : steps(b));
   const double shared = 1.1 * (b16 ? 0.47 : 0.55) * ((double)wgs(a) * steps(a) + (double)wgs(b) * steps(b)) / cus;
   const double both = (longest > shared ? longest : shared) + (a.splits > 1 || b.splits > 1 ? 6 : 0);
-  if (both > alone(t.a) + alone(t.b) + 5) return t;
+  if (both > alone(t.a) + alone(t.b) + 5 || wgs(a) + wgs(b) > kMaxTiles / 2) return t;  // one grid holds both
   t.a = a;
   t.b = b;
   t.pair = true;
