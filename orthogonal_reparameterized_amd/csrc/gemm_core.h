@@ -538,7 +538,8 @@ __device__ inline void mm_f32_body(const MmArgs &a, const Epi &epi, int id, floa
 #pragma unroll
     for (int i = 0; i < PC; ++i) {
       const int e = tid + 256 * i;
-      off[i] = km ? (int)((e / (BT / 4) * ld + e % (BT / 4) * 4) * 4) : (int)((e / (BK / 4) * ld + e % (BK / 4) * 4) * 4);
+      off[i] = km ? (int)((e / (BT / 4) * ld + e % (BT / 4) * 4) * 4)
+                  : (int)((e / (BK / 4) * ld + e % (BK / 4) * 4) * 4);
     }
   };
   auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int t, const int (&off)[PC],
@@ -549,7 +550,8 @@ __device__ inline void mm_f32_body(const MmArgs &a, const Epi &epi, int id, floa
         km ? make_rsrc(P + (kbeg + (int64_t)t * BK) * ld + r0, ((left < BK ? left : BK) * ld - r0) * 4)
            : make_rsrc(P + r0 * ld + kbeg + (int64_t)t * BK, (nr * ld - kbeg - (int64_t)t * BK) * 4);
 #pragma unroll
-    for (int i = 0; i < PC; ++i) v[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off[i], 0, 0));
+    for (int i = 0; i < PC; ++i)
+      v[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off[i], 0, 0));
     if (!km && left < BK) {
 #pragma unroll
       for (int i = 0; i < PC; ++i)
@@ -908,6 +910,8 @@ inline void plan_f32(int64_t M, int64_t N, int64_t K, int64_t cus, int halves, b
 //     768 x 3000 x 16384 80 -> 77; 2048 x 2048 x 8192, ranges of 2048, equal), or of 1792 where 128 x
 //     128 ones load the CUs unevenly (weights not in the caches: 190 x 17792 x 5384 128 -> 76 us, 512 x
 //     14336 x 4096 77 -> 66; ranges of 1024, 384 x 16000 x 2048, 40 -> 43).
+// may_split, may_share: whether k may be split, the last round's tiles shared.  halves = 2: k is split
+// as for half the GPU, which another product fills at the same time.
 inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = true, bool may_share = true,
                       int halves = 1) {
   MmPlan p;
@@ -1051,7 +1055,8 @@ inline MmTwo mm_two(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, 
 template <typename T, class EA, class EB>
 int mm_run_pair(const char *name, const MmDesc &da, const MmPlan &pa, float *part_a, const EA &ea, const MmDesc &db,
                 const MmPlan &pb, float *part_b, const EB &eb, const SumArgs &sum, hipStream_t s) {
-  const int64_t na = pa.tiles_m * pa.tiles_n * pa.splits, nb = pb.tiles_m * pb.tiles_n * pb.splits, ga = cdiv(na, 8) * 8;
+  const int64_t na = pa.tiles_m * pa.tiles_n * pa.splits, nb = pb.tiles_m * pb.tiles_n * pb.splits;
+  const int64_t ga = cdiv(na, 8) * 8;
   const int64_t ns = cdiv(sum.cols, 16);
   if (ga + nb + ns > kMaxTiles) return POETX_ERR_UNSUPPORTED;
   const MmArgs a{da.M, da.N, da.K, da.A, da.lda, da.B, da.ldb, (int)pa.tiles_m, (int)pa.tiles_n, (int)pa.splits, pa.kc};
@@ -1065,7 +1070,8 @@ int mm_run_pair(const char *name, const MmDesc &da, const MmPlan &pa, float *par
                      MaybePart<EA>{ea, sa ? part_a : nullptr, da.N, da.M * da.N}, b,
                      MaybePart<EB>{eb, sb ? part_b : nullptr, db.N, db.M * db.N}, sum, (int)ga, (int)(ga + nb)));
   if (!sa && !sb) return POETX_OK;
-  const unsigned ja = sa ? (unsigned)cdiv(da.M * cdiv(da.N, 8), 256) : 0, jb = sb ? (unsigned)cdiv(db.M * cdiv(db.N, 8), 256) : 0;
+  const unsigned ja = sa ? (unsigned)cdiv(da.M * cdiv(da.N, 8), 256) : 0;
+  const unsigned jb = sb ? (unsigned)cdiv(db.M * cdiv(db.N, 8), 256) : 0;
   return launch_k("mm_join", s, k_mm_join_pair<EA, EB>, dim3(ja + jb), dim3(256), 0, (const float *)part_a,
                   (int)pa.splits, da.M, da.N, ea, (const float *)part_b, (int)pb.splits, db.M, db.N, eb, (uint32_t)ja);
 }

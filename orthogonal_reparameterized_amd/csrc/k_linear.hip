@@ -184,7 +184,8 @@ struct PackArgs {
 template <typename T>
 __global__ __launch_bounds__(256) void k_pack_rows(PackArgs a) {
   const int id = (int)blockIdx.x, k = id < a.end[0] ? 0 : id < a.end[1] ? 1 : 2;
-  const int begin = k == 0 ? 0 : k == 1 ? a.end[0] : a.end[1], groups = (k == 0 ? a.end[0] : k == 1 ? a.end[1] : a.end[2]) - begin;
+  const int begin = k == 0 ? 0 : k == 1 ? a.end[0] : a.end[1];
+  const int groups = (k == 0 ? a.end[0] : k == 1 ? a.end[1] : a.end[2]) - begin;
   const PackJob p = k == 0 ? a.j[0] : k == 1 ? a.j[1] : a.j[2];
   const int64_t cpr = cdiv(p.ld_out, 8), total = p.rows * cpr;
   for (int64_t i = (int64_t)(id - begin) * 256 + threadIdx.x; i < total; i += (int64_t)groups * 256) {

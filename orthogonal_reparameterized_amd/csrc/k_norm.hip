@@ -25,7 +25,7 @@ struct NormArgs {
   int64_t n, d;
   const void *x, *dy, *dres;
   ParamVec gamma, beta;  // p null: gamma = 1, beta = 0
-  float eps, fd;          // fd: d, by which sums are divided (a product by 1 / d would not give a constant row its mean)
+  float eps, fd;         // fd: d, the divisor (a product by 1 / d would not give a constant row its mean)
   void *out;             // y or dx
   float *mean, *rstd;    // written by the forward (nullable), read by the backward
   float *part;           // [grid][2][d] partial dgamma, dbeta (nullable)
