@@ -16,25 +16,39 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhC = 0.79788456080286536f, kTanhA = 0.044715f;  // sqrt(2 / pi)
 
 // The activations run on every result of a product's epilogue, where the matrix cores wait for
-// them: one hardware exp and one reciprocal each (both to about 1 ulp), not the library's erf
-// and tanh (whose epilogue took 31 us of a 130 us round of 256 x 256 tiles, k = 4096; 8192
-// tokens, 4096 -> 14336 with GELU and the kept pre-activation: 904 us then, 733 us now).
-
-__device__ inline float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
-
-// Phi(p) = erfc(-p / sqrt 2) / 2 by Abramowitz and Stegun's formula 7.1.26 (erf to 1.5e-7):
-// erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0; e: exp(-p^2 / 2).
-__device__ inline float normal_cdf(float p, float e) {
-  const float x = fabsf(p) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  q *= 0.5f * t * e;
-  return p < 0.f ? q : 1.f - q;
-}
+// them.  bf16: one hardware exp and one reciprocal each (relative errors of about 2^-22, and of
+// 2^-24 of exp's argument, far below the rounding of the result), not the library's erf and tanh
+// (whose epilogue took 31 us of a 130 us round of 256 x 256 tiles, k = 4096; 8192 tokens, 4096 ->
+// 14336 with GELU and the kept pre-activation: 904 us then, 733 us now).  float32, whose products
+// run at a tenth of the rate: the library's functions, a few units in the last place (2048 tokens,
+// 1024 -> 4096 with GELU 159 us, 155 us with the forms for bf16).
+template <typename T> struct Fn;
+template <> struct Fn<bf16_t> {
+  static __device__ inline float exp(float x) { return __expf(x); }
+  static __device__ inline float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+  // Phi(p) = erfc(-p / sqrt 2) / 2, with erfc(x) exp(x^2) / 2 for x >= 0 as a polynomial in t =
+  // 1 / (1 + 0.51 x) without a constant term: a fit of least largest relative error over x <= 10,
+  // 1.2e-6 in float32, so that far negative p keep their digits too; e: exp(-p^2 / 2).
+  static __device__ inline float normal_cdf(float p, float e) {
+    const float x = fabsf(p) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(fmaf(0.51f, x, 1.f));
+    float q = fmaf(t, 0.0472500883f, -0.17956777f);
+    q = fmaf(t, q, 0.179223239f);
+    q = fmaf(t, q, 0.0275261737f);
+    q = fmaf(t, q, 0.139533147f);
+    q = fmaf(t, q, 0.14207615f);
+    q = fmaf(t, q, 0.143958747f);
+    q *= t * e;
+    return p < 0.f ? q : 1.f - q;
+  }
+};
+template <> struct Fn<float> {
+  static __device__ inline float exp(float x) { return expf(x); }
+  static __device__ inline float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+  static __device__ inline float normal_cdf(float p, float) { return 0.5f * erfcf(-0.70710678118654752f * p); }
+};
 
 // v = act(v); one branch for the eight
+template <typename T>
 __device__ inline void act_values(float (&v)[8], int act) {
   switch (act) {
     case POETX_ACT_RELU:
@@ -43,21 +57,22 @@ __device__ inline void act_values(float (&v)[8], int act) {
       break;
     case POETX_ACT_GELU:
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= normal_cdf(v[e], __expf(-0.5f * v[e] * v[e]));
+      for (int e = 0; e < 8; ++e) v[e] *= Fn<T>::normal_cdf(v[e], Fn<T>::exp(-0.5f * v[e] * v[e]));
       break;
     case POETX_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2 u)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= sigmoid(2.f * kTanhC * (v[e] + kTanhA * v[e] * v[e] * v[e]));
+      for (int e = 0; e < 8; ++e) v[e] *= Fn<T>::sigmoid(2.f * kTanhC * (v[e] + kTanhA * v[e] * v[e] * v[e]));
       break;
     case POETX_ACT_SILU:
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= sigmoid(v[e]);
+      for (int e = 0; e < 8; ++e) v[e] *= Fn<T>::sigmoid(v[e]);
       break;
     default: break;
   }
 }
 
 // v *= act'(p)
+template <typename T>
 __device__ inline void act_slopes(float (&v)[8], const float (&p)[8], int act) {
   switch (act) {
     case POETX_ACT_RELU:
@@ -67,8 +82,8 @@ __device__ inline void act_slopes(float (&v)[8], const float (&p)[8], int act) {
     case POETX_ACT_GELU:
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = __expf(-0.5f * p[e] * p[e]);
-        v[e] *= normal_cdf(p[e], d) + p[e] * kInvSqrt2Pi * d;
+        const float d = Fn<T>::exp(-0.5f * p[e] * p[e]);
+        v[e] *= Fn<T>::normal_cdf(p[e], d) + p[e] * kInvSqrt2Pi * d;
       }
       break;
     case POETX_ACT_GELU_TANH:
@@ -77,14 +92,14 @@ __device__ inline void act_slopes(float (&v)[8], const float (&p)[8], int act) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float q = p[e] < -20.f ? -20.f : p[e] > 20.f ? 20.f : p[e];
-        const float g = sigmoid(2.f * kTanhC * (q + kTanhA * q * q * q));
+        const float g = Fn<T>::sigmoid(2.f * kTanhC * (q + kTanhA * q * q * q));
         v[e] *= g + q * g * (1.f - g) * 2.f * kTanhC * (1.f + 3.f * kTanhA * q * q);
       }
       break;
     case POETX_ACT_SILU:
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float g = sigmoid(p[e]);
+        const float g = Fn<T>::sigmoid(p[e]);
         v[e] *= g * (1.f + p[e] * (1.f - g));
       }
       break;
@@ -116,7 +131,7 @@ struct LinEpi {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += c.b[e];
     if (pre) store8(pre + o, nv, v);
-    act_values(v, act);
+    act_values<T>(v, act);
     if (res) {
       float r[8];
       load8(res + o, nv, r);
@@ -149,7 +164,7 @@ __global__ __launch_bounds__(256) void k_act_grad(const T *dy, const T *pre, int
     if (act != POETX_ACT_NONE) {
       float p[8];
       load8(pre + r * cols + c, nv, p);
-      act_slopes(v, p, act);  // past nv: zero times a finite slope
+      act_slopes<T>(v, p, act);  // past nv: zero times a finite slope
     }
     // ld_out is a multiple of 8, so a partly valid group is stored whole, with its zeros
     if (dp && nv) store8(dp + r * ld_out + c, ld_out == cols ? nv : 8, v);

@@ -715,3 +715,55 @@ def test_as_many_tokens_as_there_are_tiles_for(B, dtype):
     assert torch.equal(y[:, 0], x[:, 3] * 2)  # exact in both types
     dx = B.poetx_linear_backward(None, w, y, want_dw=False, want_dbias=False)["dx"]
     assert torch.equal(dx[:, 3], y[:, 0] * 2) and not dx[:, 4].any()
+
+
+def act_errors(p, act, dtype):
+    """Bounds of an activation's and its slope's own errors at p (float64), from their steps.
+    float32: the library's functions (exp and erfc to 4 units of 2^-24 and 8), divisions to 5, the
+    rest one 2^-24 per operation.  bf16: hardware exp2 and reciprocal (2 units of 2^-24 each, exp's
+    argument times log2 e another 1.5 2^-24 of it) and a polynomial to 2^-19."""
+    e = 2.0 ** -24
+    fast = dtype == BF16
+    one = torch.ones_like(p)
+    if act == "gelu":
+        cdf, pdf = torch.special.erfc(-p * 0.5 ** 0.5) / 2, torch.exp(-p * p / 2) / (2 * np.pi) ** 0.5
+        # the argument's rounding counts p^2 + 1 fold in erfc, p^2 / 2 fold in exp(-p^2 / 2)
+        d_cdf = 2.0 ** -19 + 8 * e + 1.25 * e * p * p if fast else e * (1.5 * (p * p + 1) + 9)
+        d_pdf = e * (1.25 * p * p + 7) if fast else e * (p * p / 2 + 7)
+        slope = cdf * (d_cdf + e) + p.abs() * pdf * (d_pdf + 2 * e)
+        return (p * cdf).abs() * (d_cdf + e), slope
+    if act == "silu":
+        u, du = p, one
+        d = e * (1.5 * p.abs() * fast + 11)
+    else:
+        c = (2 / np.pi) ** 0.5
+        u, du = 2 * c * (p + 0.044715 * p ** 3), 2 * c * (1 + 3 * 0.044715 * p * p)
+        d = e * ((7 + 1.5 * fast) * u.abs() + 11)
+    g = torch.sigmoid(u)
+    rest = (1 - g) * d + g * d + e  # of 1 - g, which is a difference, and of its factor g
+    return (p * g).abs() * (d + e), g * d + 2 * e * g + p.abs() * du * g * (rest + 8 * e * (1 - g))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_activations_keep_their_digits(B, act, dtype):
+    """Values and slopes of the activations alone, element by element, far into the negative
+    tail: weights of 1 make p the input itself.  (f32: errors relative to the value, not to p.)"""
+    p = torch.linspace(-11, 11, 5001, dtype=torch.float64).to(dtype)[:, None].contiguous()
+    w = torch.ones(1, 1, dtype=dtype)
+    pd = p.double()
+    v, slope = act_ref(pd, act)
+    if act == "gelu":  # 1 + erf and 1 + tanh cancel in the tail, even in 64 bits
+        cdf = torch.special.erfc(-pd * 0.5 ** 0.5) / 2
+        v, slope = pd * cdf, cdf + pd * torch.exp(-pd * pd / 2) / (2 * np.pi) ** 0.5
+    if act == "gelu_tanh":
+        c = (2 / np.pi) ** 0.5
+        g, less = (torch.sigmoid(s * 2 * c * (pd + 0.044715 * pd ** 3)) for s in (1, -1))
+        v, slope = pd * g, g + pd * g * less * 2 * c * (1 + 3 * 0.044715 * pd * pd)
+    e_v, e_s = act_errors(pd, act, dtype)
+    for rows in (slice(None), slice(0, 16), slice(700, 716)):
+        y, _ = B.poetx_linear_forward(dev(p[rows]), dev(w), act=act)
+        within(y, v[rows], U[dtype] * v[rows].abs() + 1.01 * e_v[rows], f"{act} {rows}")
+    one = torch.ones_like(p)
+    got = B.poetx_linear_backward(dev(p), dev(w), dev(one), dev(p), act, want_dw=False)
+    within(got["dx"], slope, U[dtype] * slope.abs() + 1.01 * e_s, f"slope of {act}")
