@@ -334,35 +334,39 @@ __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
   }
 }
 
-// lse and loss from the partials [tiles][n]: C rows per workgroup of 256, 256 / C threads per
-// row (16 rows read whole 128-byte lines; few rows take all threads each).
+// lse and loss from the partials [tiles][n]: C rows per turn of a workgroup of 256, 256 / C threads
+// per row (16 rows read whole 128-byte lines; few rows take all threads each).  The grid is capped
+// and walks the rows: one workgroup per 16 of 2^28 rows would be more than a grid holds.
 template <int C>
 __global__ __launch_bounds__(256) void k_xent_join(const float2 *part, int64_t tiles, int64_t n, const int32_t *target,
                                                    int64_t vocab, const float *at_target, float *loss, float *lse) {
   constexpr int Q = 256 / C;
   __shared__ float2 red[Q][C];
   const int c = threadIdx.x % C, q = threadIdx.x / C;
-  const int64_t row = (int64_t)blockIdx.x * C + c;
-  float m = -INFINITY, s = 0.f;
-  if (row < n)
-    for (int64_t t = q; t < tiles; t += Q) {
-      const float2 p = part[t * n + row];
-      join_stats(m, s, p.x, p.y);
-    }
-  red[q][c] = make_float2(m, s);
+  for (int64_t row0 = (int64_t)blockIdx.x * C; row0 < n; row0 += (int64_t)gridDim.x * C) {
+    const int64_t row = row0 + c;
+    float m = -INFINITY, s = 0.f;
+    if (row < n)
+      for (int64_t t = q; t < tiles; t += Q) {
+        const float2 p = part[t * n + row];
+        join_stats(m, s, p.x, p.y);
+      }
+    __syncthreads();  // the turn before has been read
+    red[q][c] = make_float2(m, s);
 #pragma unroll
-  for (int o = Q / 2; o; o >>= 1) {
-    __syncthreads();
-    if (q < o) {
-      join_stats(m, s, red[q + o][c].x, red[q + o][c].y);
-      red[q][c] = make_float2(m, s);
+    for (int o = Q / 2; o; o >>= 1) {
+      __syncthreads();
+      if (q < o) {
+        join_stats(m, s, red[q + o][c].x, red[q + o][c].y);
+        red[q][c] = make_float2(m, s);
+      }
     }
+    if (q || row >= n) continue;
+    const float z = safe_ref(m) + logf(s);
+    lse[row] = z;
+    const int32_t t = target[row];
+    loss[row] = t >= 0 && t < vocab ? z - at_target[row] : 0.f;
   }
-  if (q || row >= n) return;
-  const float z = safe_ref(m) + logf(s);
-  lse[row] = z;
-  const int32_t t = target[row];
-  loss[row] = t >= 0 && t < vocab ? z - at_target[row] : 0.f;
 }
 
 namespace {
@@ -551,8 +555,9 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
   if (d.n <= 256)
     return launch_k("xent_join", s, k_xent_join<1>, dim3((unsigned)d.n), dim3(256), 0, (const float2 *)part, tiles,
                     d.n, d.target, d.v, (const float *)at, d.loss, d.lse);
-  return launch_k("xent_join", s, k_xent_join<16>, dim3((unsigned)cdiv(d.n, 16)), dim3(256), 0, (const float2 *)part,
-                  tiles, d.n, d.target, d.v, (const float *)at, d.loss, d.lse);
+  const int64_t turns = cdiv(d.n, 16);
+  return launch_k("xent_join", s, k_xent_join<16>, dim3((unsigned)(turns < 65536 ? turns : 65536)), dim3(256), 0,
+                  (const float2 *)part, tiles, d.n, d.target, d.v, (const float *)at, d.loss, d.lse);
 }
 
 }  // namespace

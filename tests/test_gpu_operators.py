@@ -767,3 +767,36 @@ def test_activations_keep_their_digits(B, act, dtype):
     one = torch.ones_like(p)
     got = B.poetx_linear_backward(dev(p), dev(w), dev(one), dev(p), act, want_dw=False)
     within(got["dx"], slope, U[dtype] * slope.abs() + 1.01 * e_s, f"slope of {act}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_xent_of_more_than_2_28_tokens(B, dtype):
+    """More tokens than a grid has workgroups of 16 for: losses and dh of a batch that repeats
+    753 rows."""
+    n, d, v, period = 753 * 356500, 4, 3, 753
+    assert n > 1 << 28
+    h, w = rand(360, period, d, dtype=dtype), rand(361, v, d, dtype=dtype)
+    t = torch.arange(period, dtype=torch.int32) % 4 - 1  # -1: takes no part
+    logits = h.double() @ w.double().t()
+    z = torch.logsumexp(logits, 1)
+    on = t >= 0
+    at = t.long().clamp(0)[:, None]
+    ref = torch.where(on, z - logits.gather(1, at)[:, 0], torch.zeros_like(z))
+    dl = (torch.exp(logits - z[:, None]) - torch.zeros_like(logits).scatter_(1, at, 1.0)) * on[:, None]
+    dh = dl @ w.double()
+    big, ts = dev(h).repeat(n // period, 1), dev(t).repeat(n // period)
+    loss, lse = B.poetx_xent_forward(big, dev(w), ts)
+    # as in check_xent: the products, exp with its argument's rounding, the sum of three, log
+    arg = 2 * float(logits.abs().amax()) + 1
+    e_l = acc(d) * float((h.double().abs() @ w.double().abs().t()).amax())
+    e_z = e_l + 4 * 2.0 ** -24 + 2.0 ** -22 + arg * 2.0 ** -22 + 4 * U[F32] * arg
+    for got, want, e in ((loss, ref, e_z + e_l + 8 * U[F32] * arg), (lse, z, e_z)):
+        assert float((got.view(-1, period) - dev(want).float()).abs().amax()) <= e + U[F32] * arg
+    g = B.poetx_xent_backward(big, dev(w), ts, lse, torch.ones(n, device="cuda"), want_dw=False)["dh"]
+    # dl and dh rounded to the type, and the sum over the vocabulary
+    e_p = e_l + e_z + arg * 2.0 ** -22 + 2.0 ** -21
+    mag = dl.abs() @ w.double().abs()
+    tol = dev((2.02 * U[dtype] + acc(v)) * mag + e_p * w.double().abs().sum(0)).float()
+    for k in range(0, n // period, 1 << 16):
+        rows = g[k * period:(k + (1 << 16)) * period].float().view(-1, period, d)
+        assert bool(((rows - dev(dh).float()).abs() <= tol).all()), k
