@@ -384,7 +384,7 @@ int poetx_xent_forward(int64_t n_tokens, int64_t d, int64_t vocab, int32_t dtype
  *     dl_iv = (exp(l_iv - lse_i) - [v = target_i]) dloss_i,  dh = dl . w,  dw = dl^T . h
  * dh: [n_tokens][d], dw: [vocab][d], both in dtype, each may be NULL, not both.  A token whose
  * target lies outside [0, vocab) gets dh = 0 and leaves dw alone, whatever its h, lse and dloss
- * hold.  With n_tokens == 0, dw is zeros.  For bf16 the products read dl rounded to bf16.
+ * (and w) hold.  With n_tokens == 0, dw is zeros.  For bf16 the products read dl rounded to bf16.
  * Workspace: query with ws == NULL, with the same outputs NULL or not: dl of one piece (at most
  * 512 MB, or 2048 vocabulary entries where those take more), float32 sums of dh when there are
  * several pieces, a copy of h for dw.  Errors: as poetx_xent_forward.

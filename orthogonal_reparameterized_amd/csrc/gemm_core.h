@@ -187,7 +187,7 @@ __device__ inline void finish(const V (&acc)[FM][FN], const MmArgs &a, const MmT
       __syncthreads();
     }
     put_rows<FM, FN>(acc, m0 + wm, n0 + wn, a.M, a.N, lds + wave * R * (WTN + 4), epi.at(tile.split),
-                     rows + wm * Epi::kRows - (m0 + wm) * Epi::kRows);
+                     Epi::kRows > 0 ? rows + wm * Epi::kRows - (m0 + wm) * Epi::kRows : nullptr);
   }
 }
 
@@ -631,13 +631,14 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
 template <class Epi>
 struct MaybePart {
   static constexpr bool kStats = false;
-  static constexpr int kRows = 0;
+  static constexpr int kRows = Epi::kRows;
   using Tag_ = typename Epi::Tag_;
   using Cols = typename Epi::Cols;
   Epi epi;
   float *part; int64_t N, stride;
   __device__ MaybePart at(int split) const { return MaybePart{epi, part ? part + split * stride : nullptr, N, stride}; }
   __device__ Cols cols(int64_t n, int nv, const float *rows) const { return epi.cols(n, nv, rows); }
+  __device__ float stage(int64_t m0, int64_t M, int i) const { return epi.stage(m0, M, i); }
   __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
     if (part) store8(part + m * N + n, nv, v);
     else epi.put(c, m, n, v, nv);

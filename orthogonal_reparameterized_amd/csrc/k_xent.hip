@@ -136,20 +136,26 @@ struct XentDl {
   }
 };
 
-// dh over the pieces: float32 sums in `sum` between the first and the last piece.
+// dh over the pieces: float32 sums in `sum` between the first and the last piece.  A row that takes
+// no part is written as zeros: its dl is zero, but zero times an infinity of W would not be.
 template <typename T>
 struct XentDh {
   static constexpr bool kStats = false;
-  static constexpr int kRows = 0;
+  static constexpr int kRows = 1;
   using Tag_ = XentTag;
-  struct Cols { float g; };
+  struct Cols { float g; const float *rows; };
   float *sum;
   T *dh;
   const float *scale;
-  int64_t ld;
+  const int32_t *target;
+  int64_t vocab, ld;
   int first, last;
   __device__ const XentDh &at(int) const { return *this; }
-  __device__ Cols cols(int64_t, int, const float *) const { return {scale ? *scale : 1.f}; }
+  __device__ Cols cols(int64_t, int, const float *rows) const { return {scale ? *scale : 1.f, rows}; }
+  __device__ float stage(int64_t m0, int64_t M, int i) const {  // whether the row takes part
+    const int64_t m = m0 + i;
+    return m < M && target[m] >= 0 && target[m] < vocab ? 1.f : 0.f;
+  }
   __device__ void put(const Cols &c, int64_t m, int64_t n, float (&v)[8], int nv) const {
     const int64_t o = m * ld + n;
     if (!first) {
@@ -159,8 +165,9 @@ struct XentDh {
       for (int e = 0; e < 8; ++e) v[e] += w[e];
     }
     if (last) {
+      const bool on = (c.rows ? c.rows[m] : stage(m, m + 1, 0)) != 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= c.g;
+      for (int e = 0; e < 8; ++e) v[e] = on ? v[e] * c.g : 0.f;
       store8(dh + o, nv, v);
     } else {
       store8(sum + o, nv, v);
@@ -469,7 +476,7 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt), part,
                                     XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, scale, v0, d.v}, s)));
     const MmTwo q = products(d, vc, flip);
-    const XentDh<T> eh{sum, (T *)d.dh, scale, d.d, v0 == 0, v0 + vc == d.v};
+    const XentDh<T> eh{sum, (T *)d.dh, scale, d.target, d.v, d.d, v0 == 0, v0 + vc == d.v};
     const XentDw<T> ew{d.dw ? (T *)d.dw + v0 * d.d : nullptr, scale, d.d};
     MmDesc gh, gw;
     gh.M = d.n; gh.N = d.d; gh.K = vc; gh.name = "xent_dh";

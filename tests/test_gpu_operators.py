@@ -800,3 +800,31 @@ def test_xent_of_more_than_2_28_tokens(B, dtype):
     for k in range(0, n // period, 1 << 16):
         rows = g[k * period:(k + (1 << 16)) * period].float().view(-1, period, d)
         assert bool(((rows - dev(dh).float()).abs() <= tol).all()), k
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,d,v", [(12, 72, 700), (60, 77, 700), (3000, 392, 1200), (3300, 4100, 520)])
+def test_xent_masked_rows_are_zero_whatever_w_holds(B, n, d, v, dtype):
+    """A row of W that is not finite reaches the tokens that take part, not the others' dh."""
+    h, w, t, dl = xent_case(370, n, d, v, dtype)
+    w[3, 5], w[v - 1, 7] = float("inf"), float("nan")
+    w[4] = float("-inf")
+    t[0], t[1], t[n - 1] = -1, v, 5
+    on = (t >= 0) & (t < v)
+    z = torch.zeros(n)  # any statistics: the masked rows do not depend on them
+    g = B.poetx_xent_backward(dev(h), dev(w), dev(t), dev(z), dev(dl))["dh"].cpu()
+    assert not g[~on].any()  # (a NaN would count as true)
+    assert torch.isnan(g[on][:, 7]).all()
+
+
+def test_xent_masked_rows_are_zero_over_pieces(B):
+    """The same where dh is summed over several pieces of the vocabulary."""
+    n, d, v = 40000, 64, 20000
+    g = torch.Generator(device="cuda").manual_seed(380)
+    h = torch.randn(n, d, generator=g, device="cuda").to(BF16)
+    w = (torch.randn(v, d, generator=g, device="cuda") * 0.25).to(BF16)
+    w[11] = float("inf")
+    t = torch.randint(0, v, (n,), generator=g, device="cuda", dtype=torch.int32)
+    t[::3] = -1
+    got = B.poetx_xent_backward(h, w, t, torch.zeros(n, device="cuda"), torch.ones(n, device="cuda"), want_dw=False)
+    assert not got["dh"][::3].any() and torch.isnan(got["dh"][1::3]).any()
