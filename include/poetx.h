@@ -36,7 +36,10 @@
  *  - Every call is asynchronous on `stream` (a hipStream_t passed as void*;
  *    NULL = the default stream) and never synchronizes.
  *  - Workspace: calls taking (ws, ws_bytes) report the bytes they need when
- *    called with ws == NULL (writing *ws_bytes, launching nothing).  With
+ *    called with ws == NULL (writing *ws_bytes, launching nothing).  ws == NULL
+ *    is that query always, also where the answer is 0: a call that needs no
+ *    workspace still takes a ws that is not NULL (any 16-byte aligned device
+ *    address, *ws_bytes 0), or it returns POETX_OK with its outputs unwritten.  With
  *    ws != NULL, *ws_bytes below the requirement is POETX_ERR_WORKSPACE.  The
  *    requirement can depend on the current device (its compute-unit count sets
  *    how the W' products split their last round of tiles): query on the device

@@ -828,3 +828,27 @@ def test_xent_masked_rows_are_zero_over_pieces(B):
     t[::3] = -1
     got = B.poetx_xent_backward(h, w, t, torch.zeros(n, device="cuda"), torch.ones(n, device="cuda"), want_dw=False)
     assert not got["dh"][::3].any() and torch.isnan(got["dh"][1::3]).any()
+
+
+def test_calls_that_need_no_workspace(B):
+    """A requirement of 0: the call runs with any aligned ws and 0 bytes; with ws == NULL it is
+    the size query and leaves the outputs alone."""
+    import ctypes
+    n, d = 4, 64
+    x, w, dy = (dev(rand(390 + k, r, d, dtype=BF16)) for k, r in enumerate((n, d, n)))
+    _, mean, rstd = B.poetx_layernorm_forward(x)
+    s = torch.cuda.current_stream().cuda_stream
+    y, dx, dw = torch.full_like(x, 7.0), torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    ws = torch.full((64,), 5, dtype=torch.uint8, device="cuda")
+    calls = [(y, B.raw.poetx_linear_forward, (n, d, d, 1, x.data_ptr(), w.data_ptr(), None, 0, None, 0, y.data_ptr(),
+                                              None)),
+             (dx, B.raw.poetx_layernorm_backward, (n, d, 1, x.data_ptr(), dy.data_ptr(), None, 0, mean.data_ptr(),
+                                                   rstd.data_ptr(), None, dx.data_ptr(), None, None)),
+             (dw, B.raw.poetx_linear_backward, (0, d, d, 1, None, None, None, None, 0, None, dw.data_ptr(), None))]
+    for out, f, args in calls:
+        size = ctypes.c_size_t(99)
+        assert f(*args, None, ctypes.byref(size), s) == B.POETX_OK and size.value == 0
+        assert bool((out == 7).all())
+        assert f(*args, ws.data_ptr(), ctypes.byref(size), s) == B.POETX_OK
+    assert torch.equal(y, B.poetx_linear_forward(x, w)[0]) and not dw.any() and bool((ws == 5).all())
+    assert torch.equal(dx, B.poetx_layernorm_backward(x, dy, None, mean, rstd, want_params=False)["dx"])

@@ -176,3 +176,15 @@ def test_binding_refusals(B):
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"case {k} was accepted")
+
+
+def test_a_null_workspace_is_the_query_also_where_none_is_needed(B):
+    """With every buffer given and a requirement of 0, ws == NULL still asks for the size and
+    launches nothing (a launch on these addresses, or without a GPU, would not return OK)."""
+    for f, kw in ((norm_bwd, dict(dg=None, db=None)), (lin_fwd, dict(n=4)), (lin_fwd, dict(n=0)),
+                  (norm_bwd, dict(n=0, dg=None, db=None)), (lin_bwd, dict(n=0, db=None))):
+        assert f(B, ws=None, nb=1 << 30, **kw) == B.POETX_OK, (f, kw)
+    r, none = B.raw, [None] * 4
+    assert query(r.poetx_linear_forward, 4, 64, 64, 1, A, C, None, 0, None, 0, D, None) == 0
+    assert query(r.poetx_layernorm_backward, 4, 64, 1, A, C, None, 0, D, E, None, 0x50000, None, None) == 0
+    assert query(r.poetx_linear_backward, 0, 64, 64, 1, *none, 0, A, C, None) == 0
