@@ -19,6 +19,7 @@ import ctypes
 import functools
 import os
 import threading
+import weakref
 from dataclasses import dataclass
 from typing import Optional
 
@@ -153,17 +154,25 @@ def _stream(dev: torch.device):
 # being captured into a graph takes a workspace of its own from the graph's memory pool: it
 # lives as long as the graph, and no eager call or other graph shares it.  Each thread has its
 # own workspaces: a call launches several kernels, and another thread's may come between them
-# on the same stream.
-_ws_local = threading.local()
+# on the same stream.  They go with their thread, or all at once by release_workspace().
+class _WsCache(dict):
+    __slots__ = ("__weakref__",)
+    __hash__, __eq__ = object.__hash__, object.__eq__  # an element of a WeakSet by identity
+
+
+_ws_all: weakref.WeakSet = weakref.WeakSet()
+_ws_lock = threading.Lock()
+
+
+class _WsLocal(threading.local):
+    def __init__(self):  # runs once in every thread that reaches for its workspaces
+        self.cache = _WsCache()
+        with _ws_lock:
+            _ws_all.add(self.cache)
+
+
+_ws_local = _WsLocal()
 _capturing = torch._C._cuda_isCurrentStreamCapturing
-
-
-def _ws_cache() -> dict:
-    try:
-        return _ws_local.cache
-    except AttributeError:
-        _ws_local.cache = {}
-        return _ws_local.cache
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
@@ -171,7 +180,7 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     if _capturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
     key = (idx, _raw_stream(idx))
-    cache = _ws_cache()
+    cache = _ws_local.cache
     t = cache.get(key)
     if t is None or t.numel() < nbytes:
         with torch.cuda.device(idx):
@@ -181,8 +190,13 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
 
 
 def release_workspace():
-    """Drop the calling thread's cached workspaces."""
-    _ws_cache().clear()
+    """Drop every cached workspace, those of other threads as well.  (A call that is under way in
+    another thread holds its own until its kernels are launched; the allocator hands the memory
+    on in the order of the stream they run on.)"""
+    with _ws_lock:
+        caches = list(_ws_all)
+    for cache in caches:
+        cache.clear()
 
 
 # --------------------------------------------------------------------------

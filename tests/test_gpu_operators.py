@@ -852,3 +852,50 @@ def test_calls_that_need_no_workspace(B):
         assert f(*args, ws.data_ptr(), ctypes.byref(size), s) == B.POETX_OK
     assert torch.equal(y, B.poetx_linear_forward(x, w)[0]) and not dw.any() and bool((ws == 5).all())
     assert torch.equal(dx, B.poetx_layernorm_backward(x, dy, None, mean, rstd, want_params=False)["dx"])
+
+
+def test_release_drops_every_threads_workspaces(B):
+    """release_workspace() frees the workspaces of threads that are alive and idle, and a thread
+    whose workspace went gets another."""
+    import threading
+    h, w, t, dl = (dev(a) for a in xent_case(400, 400, 64, 50000, BF16))
+    loss, lse = B.poetx_xent_forward(h, w, t)
+    want = B.poetx_xent_backward(h, w, t, lse, dl)
+    need = 400 * 50000 * 2  # dl alone
+    done, go, bad = threading.Event(), threading.Event(), []
+
+    def work():
+        torch.cuda.set_device(h.device)
+        for _ in range(2):
+            got = B.poetx_xent_backward(h, w, t, lse, dl)
+            torch.cuda.synchronize()
+            bad.extend(k for k in want if not torch.equal(got[k], want[k]))
+            del got
+            done.set()
+            go.wait(60)
+
+    B.release_workspace()
+    before = torch.cuda.memory_allocated()
+    th = threading.Thread(target=work)
+    th.start()
+    assert done.wait(60)
+    held = torch.cuda.memory_allocated()
+    B.release_workspace()
+    after = torch.cuda.memory_allocated()
+    go.set()
+    th.join()
+    assert held - before >= need and after <= before and not bad
+
+
+def test_a_threads_workspaces_go_with_it(B):
+    import gc
+    import threading
+    h, w, t, dl = (dev(a) for a in xent_case(410, 400, 64, 50000, BF16))
+    _, lse = B.poetx_xent_forward(h, w, t)
+    B.release_workspace()
+    before = torch.cuda.memory_allocated()
+    th = threading.Thread(target=lambda: B.poetx_xent_backward(h, w, t, lse, dl))
+    th.start()
+    th.join()
+    gc.collect()
+    assert torch.cuda.memory_allocated() <= before
