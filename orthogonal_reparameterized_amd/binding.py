@@ -140,7 +140,9 @@ def _ptr(t: Optional[torch.Tensor], align: int = 16):
 
 
 # the current HIP stream of a device by its index, without building a torch Stream object (2 us)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# where torch has that internal function
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda idx: torch.cuda.current_stream(idx).cuda_stream)
 
 
 def _stream(dev: torch.device):
@@ -172,7 +174,7 @@ class _WsLocal(threading.local):
 
 
 _ws_local = _WsLocal()
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:

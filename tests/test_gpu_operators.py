@@ -899,3 +899,11 @@ def test_a_threads_workspaces_go_with_it(B):
     th.join()
     gc.collect()
     assert torch.cuda.memory_allocated() <= before
+
+
+def test_current_stream_lookup(B):
+    """The stream handle that the calls launch on is torch's current one, by either way of asking."""
+    s = torch.cuda.Stream()
+    for ctx in (torch.cuda.stream(s), torch.cuda.stream(torch.cuda.default_stream())):
+        with ctx:
+            assert B._raw_stream(0) == torch.cuda.current_stream(0).cuda_stream

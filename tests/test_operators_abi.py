@@ -188,3 +188,17 @@ def test_a_null_workspace_is_the_query_also_where_none_is_needed(B):
     assert query(r.poetx_linear_forward, 4, 64, 64, 1, A, C, None, 0, None, 0, D, None) == 0
     assert query(r.poetx_layernorm_backward, 4, 64, 1, A, C, None, 0, D, E, None, 0x50000, None, None) == 0
     assert query(r.poetx_linear_backward, 0, 64, 64, 1, *none, 0, A, C, None) == 0
+
+
+def test_binding_imports_without_torchs_internal_functions():
+    """The binding takes torch's internal stream lookup where it is there and does without
+    otherwise."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_isCurrentStreamCapturing'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "from orthogonal_reparameterized_amd import binding\n"
+            "assert callable(binding._raw_stream) and callable(binding._capturing)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
