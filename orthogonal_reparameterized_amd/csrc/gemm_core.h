@@ -863,7 +863,7 @@ struct MmDesc {
   int64_t M = 0, N = 0, K = 0;
   const void *A = nullptr; int64_t lda = 0;
   const void *B = nullptr; int64_t ldb = 0;
-  const char *name = "mm";
+  const char *name = "mm", *large = "mm_large";  // launch labels: of the smaller and the larger tile
 };
 
 // float32: the kernels are bound by the matrix cores, so a CU's time is that of the tiles dealt to
@@ -967,7 +967,7 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
 }
 
 template <bool AKM, bool BKM, class Epi>
-int mm_launch(const MmArgs &a, int64_t bt, const char *name, const Epi &epi, hipStream_t s) {
+int mm_launch(const MmArgs &a, int64_t bt, const MmDesc &d, const Epi &epi, hipStream_t s) {
   const int tiles = a.tiles_m * a.tiles_n;
   const dim3 grid((unsigned)(a.full < tiles ? a.full + (tiles - a.full) * a.tail_splits : tiles * a.splits));
   if (bt == 256) {
@@ -975,23 +975,23 @@ int mm_launch(const MmArgs &a, int64_t bt, const char *name, const Epi &epi, hip
     auto kern = &k_mm8<AKM, BKM, false, Epi>;
     static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
     POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
-    return launch_k(name, s, kern, grid, dim3(512), lds, a, epi);
+    return launch_k(d.large, s, kern, grid, dim3(512), lds, a, epi);
   }
   constexpr size_t lds = (size_t)2 * 2 * 128 * 64 * 2;
   auto kern = &k_mm<128, 128, 2, 2, AKM, BKM, Epi>;
   static std::atomic<uint64_t> attr{0};
   POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
-  return launch_k(name, s, kern, grid, dim3(256), lds, a, epi);
+  return launch_k(d.name, s, kern, grid, dim3(256), lds, a, epi);
 }
 
 template <typename T, bool AKM, bool BKM, class Epi>
-int mm_run_as(const MmArgs &a, const MmPlan &p, const char *name, const Epi &epi, hipStream_t s) {
+int mm_run_as(const MmArgs &a, const MmPlan &p, const MmDesc &d, const Epi &epi, hipStream_t s) {
   if constexpr (sizeof(T) == 4) {
     const dim3 grid((unsigned)(a.tiles_m * a.tiles_n * a.splits));
-    if (p.bt == 128) return launch_k(name, s, k_mm_f32<128, 16, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
-    return launch_k(name, s, k_mm_f32<64, 32, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
+    if (p.bt == 128) return launch_k(d.large, s, k_mm_f32<128, 16, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
+    return launch_k(d.name, s, k_mm_f32<64, 32, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
   } else {
-    return mm_launch<AKM, BKM>(a, p.bt, name, epi, s);
+    return mm_launch<AKM, BKM>(a, p.bt, d, epi, s);
   }
 }
 
@@ -1006,12 +1006,12 @@ int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStr
   if constexpr (!Epi::kStats && sizeof(T) == 2) {
     if (p.full < tiles) {
       a.full = (int)p.full; a.tail_splits = (int)p.tail_splits; a.tail_kc = p.tail_kc; a.tail_part = part;
-      POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s)));
+      POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d, epi, s)));
       return launch_k("mm_tail", s, k_mm_tail<Epi>, dim3((unsigned)((tiles - p.full) * 32)), dim3(256), 0, a, epi);
     }
   }
-  if (p.splits == 1) return mm_run_as<T, AKM, BKM>(a, p, d.name, epi, s);
-  POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d.name, StoreEpi<float, typename Epi::Tag_>{part, d.N, d.M * d.N}, s)));
+  if (p.splits == 1) return mm_run_as<T, AKM, BKM>(a, p, d, epi, s);
+  POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d, StoreEpi<float, typename Epi::Tag_>{part, d.N, d.M * d.N}, s)));
   if constexpr (Epi::kStats) {
     return POETX_OK;
   } else {
@@ -1098,7 +1098,7 @@ int mm_run_flipped(const MmDesc &d, const Epi &epi, hipStream_t s) {
   auto kern = &k_mm8<false, true, true, Epi>;
   static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
   POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
-  return launch_k(d.name, s, kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), lds, a, epi);
+  return launch_k(d.large, s, kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), lds, a, epi);
 }
 
 }  // namespace poetx

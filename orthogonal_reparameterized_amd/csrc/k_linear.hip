@@ -314,7 +314,7 @@ template <typename T>
 int fwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const LinEpi<T> epi{(T *)d.y, (T *)d.pre, (const T *)d.residual, {d.bias, d.bias_bf16}, d.act, d.d_out};
   MmDesc m;
-  m.M = d.n; m.N = d.d_out; m.K = d.d_in; m.name = "linear_fwd";
+  m.M = d.n; m.N = d.d_out; m.K = d.d_in; m.name = "linear_fwd"; m.large = "linear_fwd_large";
   m.A = d.x; m.lda = d.d_in; m.B = d.w; m.ldb = d.d_in;
   if (d.n <= 16) {  // reading W bounds these: no LDS tiles, any alignment
     if (measure) return POETX_OK;
@@ -377,13 +377,13 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
   PackList l;
   if (d.dx) {
     const Packed w = packed(d.w, d.d_out, d.d_in, d.dt, ar, l);
-    mx.M = d.n; mx.N = d.d_in; mx.K = d.d_out; mx.name = "linear_dx";
+    mx.M = d.n; mx.N = d.d_in; mx.K = d.d_out; mx.name = "linear_dx"; mx.large = "linear_dx_large";
     mx.A = dp; mx.lda = ld; mx.B = w.p; mx.ldb = w.ld;
   }
   const bool flip = b16 && d.dw && dw_flips(d.d_out, d.d_in, d.n, d.dt);
   if (d.dw && !flip) {
     const Packed x = packed(d.x, d.n, d.d_in, d.dt, ar, l);
-    mw.M = d.d_out; mw.N = d.d_in; mw.K = d.n; mw.name = "linear_dw";
+    mw.M = d.d_out; mw.N = d.d_in; mw.K = d.n; mw.name = "linear_dw"; mw.large = "linear_dw_large";
     mw.A = dp; mw.lda = ld; mw.B = x.p; mw.ldb = x.ld;
   }
   const MmTwo two = mm_two(mx.M, mx.N, mx.K, mw.M, mw.N, mw.K, d.dt);
@@ -405,7 +405,7 @@ int bwd_t(const LinDesc &d, Arena &ar, bool measure, hipStream_t s) {
       if (measure) return POETX_OK;
       POETX_TRY(pack_rows_t(d.x, d.n, d.d_in, xt, ldt, nullptr, 0, s));
       MmDesc m;
-      m.M = d.d_in; m.N = d.d_out; m.K = d.n; m.name = "linear_dw";
+      m.M = d.d_in; m.N = d.d_out; m.K = d.n; m.large = "linear_dw_large";
       m.A = xt; m.lda = ldt; m.B = dp; m.ldb = ld;
       return mm_run_flipped(m, ew, s);
     }

@@ -420,9 +420,10 @@ int w_piece(const XentDesc &d, const Operands &o, int64_t v0, int64_t vc, PackLi
   return pack_rows(l, d.dt, s);
 }
 
-MmDesc logits_desc(const XentDesc &d, const Operands &o, const void *w, int64_t vc, const char *name) {
+MmDesc logits_desc(const XentDesc &d, const Operands &o, const void *w, int64_t vc, const char *name,
+                   const char *large) {
   MmDesc m;
-  m.M = d.n; m.N = vc; m.K = pads(d) ? o.ld : d.d; m.name = name;
+  m.M = d.n; m.N = vc; m.K = pads(d) ? o.ld : d.d; m.name = name; m.large = large;
   m.A = o.h; m.lda = o.ld; m.B = w; m.ldb = o.ld;
   return m;
 }
@@ -472,16 +473,16 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
     const void *w = nullptr;
     POETX_TRY(w_piece(d, o, v0, vc, l, s, &w));
-    const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits");
+    const MmDesc m = logits_desc(d, o, w, vc, "xent_dlogits", "xent_dlogits_large");
     POETX_TRY((mm_run<T, false, false>(m, mm_plan(m.M, m.N, m.K, d.dt), part,
                                     XentDl<T>{dl, ldl, d.target, d.lse_in, d.dloss, scale, v0, d.v}, s)));
     const MmTwo q = products(d, vc, flip);
     const XentDh<T> eh{sum, (T *)d.dh, scale, d.target, d.v, d.d, v0 == 0, v0 + vc == d.v};
     const XentDw<T> ew{d.dw ? (T *)d.dw + v0 * d.d : nullptr, scale, d.d};
     MmDesc gh, gw;
-    gh.M = d.n; gh.N = d.d; gh.K = vc; gh.name = "xent_dh";
+    gh.M = d.n; gh.N = d.d; gh.K = vc; gh.name = "xent_dh"; gh.large = "xent_dh_large";
     gh.A = dl; gh.lda = ldl; gh.B = w; gh.ldb = o.ld;
-    gw.M = vc; gw.N = d.d; gw.K = d.n; gw.name = "xent_dw";
+    gw.M = vc; gw.N = d.d; gw.K = d.n; gw.name = "xent_dw"; gw.large = "xent_dw_large";
     gw.A = dl; gw.lda = ldl; gw.B = hz; gw.ldb = o.ld;
     if (q.pair) {
       POETX_TRY(mm_run_pair<T>("xent_dh_dw", gh, q.a, part, eh, gw, q.b, part_w, ew, {}, s));
@@ -491,7 +492,7 @@ int bwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
       if (flip) {
         MmDesc g;
-        g.M = d.d; g.N = vc; g.K = d.n; g.name = "xent_dw";
+        g.M = d.d; g.N = vc; g.K = d.n; g.large = "xent_dw_large";
         g.A = hz; g.lda = ldt; g.B = dl; g.ldb = ldl;
         POETX_TRY(mm_run_flipped(g, ew, s));
       }
@@ -549,7 +550,7 @@ int fwd_t(const XentDesc &d, Arena &ar, bool measure, hipStream_t s) {
       const int64_t vc = d.v - v0 < piece ? d.v - v0 : piece;
       const void *w = nullptr;
       POETX_TRY(w_piece(d, o, v0, vc, l, s, &w));
-      const MmDesc m = logits_desc(d, o, w, vc, "xent_fwd");
+      const MmDesc m = logits_desc(d, o, w, vc, "xent_fwd", "xent_fwd_large");
       const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt, true, false);
       const XentStats epi{part, d.target, at, v0, (int)t0};
       POETX_TRY((mm_run<T, false, false>(m, p, split, epi, s)));

@@ -907,3 +907,95 @@ def test_current_stream_lookup(B):
     for ctx in (torch.cuda.stream(s), torch.cuda.stream(torch.cuda.default_stream())):
         with ctx:
             assert B._raw_stream(0) == torch.cuda.current_stream(0).cuda_stream
+
+
+# ---------------------------------------------------------- the large tiles, element by element ----
+# The launch labels say which way a product went, so that these cases cannot drift off the paths
+# they are for: "_large" is the larger tile (bf16 256 x 256, float32 128 x 128), "mm_join" a k split
+# of all its tiles, "mm_tail" of the last round's, "pack_rows_t" a transposed copy for dW.
+
+def labelled(B, f):
+    """(f(), the labels of the kernels it launched)."""
+    torch.cuda.synchronize()
+    B.prof_read()
+    B.prof_enable(True)
+    try:
+        r = f()
+        torch.cuda.synchronize()
+        return r, set(B.prof_read())
+    finally:
+        B.prof_enable(False)
+
+
+def within_dev(got, ref, tol, what):
+    """`within` on the device, for results of millions of elements."""
+    d = (got.double() - ref).abs()
+    bad = ~(d <= tol + TINY)
+    if bad.any():
+        i = int(torch.nonzero(bad.reshape(-1))[0])
+        pytest.fail(f"{what}: {int(bad.sum())} of {bad.numel()} off, first {i}: got {got.reshape(-1)[i].item():.9g} "
+                    f"ref {ref.reshape(-1)[i].item():.9g} tol {tol.reshape(-1)[i].item():.3g}")
+
+
+def drand(seed, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda") * scale).to(dtype)
+
+
+def check_linear_large(B, n, i, o, dtype, act, bias, fwd, bwd, seed=420):
+    """Forward with bias, residual and the kept pre-activation, and backward, against float64 with
+    the bounds of check_linear_fwd and check_linear_bwd; fwd, bwd: the labels they must have."""
+    x, w = drand(seed, n, i, dtype=dtype), drand(seed + 1, o, i, dtype=dtype, scale=i ** -0.5)
+    b, res = drand(seed + 2, o, dtype=bias, scale=0.5), drand(seed + 3, n, o, dtype=dtype)
+    (y, pre), ran = labelled(B, lambda: B.poetx_linear_forward(x, w, b, res, act, save_pre=True))
+    assert fwd <= ran and ran & {"mm_join", "mm_tail"} <= fwd, ran
+    xd, wd = x.double(), w.double()
+    p, mag = xd @ wd.t() + b.double(), xd.abs() @ wd.abs().t() + b.double().abs()
+    e_p = acc(i) * mag
+    within_dev(pre, p, U[dtype] * p.abs() + 1.01 * e_p, "pre")
+    v, _ = act_ref(p, act)
+    ref = v + res.double()
+    e = 1.13 * e_p + FN * (p.abs() + v.abs()) * (act not in ("none", "relu")) + 2 * U[F32] * ref.abs()
+    within_dev(y, ref, U[dtype] * ref.abs() + 1.01 * e, "y")
+    del y, p, mag, e_p, v, ref, e, res
+
+    dy = drand(seed + 4, n, o, dtype=dtype)
+    got, ran = labelled(B, lambda: B.poetx_linear_backward(x, w, dy, pre, act))
+    assert bwd <= ran and ran & {"mm_join", "mm_tail", "pack_rows_t"} <= bwd, ran
+    _, slope = act_ref(pre.double(), act)
+    dp = dy.double() * slope
+    e_dp = (FN * dy.double().abs() * (1 + pre.double().abs()) + U[F32] * dp.abs()) * (act not in ("none", "relu"))
+    e_op = e_dp + (U[dtype] * dp.abs() if act != "none" else 0)
+    for name, ref, mag, e_in, k in (("dx", dp @ wd, dp.abs() @ wd.abs(), e_op @ wd.abs(), o),
+                                    ("dw", dp.t() @ xd, dp.abs().t() @ xd.abs(), e_op.t() @ xd.abs(), n)):
+        within_dev(got[name], ref, U[dtype] * ref.abs() + 1.02 * (acc(k) * mag + (e_in if act != "none" else 0)), name)
+    within_dev(got["dbias"], dp.sum(0), acc(n) * dp.abs().sum(0) + e_dp.sum(0), "dbias")
+
+
+LARGE_FWD, LARGE_BWD = {"linear_fwd_large"}, {"linear_dx_large", "linear_dw_large"}
+
+
+@pytest.mark.parametrize("n,i,o,act,bias,fwd,bwd", [
+    (3500, 3400, 3593, "gelu", F32, set(), set()),                       # whole, widths that are padded
+    (3593, 3401, 3528, "none", BF16, set(), set()),
+    (4100, 4097, 4352, "silu", F32, {"mm_tail"}, {"mm_tail"}),           # a shared last round
+    (1500, 4700, 5300, "gelu_tanh", BF16, {"mm_join"}, {"mm_join"}),     # split over k
+    (3500, 1100, 12300, "gelu", F32, set(), {"pack_rows_t", "mm_join"}),  # dW by way of x transposed, dx split
+])
+def test_linear_large_tiles(B, n, i, o, act, bias, fwd, bwd):
+    check_linear_large(B, n, i, o, BF16, act, bias, LARGE_FWD | fwd, LARGE_BWD | bwd)
+
+
+@pytest.mark.parametrize("n,tail", [(413, 29), (64 * 7, 0)])
+def test_linear_wide_weight_gradient_transposed(B, n, tail):
+    """Few tokens, of which the last k step holds `tail` (0: all of it is full)."""
+    assert n % 64 == tail
+    x, w = drand(430, n, 1100, dtype=BF16), drand(431, 12300, 1100, dtype=BF16)
+    dy = drand(432, n, 12300, dtype=BF16)
+    got, ran = labelled(B, lambda: B.poetx_linear_backward(x, w, dy, want_dx=False))
+    assert {"pack_rows_t", "linear_dw_large"} <= ran, ran
+    ref, mag = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+    within_dev(got["dw"], ref, U[BF16] * ref.abs() + 1.02 * acc(n) * mag, "dw")
+
+
+def test_linear_large_tiles_float32(B):
+    check_linear_large(B, 4093, 4087, 4090, F32, "gelu", F32, LARGE_FWD, LARGE_BWD, seed=440)
