@@ -999,3 +999,60 @@ def test_linear_wide_weight_gradient_transposed(B, n, tail):
 
 def test_linear_large_tiles_float32(B):
     check_linear_large(B, 4093, 4087, 4090, F32, "gelu", F32, LARGE_FWD, LARGE_BWD, seed=440)
+
+
+def check_xent_large(B, n, d, v, dtype, bwd, ignored=0.2, seed=450):
+    """check_xent on the device: whole products of the larger tile in the forward, those of `bwd`
+    in the backward."""
+    h, w = drand(seed, n, d, dtype=dtype), drand(seed + 1, v, d, dtype=dtype, scale=2 * d ** -0.5)
+    gen = torch.Generator("cuda").manual_seed(seed + 2)
+    t = torch.randint(0, v, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    drop = torch.rand(n, generator=gen, device="cuda") < ignored
+    t = torch.where(drop, torch.where(torch.arange(n, device="cuda") % 2 == 0, -1, v), t).int()
+    dl = torch.rand(n, generator=gen, device="cuda") + 0.5
+    (loss, lse), ran = labelled(B, lambda: B.poetx_xent_forward(h, w, t))
+    assert "xent_fwd_large" in ran and "xent_parts" not in ran, ran
+    hd, wd, on = h.double(), w.double(), ~drop
+    logits = hd @ wd.t()
+    e_l = acc(d) * (hd.abs() @ wd.abs().t()).amax(1)
+    z = torch.logsumexp(logits, 1)
+    arg = 2 * logits.abs().amax(1) + 1
+    e_z = e_l + (v / 16 + 64) * 2.0 ** -24 + 2.0 ** -22 + arg * 2.0 ** -22 + 4 * U[F32] * z.abs()
+    within_dev(lse, z, e_z, "lse")
+    at = t.long().clamp(0, v - 1)[:, None]
+    lt = logits.gather(1, at)[:, 0]
+    none = torch.zeros_like(z)
+    within_dev(loss, torch.where(on, z - lt, none),
+               torch.where(on, e_z + e_l + 4 * U[F32] * (z.abs() + lt.abs()), none), "loss")
+
+    got, ran = labelled(B, lambda: B.poetx_xent_backward(h, w, t, lse, dl))
+    every = {"xent_dlogits_large", "xent_dh_large", "xent_dw_large"}
+    assert every | bwd <= ran and ran & {"mm_join", "mm_tail", "pack_rows_t"} <= bwd, ran
+    p = torch.exp(logits - z[:, None])
+    del logits
+    one = torch.zeros_like(p).scatter_(1, at, 1.0)
+    g = torch.where(on, dl.double(), none)[:, None]
+    dlog = (p - one) * g
+    e_d = p * (e_l + e_z + arg * 2.0 ** -22 + 2.0 ** -21)[:, None]
+    e_d = (e_d + 2 * U[F32] * (p + one)) * g + U[dtype] * dlog.abs()
+    del p, one
+    for name, r, mag, e, k in (("dh", dlog @ wd, dlog.abs() @ wd.abs(), e_d @ wd.abs(), v),
+                               ("dw", dlog.t() @ hd, dlog.abs().t() @ hd.abs(), e_d.t() @ hd.abs(), n)):
+        within_dev(got[name], r, U[dtype] * r.abs() + 1.02 * (acc(k) * mag + e), f"{name} {n} {d} {v}")
+    assert not got["dh"][drop].any()
+
+
+@pytest.mark.parametrize("n,d,v,bwd", [
+    (3400, 3401, 3333, set()),                        # whole, padded d, tails on every axis
+    (3340, 3528, 3593, set()),
+    (4100, 4097, 4352, {"mm_tail"}),                  # a shared last round in all three
+    (40000, 700, 15000, {"mm_join"}),                 # three pieces, dh whole, dW split over the tokens
+    (40000, 392, 15000, {"mm_join", "mm_tail"}),      # and with dh's last round shared
+    (16384, 1100, 25000, {"pack_rows_t", "mm_tail"}),  # two pieces, dW by way of h transposed
+])
+def test_xent_whole_large_tiles(B, n, d, v, bwd):
+    check_xent_large(B, n, d, v, BF16, bwd)
+
+
+def test_xent_large_tiles_float32(B):
+    check_xent_large(B, 4093, 4087, 4090, F32, set(), seed=460)
