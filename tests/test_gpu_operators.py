@@ -1056,3 +1056,36 @@ def test_xent_whole_large_tiles(B, n, d, v, bwd):
 
 def test_xent_large_tiles_float32(B):
     check_xent_large(B, 4093, 4087, 4090, F32, set(), seed=460)
+
+
+@pytest.mark.parametrize("n,d,v", [(12, 72, 700), (60, 77, 700), (301, 520, 1007), (3400, 3401, 3333),
+                                   (421, 1004, 12500)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_xent_one_gradient_alone(B, n, d, v, dtype):
+    """A frozen head (dh alone) and dW alone.  Each is right element by element, and leaves no
+    key of the other; where both are wanted the products may share a launch, so the sums' order
+    may differ between the calls."""
+    h, w = drand(470, n, d, dtype=dtype), drand(471, v, d, dtype=dtype, scale=2 * d ** -0.5)
+    t = (torch.arange(n, device="cuda", dtype=torch.int32) * 7919) % v
+    t[::4] = -1
+    dl = drand(472, n)
+    _, lse = B.poetx_xent_forward(h, w, t)
+    a = B.poetx_xent_backward(h, w, t, lse, dl, want_dw=False)
+    b = B.poetx_xent_backward(h, w, t, lse, dl, want_dh=False)
+    assert set(a) == {"dh"} and set(b) == {"dw"}
+    hd, wd, on = h.double(), w.double(), t >= 0
+    logits = hd @ wd.t()
+    z = torch.logsumexp(logits, 1)
+    e_l = acc(d) * (hd.abs() @ wd.abs().t()).amax(1)
+    arg = 2 * logits.abs().amax(1) + 1
+    e_z = e_l + (v / 16 + 64) * 2.0 ** -24 + 2.0 ** -22 + arg * 2.0 ** -22 + 4 * U[F32] * z.abs()
+    p = torch.exp(logits - z[:, None])
+    one = torch.zeros_like(p).scatter_(1, t.long().clamp(0)[:, None], 1.0)
+    g = torch.where(on, dl.double(), torch.zeros_like(z))[:, None]
+    dlog = (p - one) * g
+    e_d = p * (e_l + e_z + arg * 2.0 ** -22 + 2.0 ** -21)[:, None]
+    e_d = (e_d + 2 * U[F32] * (p + one)) * g.abs() + U[dtype] * dlog.abs()
+    for got, r, mag, e, k in ((a["dh"], dlog @ wd, dlog.abs() @ wd.abs(), e_d @ wd.abs(), v),
+                              (b["dw"], dlog.t() @ hd, dlog.abs().t() @ hd.abs(), e_d.t() @ hd.abs(), n)):
+        within_dev(got, r, U[dtype] * r.abs() + 1.02 * (acc(k) * mag + e), f"{n} {d} {v}")
+    assert not a["dh"][~on].any()
