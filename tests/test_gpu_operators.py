@@ -1089,3 +1089,59 @@ def test_xent_one_gradient_alone(B, n, d, v, dtype):
                               (b["dw"], dlog.t() @ hd, dlog.abs().t() @ hd.abs(), e_d.t() @ hd.abs(), n)):
         within_dev(got, r, U[dtype] * r.abs() + 1.02 * (acc(k) * mag + e), f"{n} {d} {v}")
     assert not a["dh"][~on].any()
+
+
+@pytest.mark.parametrize("variant", ["fast", "mem"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_block_step_bf16(B, act, variant):
+    """test_block_step in bf16, both variants of the layer: loss and every gradient against
+    float64 on the same bf16 inputs."""
+    import torch.nn.functional as F
+    from orthogonal_reparameterized_amd import workloads as WL
+    from orthogonal_reparameterized_amd.step import BlockStep, LayerStep
+    d, f, v, n, b = 512, 1160, 2003, 333, 64
+    wl = WL.Workload(97, "block", n, d, d, b, "bf16", "bf16", "bf16", 0.02, d)
+    inp = WL.make_layer_inputs(wl)
+    p = {"gamma1": 1 + rand(1, d, scale=0.2), "beta1": rand(2, d, scale=0.2),
+         "w1": rand(3, f, d, dtype=BF16, scale=d ** -0.5), "b1": rand(4, f, scale=0.2),
+         "w2": rand(5, d, f, dtype=BF16, scale=f ** -0.5), "b2": rand(6, d, dtype=BF16, scale=0.2),
+         "gamma2": (1 + rand(7, d, scale=0.2)).to(BF16), "beta2": rand(8, d, dtype=BF16, scale=0.2),
+         "head": rand(9, v, d, dtype=BF16, scale=d ** -0.5)}
+    x0 = rand(10, n, d, dtype=BF16)
+    t = torch.randint(0, v, (n,), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    t[::7] = -1
+    on = t >= 0
+    dl = on.float() / on.sum()
+    step = BlockStep(LayerStep(wl, inp, variant), {k: dev(q) for k, q in p.items()}, act=act)
+    loss, got = step.step(dev(x0), dev(t), dev(dl))
+
+    P = {k: q.double().requires_grad_(True) for k, q in p.items()}
+    X = x0.double().requires_grad_(True)
+    G, th = [], []
+    for side in ("theta_r", "theta_p"):
+        th.append(torch.from_numpy(inp[side].astype(np.float64)).requires_grad_(True))
+        iu = torch.triu_indices(b, b, 1)
+        Q = torch.zeros(th[-1].shape[0], b, b, dtype=torch.float64)
+        Q = Q.index_put((torch.arange(Q.shape[0])[:, None], iu[0][None], iu[1][None]), th[-1])
+        Q = Q - Q.transpose(1, 2)
+        Q2 = Q @ Q
+        G.append(torch.eye(b, dtype=torch.float64) + 2 * (Q + Q2 + Q2 @ Q) + Q2 @ Q2)
+    W = torch.from_numpy(np.ascontiguousarray(inp["w"]).view(np.int16)).view(BF16).double()
+    pin, pout = (torch.from_numpy(inp[k].astype(np.int64)) for k in ("perm_in", "perm_out"))
+    wm = W[pout][:, pin]
+    a = F.layer_norm(X, (d,), P["gamma1"], P["beta1"], 1e-5)
+    blocks = lambda m, g: torch.cat([m[:, j * b:(j + 1) * b] @ g[j] for j in range(d // b)], 1)  # noqa: E731
+    zt = blocks(blocks(a[:, pin], G[0]) @ wm.t(), G[1])
+    z = torch.zeros_like(zt).index_copy(1, pout, zt)
+    y = F.linear(getattr(F, act)(F.linear(z, P["w1"], P["b1"])), P["w2"], P["b2"]) + X
+    h = F.layer_norm(y, (d,), P["gamma2"], P["beta2"], 1e-5)
+    ref = F.cross_entropy(F.linear(h, P["head"]), t.long(), ignore_index=-1, reduction="none")
+    leaves = dict(P, theta_r=th[0], theta_p=th[1], x0=X)
+    grads = torch.autograd.grad((ref * dl.double()).sum(), list(leaves.values()))
+    # about twenty tensors are rounded to bf16 on the way (eight forward, ten backward, both G), each
+    # by at most u = 2^-8 of an element and u / sqrt(3) in the mean square, independently, with
+    # condition numbers of a few as in test_block_step: sqrt(20 / 3) u 4
+    most = (20 / 3) ** 0.5 * U[BF16] * 4
+    assert off(loss, ref.detach()) <= most
+    for (k, _), r in zip(leaves.items(), grads):
+        assert off(got[k].reshape(r.shape), r) <= most, (k, off(got[k].reshape(r.shape), r))
