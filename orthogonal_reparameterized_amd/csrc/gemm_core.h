@@ -109,12 +109,11 @@ struct StageKM {
   static constexpr int CH = R / 8, RPI = 64 / CH, INSTR = 64 / RPI / NW;
   int voff[INSTR];
   const bf16_t *base;
-  int64_t ld, cols;
+  int64_t ld;
   __device__ void init(const bf16_t *P, int64_t ld_, int64_t col0, int64_t, int64_t kbeg) {
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
     ld = ld_;
     base = P + kbeg * ld;
-    cols = col0;
 #pragma unroll
     for (int i = 0; i < INSTR; ++i) {
       const int row = (w * INSTR + i) * RPI + l / CH;
@@ -132,18 +131,15 @@ struct StageKM {
   }
 };
 
-// Accumulator layout of one MFMA result with the operands swapped (B fragment first): lane l
-// holds row l % ROWS; element 4 q + e is column 8 q + 4 (l / ROWS) + e.
-template <class V> struct FragOf;
-template <> struct FragOf<f32x4> { static constexpr int ROWS = 16, QUADS = 1; };    // 16 x 16
+// Accumulator layout of one 16 x 16 MFMA result with the operands swapped (B fragment first):
+// lane l holds row l % 16; element e is column 4 (l / 16) + e.
 
 // The accumulators of a wave's patch (FM x FN results), handed to the epilogue as rows.  One
-// row of results at a time goes through `st`, this wave's own ROWS x (columns + 4) floats.
-template <int FM, int FN, class V, class Epi>
-__device__ inline void put_rows(const V (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, float *st,
+// row of results at a time goes through `st`, this wave's own 16 x (columns + 4) floats.
+template <int FM, int FN, class Epi>
+__device__ inline void put_rows(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, float *st,
                                 const Epi &epi, const float *rows = nullptr) {
-  constexpr int R = FragOf<V>::ROWS, Q = FragOf<V>::QUADS;
-  constexpr int W = FN * R, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
+  constexpr int R = 16, W = FN * R, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
   const int l = threadIdx.x & 63, c = (l % LPR) * 8;
   const int64_t n = n0 + c;
   const int nv = N - n >= 8 ? 8 : N - n > 0 ? (int)(N - n) : 0;
@@ -151,11 +147,7 @@ __device__ inline void put_rows(const V (&acc)[FM][FN], int64_t m0, int64_t n0, 
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-        *(f32x4 *)(st + (l % R) * LD + R * j + 8 * q + 4 * (l / R)) =
-            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    for (int j = 0; j < FN; ++j) *(f32x4 *)(st + (l % R) * LD + R * j + 4 * (l / R)) = acc[i][j];
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int p = 0; p < R / RPP; ++p) {
@@ -173,9 +165,10 @@ __device__ inline void put_rows(const V (&acc)[FM][FN], int64_t m0, int64_t n0, 
 
 // The epilogue of a kernel's BM x BN tile; lds: free, at least 16 (columns + 4) floats per wave
 // and kRows BM floats more.
-template <int BM, int BN, int WGM, int WGN, int FM, int FN, class V, class Epi>
-__device__ inline void finish(const V (&acc)[FM][FN], const MmArgs &a, const MmTile &tile, float *lds, const Epi &epi) {
-  constexpr int R = FragOf<V>::ROWS, WTM = BM / WGM, WTN = BN / WGN;
+template <int BM, int BN, int WGM, int WGN, int FM, int FN, class Epi>
+__device__ inline void finish(const f32x4 (&acc)[FM][FN], const MmArgs &a, const MmTile &tile, float *lds,
+                              const Epi &epi) {
+  constexpr int R = 16, WTM = BM / WGM, WTN = BN / WGN;
   const int64_t m0 = (int64_t)tile.tm * BM, n0 = (int64_t)tile.tn * BN;
   if constexpr (Epi::kStats) {
     epi.template reduce<BM, BN, WGM, WGN>(acc, m0, n0, a.M, a.N, tile.tn, lds);
@@ -668,8 +661,8 @@ __device__ inline void sum_parts_body(const SumArgs &a, int64_t id, float *red) 
 }
 
 // The two products of a backward pass, D W (W k-major) and D^T X (both k-major), in one launch:
-// small ones fill the GPU together and wait for one launch and one fill instead of two.
-// 513 x 1001 x 777 float32: PAIRUS.  The first has workgroups [0, ga), ga a multiple of 8 so that
+// small ones fill the GPU together and wait for one launch and one fill instead of two.  513 x
+// 1001 x 777 float32: PAIRUS.  The first has workgroups [0, ga), ga a multiple of 8 so that
 // both deal their tiles to the XCDs alike.
 template <typename T, class EA, class EB>
 __global__ __launch_bounds__(256) void k_mm_pair(MmArgs a, EA ea, MmArgs b, EB eb, SumArgs sum, int ga,

@@ -41,13 +41,13 @@ struct XentStats {
   int tile0;      // first row of `part`
   __device__ const XentStats &at(int) const { return *this; }
 
-  template <int BM, int BN, int WGM, int WGN, int FM, int FN, class V>
-  __device__ void reduce(const V (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, int tn,
+  template <int BM, int BN, int WGM, int WGN, int FM, int FN>
+  __device__ void reduce(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t N, int tn,
                          float *lds) const {
-    constexpr int R = FragOf<V>::ROWS, Q = FragOf<V>::QUADS;
+    constexpr int R = 16;
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
-    const int64_t nb = n0 + wn + 4 * (l / R);  // this lane's columns: nb + R j + 8 q + e
+    const int64_t nb = n0 + wn + 4 * (l / R);  // this lane's columns: nb + R j + e
     const int left = N - nb < 65536 ? (int)(N - nb) : 65536;
     float2 *st = (float2 *)lds;                // [WGN][BM]
 #pragma unroll
@@ -60,22 +60,18 @@ struct XentStats {
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = R * j + 8 * q + e;
-            const float v = c < left ? acc[i][j][4 * q + e] : -INFINITY;
-            if (t == c) at_target[m] = v;
-            mx = fmaxf(mx, v);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int c = R * j + e;
+          const float v = c < left ? acc[i][j][e] : -INFINITY;
+          if (t == c) at_target[m] = v;
+          mx = fmaxf(mx, v);
+        }
       const float ref = safe_ref(mx);
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s += R * j + 8 * q + e < left ? __expf(acc[i][j][4 * q + e] - ref) : 0.f;
+        for (int e = 0; e < 4; ++e) s += R * j + e < left ? __expf(acc[i][j][e] - ref) : 0.f;
 #pragma unroll
       for (int o = R; o <= 32; o <<= 1) {
         const float m2 = __shfl_xor(mx, o), s2 = __shfl_xor(s, o);
