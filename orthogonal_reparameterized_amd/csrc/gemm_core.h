@@ -287,13 +287,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
 // the next phase reads have landed for all waves, and those just read may be overwritten.
 // Loads past the k range read zeros.
 //
-// What bounds it: the chip's power.  At 8192^3 the matrix cores are busy 0.83 of the time at a
-// clock of 1.74 GHz (the vendor library: 0.88 at 1.78); 1.47 PFLOP/s with both operands
-// k-contiguous, 1.40 with a k-major B, 1.34 with both k-major (those issue two 8-byte
-// transposing LDS reads per fragment instead of one of 16 bytes; library 1.63).  One phase of 16
-// MFMAs per pair of halves instead of one of 32 per A half: 1.40, 1.30 and 1.25.  32 x 32 x 16
-// MFMAs in the same schedule were 2 to 6 % slower, four waves of 128 x 128 30 % (the compiler
-// moves accumulators between register files).
+// What bounds it: the chip's power.  At 8192^3, 20 calls in a row, it runs at 1.45 PFLOP/s at best
+// and 1.31 in the median with both operands k-contiguous (the vendor library 1.56 and 1.42), the
+// matrix cores busy 0.82 of the time (library 0.87) at a clock that falls to about 1.4 GHz under
+// either; with a k-major B 1.40 and 1.38 (library 1.36 and 1.24), with both k-major 1.33 and 1.32
+// (those issue two 8-byte transposing LDS reads per fragment instead of one of 16 bytes).  Where
+// the three forms ran at 1.47, 1.40 and 1.34, one phase of 16 MFMAs per pair of halves instead of
+// one of 32 per A half gave 1.40, 1.30 and 1.25; 32 x 32 x 16 MFMAs in the same schedule were 2 to
+// 6 % slower, four waves of 128 x 128 30 % (the compiler moves accumulators between register files).
 template <int HALF_ROWS, bool KM>
 struct Half;
 
@@ -662,7 +663,7 @@ __device__ inline void sum_parts_body(const SumArgs &a, int64_t id, float *red) 
 
 // The two products of a backward pass, D W (W k-major) and D^T X (both k-major), in one launch:
 // small ones fill the GPU together and wait for one launch and one fill instead of two.  513 x
-// 1001 x 777 float32: PAIRUS.  The first has workgroups [0, ga), ga a multiple of 8 so that
+// 1001 x 777 float32: 32 us for both.  The first has workgroups [0, ga), ga a multiple of 8 so that
 // both deal their tiles to the XCDs alike.
 template <typename T, class EA, class EB>
 __global__ __launch_bounds__(256) void k_mm_pair(MmArgs a, EA ea, MmArgs b, EB eb, SumArgs sum, int ga,

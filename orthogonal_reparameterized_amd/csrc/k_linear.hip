@@ -19,7 +19,7 @@ constexpr float kTanhC = 0.79788456080286536f, kTanhA = 0.044715f;  // sqrt(2 / 
 // them.  bf16: one hardware exp and one reciprocal each (relative errors of about 2^-22, and of
 // 2^-24 of exp's argument, far below the rounding of the result), not the library's erf and tanh
 // (whose epilogue took 31 us of a 130 us round of 256 x 256 tiles, k = 4096; 8192 tokens, 4096 ->
-// 14336 with GELU and the kept pre-activation: 904 us then, 733 us now).  float32, whose products
+// 14336 with GELU and the kept pre-activation: 904 us then, 743 us now).  float32, whose products
 // run at a tenth of the rate: the library's functions, a few units in the last place (2048 tokens,
 // 1024 -> 4096 with GELU 159 us, 155 us with the forms for bf16).
 template <typename T> struct Fn;

@@ -9,9 +9,9 @@
 // through the workspace first.)  Backward: the
 // logits of a piece of the vocabulary are computed again and leave the epilogue as dl (bf16
 // for bf16 operands, the operand type of the two products that read it), then dh += dl W and
-// dW of the piece follow while dl is in the caches.  8 n d v flops in all, where keeping the
-// logits would take 6 n d v and n v values of memory.  Bound by the matrix cores for many
-// tokens (4096 x 4096 x 65536: forward 1.52, dl 1.59, dh 1.54, dW 1.71 ms, 1.29 to 1.45 PFLOP/s)
+// dW of the piece follow while dl is in the caches.  8 n d v flops in all, chosen for the memory
+// (keeping the logits would take 6 n d v and n v values).  Bound by the matrix cores for many
+// tokens (4096 x 4096 x 65536: forward 1.59, dl 1.63, dh 1.55, dW 1.70 ms, 1.29 to 1.41 PFLOP/s)
 // and by reading W for few.
 #include "gemm_core.h"
 
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(256) void k_xent_parts(const float *src, int splits
 // each takes every KW-th turn of the group's k (the next U fragments in flight while these
 // multiply) and keeps (max, sum) per lane (row l % 16, its 4 columns of the group); one partial per
 // workgroup.  KW = 1 walks groups and keeps a running (max, sum): 8 tokens, d = 4096, 131072 rows,
-// bf16: 199 us, 5.4 TB/s, the rate of a large copy (242 us without the loads ahead; 222 us with
+// bf16: 206 us, 5.2 TB/s, the rate of a large copy (242 us without the loads ahead; 222 us with
 // half or twice the workgroups).
 template <typename T, int KW, bool ODD>
 __global__ __launch_bounds__(512) void k_xent_few(MmArgs a, XentStats epi) {
