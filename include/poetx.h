@@ -396,6 +396,117 @@ int poetx_xent_backward(int64_t n_tokens, int64_t d, int64_t vocab, int32_t dtyp
                         const int32_t *target, const float *lse, const float *dloss, void *dh, void *dw, void *ws,
                         size_t *ws_bytes, void *stream);
 
+/*
+ * Operators of a fine-tuning step.  The block's gated feed-forward part, a clipped policy loss
+ * on the log-probabilities that poetx_xent_forward's losses are (its gradient is
+ * poetx_xent_backward's dloss), and the norm of all gradients with clipping, which comes before
+ * poetx_adam_step.  The conventions are those of the operators around the layer.
+ */
+
+/*
+ * poetx_glu_forward -- gated feed-forward projections:
+ *     g = x . w_gate^T,  u = x . w_up^T,  h = act(g) u
+ * x: [n_tokens][d]; w_gate, w_up: [d_ff][d]; act: a poetx_act (POETX_ACT_NONE: the bilinear
+ * form); h: [n_tokens][d_ff].  gate, up: outputs g and u [n_tokens][d_ff], rounded to dtype, for
+ * the backward, both or neither (h itself takes the unrounded g and u).  Any widths; bf16 widths
+ * d that are not multiples of 8 are copied to padded rows in the workspace (not for n_tokens <=
+ * 16).  n_tokens == 0 is a no-op.  Workspace: query with ws == NULL (it may depend on the current
+ * device).  Errors: NULL x, w_gate, w_up or h, one of gate and up without the other, n_tokens < 0,
+ * bad enum, misaligned pointer, an output that equals an input or another output -> INVALID_ARG;
+ * d or d_ff < 1 -> POETX_ERR_SHAPE; d or d_ff > 2^20, or more than 2^22 tiles of 128 x 128
+ * results -> UNSUPPORTED.
+ */
+int poetx_glu_forward(int64_t n_tokens, int64_t d, int64_t d_ff, int32_t dtype, const void *x, const void *w_gate,
+                      const void *w_up, int32_t act, void *h, void *gate, void *up, void *ws, size_t *ws_bytes,
+                      void *stream);
+
+/*
+ * poetx_glu_backward -- from dh = dL/dh and the forward's gate and up:
+ *     dg = dh u act'(g),  du = dh act(g),
+ *     dx = dg . w_gate + du . w_up,  dw_gate = dg^T . x,  dw_up = du^T . x
+ * dx: [n_tokens][d], nullable; dw_gate, dw_up: [d_ff][d], both or neither; all in dtype, not all
+ * NULL.  With n_tokens == 0, dw_gate and dw_up are zeros.  For bf16 the products read dg and du
+ * rounded to bf16; dx is one sum over both, rounded once.  x may be NULL without dw_gate, the
+ * weights without dx.  Workspace: query with ws == NULL, with the same output pointers NULL or
+ * not.  Errors: as the forward.
+ */
+int poetx_glu_backward(int64_t n_tokens, int64_t d, int64_t d_ff, int32_t dtype, const void *x, const void *w_gate,
+                       const void *w_up, const void *dh, const void *gate, const void *up, int32_t act, void *dx,
+                       void *dw_gate, void *dw_up, void *ws, size_t *ws_bytes, void *stream);
+
+/* how poetx_policy_loss adds its tokens up */
+typedef enum { POETX_REDUCE_TOKEN = 0, POETX_REDUCE_SEQUENCE = 1, POETX_REDUCE_SUM = 2 } poetx_reduce;
+
+typedef struct {
+  double clip_low, clip_high;  /* lo and hi: the ratio is clipped to [1 - lo, 1 + hi]; both >= 0,
+                                  infinity for no bound (a lo of 1 or more is none either)   */
+  double beta;                 /* weight of the KL term                                       */
+  double scale;                /* factor of dnll (1 / accumulation steps), not of stats       */
+  int32_t reduce;              /* a poetx_reduce                                              */
+  int32_t adv_per_token;       /* 0: adv is [n_seqs], else [n_tokens]                         */
+} poetx_policy;
+
+/*
+ * poetx_policy_loss -- clipped policy loss with a KL term, and its gradient, from the tokens'
+ * negative log-probabilities nll_i under the current weights (poetx_xent_forward's loss), under
+ * the weights that sampled them (nll_old) and under a reference (nll_ref), with advantages A:
+ *     r_i = exp(nll_old_i - nll_i),      pg_i = -min(r_i A_i, clip(r_i, 1 - lo, 1 + hi) A_i),
+ *     e_i = nll_i - nll_ref_i,           kl_i = exp(e_i) - e_i - 1,
+ *     loss = mean(pg) + beta mean(kl),   dnll_i = scale dloss / dnll_i
+ * where a ratio that the minimum holds at its border has no gradient.  The mean is over the
+ * tokens that count, m_i = 1, by reduce:
+ *     TOKEN     sum_i m_i v_i / max(sum_i m_i, 1)
+ *     SEQUENCE  1 / n_seqs  sum_s ( sum_{i in s} m_i v_i / max(sum_{i in s} m_i, 1) )
+ *     SUM       sum_i m_i v_i
+ * offsets: [n_seqs + 1] int64, ascending: sequence s is tokens [offsets[s], offsets[s + 1]) (empty
+ * ones may occur); NULL with n_seqs == 1: all tokens.  mask (nullable): [n_tokens] bytes, 0 for a
+ * token that does not count.  Tokens outside every sequence do not count.  A token that does not
+ * count gets dnll 0 and adds nothing, whatever its other values hold.  nll_old NULL: r = 1 (the
+ * weights are those that sampled).  nll_ref NULL: no KL term (kl 0, beta must be 0).
+ * adv: float32 [n_seqs], or [n_tokens] with adv_per_token.  stats: float32 [4] output: loss,
+ * mean(pg), mean(kl), and the mean of 1 for held ratios, 0 else.  dnll: float32 [n_tokens] output,
+ * nullable.  Ratios are compared with their borders in 64 bits, sums over tokens are taken there.
+ * offsets that do not ascend, or lie outside [0, n_tokens], give unspecified results but no access
+ * out of bounds.  Workspace: query with ws == NULL.  Errors: NULL p, nll, adv or stats, offsets NULL
+ * with n_seqs != 1, beta without nll_ref, negative or NaN bounds, beta or scale not finite, bad
+ * reduce, n_tokens or n_seqs < 0, misaligned pointer, an output that equals an input or the other
+ * output -> INVALID_ARG; more than 2^31 - 1 tokens or sequences -> UNSUPPORTED.
+ */
+int poetx_policy_loss(int64_t n_tokens, int64_t n_seqs, const int64_t *offsets, const float *nll,
+                      const float *nll_old, const float *nll_ref, const float *adv, const uint8_t *mask,
+                      const poetx_policy *p /*[host]*/, float *stats, float *dnll, void *ws, size_t *ws_bytes,
+                      void *stream);
+
+/* [host] one gradient of a list: n elements of dtype (F32 or BF16) at g; where the clipped ones go */
+typedef struct {
+  const void *g;
+  void *out;      /* g itself (in place) or a buffer that overlaps no gradient of the list */
+  int64_t n;
+  int32_t dtype;
+} poetx_grad;
+
+/*
+ * poetx_grad_norm -- norm of all gradients of a list together, and the factor that clips it:
+ *     norm = sqrt(sum_k sum_i g_k[i]^2),  coef = 1 if norm <= max_norm, else max_norm / norm
+ * grads [host]: read during the call.  Its device pointers need only be aligned to their elements;
+ * gradients with n == 0 are passed over (their pointers may be NULL), `out` is not used.  Types may
+ * be mixed.  max_norm >= 0, infinity for the norm alone.  norm, coef: float32 device outputs, 4-byte
+ * aligned.  Squares and their sum are taken in 64 bits.  A NaN anywhere makes both NaN; an infinity
+ * makes norm infinite and coef 0.  n_grads == 0: norm 0, coef 1.  Workspace: query with ws == NULL
+ * (the same lengths).  Errors: NULL grads, g, norm or coef, a length < 0, bad dtype, misaligned
+ * pointer, max_norm < 0 or NaN -> INVALID_ARG; more than 2^20 gradients or 2^48 elements -> UNSUPPORTED.
+ */
+int poetx_grad_norm(int64_t n_grads, const poetx_grad *grads /*[host]*/, float max_norm, float *norm, float *coef,
+                    void *ws, size_t *ws_bytes, void *stream);
+
+/*
+ * poetx_grad_clip -- poetx_grad_norm, then out_k = coef g_k (rounded to its dtype) for every gradient.
+ * In place with out == g: a gradient is then not touched where coef is 1.  The list must not name
+ * the same elements twice as out.  Errors: as poetx_grad_norm; NULL out -> INVALID_ARG.
+ */
+int poetx_grad_clip(int64_t n_grads, const poetx_grad *grads /*[host]*/, float max_norm, float *norm, float *coef,
+                    void *ws, size_t *ws_bytes, void *stream);
+
 /* Human-readable name of a poetx_status code (static string). */
 const char *poetx_status_string(int status);
 

@@ -9,7 +9,9 @@ fallback path.
 Python names mirror the C entry points:
     poetx_merge_perm, poetx_cnp, poetx_forward, poetx_backward,
     poetx_layernorm_forward / _backward, poetx_linear_forward / _backward,
-    poetx_xent_forward / _backward (the operators around the layer)
+    poetx_xent_forward / _backward (the operators around the layer),
+    poetx_glu_forward / _backward, poetx_policy_loss, poetx_grad_norm, poetx_grad_clip
+    (those of a fine-tuning step)
 plus ``Layer`` (the poetx_layer descriptor) and the measurement hooks.
 """
 
@@ -38,6 +40,8 @@ POETX_FAST, POETX_MEM = 0, 1
 POETX_CNP_FWD, POETX_CNP_BWD = 0, 1
 POETX_ACT_NONE, POETX_ACT_RELU, POETX_ACT_GELU, POETX_ACT_GELU_TANH, POETX_ACT_SILU = 0, 1, 2, 3, 4
 
+POETX_REDUCE_TOKEN, POETX_REDUCE_SEQUENCE, POETX_REDUCE_SUM = 0, 1, 2
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 
 
@@ -57,6 +61,17 @@ class PoetxAdamC(ctypes.Structure):
         ("gamma", ctypes.c_float), ("step", _i64),
         ("m_r", _vp), ("v_r", _vp), ("m_p", _vp), ("v_p", _vp), ("theta_r_out", _vp), ("theta_p_out", _vp),
     ]
+
+
+class PoetxPolicyC(ctypes.Structure):
+    _fields_ = [
+        ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("beta", ctypes.c_double),
+        ("scale", ctypes.c_double), ("reduce", _i32), ("adv_per_token", _i32),
+    ]
+
+
+class PoetxGradC(ctypes.Structure):
+    _fields_ = [("g", _vp), ("out", _vp), ("n", _i64), ("dtype", _i32)]
 
 
 _lib.poetx_merge_perm.argtypes = [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -81,6 +96,12 @@ _lib.poetx_linear_forward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _i3
 _lib.poetx_linear_backward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _szp, _vp]
 _lib.poetx_xent_forward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp]
 _lib.poetx_xent_backward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_glu_forward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_glu_backward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp,
+                                    _szp, _vp]
+_lib.poetx_policy_loss.argtypes = [_i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_grad_norm.argtypes = [_i64, _vp, ctypes.c_float, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_grad_clip.argtypes = [_i64, _vp, ctypes.c_float, _vp, _vp, _vp, _szp, _vp]
 _lib.poetx_status_string.argtypes = [ctypes.c_int]
 _lib.poetx_status_string.restype = ctypes.c_char_p
 _lib.poetx_version.restype = ctypes.c_char_p
@@ -89,13 +110,15 @@ _lib.poetx_prof_read.argtypes = [ctypes.c_char_p, _sz]
 _lib.poetx_prof_only.argtypes = [ctypes.c_char_p]
 for _f in ("poetx_merge_perm", "poetx_cnp", "poetx_cnp_noalloc", "poetx_forward", "poetx_backward", "poetx_backward_adam", "poetx_fold",
            "poetx_adam_step", "poetx_layernorm_forward", "poetx_layernorm_backward", "poetx_linear_forward",
-           "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward",
+           "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward", "poetx_glu_forward",
+           "poetx_glu_backward", "poetx_policy_loss", "poetx_grad_norm", "poetx_grad_clip",
            "poetx_prof_enable", "poetx_prof_only", "poetx_prof_read"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("poetx_merge_perm", "poetx_cnp", "poetx_cnp_noalloc", "poetx_forward", "poetx_backward", "poetx_backward_adam", "poetx_fold",
             "poetx_adam_step", "poetx_layernorm_forward", "poetx_layernorm_backward", "poetx_linear_forward",
-            "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward",
+            "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward", "poetx_glu_forward",
+            "poetx_glu_backward", "poetx_policy_loss", "poetx_grad_norm", "poetx_grad_clip",
             "poetx_status_string", "poetx_version", "poetx_prof_enable", "poetx_prof_only", "poetx_prof_read")
 
 
@@ -530,9 +553,10 @@ _current_device = torch.cuda.current_device
 _byref = ctypes.byref
 
 
-def _run(fn, dev: torch.device, args: tuple, query: Optional[tuple] = None) -> None:
+def _run(fn, dev: torch.device, args: tuple, query=None) -> None:
     """The call on dev's current stream, with its workspace when `query` has its size query's
-    arguments.  The library launches on the current device, so that is made dev's."""
+    arguments (or the size itself).  The library launches on the current device, so that is made
+    dev's."""
     idx = dev.index
     if dev.type != "cuda":
         raise ValueError("tensors must be on the GPU")
@@ -542,7 +566,7 @@ def _run(fn, dev: torch.device, args: tuple, query: Optional[tuple] = None) -> N
     if query is None:
         code = fn(*args, _raw_stream(idx))
     else:
-        ws = _workspace(dev, _ws_query(fn.__name__, idx, query))
+        ws = _workspace(dev, query if type(query) is int else _ws_query(fn.__name__, idx, query))
         code = fn(*args, ws.data_ptr(), _byref(_sz(ws.numel())), _raw_stream(idx))
     if code != POETX_OK:
         _check(code, fn.__name__)
@@ -691,6 +715,177 @@ def poetx_xent_backward(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor, 
           out["dw"].data_ptr() if want_dw else None),
          (n, d, vocab, code, None, None, None, None, None, _SOME if want_dh else None, _SOME if want_dw else None))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators of a fine-tuning step: gated feed-forward projections, clipped policy loss, gradient
+# norm and clipping.
+# ---------------------------------------------------------------------------
+def poetx_glu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act="silu", *,
+                      h: Optional[torch.Tensor] = None, save: bool = False):
+    """act(x . w_gate^T) (x . w_up^T).  Returns (h, gate, up): gate and up, the two projections, for
+    the backward when save is set, else None.  act: as in poetx_linear_forward."""
+    n, d = _tokens(x, "x")
+    dev, dt = x.device, (x.dtype,)
+    f = w_gate.shape[0]
+    a = _act(act)
+    shape = x.shape[:-1] + (f,)
+    ins = (_buf(x, "x", x.shape, _FLOATS, dev), _buf(w_gate, "w_gate", (f, d), dt, dev),
+           _buf(w_up, "w_up", (f, d), dt, dev))
+    h, ph = _out(h, "h", shape, x.dtype, x)
+    gate = up = pg = pu = None
+    if save:
+        gate, up = torch.empty_like(h), torch.empty_like(h)
+        pg, pu = gate.data_ptr(), up.data_ptr()
+    code, some = _DT[x.dtype], _SOME if save else None
+    _run(_lib.poetx_glu_forward, dev, (n, d, f, code, *ins, a, ph, pg, pu),
+         (n, d, f, code, None, None, None, a, None, some, some))
+    return h, gate, up
+
+
+def poetx_glu_backward(x: Optional[torch.Tensor], w_gate: Optional[torch.Tensor], w_up: Optional[torch.Tensor],
+                       dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, act="silu", *, want_dx: bool = True,
+                       want_dw: bool = True):
+    """Returns dict with those of dx and (dw_gate, dw_up) that are wanted, in dh's dtype.  gate, up:
+    what poetx_glu_forward(save=True) returned.  x is needed for dw, the weights for dx."""
+    n, f = _tokens(dh, "dh")
+    dev, dt = dh.device, (dh.dtype,)
+    a = _act(act)
+    if not (want_dx or want_dw):
+        raise ValueError("neither dx nor dw is wanted")
+    if want_dx and (w_gate is None or w_up is None) or want_dw and x is None:
+        raise ValueError("dx needs w_gate and w_up, dw needs x")
+    if gate is None or up is None:
+        raise ValueError("gate and up are required")
+    d = (x if x is not None else w_gate).shape[-1]
+    shape = dh.shape[:-1] + (d,)
+    pdh = _buf(dh, "dh", dh.shape, _FLOATS, dev)
+    ins = (_buf(x, "x", shape, dt, dev), _buf(w_gate, "w_gate", (f, d), dt, dev), _buf(w_up, "w_up", (f, d), dt, dev),
+           pdh, _buf(gate, "gate", dh.shape, dt, dev), _buf(up, "up", dh.shape, dt, dev))
+    out, ptrs = {}, [None, None, None]
+    if want_dx:
+        out["dx"] = dh.new_empty(shape)
+        ptrs[0] = out["dx"].data_ptr()
+    if want_dw:
+        out["dw_gate"], out["dw_up"] = dh.new_empty((f, d)), dh.new_empty((f, d))
+        ptrs[1:] = out["dw_gate"].data_ptr(), out["dw_up"].data_ptr()
+    if n == 0 and not want_dw:
+        return out
+    code = _DT[dh.dtype]
+    _run(_lib.poetx_glu_backward, dev, (n, d, f, code, *ins, a, *ptrs),
+         (n, d, f, code, None, None, None, None, None, None, a, *(None if p is None else _SOME for p in ptrs)))
+    return out
+
+
+_REDUCE = {"token": POETX_REDUCE_TOKEN, "sequence": POETX_REDUCE_SEQUENCE, "sum": POETX_REDUCE_SUM}
+_FLAGS = (torch.bool, torch.uint8)
+_I64 = (torch.int64,)
+
+
+@functools.lru_cache(maxsize=64)
+def _policy(low: float, high: float, beta: float, scale: float, reduce: int, per_token: bool):
+    """A pointer to the parameters, which it keeps alive."""
+    return _byref(PoetxPolicyC(low, high, beta, scale, reduce, int(per_token)))
+
+
+def poetx_policy_loss(nll: torch.Tensor, adv: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
+                      nll_old: Optional[torch.Tensor] = None, nll_ref: Optional[torch.Tensor] = None,
+                      mask: Optional[torch.Tensor] = None, per_token: bool = False, clip=(0.2, 0.2),
+                      beta: float = 0.0, reduce: str = "token", scale: float = 1.0, want_grad: bool = True,
+                      dnll: Optional[torch.Tensor] = None):
+    """Clipped policy loss with a KL term on negative log-probabilities, float32, one per token
+    (poetx_xent_forward's loss).  Returns (stats, dnll): stats float32 [4], loss, its policy part,
+    the KL and the share of ratios held at a border; dnll the loss's gradient (None without
+    want_grad), poetx_xent_backward's dloss.  adv: float32, one per sequence, or per token with
+    per_token.  offsets: int64 [sequences + 1], where each sequence begins in nll's flat order and
+    the last ends; None: one sequence of all tokens.  mask: bool or uint8 like nll, 0 for a token
+    that does not count.  nll_old None: on-policy, ratio 1; nll_ref None: no KL.  reduce: "token",
+    "sequence" or "sum"; clip: (low, high), the ratio's way below and above 1; scale: a factor of dnll."""
+    dev, shape, n = nll.device, nll.shape, nll.numel()
+    if reduce not in _REDUCE:
+        raise ValueError(f"reduce: {reduce!r}, expected one of {tuple(_REDUCE)}")
+    if beta != 0 and nll_ref is None:
+        raise ValueError("beta needs nll_ref")
+    low, high = clip
+    seqs = 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected [sequences + 1]")
+        seqs = offsets.numel() - 1
+    ins = (_buf(offsets, "offsets", (seqs + 1,), _I64, dev), _buf(nll, "nll", shape, _F32, dev),
+           _buf(nll_old, "nll_old", shape, _F32, dev), _buf(nll_ref, "nll_ref", shape, _F32, dev),
+           _buf(adv, "adv", shape if per_token else (seqs,), _F32, dev), _buf(mask, "mask", shape, _FLAGS, dev))
+    p = _policy(float(low), float(high), float(beta), float(scale), _REDUCE[reduce], bool(per_token))
+    stats = nll.new_empty(4)
+    pd = None
+    if want_grad or dnll is not None:
+        dnll, pd = _out(dnll, "dnll", None, torch.float32, nll)
+    _run(_lib.poetx_policy_loss, dev, (n, seqs, *ins, p, stats.data_ptr(), pd),
+         (n, seqs, None, None, None, None, None, _SOME if mask is not None else None, p, None, None))
+    return stats, dnll
+
+
+class GradList:
+    """The gradients of a training step, for poetx_grad_norm and poetx_grad_clip: contiguous float32
+    or bf16 tensors on one device, of any shapes.  out: where the clipped gradients go, tensors like
+    them that share no memory with them; None: in place.  The list keeps its tensors; a program
+    whose gradients stay where they are makes it once."""
+
+    def __init__(self, grads, out=None):
+        self.grads = tuple(grads)
+        self.out = None if out is None else tuple(out)
+        if self.out is not None and len(self.out) != len(self.grads):
+            raise ValueError(f"out: {len(self.out)} tensors, expected {len(self.grads)}")
+        if not self.grads:
+            raise ValueError("no gradients")
+        self.device = self.grads[0].device
+        self.array = (PoetxGradC * len(self.grads))()
+        for k, g in enumerate(self.grads):
+            o = g if self.out is None else self.out[k]
+            for t, name in ((g, f"gradient {k}"), (o, f"out {k}")):
+                if t.dtype not in _FLOATS:
+                    raise ValueError(f"{name}: dtype {t.dtype}, expected one of {_FLOATS}")
+                if t.device != self.device:
+                    raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError(f"out {k}: {o.dtype} {tuple(o.shape)}, expected {g.dtype} {tuple(g.shape)}")
+            self.array[k] = PoetxGradC(g.data_ptr(), o.data_ptr(), g.numel(), _DT[g.dtype])
+        # every element is written once, and none that another gradient is read from
+        spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                 for t in self.grads + (self.out or ()) if t.numel()]
+        spans.sort()
+        for (_, end), (begin, _) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError("gradients" + ("" if self.out is None else " and out") + " share memory")
+        need = _sz(0)
+        _check(_lib.poetx_grad_norm(len(self.grads), self.array, 0.0, None, None, None, _byref(need), None),
+               "poetx_grad_norm(size)")
+        self.workspace_bytes = need.value
+
+
+def _grad_call(fn, grads, max_norm: float, out=None):
+    if not isinstance(grads, GradList):
+        grads = GradList(grads, out)
+    elif out is not None:
+        raise ValueError("out is the list's own")
+    r = torch.empty(2, dtype=torch.float32, device=grads.device)
+    p = r.data_ptr()
+    _run(fn, grads.device, (len(grads.grads), grads.array, max_norm, p, p + 4), grads.workspace_bytes)
+    return r[0], r[1]
+
+
+def poetx_grad_norm(grads, max_norm: float = float("inf")):
+    """(norm, coef), float32 scalars on the device: the norm of all gradients together, and the
+    factor min(1, max_norm / norm) that clips them.  grads: a GradList or a sequence of tensors."""
+    return _grad_call(_lib.poetx_grad_norm, grads, max_norm)
+
+
+def poetx_grad_clip(grads, max_norm: float, out=None):
+    """poetx_grad_norm, and the gradients times coef, in place or into out (a GradList has its
+    own).  Returns (norm, coef)."""
+    return _grad_call(_lib.poetx_grad_clip, grads, max_norm, out)
 
 
 def prof_enable(on: bool = True):

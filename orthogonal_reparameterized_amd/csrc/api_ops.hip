@@ -184,3 +184,126 @@ extern "C" int poetx_xent_backward(int64_t n_tokens, int64_t d, int64_t vocab, i
   if (!distinct({dh, dw}, {h, w, target, lse, dloss})) return POETX_ERR_INVALID_ARG;
   return xent_backward(x, ar, false, (hipStream_t)stream);
 }
+
+namespace {
+int glu_shape(int64_t n, int64_t d, int64_t f, int32_t dtype, int32_t act) {
+  if (n < 0 || !float_dtype(dtype)) return POETX_ERR_INVALID_ARG;
+  if (act < POETX_ACT_NONE || act > POETX_ACT_SILU) return POETX_ERR_INVALID_ARG;
+  if (d < 1 || f < 1) return POETX_ERR_SHAPE;
+  if (d > kMaxWidth || f > kMaxWidth || n > ((int64_t)1 << 40)) return POETX_ERR_UNSUPPORTED;
+  // both projections side by side, each up to 63 rows longer than it is
+  const int64_t f2 = 2 * (f + 63);
+  if (!tiles_fit(n, f2) || !tiles_fit(n, d) || !tiles_fit(f2, d)) return POETX_ERR_UNSUPPORTED;
+  return POETX_OK;
+}
+}  // namespace
+
+extern "C" int poetx_glu_forward(int64_t n_tokens, int64_t d, int64_t d_ff, int32_t dtype, const void *x,
+                                 const void *w_gate, const void *w_up, int32_t act, void *h, void *gate, void *up,
+                                 void *ws, size_t *ws_bytes, void *stream) {
+  POETX_TRY(glu_shape(n_tokens, d, d_ff, dtype, act));
+  if (!ws_bytes || !gate != !up) return POETX_ERR_INVALID_ARG;
+  GluDesc g;
+  g.n = n_tokens; g.d = d; g.f = d_ff; g.dt = dtype; g.act = act;
+  g.x = x; g.wg = w_gate; g.wu = w_up; g.h = h; g.gate = gate; g.up = up;
+  Arena need(nullptr), ar(ws);
+  POETX_TRY(glu_forward(g, need, true, nullptr));
+  bool query;
+  POETX_TRY(ws_check(ws, ws_bytes, need.used, &query));
+  if (query || n_tokens == 0) return POETX_OK;
+  if (!x || !w_gate || !w_up || !h || !aligned({x, w_gate, w_up, h, gate, up, ws})) return POETX_ERR_INVALID_ARG;
+  if (!distinct({h, gate, up}, {x, w_gate, w_up})) return POETX_ERR_INVALID_ARG;
+  return glu_forward(g, ar, false, (hipStream_t)stream);
+}
+
+extern "C" int poetx_glu_backward(int64_t n_tokens, int64_t d, int64_t d_ff, int32_t dtype, const void *x,
+                                  const void *w_gate, const void *w_up, const void *dh, const void *gate,
+                                  const void *up, int32_t act, void *dx, void *dw_gate, void *dw_up, void *ws,
+                                  size_t *ws_bytes, void *stream) {
+  POETX_TRY(glu_shape(n_tokens, d, d_ff, dtype, act));
+  if (!ws_bytes || !dw_gate != !dw_up || (!dx && !dw_gate)) return POETX_ERR_INVALID_ARG;
+  GluDesc g;
+  g.n = n_tokens; g.d = d; g.f = d_ff; g.dt = dtype; g.act = act;
+  g.x = x; g.wg = w_gate; g.wu = w_up; g.dh = dh; g.gate_in = gate; g.up_in = up;
+  g.dx = dx; g.dwg = dw_gate; g.dwu = dw_up;
+  Arena need(nullptr), ar(ws);
+  POETX_TRY(glu_backward(g, need, true, nullptr));
+  bool query;
+  POETX_TRY(ws_check(ws, ws_bytes, need.used, &query));
+  if (query) return POETX_OK;
+  if (n_tokens > 0 && (!dh || !gate || !up || (dx && (!w_gate || !w_up)) || (dw_gate && !x)))
+    return POETX_ERR_INVALID_ARG;
+  if (!aligned({x, w_gate, w_up, dh, gate, up, dx, dw_gate, dw_up, ws})) return POETX_ERR_INVALID_ARG;
+  if (!distinct({dx, dw_gate, dw_up}, {x, w_gate, w_up, dh, gate, up})) return POETX_ERR_INVALID_ARG;
+  return glu_backward(g, ar, false, (hipStream_t)stream);
+}
+
+extern "C" int poetx_policy_loss(int64_t n_tokens, int64_t n_seqs, const int64_t *offsets, const float *nll,
+                                 const float *nll_old, const float *nll_ref, const float *adv, const uint8_t *mask,
+                                 const poetx_policy *p, float *stats, float *dnll, void *ws, size_t *ws_bytes,
+                                 void *stream) {
+  if (!p || !ws_bytes || n_tokens < 0 || n_seqs < 0) return POETX_ERR_INVALID_ARG;
+  if (p->reduce < POETX_REDUCE_TOKEN || p->reduce > POETX_REDUCE_SUM) return POETX_ERR_INVALID_ARG;
+  if (!(p->clip_low >= 0) || !(p->clip_high >= 0)) return POETX_ERR_INVALID_ARG;
+  if (!std::isfinite(p->beta) || !std::isfinite(p->scale)) return POETX_ERR_INVALID_ARG;
+  if (n_tokens > kPolicyMaxTokens || n_seqs > kPolicyMaxTokens) return POETX_ERR_UNSUPPORTED;
+  PolicyDesc d;
+  d.n = n_tokens; d.seqs = n_seqs; d.offsets = offsets;
+  d.nll = nll; d.old = nll_old; d.ref = nll_ref; d.adv = adv; d.mask = mask;
+  d.reduce = p->reduce; d.per_token = p->adv_per_token != 0;
+  d.low = p->clip_low < 1 ? std::log1p(-p->clip_low) : -INFINITY;
+  d.high = std::log1p(p->clip_high);
+  d.r_low = (float)(1 - p->clip_low); d.r_high = (float)(1 + p->clip_high);
+  d.beta = (float)p->beta; d.scale = p->scale;
+  d.stats = stats; d.dnll = dnll;
+  Arena need(nullptr), ar(ws);
+  POETX_TRY(policy_loss(d, need, true, nullptr));
+  bool query;
+  POETX_TRY(ws_check(ws, ws_bytes, need.used, &query));
+  if (query) return POETX_OK;
+  if (!stats || (n_tokens > 0 && (!nll || (!adv && (n_seqs > 0 || d.per_token))))) return POETX_ERR_INVALID_ARG;
+  if ((!offsets && n_seqs != 1) || (!nll_ref && p->beta != 0)) return POETX_ERR_INVALID_ARG;
+  if (!aligned({offsets, nll, nll_old, nll_ref, adv, mask, stats, dnll, ws})) return POETX_ERR_INVALID_ARG;
+  if (!distinct({stats, dnll}, {offsets, nll, nll_old, nll_ref, adv, mask})) return POETX_ERR_INVALID_ARG;
+  return policy_loss(d, ar, false, (hipStream_t)stream);
+}
+
+namespace {
+int grad_call(int64_t n, const poetx_grad *g, float max_norm, float *norm, float *coef, bool clip, void *ws,
+              size_t *ws_bytes, void *stream) {
+  if (n < 0 || (n > 0 && !g) || !ws_bytes || !(max_norm >= 0.f)) return POETX_ERR_INVALID_ARG;
+  if (n > kGradMaxList) return POETX_ERR_UNSUPPORTED;
+  int64_t total = 0;
+  for (int64_t k = 0; k < n; ++k) {
+    if (g[k].n < 0 || !float_dtype(g[k].dtype)) return POETX_ERR_INVALID_ARG;
+    if (g[k].n > kGradMaxTotal - total) return POETX_ERR_UNSUPPORTED;
+    total += g[k].n;
+  }
+  GradDesc d;
+  d.n = n; d.g = g; d.max_norm = max_norm; d.clip = clip; d.norm = norm; d.coef = coef;
+  Arena need(nullptr), ar(ws);
+  POETX_TRY(grad_norm(d, need, true, nullptr));
+  bool query;
+  POETX_TRY(ws_check(ws, ws_bytes, need.used, &query));
+  if (query) return POETX_OK;
+  for (int64_t k = 0; k < n; ++k) {
+    if (g[k].n == 0) continue;
+    const uintptr_t e = dtype_size(g[k].dtype) - 1;
+    if (!g[k].g || ((uintptr_t)g[k].g & e) || (clip && (!g[k].out || ((uintptr_t)g[k].out & e))))
+      return POETX_ERR_INVALID_ARG;
+  }
+  if (!norm || !coef || norm == coef || (((uintptr_t)norm | (uintptr_t)coef) & 3) || !aligned({ws}))
+    return POETX_ERR_INVALID_ARG;
+  return grad_norm(d, ar, false, (hipStream_t)stream);
+}
+}  // namespace
+
+extern "C" int poetx_grad_norm(int64_t n_grads, const poetx_grad *grads, float max_norm, float *norm, float *coef,
+                               void *ws, size_t *ws_bytes, void *stream) {
+  return grad_call(n_grads, grads, max_norm, norm, coef, false, ws, ws_bytes, stream);
+}
+
+extern "C" int poetx_grad_clip(int64_t n_grads, const poetx_grad *grads, float max_norm, float *norm, float *coef,
+                               void *ws, size_t *ws_bytes, void *stream) {
+  return grad_call(n_grads, grads, max_norm, norm, coef, true, ws, ws_bytes, stream);
+}

@@ -1,0 +1,390 @@
+// Clipped policy loss with its KL term, forward and backward in one pass over the tokens.  Per
+// token, from negative log-probabilities nll (current), old and ref:
+//   d = old - nll,  r = exp d,  pg = -min(r A, clip(r, 1 - lo, 1 + hi) A),
+//   e = nll - ref,  kl = exp e - e - 1,  loss = pg + beta kl,
+//   dloss / dnll = (r A where not clipped, else 0) + beta (exp e - 1)
+// averaged over the tokens that count (all, or within each sequence and then over sequences).
+//
+// The differences d and e are taken in 64 bits: a ratio is compared with its borders as a log
+// ratio, d against log(1 - lo) and log(1 + hi), which decides right next to a border, where a
+// float32 exp would not.  exp e - e - 1 is a small difference for small e: below |e| = 1/2 it
+// comes from its series (the first term left out is 2 e^7 / 9! of it, 4e-8).  The rest is float32,
+// the sums over tokens 64 bits.
+//
+// A wave walks a run of consecutive tokens in segments of 256, four per lane, and knows the
+// sequence of each from the boundaries that the segment holds, 64 offsets at a time: one search
+// per run, no per-token search and no per-token index in memory.
+#include "kernels.h"
+#include "vec.h"
+
+namespace poetx {
+
+namespace {
+
+constexpr int kSeg = 256;         // tokens of a wave's segment
+constexpr int64_t kCountParts = 1024;
+
+struct PolicyArgs {
+  int64_t n, seqs;
+  const int64_t *offsets;  // null: one sequence of all tokens
+  const float *nll, *old, *ref, *adv;
+  const uint8_t *mask;
+  int reduce, per_token;
+  double low, high;
+  float r_low, r_high, beta, scale;
+  float *stats, *dnll;
+  int *cnt;        // [seqs] tokens that count, of a masked call's sequences
+  int *parts;      // [nparts] tokens that count, over all sequences
+  int nparts;
+  double *sums;    // [gridDim.x][3] partials of pg, kl, clipped
+  int64_t run;     // segments per wave
+};
+
+__device__ inline int64_t offset_at(const PolicyArgs &a, int64_t j) {
+  if (j < 0) return INT64_MIN;
+  if (j > a.seqs) return INT64_MAX;
+  if (!a.offsets) return j ? a.n : 0;
+  return a.offsets[j];
+}
+
+// Number of offsets <= i (of ascending ones): 64 probes a round, all lanes together.
+__device__ inline int64_t offsets_up_to(const PolicyArgs &a, int64_t i) {
+  const int l = threadIdx.x & 63;
+  int64_t lo = 0, hi = a.seqs + 1;  // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int64_t step = cdiv(hi - lo, 64), j = lo + (l + 1) * step - 1;  // probe j: is offset j <= i?
+    const bool le = j < hi && offset_at(a, j) <= i;
+    const int c = __popcll(__ballot(le));
+    const int64_t at = lo + c * step;  // the first c probes hold: at least that many
+    const int64_t end = at + step - 1;
+    lo = at < hi ? at : hi;
+    hi = end < hi ? end : hi;
+  }
+  return lo;
+}
+
+// The mask bytes of tokens i .. i + 3 as bits; tokens past the last are off.
+__device__ inline uint32_t mask4(const PolicyArgs &a, int64_t i) {
+  if (!a.mask) return i + 4 <= a.n ? 15u : i >= a.n ? 0u : (1u << (a.n - i)) - 1;
+  uint32_t m = 0;
+  if (i + 4 <= a.n) {
+    const uint32_t u = *(const uint32_t *)(a.mask + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m |= (u >> (8 * k) & 255u ? 1u : 0u) << k;
+  } else {
+    for (int k = 0; k < 4; ++k)
+      if (i + k < a.n && a.mask[i + k]) m |= 1u << k;
+  }
+  return m;
+}
+
+__device__ inline int wave_sum_i(int v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ inline double wave_sum_d(double v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Adds the counted tokens of segments [s0, s1) to cnt (int sums: any order gives the same).
+template <class Add>
+__device__ inline void count_run(const PolicyArgs &a, int64_t s0, int64_t s1, const Add &add) {
+  const int l = threadIdx.x & 63;
+  if (s0 >= s1) return;
+  int64_t open = offsets_up_to(a, s0 * kSeg - 1);  // offsets passed; the open sequence is open - 1
+  int acc = 0;                                     // its tokens so far
+  for (int64_t s = s0; s < s1; ++s) {
+    const int64_t t0 = s * kSeg, i = t0 + 4 * l;
+    const uint32_t m = mask4(a, i);
+    int before = __popc(m);  // becomes the tokens of the lanes before this one
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(before, o);
+      if (l >= o) before += v;
+    }
+    const int total = __shfl(before, 63);
+    before -= __popc(m);
+    int done = 0;  // tokens of this segment already given to a sequence
+    while (true) {
+      const int64_t b = offset_at(a, open + l);
+      const bool in = b < t0 + kSeg;
+      const int c = __popcll(__ballot(in));
+      if (c == 0) break;
+      // tokens of the segment before this lane's offset
+      const int rel = b <= t0 ? 0 : b < t0 + kSeg ? (int)(b - t0) : kSeg - 1;
+      int pre = __shfl(before, rel >> 2) + __popc(__shfl(m, rel >> 2) & ((1u << (rel & 3)) - 1));
+      if (pre < done) pre = done;  // (offsets that do not ascend: nothing is counted twice)
+      int prev = __shfl_up(pre, 1);
+      if (l == 0) prev = done;
+      const int give = pre - prev + (l == 0 ? acc : 0);
+      const int64_t q = open - 1 + l;
+      if (l < c && give > 0 && q >= 0 && q < a.seqs) add(q, give);
+      acc = 0;
+      done = __shfl(pre, c - 1);
+      open += c;
+      if (c < 64) break;
+    }
+    acc += total - done;
+  }
+  if (l == 0 && acc > 0 && open >= 1 && open <= a.seqs) add(open - 1, acc);
+}
+
+// Tokens that count among [lo, hi) for this thread of `threads`.
+__device__ inline int count_all(const PolicyArgs &a, int64_t lo, int64_t hi, int64_t thread, int64_t threads) {
+  int c = 0;
+  for (int64_t i = (lo & ~(int64_t)15) + 16 * thread; i < hi; i += 16 * threads) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+      uint32_t m = mask4(a, i + k);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + k + q < lo || i + k + q >= hi) m &= ~(1u << q);
+      c += __popc(m);
+    }
+  }
+  return c;
+}
+
+// first and last token that lies in a sequence
+__device__ inline void bounds(const PolicyArgs &a, int64_t &lo, int64_t &hi) {
+  const int64_t f = offset_at(a, 0), e = offset_at(a, a.seqs);
+  lo = f < 0 ? 0 : f < a.n ? f : a.n;
+  hi = e < lo ? lo : e < a.n ? e : a.n;
+}
+
+// The tokens of segments [s0, s1): their gradients, and this lane's share of the sums.
+// whole: the weight of a token where it is the same for all (0: by sequence, from tokens_of).
+template <class Count>
+__device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, float whole, const Count &tokens_of,
+                                  double (&sum)[3]) {
+  const int l = threadIdx.x & 63;
+  if (s0 >= s1) return;
+  const bool by_seq = whole == 0.f, lookup = by_seq || !a.per_token;
+  int64_t lo, hi;
+  bounds(a, lo, hi);
+  int64_t open = lookup ? offsets_up_to(a, s0 * kSeg - 1) : 0;
+  for (int64_t s = s0; s < s1; ++s) {
+    const int64_t t0 = s * kSeg, i = t0 + 4 * l;
+    uint32_t m = mask4(a, i);
+    const int nv = a.n - i >= 4 ? 4 : a.n - i > 0 ? (int)(a.n - i) : 0;
+    f32v4 x = {0.f, 0.f, 0.f, 0.f}, o = x, r = x, A = x;
+    auto get = [&](const float *p, f32v4 &v) {
+      if (nv == 4) {
+        v = *(const f32v4 *)(p + i);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < nv) v[k] = p[i + k];
+      }
+    };
+    get(a.nll, x);
+    if (a.old) get(a.old, o);
+    if (a.ref) get(a.ref, r);
+    if (a.per_token) get(a.adv, A);
+    f32v4 w = {whole, whole, whole, whole};
+    if (lookup) {
+      int past[4] = {0, 0, 0, 0};  // offsets at or before each token, beyond `open`
+      int64_t next = open;
+      while (true) {
+        const int64_t b = offset_at(a, next + l);
+        const int c = __popcll(__ballot(b < t0 + kSeg));
+        for (int j = 0; j < c; ++j) {
+          const int64_t bj = __shfl(b, j);
+          const int rel = bj <= t0 ? 0 : (int)(bj - t0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) past[k] += rel <= 4 * l + k ? 1 : 0;
+        }
+        next += c;
+        if (c < 64) break;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t q = open - 1 + past[k];
+        if (q < 0 || q >= a.seqs || i + k >= a.n) {
+          m &= ~(1u << k);
+        } else {
+          if (!a.per_token) A[k] = a.adv[q];
+          if (by_seq) w[k] = 1.f / ((float)tokens_of(q) * (float)a.seqs);
+        }
+      }
+      open = next;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k < lo || i + k >= hi) m &= ~(1u << k);
+    }
+    f32v4 g;
+    float part[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const double d = a.old ? (double)o[k] - (double)x[k] : 0.0;
+      const float free = expf((float)d) * A[k];
+      const bool over = d > a.high && A[k] > 0.f, under = d < a.low && A[k] < 0.f;
+      const float pg = over ? -a.r_high * A[k] : under ? -a.r_low * A[k] : -free;
+      float slope = over || under ? 0.f : free, kl = 0.f;
+      if (a.ref) {
+        const float e = (float)((double)x[k] - (double)r[k]);
+        float p = fmaf(e, 1.f / 40320.f, 1.f / 5040.f);
+        p = fmaf(e, p, 1.f / 720.f);
+        p = fmaf(e, p, 1.f / 120.f);
+        p = fmaf(e, p, 1.f / 24.f);
+        p = fmaf(e, p, 1.f / 6.f);
+        p = fmaf(e, p, 0.5f);
+        p *= e * e;
+        const float z = expf(e) - 1.f;
+        const bool near = fabsf(e) < 0.5f;
+        kl = near ? p : z - e;
+        slope += a.beta * (near ? e + p : z);
+      }
+      const bool on = m >> k & 1;
+      g[k] = on ? slope * w[k] * a.scale : 0.f;
+      part[0] += on ? pg * w[k] : 0.f;
+      part[1] += on ? kl * w[k] : 0.f;
+      part[2] += on && (over || under) ? w[k] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] += (double)part[k];
+    if (a.dnll) {
+      if (nv == 4) {
+        *(f32v4 *)(a.dnll + i) = g;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < nv) a.dnll[i + k] = g[k];
+      }
+    }
+  }
+}
+
+__device__ inline void write_stats(const PolicyArgs &a, const double (&s)[3]) {
+  a.stats[0] = (float)(s[0] + (double)a.beta * s[1]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) a.stats[1 + k] = (float)s[k];
+}
+
+// tokens of sequence q by its offsets alone
+__device__ inline int length_of(const PolicyArgs &a, int64_t q) {
+  int64_t b = offset_at(a, q), e = offset_at(a, q + 1);
+  b = b < 0 ? 0 : b;
+  e = e < a.n ? e : a.n;
+  return e - b > 1 ? (int)(e - b) : 1;
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(256) void k_policy_zero(int *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+__global__ __launch_bounds__(256) void k_policy_count(PolicyArgs a, int64_t segs) {
+  if (a.reduce == POETX_REDUCE_SEQUENCE) {
+    const int64_t s0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * a.run;
+    count_run(a, s0, s0 + a.run < segs ? s0 + a.run : segs, [&](int64_t q, int c) { atomicAdd(a.cnt + q, c); });
+    return;
+  }
+  __shared__ int red[4];
+  int64_t lo, hi;
+  bounds(a, lo, hi);
+  const int c = wave_sum_i(count_all(a, lo, hi, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
+  __syncthreads();
+  if (threadIdx.x == 0) a.parts[blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+}
+
+// the weight that all tokens share, from the number of those that count
+__device__ inline float shared_weight(const PolicyArgs &a, int64_t count) {
+  return a.reduce == POETX_REDUCE_TOKEN ? (float)(1.0 / (double)(count > 1 ? count : 1)) : 1.f;
+}
+
+__global__ __launch_bounds__(256) void k_policy_tokens(PolicyArgs a, int64_t segs) {
+  __shared__ int64_t redi[4];
+  __shared__ double red[4][3];
+  const int wave = threadIdx.x >> 6;
+  float whole = 0.f;
+  if (a.reduce != POETX_REDUCE_SEQUENCE) {
+    int64_t count = 0;
+    if (a.reduce == POETX_REDUCE_TOKEN) {
+      if (a.mask) {
+        int c = 0;  // (at most 2^31 - 1 tokens)
+        for (int i = threadIdx.x; i < a.nparts; i += 256) c += a.parts[i];
+        c = wave_sum_i(c);
+        if ((threadIdx.x & 63) == 0) redi[wave] = c;
+        __syncthreads();
+        count = redi[0] + redi[1] + redi[2] + redi[3];
+      } else {
+        int64_t lo, hi;
+        bounds(a, lo, hi);
+        count = hi - lo;
+      }
+    }
+    whole = shared_weight(a, count);
+  }
+  double sum[3] = {0, 0, 0};
+  const int64_t s0 = ((int64_t)blockIdx.x * 4 + wave) * a.run;
+  policy_run(a, s0, s0 + a.run < segs ? s0 + a.run : segs, whole,
+             [&](int64_t q) { return a.mask ? (a.cnt[q] > 1 ? a.cnt[q] : 1) : length_of(a, q); }, sum);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const double v = wave_sum_d(sum[k]);
+    if ((threadIdx.x & 63) == 0) red[wave][k] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    const int k = threadIdx.x;
+    a.sums[(int64_t)blockIdx.x * 3 + k] = ((red[0][k] + red[1][k]) + red[2][k]) + red[3][k];
+  }
+}
+
+__global__ __launch_bounds__(256) void k_policy_stats(PolicyArgs a, int blocks) {
+  __shared__ double red[4][3];
+  double s[3] = {0, 0, 0};
+  for (int i = threadIdx.x; i < blocks; i += 256)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] += a.sums[(int64_t)i * 3 + k];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const double v = wave_sum_d(s[k]);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][k] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) s[k] = ((red[0][k] + red[1][k]) + red[2][k]) + red[3][k];
+  write_stats(a, s);
+}
+
+int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  PolicyArgs a{};
+  a.n = d.n; a.seqs = d.seqs; a.offsets = d.offsets;
+  a.nll = d.nll; a.old = d.old; a.ref = d.ref; a.adv = d.adv; a.mask = d.mask;
+  a.reduce = d.reduce; a.per_token = d.per_token;
+  a.low = d.low; a.high = d.high; a.r_low = d.r_low; a.r_high = d.r_high; a.beta = d.beta; a.scale = (float)d.scale;
+  a.stats = d.stats; a.dnll = d.dnll;
+  const int64_t segs = cdiv(d.n, kSeg), cus = device_cus() > 0 ? device_cus() : 256;
+  a.run = cdiv(segs, 4 * 8 * cus);
+  if (a.run < 1) a.run = 1;
+  const int64_t blocks = segs > 0 ? cdiv(segs, 4 * a.run) : 1;
+  const bool by_seq = d.reduce == POETX_REDUCE_SEQUENCE;
+  a.sums = (double *)ar.take((size_t)blocks * 3 * 8);
+  if (by_seq) a.cnt = (int *)ar.take((size_t)d.seqs * 4);
+  int64_t parts = cdiv(d.n, 4096);
+  a.nparts = (int)(parts < 1 ? 1 : parts < kCountParts ? parts : kCountParts);
+  if (!by_seq) a.parts = (int *)ar.take((size_t)a.nparts * 4);
+  if (measure) return POETX_OK;
+  if (d.mask && d.reduce != POETX_REDUCE_SUM) {
+    if (by_seq && d.seqs > 0) {
+      const int64_t z = cdiv(d.seqs, 256);
+      POETX_TRY(launch_k("policy_zero", s, k_policy_zero, dim3((unsigned)(z < 1024 ? z : 1024)), dim3(256), 0, a.cnt,
+                         d.seqs));
+    }
+    POETX_TRY(launch_k("policy_count", s, k_policy_count, dim3((unsigned)(by_seq ? blocks : a.nparts)), dim3(256), 0,
+                       a, segs));
+  }
+  POETX_TRY(launch_k("policy_tokens", s, k_policy_tokens, dim3((unsigned)blocks), dim3(256), 0, a, segs));
+  return launch_k("policy_stats", s, k_policy_stats, dim3(1), dim3(256), 0, a, (int)blocks);
+}
+
+}  // namespace poetx

@@ -273,4 +273,48 @@ struct XentDesc {
 int xent_forward(const XentDesc &d, Arena &ar, bool measure, hipStream_t s);
 int xent_backward(const XentDesc &d, Arena &ar, bool measure, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// Gated feed-forward projections (k_glu.hip): h = act(x Wg^T) (x Wu^T).
+// ---------------------------------------------------------------------------
+struct GluDesc {
+  int64_t n = 0, d = 0, f = 0;
+  int dt = POETX_BF16, act = POETX_ACT_SILU;
+  const void *x = nullptr, *wg = nullptr, *wu = nullptr;
+  void *h = nullptr, *gate = nullptr, *up = nullptr;  // forward results, gate and up nullable
+  const void *dh = nullptr, *gate_in = nullptr, *up_in = nullptr;
+  void *dx = nullptr, *dwg = nullptr, *dwu = nullptr;  // backward results: dx nullable, dwg and dwu together
+};
+int glu_forward(const GluDesc &d, Arena &ar, bool measure, hipStream_t s);
+int glu_backward(const GluDesc &d, Arena &ar, bool measure, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Clipped policy loss (k_policy.hip).
+// ---------------------------------------------------------------------------
+constexpr int64_t kPolicyMaxTokens = 0x7fffffff;
+struct PolicyDesc {
+  int64_t n = 0, seqs = 1;
+  const int64_t *offsets = nullptr;
+  const float *nll = nullptr, *old = nullptr, *ref = nullptr, *adv = nullptr;
+  const uint8_t *mask = nullptr;
+  int reduce = POETX_REDUCE_TOKEN, per_token = 0;
+  double low = 0, high = 0;  // least and largest log ratio that is not clipped
+  float r_low = 1.f, r_high = 1.f, beta = 0.f;
+  double scale = 1.0;
+  float *stats = nullptr, *dnll = nullptr;
+};
+int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Norm and clipping of many gradients (k_grad.hip).
+// ---------------------------------------------------------------------------
+constexpr int64_t kGradMaxList = 1 << 20, kGradMaxTotal = (int64_t)1 << 48;
+struct GradDesc {
+  int64_t n = 0;
+  const poetx_grad *g = nullptr;
+  float max_norm = 0.f;
+  bool clip = false;
+  float *norm = nullptr, *coef = nullptr;
+};
+int grad_norm(const GradDesc &d, Arena &ar, bool measure, hipStream_t s);
+
 }  // namespace poetx

@@ -190,3 +190,76 @@ class BlockStep:
         """(loss per token, gradients by name)."""
         s = self.forward(x0, target)
         return s["loss"], self.backward(s, dloss)
+
+
+class PolicyStep:
+    """One policy update of a pre-norm block with a gated feed-forward part and a vocabulary head
+    around a POET-X layer:
+
+        a = norm(x0),  z = POET-X(a),  u = act(z . w_gate^T) (z . w_up^T),  y = u . w_down^T + x0,
+        h = norm(y),   nll_i = cross entropy of h_i . head^T at target_i,
+        loss = clipped policy loss of nll with its KL term
+
+    the gradients of loss, their common norm clipped to max_norm, and one Adam step of the layer's
+    packed thetas.  ``layer`` and ``params`` are BlockStep's, the dense weights being w_gate, w_up
+    ([f][d]), w_down ([d][f]) and head ([vocab][d]).  Marshalling only.
+    """
+
+    NAMES = ("gamma1", "beta1", "w_gate", "w_up", "w_down", "gamma2", "beta2", "head")
+
+    def __init__(self, layer: LayerStep, params: dict, act: str = "silu", eps: float = 1e-5):
+        missing = [k for k in self.NAMES if k not in params]
+        if missing:
+            raise ValueError(f"params lacks {missing}")
+        if layer.wl.d_in != layer.wl.d_out:
+            raise ValueError("the block's layer maps its width to itself")
+        self.layer, self.p, self.act, self.eps = layer, params, act, eps
+        self.adam = None
+
+    def forward(self, x0, target):
+        """The activations by name, nll (one per token) among them."""
+        p, s = self.p, {"x0": x0, "target": target}
+        s["a"], s["mean1"], s["rstd1"] = B.poetx_layernorm_forward(x0, p["gamma1"], p["beta1"], self.eps)
+        self.layer.cnp()
+        s["z"], s["saved_b"] = B.poetx_forward(self.layer.layer, s["a"])
+        s["u"], s["gate"], s["up"] = B.poetx_glu_forward(s["z"], p["w_gate"], p["w_up"], self.act, save=True)
+        s["y"], _ = B.poetx_linear_forward(s["u"], p["w_down"], None, x0)
+        s["h"], s["mean2"], s["rstd2"] = B.poetx_layernorm_forward(s["y"], p["gamma2"], p["beta2"], self.eps)
+        s["nll"], s["lse"] = B.poetx_xent_forward(s["h"], p["head"], target)
+        return s
+
+    def backward(self, s, dnll):
+        """Gradients by name: the parameters', theta_r, theta_p and x0."""
+        p, g = self.p, {}
+        top = B.poetx_xent_backward(s["h"], p["head"], s["target"], s["lse"], dnll)
+        g["head"] = top["dw"]
+        n2 = B.poetx_layernorm_backward(s["y"], top["dh"], p["gamma2"], s["mean2"], s["rstd2"])
+        g["gamma2"], g["beta2"], dy = n2["dgamma"], n2["dbeta"], n2["dx"]
+        down = B.poetx_linear_backward(s["u"], p["w_down"], dy, want_dbias=False)
+        g["w_down"] = down["dw"]
+        glu = B.poetx_glu_backward(s["z"], p["w_gate"], p["w_up"], down["dx"], s["gate"], s["up"], self.act)
+        g["w_gate"], g["w_up"] = glu["dw_gate"], glu["dw_up"]
+        mid = B.poetx_backward(self.layer.layer, s["a"], glu["dx"], s["saved_b"])
+        g["theta_r"], g["theta_p"] = mid["dtheta_r"], mid["dtheta_p"]
+        n1 = B.poetx_layernorm_backward(s["x0"], mid["dx"], p["gamma1"], s["mean1"], s["rstd1"], dres=dy)
+        g["gamma1"], g["beta1"], g["x0"] = n1["dgamma"], n1["dbeta"], n1["dx"]
+        return g
+
+    def step(self, x0, target, adv, offsets=None, *, max_norm: float = 1.0, lr: float = 1e-3, betas=(0.9, 0.999),
+             adam_eps: float = 1e-8, gamma: float = 1.0, **policy):
+        """(stats, gradients by name, norm): a whole update.  policy: poetx_policy_loss's other
+        arguments (nll_old, nll_ref, mask, clip, beta, reduce, ...).  The parameters' gradients come
+        back clipped; the one of x0 belongs to the part of the model before the block and is not
+        among the clipped ones."""
+        s = self.forward(x0, target)
+        stats, dnll = B.poetx_policy_loss(s["nll"], adv, offsets, **policy)
+        g = self.backward(s, dnll)
+        norm, _ = B.poetx_grad_clip([t for k, t in g.items() if k != "x0"], max_norm)
+        if self.adam is None:
+            self.adam = B.AdamState.zeros_like(self.layer.layer)
+        st = self.adam
+        st.step += 1
+        for theta, grad, m, v in ((self.layer.theta_r, g["theta_r"], st.m_r, st.v_r),
+                                  (self.layer.theta_p, g["theta_p"], st.m_p, st.v_p)):
+            B.poetx_adam_step(theta, grad, m, v, lr=lr, step=st.step, betas=betas, eps=adam_eps, gamma=gamma)
+        return stats, g, norm

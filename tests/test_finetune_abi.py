@@ -1,0 +1,185 @@
+"""Refusals and workspace queries of the operators of a fine-tuning step (gated feed-forward
+projections, clipped policy loss, gradient norm and clipping).  No GPU: every call fails
+validation, or only asks for its workspace, before anything is launched."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def B():
+    from orthogonal_reparameterized_amd import binding
+    return binding
+
+
+A = [0x10000 * (k + 1) for k in range(12)]  # distinct addresses, never dereferenced
+BIG = 1 << 50
+
+
+def size(n=0):
+    return ctypes.byref(ctypes.c_size_t(n))
+
+
+def glu_fwd(B, n=4, d=64, f=96, dt=1, x=A[0], wg=A[1], wu=A[2], act=4, h=A[3], gate=A[4], up=A[5], ws=A[6], nb=BIG):
+    return B.raw.poetx_glu_forward(n, d, f, dt, x, wg, wu, act, h, gate, up, ws, size(nb), None)
+
+
+def glu_bwd(B, n=4, d=64, f=96, dt=1, x=A[0], wg=A[1], wu=A[2], dh=A[3], gate=A[4], up=A[5], act=4, dx=A[6], dwg=A[7],
+            dwu=A[8], ws=A[9], nb=BIG):
+    return B.raw.poetx_glu_backward(n, d, f, dt, x, wg, wu, dh, gate, up, act, dx, dwg, dwu, ws, size(nb), None)
+
+
+def policy(B, n=10, s=2, off=A[0], nll=A[1], old=A[2], ref=A[3], adv=A[4], mask=A[5], low=0.2, high=0.2, beta=0.0,
+           scale=1.0, reduce=0, per_token=0, stats=A[6], dnll=A[7], ws=A[8], nb=BIG, p=True):
+    q = B.PoetxPolicyC(low, high, beta, scale, reduce, per_token)
+    return B.raw.poetx_policy_loss(n, s, off, nll, old, ref, adv, mask, ctypes.byref(q) if p else None, stats, dnll,
+                                   ws, size(nb), None)
+
+
+def grads(B, *items):
+    a = (B.PoetxGradC * max(1, len(items)))()
+    for k, (g, out, n, dt) in enumerate(items):
+        a[k] = B.PoetxGradC(g, out, n, dt)
+    return a
+
+
+def clip(B, *items, n=None, a=True, max_norm=1.0, norm=A[8], coef=A[9], ws=A[10], nb=BIG, f="poetx_grad_clip"):
+    arr = grads(B, *items)
+    return getattr(B.raw, f)(len(items) if n is None else n, arr if a else None, max_norm, norm, coef, ws, size(nb),
+                             None)
+
+
+def test_glu_refusals(B):
+    bad = B.POETX_ERR_INVALID_ARG
+    for kw in (dict(n=-1), dict(dt=2), dict(act=-1), dict(act=5), dict(x=None), dict(wg=None), dict(wu=None),
+               dict(h=None), dict(gate=None), dict(up=None), dict(x=A[0] + 8), dict(up=A[5] + 2), dict(h=A[0]),
+               dict(gate=A[1]), dict(up=A[3]), dict(ws=A[6] + 4)):
+        assert glu_fwd(B, **kw) == bad, kw
+    for kw in (dict(n=-1), dict(dt=2), dict(act=9), dict(dh=None), dict(gate=None), dict(up=None), dict(x=None),
+               dict(wg=None), dict(wu=None), dict(dwg=None), dict(dwu=None), dict(dx=None, dwg=None, dwu=None),
+               dict(dx=A[0]), dict(dwg=A[3]), dict(dwu=A[7]), dict(dh=A[3] + 4)):
+        assert glu_bwd(B, **kw) == bad, kw
+    for kw in (dict(d=0), dict(f=0), dict(d=-3)):
+        assert glu_fwd(B, **kw) == B.POETX_ERR_SHAPE, kw
+        assert glu_bwd(B, **kw) == B.POETX_ERR_SHAPE, kw
+    for kw in (dict(d=(1 << 20) + 1), dict(f=(1 << 20) + 1), dict(n=1 << 41), dict(n=1 << 30, f=1 << 20)):
+        assert glu_fwd(B, **kw) == B.POETX_ERR_UNSUPPORTED, kw
+        assert glu_bwd(B, **kw) == B.POETX_ERR_UNSUPPORTED, kw
+    assert glu_fwd(B, n=0, x=None, wg=None, wu=None, h=None) == B.POETX_OK
+    assert glu_fwd(B, n=400, d=63, nb=64) == B.POETX_ERR_WORKSPACE
+    assert glu_bwd(B, nb=16) == B.POETX_ERR_WORKSPACE
+    r = B.raw
+    assert r.poetx_glu_forward(4, 64, 96, 1, A[0], A[1], A[2], 4, A[3], None, None, A[4], None, None) == bad
+    assert r.poetx_glu_backward(4, 64, 96, 1, *A[:6], 4, A[6], A[7], A[8], A[9], None, None) == bad
+
+
+def test_policy_refusals(B):
+    bad, nan, inf = B.POETX_ERR_INVALID_ARG, float("nan"), float("inf")
+    for kw in (dict(n=-1), dict(s=-1), dict(p=False), dict(nll=None), dict(adv=None), dict(stats=None),
+               dict(off=None), dict(beta=0.1, ref=None), dict(beta=nan), dict(beta=inf), dict(scale=nan),
+               dict(low=-0.1), dict(low=nan), dict(high=-1.0), dict(high=nan), dict(reduce=3), dict(reduce=-1),
+               dict(nll=A[1] + 4), dict(off=A[0] + 8), dict(mask=A[5] + 1), dict(dnll=A[1]), dict(dnll=A[2]),
+               dict(stats=A[7]), dict(stats=A[4]), dict(ws=A[8] + 8)):
+        assert policy(B, **kw) == bad, kw
+    for kw in (dict(n=1 << 31), dict(s=1 << 31)):
+        assert policy(B, **kw) == B.POETX_ERR_UNSUPPORTED, kw
+    for kw in (dict(), dict(reduce=1), dict(reduce=2), dict(low=inf, high=inf)):
+        assert policy(B, nb=16, **kw) == B.POETX_ERR_WORKSPACE, kw
+        assert policy(B, ws=None, nb=0, **kw) == B.POETX_OK, kw
+    q = B.PoetxPolicyC(0.2, 0.2, 0.0, 1.0, 0, 0)
+    assert B.raw.poetx_policy_loss(10, 2, *A[:6], ctypes.byref(q), A[6], A[7], A[8], None, None) == bad
+
+
+def test_grad_refusals(B):
+    bad = B.POETX_ERR_INVALID_ARG
+    ok = (A[0], A[1], 100, 0)
+    for f in ("poetx_grad_norm", "poetx_grad_clip"):
+        for items, kw in (([(None, A[1], 100, 0)], {}), ([(A[0] + 2, A[1], 100, 0)], {}),
+                          ([(A[0] + 1, A[1], 100, 1)], {}), ([(A[0], A[1], -1, 0)], {}), ([(A[0], A[1], 5, 2)], {}),
+                          ([ok], dict(max_norm=-1.0)), ([ok], dict(max_norm=float("nan"))), ([ok], dict(norm=None)),
+                          ([ok], dict(coef=None)), ([ok], dict(coef=A[8])), ([ok], dict(norm=A[8] + 2)),
+                          ([ok], dict(ws=A[10] + 8)), ([ok], dict(n=-1)), ([ok], dict(a=False))):
+            assert clip(B, *items, f=f, **kw) == bad, (f, items, kw)
+        assert clip(B, ok, f=f, nb=4) == B.POETX_ERR_WORKSPACE
+        assert clip(B, (A[0], A[1], (1 << 48) + 1, 0), f=f) == B.POETX_ERR_UNSUPPORTED
+        assert clip(B, *[(A[0], A[1], 1 << 47, 1)] * 3, f=f) == B.POETX_ERR_UNSUPPORTED
+        assert clip(B, ok, f=f, ws=None) == B.POETX_OK
+        assert clip(B, f=f, a=False, ws=None) == B.POETX_OK
+        assert getattr(B.raw, f)(1, grads(B, ok), 1.0, A[8], A[9], A[10], None, None) == bad
+    assert clip(B, (A[0], None, 100, 0)) == bad
+    assert clip(B, (A[0], A[1] + 2, 100, 0)) == bad
+
+
+def query(f, *args):
+    nb = ctypes.c_size_t(0)
+    assert f(*args, None, ctypes.byref(nb), None) == 0
+    return nb.value
+
+
+def test_workspace_queries(B):
+    r = B.raw
+    assert query(r.poetx_glu_forward, 0, 64, 96, 1, *[None] * 3, 4, *[None] * 3) == 0
+    assert query(r.poetx_glu_backward, 0, 64, 96, 1, *[None] * 6, 4, A[0], A[1], A[2]) == 0
+    # the operands of the backward's products, dg and du, live in the workspace
+    assert query(r.poetx_glu_backward, 100, 64, 96, 1, *[None] * 6, 4, A[0], A[1], A[2]) >= 2 * 100 * 96 * 2
+    p = B.PoetxPolicyC(0.2, 0.2, 0.0, 1.0, 1, 0)
+    big = query(r.poetx_policy_loss, 1 << 24, 1 << 20, *[None] * 6, ctypes.byref(p), None, None)
+    assert 4 << 20 <= big < 8 << 20  # one count per sequence, nothing per token
+    assert query(r.poetx_policy_loss, 0, 0, *[None] * 6, ctypes.byref(p), None, None) < 4096
+    assert query(r.poetx_grad_norm, 1, grads(B, (A[0], None, 1 << 40, 0)), 1.0, None, None) <= 1 << 16
+
+
+def test_binding_refusals(B):
+    """The binding refuses shapes, dtypes and layouts before it touches a device."""
+    x, w, h = (torch.zeros(*s, dtype=torch.bfloat16) for s in ((4, 64), (32, 64), (4, 32)))
+    t, off = torch.zeros(6), torch.tensor([0, 4, 6])
+    a2 = torch.zeros(2)
+    cases = [
+        lambda: B.poetx_glu_forward(x, w, w.float()),
+        lambda: B.poetx_glu_forward(x, w, w[:31]),
+        lambda: B.poetx_glu_forward(x, w[:, :32], w),
+        lambda: B.poetx_glu_forward(x, w, w, act="swish"),
+        lambda: B.poetx_glu_forward(x, w, w),  # on the CPU
+        lambda: B.poetx_glu_backward(x, w, w, h, None, h),
+        lambda: B.poetx_glu_backward(None, w, w, h, h, h),
+        lambda: B.poetx_glu_backward(x, None, w, h, h, h),
+        lambda: B.poetx_glu_backward(x, w, w, h, h, h[:3]),
+        lambda: B.poetx_glu_backward(x, w, w, h, h, h, want_dx=False, want_dw=False),
+        lambda: B.poetx_policy_loss(t.double(), a2, off),
+        lambda: B.poetx_policy_loss(t, torch.zeros(3), off),
+        lambda: B.poetx_policy_loss(t, a2),
+        lambda: B.poetx_policy_loss(t, a2, off.int()),
+        lambda: B.poetx_policy_loss(t, a2, off, per_token=True),
+        lambda: B.poetx_policy_loss(t, a2, off, mask=torch.ones(6)),
+        lambda: B.poetx_policy_loss(t, a2, off, mask=torch.ones(5, dtype=torch.bool)),
+        lambda: B.poetx_policy_loss(t, a2, off, nll_old=t[:5]),
+        lambda: B.poetx_policy_loss(t, a2, off, beta=0.1),
+        lambda: B.poetx_policy_loss(t, a2, off, reduce="mean"),
+        lambda: B.poetx_policy_loss(t, a2, off[:0]),
+        lambda: B.poetx_policy_loss(t, a2, off),  # on the CPU
+        lambda: B.GradList([]),
+        lambda: B.GradList([t.double()]),
+        lambda: B.GradList([torch.zeros(4, 4).t()[:3]]),
+        lambda: B.GradList([t, t]),
+        lambda: B.GradList([t[:4], t[3:]]),
+        lambda: B.GradList([t[:3]], [t[2:5]]),
+        lambda: B.GradList([t], [t]),
+        lambda: B.GradList([t], [torch.zeros(5)]),
+        lambda: B.GradList([t], [torch.zeros(6, dtype=torch.bfloat16)]),
+        lambda: B.GradList([t], []),
+        lambda: B.poetx_grad_norm([t]),  # on the CPU
+        lambda: B.poetx_grad_clip(B.GradList([t]), 1.0, [torch.zeros(6)]),
+    ]
+    for k, f in enumerate(cases):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"case {k} was accepted")
+
+
+def test_a_null_workspace_is_the_query(B):
+    """With every buffer given, ws == NULL still asks for the size and launches nothing (a launch
+    on these addresses, or without a GPU, would not return OK)."""
+    assert glu_fwd(B, ws=None) == glu_bwd(B, ws=None) == policy(B, ws=None) == B.POETX_OK
+    assert clip(B, (A[0], A[1], 100, 0), ws=None) == B.POETX_OK

@@ -1,0 +1,878 @@
+"""The operators of a fine-tuning step on MI355X against float64: gated feed-forward
+projections, clipped policy loss, gradient norm and clipping.
+
+Tolerances are derived, element by element, from the arithmetic the calls document:
+  - a value rounded to a type is off by at most u(type) = finfo.eps / 2 of itself;
+  - a float32 sum of K terms, in any order, is off by at most about K 2^-24 of the sum of
+    their magnitudes (`acc(K)`, with 8 more for the steps around it);
+  - bf16 products of the backward read dg and du rounded to bf16: u(bf16) of each term;
+  - activations, their slopes and exp in float32: a few units in the last place, taken as
+    2^-20 of the argument's and the value's scale.
+"""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+U = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+FN = 2.0 ** -20
+TINY = 1e-30
+INF, NAN = float("inf"), float("nan")
+
+
+def acc(k):
+    return (k + 8) * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def B():
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    from orthogonal_reparameterized_amd import binding
+    return binding
+
+
+def rand(seed, *shape, dtype=F32, scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def within(got, ref, tol, what):
+    """|got - ref| <= tol everywhere (float64), NaN where and only where ref is NaN; equal
+    infinities."""
+    assert got.shape == ref.shape, what
+    d = torch.where(got.double() == ref, torch.zeros_like(ref), (got.double() - ref).abs())
+    nan = torch.isnan(ref)
+    assert torch.equal(torch.isnan(got), nan), what
+    bad = ~(d <= tol + TINY) & ~nan
+    if bad.any():
+        i = int(torch.nonzero(bad.reshape(-1))[0])
+        t = torch.as_tensor(tol, dtype=torch.float64, device=ref.device).expand_as(ref)
+        pytest.fail(f"{what}: {int(bad.sum())} of {bad.numel()} off, first {i}: got {got.reshape(-1)[i].item():.9g} "
+                    f"ref {ref.reshape(-1)[i].item():.9g} tol {t.reshape(-1)[i].item():.3g}")
+
+
+def off(got, ref):
+    return float((got.double() - ref).norm() / ref.norm().clamp(min=TINY))
+
+
+def labelled(B, f):
+    """(f(), the labels of the kernels it launched)."""
+    torch.cuda.synchronize()
+    B.prof_read()
+    B.prof_enable(True)
+    try:
+        r = f()
+        torch.cuda.synchronize()
+        return r, set(B.prof_read())
+    finally:
+        B.prof_enable(False)
+
+
+# ------------------------------------------------------- gated feed-forward projections ----
+
+ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+
+
+def act_ref(p, act):
+    """(value, slope) in float64."""
+    if act == "none":
+        return p, torch.ones_like(p)
+    q = p.clone().requires_grad_(True)
+    f = {"relu": torch.relu, "gelu": torch.nn.functional.gelu, "silu": torch.nn.functional.silu,
+         "gelu_tanh": lambda t: torch.nn.functional.gelu(t, approximate="tanh")}[act]
+    v = f(q)
+    s, = torch.autograd.grad(v.sum(), q)
+    return v.detach(), s
+
+
+def check_glu_fwd(B, n, d, f, dtype, act, save, seed=20):
+    x = rand(seed, n, d, dtype=dtype)
+    wg, wu = (rand(seed + k, f, d, dtype=dtype, scale=d ** -0.5) for k in (1, 2))
+    (h, gate, up), ran = labelled(B, lambda: B.poetx_glu_forward(x, wg, wu, act, save=save))
+    xd = x.double()
+    g, u = xd @ wg.double().t(), xd @ wu.double().t()
+    e_g, e_u = (acc(d) * (xd.abs() @ w.double().abs().t()) for w in (wg, wu))
+    v, _ = act_ref(g, act)
+    ref = v * u
+    # |act'| <= 1.13; act's own error is on the scale of its argument and value
+    e_v = 1.13 * e_g + FN * (g.abs() + v.abs()) * (act not in ("none", "relu"))
+    e = e_v * u.abs() + v.abs() * e_u + e_v * e_u + U[F32] * ref.abs()
+    what = f"{n} {d} {f} {act}"
+    within(h, ref, U[dtype] * ref.abs() + 1.01 * e, f"h {what}")
+    assert (gate is not None) == (up is not None) == save
+    if save:
+        within(gate, g, U[dtype] * g.abs() + 1.01 * e_g, f"gate {what}")
+        within(up, u, U[dtype] * u.abs() + 1.01 * e_u, f"up {what}")
+    return ran
+
+
+def check_glu_bwd(B, n, d, f, dtype, act, seed=40, **want):
+    x, dh = rand(seed, n, d, dtype=dtype), rand(seed + 1, n, f, dtype=dtype)
+    wg, wu = (rand(seed + k, f, d, dtype=dtype, scale=d ** -0.5) for k in (2, 3))
+    gate, up = (rand(seed + k, n, f, dtype=dtype, scale=1.5) for k in (4, 5))
+    got, ran = labelled(B, lambda: B.poetx_glu_backward(x, wg, wu, dh, gate, up, act, **want))
+    v, slope = act_ref(gate.double(), act)
+    dhd, ud, gd = dh.double(), up.double(), gate.double().abs()
+    dg, du = dhd * ud * slope, dhd * v
+    curved = act not in ("none", "relu")
+    # the slope's (value's) own error, two products, then the rounding as an operand
+    e_dg = FN * (dhd * ud).abs() * (1 + gd) * curved + (U[dtype] + 3 * U[F32]) * dg.abs()
+    e_du = FN * dhd.abs() * (gd + v.abs()) * curved + (U[dtype] + 3 * U[F32]) * du.abs()
+    wgd, wud, xd = wg.double(), wu.double(), x.double()
+    refs = {}
+    if want.get("want_dx", True):
+        refs["dx"] = (dg @ wgd + du @ wud, dg.abs() @ wgd.abs() + du.abs() @ wud.abs(),
+                      e_dg @ wgd.abs() + e_du @ wud.abs(), 2 * f)
+    if want.get("want_dw", True):
+        refs["dw_gate"] = (dg.t() @ xd, dg.abs().t() @ xd.abs(), e_dg.t() @ xd.abs(), n)
+        refs["dw_up"] = (du.t() @ xd, du.abs().t() @ xd.abs(), e_du.t() @ xd.abs(), n)
+    assert set(got) == set(refs)
+    for name, (ref, mag, e_in, k) in refs.items():
+        within(got[name], ref, U[dtype] * ref.abs() + 1.02 * (acc(k) * mag + e_in), f"{name} {n} {d} {f} {act}")
+        if ref.numel() > 4096:
+            # independent roundings of operand and result, each u / sqrt(3) in the mean square
+            assert off(got[name], ref) <= U[dtype] + acc(k), name
+    return ran
+
+
+# rows, width, inner width: single ones, widths that nothing divides, both sides of every border
+# between the ways a product is computed (16 rows; tiles of 64, 128, 256; k split or not)
+GLU_SHAPES = [(1, 64, 64), (1, 1, 1), (2, 9, 5), (3, 7, 130), (1, 4096, 700), (16, 100, 33), (16, 4097, 31),
+              (15, 2048, 17000), (17, 64, 128), (64, 513, 777), (130, 257, 300), (300, 1000, 2040), (257, 4096, 512),
+              (2048, 256, 256), (40, 5000, 95), (129, 31, 65), (200, 72, 63), (1000, 40, 1)]
+
+
+@pytest.mark.parametrize("n,d,f", GLU_SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_glu_forward(B, n, d, f, dtype):
+    for k, act in enumerate(ACTS):
+        check_glu_fwd(B, n, d, f, dtype, act, save=k % 2 == 0, seed=20 + 7 * k)
+
+
+@pytest.mark.parametrize("n,d,f", GLU_SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_glu_backward(B, n, d, f, dtype):
+    for k, act in enumerate(ACTS):
+        check_glu_bwd(B, n, d, f, dtype, act, seed=60 + 7 * k)
+
+
+@pytest.mark.parametrize("n,d,f,act", [(3500, 3400, 1797, "silu"), (3593, 3401, 1764, "none"),
+                                       (4100, 4097, 2176, "gelu"), (1500, 4700, 2650, "gelu_tanh"),
+                                       (3500, 1100, 6150, "silu"), (2100, 520, 9000, "relu")])
+def test_glu_large(B, n, d, f, act):
+    """Products on the large tiles: whole, padded widths, a shared last round, split over k, weight
+    gradients by way of a transposed copy."""
+    check_glu_fwd(B, n, d, f, BF16, act, save=True, seed=110)
+    check_glu_bwd(B, n, d, f, BF16, act, seed=120)
+
+
+@pytest.mark.parametrize("n,d,f", [(2600, 900, 1500), (700, 2100, 1300)])
+def test_glu_large_float32(B, n, d, f):
+    check_glu_fwd(B, n, d, f, F32, "silu", save=True, seed=130)
+    check_glu_bwd(B, n, d, f, F32, "gelu", seed=140)
+
+
+@pytest.mark.parametrize("n", [5, 100, 413])
+def test_glu_outputs_not_wanted(B, n):
+    for dtype in (BF16, F32):
+        check_glu_bwd(B, n, 96, 200, dtype, "silu", want_dw=False)
+        check_glu_bwd(B, n, 96, 200, dtype, "silu", want_dx=False)
+    x, dh = rand(1, n, 96), rand(2, n, 200)
+    w, g = [rand(3 + k, 200, 96) for k in range(2)], [rand(5 + k, n, 200) for k in range(2)]
+    both = B.poetx_glu_backward(x, *w, dh, *g)
+    for p, q in ((B.poetx_glu_backward(None, *w, dh, *g, want_dw=False), ("dx",)),
+                 (B.poetx_glu_backward(x, None, None, dh, *g, want_dx=False), ("dw_gate", "dw_up"))):
+        assert set(p) == set(q)
+        for k in q:
+            assert off(p[k], both[k].double()) <= acc(400) * 30  # (another split of the sums at most)
+
+
+def test_glu_no_tokens(B):
+    for dtype in (BF16, F32):
+        x, w = torch.empty(0, 24, dtype=dtype, device="cuda"), rand(1, 40, 24, dtype=dtype)
+        h, gate, up = B.poetx_glu_forward(x, w, w, save=True)
+        assert h.shape == gate.shape == up.shape == (0, 40)
+        got = B.poetx_glu_backward(x, w, w, h, gate, up)
+        assert got["dx"].shape == (0, 24) and got["dw_gate"].shape == (40, 24)
+        assert not got["dw_gate"].any() and not got["dw_up"].any()
+
+
+@pytest.mark.parametrize("n", [4, 70, 300])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_glu_nan_stays_in_its_row(B, n, dtype):
+    """Infinities and NaN of one token, and of one row of a weight, reach what the formulas say."""
+    d, f = 77, 90
+    x, wg, wu = rand(1, n, d, dtype=dtype), rand(2, f, d, dtype=dtype), rand(3, f, d, dtype=dtype)
+    clean, _, _ = B.poetx_glu_forward(x, wg, wu)
+    x[1, 3], x[2, 76] = NAN, INF
+    h, gate, up = B.poetx_glu_forward(x, wg, wu, save=True)
+    keep = [k for k in range(n) if k not in (1, 2)]
+    assert torch.equal(h[keep], clean[keep]) and torch.isnan(h[1]).all() and not torch.isfinite(up[2]).any()
+    dh = rand(4, n, f, dtype=dtype)
+    got = B.poetx_glu_backward(x, wg, wu, dh, gate, up, want_dw=False)
+    assert torch.isfinite(got["dx"][keep]).all() and torch.isnan(got["dx"][1]).all()
+    x[1:3] = 0
+    wu[5, 7], wg[89, 0] = NAN, INF
+    h, _, _ = B.poetx_glu_forward(x, wg, wu)
+    cols = [k for k in range(f) if k not in (5, 89)]
+    assert torch.equal(h[keep][:, cols], clean[keep][:, cols]) and torch.isnan(h[:, 5]).all()
+
+
+def test_glu_leading_axes_and_fused_weight(B):
+    """[batch, time, d] inputs; the two weights as the halves of one tensor; strided ones refused."""
+    x = rand(1, 3, 5, 64, dtype=BF16)
+    w = rand(2, 96, 64, dtype=BF16)
+    h, gate, up = B.poetx_glu_forward(x, w[:48], w[48:], save=True)
+    assert h.shape == (3, 5, 48)
+    flat, _, _ = B.poetx_glu_forward(x.reshape(15, 64), w[:48].clone(), w[48:].clone())
+    assert torch.equal(h.reshape(15, 48), flat)
+    got = B.poetx_glu_backward(x, w[:48], w[48:], h, gate, up)
+    assert got["dx"].shape == x.shape
+    for bad in (lambda: B.poetx_glu_forward(x[:, :, ::2], w[:48, :32], w[48:, :32]),
+                lambda: B.poetx_glu_forward(x.transpose(0, 1), w[:48], w[48:]),
+                lambda: B.poetx_glu_forward(x, w[::2], w[1::2])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(B.PoetxError):
+        B.poetx_glu_forward(x, w[:64], w[:64], h=x)
+
+
+def test_glu_same_weight_twice(B):
+    """Both projections by one tensor: h = act(p) p."""
+    x, w = rand(1, 33, 64, dtype=BF16), rand(2, 80, 64, dtype=BF16, scale=0.1)
+    h, gate, up = B.poetx_glu_forward(x, w, w, "relu", save=True)
+    assert torch.equal(gate, up)
+    p = x.double() @ w.double().t()
+    within(h, torch.relu(p) * p, U[BF16] * p * p + 3 * acc(64) * (x.double().abs() @ w.double().abs().t()) * p.abs()
+           + 1e-9, "h")
+
+
+def test_glu_against_differences(B):
+    """Steps of a float32 loss sum(h c) along each gradient against the gradient's length."""
+    n, d, f = 24, 48, 40
+    t = [rand(1, n, d), rand(2, f, d, scale=0.2), rand(3, f, d, scale=0.2)]
+    c = rand(4, n, f)
+
+    def loss(a):
+        return float((B.poetx_glu_forward(*a, "gelu")[0].double() * c.double()).sum())
+
+    _, gate, up = B.poetx_glu_forward(*t, "gelu", save=True)
+    g = B.poetx_glu_backward(*t, c, gate, up, "gelu")
+    mag = float((B.poetx_glu_forward(*t, "gelu")[0].double() * c.double()).abs().sum())
+    for k, grad in enumerate((g["dx"], g["dw_gate"], g["dw_up"])):
+        direc, eps = grad / grad.norm(), 2.0 ** -7
+        lo, hi = ([t[j] + (s * eps * direc if j == k else 0) for j in range(3)] for s in (-1, 1))
+        diff, want = (loss(hi) - loss(lo)) / (2 * eps), float((grad.double() * direc.double()).sum())
+        # float32 products of 48 terms in each loss; the third derivative's term eps^2 / 6
+        assert abs(diff - want) <= 2 * acc(d) * mag / eps + 50 * eps ** 2 * abs(want) / 6, (k, diff, want)
+
+
+def test_glu_more_than_2_31_elements(B):
+    """Results and operands whose offsets pass 32 bits: the last rows are right."""
+    n, d, f = 33000, 8, 65600
+    x, wg, wu = rand(1, n, d, dtype=BF16), rand(2, f, d, dtype=BF16), rand(3, f, d, dtype=BF16)
+    h, gate, up = B.poetx_glu_forward(x, wg, wu, "none", save=True)
+    assert h.numel() > 1 << 31
+    g, u = (x[-3:].double() @ w.double().t() for w in (wg, wu))
+    mg, mu = (x[-3:].double().abs() @ w.double().abs().t() for w in (wg, wu))
+    e = 3 * acc(d) * mg * mu + U[F32] * (g * u).abs()
+    within(h[-3:], g * u, U[BF16] * (g * u).abs() + e, "h")
+    within(up[-3:], u, U[BF16] * u.abs() + acc(d) * mu, "up")
+    got = B.poetx_glu_backward(x, wg, wu, h, gate, up, "none")
+    hd, gd, ud = h[-3:].double(), gate[-3:].double(), up[-3:].double()
+    dg, du = hd * ud, hd * gd
+    ref = dg @ wg.double() + du @ wu.double()
+    mag = dg.abs() @ wg.double().abs() + du.abs() @ wu.double().abs()
+    within(got["dx"][-3:], ref, U[BF16] * ref.abs() + 1.02 * (acc(2 * f) + U[BF16] + 3 * U[F32]) * mag, "dx")
+    c = (h[:, -3:].double() * gate[:, -3:].double())
+    ref, mag = c.t() @ x.double(), c.t().abs() @ x.double().abs()
+    within(got["dw_up"][-3:], ref, U[BF16] * ref.abs() + 1.02 * (acc(n) + U[BF16] + 3 * U[F32]) * mag, "dw_up")
+
+
+# ------------------------------------------------------------------ clipped policy loss ----
+
+def policy_ref(nll, adv, offsets, old, ref, mask, per_token, clip, beta, reduce, scale):
+    """(stats, dnll, tolerances of both) in float64, by sequences.
+
+    dnll: r A (an exp of a float32 argument: its rounding |d| u and 2 units, two products) and
+    beta (exp e - 1) (exp's 2 units and e's rounding, on the scale of exp e, or of e itself where
+    |e| < 1/2), each times a weight of 3 roundings.  The sums are of 64 bits over float32 terms."""
+    n = nll.numel()
+    x = nll.detach().double().reshape(-1).requires_grad_(True)
+    off_ = [0, n] if offsets is None else [int(v) for v in offsets]
+    seqs = len(off_) - 1
+    m = torch.ones(n, dtype=torch.bool) if mask is None else mask.reshape(-1).cpu().bool()
+    of = torch.full((n,), -1, dtype=torch.long)
+    for s in range(seqs):
+        of[off_[s]:off_[s + 1]] = s
+    m &= of >= 0
+    idx = torch.nonzero(m)[:, 0]
+    of, x_ = of[idx], x.cpu()[idx] if x.is_cuda else x[idx]
+    pick = lambda t: t.detach().cpu().double().reshape(-1)[idx]  # noqa: E731
+    a = pick(adv) if per_token else adv.detach().cpu().double()[of] if seqs else torch.zeros(0, dtype=torch.float64)
+    d = pick(old) - x_ if old is not None else x_.detach() - x_
+    r = torch.exp(d)
+    lo, hi = 1 - clip[0], 1 + clip[1]
+    over, under = (r > hi) & (a > 0), (r < lo) & (a < 0)
+    held = over | under
+    pg = torch.where(over, -hi * a, torch.where(under, -lo * a, -r * a))
+    e = x_ - pick(ref) if ref is not None else torch.zeros_like(x_)
+    kl = torch.expm1(e) - e
+    if reduce == "sequence":
+        cnt = torch.bincount(of, minlength=max(seqs, 1)).clamp(min=1).double()
+        w = 1 / (cnt[of] * seqs)
+    elif reduce == "token":
+        w = torch.full((len(idx),), 1.0 / max(len(idx), 1), dtype=torch.float64)
+    else:
+        w = torch.ones(len(idx), dtype=torch.float64)
+    terms = [w * pg, w * kl, w * held.double()]
+    loss = terms[0].sum() + beta * terms[1].sum()
+    dn = torch.zeros(n, dtype=torch.float64)
+    g, = torch.autograd.grad(loss, x, allow_unused=True) if len(idx) else (None,)
+    if g is not None:
+        dn = scale * g.cpu()
+    d, e, r, pg, kl = (t.detach() for t in (d, e, r, pg, kl))
+    u = 2.0 ** -24
+    e_free = (d.abs() + 8) * u * (r * a).abs()
+    e_kl = torch.where(e.abs() < 0.5, 16 * u * e * e, (e.abs() + 8) * u * (torch.exp(e) + 1 + e.abs()))
+    e_z = torch.where(e.abs() < 0.5, 8 * u * e.abs(), (e.abs() + 8) * u * (torch.exp(e) + 1))
+    tol = torch.zeros(n, dtype=torch.float64)
+    tol[idx] = scale * w * (e_free * ~held + beta * (e_z + 4 * u * torch.expm1(e).abs())) + 8 * u * dn[idx].abs()
+    stats = torch.stack([loss.detach()] + [t.detach().sum() for t in terms])
+    e_pg = (w * (e_free + 4 * u * pg.abs() + 4 * u * pg.abs())).sum()
+    e_k = (w * (e_kl + 8 * u * kl)).sum()
+    tols = torch.stack([e_pg + beta * e_k, e_pg, e_k, 8 * u * stats[3]]) + 2 * u * stats.abs()
+    return stats, dn, tols, tol
+
+
+def policy_case(seed, lengths, tail=0, per_token=False, masked=True, old=True, ref=True, dropped=0.2, first=0):
+    g = torch.Generator().manual_seed(seed)
+    n = first + sum(lengths) + tail
+    nll = -torch.log(torch.rand(n, generator=g).clamp(min=1e-9))
+    ends = torch.cumsum(torch.tensor([first] + list(lengths), dtype=torch.int64), 0)
+    mask = None
+    if masked:
+        mask = torch.rand(n, generator=g) < 0.7
+        for s in range(len(lengths)):
+            if torch.rand((), generator=g) < dropped:
+                mask[ends[s]:ends[s + 1]] = False
+    return dict(nll=nll, offsets=ends, old=nll + 0.25 * torch.randn(n, generator=g) if old else None,
+                ref=nll + 0.5 * torch.randn(n, generator=g) if ref else None,
+                adv=torch.randn(n if per_token else len(lengths), generator=g), mask=mask, per_token=per_token)
+
+
+def check_policy(B, c, reduce="token", clip=(0.2, 0.28), beta=0.05, scale=1.0, offsets=True):
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    beta = beta if c["ref"] is not None else 0.0
+    stats, dnll = B.poetx_policy_loss(dev(c["nll"]), dev(c["adv"]), dev(c["offsets"]) if offsets else None,
+                                      nll_old=dev(c["old"]), nll_ref=dev(c["ref"]), mask=dev(c["mask"]),
+                                      per_token=c["per_token"], clip=clip, beta=beta, reduce=reduce, scale=scale)
+    want, dn, tols, tol = policy_ref(c["nll"], c["adv"], c["offsets"] if offsets else None, c["old"], c["ref"],
+                                     c["mask"], c["per_token"], clip, beta, reduce, scale)
+    within(dnll.cpu().reshape(-1), dn, tol, f"dnll {reduce}")
+    within(stats.cpu(), want, tols, f"stats {reduce}")
+    return stats, dnll
+
+
+LENGTHS = {
+    "one token": [1], "one": [1000], "few": [5, 0, 17, 256, 1], "edges": [255, 1, 256, 257, 511, 0, 0, 4],
+    "ragged": [1 + (k * 7919) % 613 for k in range(200)], "tiny": [k % 4 for k in range(5000)],
+    "empty ones": [0] * 300 + [700] + [0] * 900 + [3], "long": [40000, 3, 90001], "singles": [1] * 2000,
+}
+
+
+@pytest.mark.parametrize("reduce", ["token", "sequence", "sum"])
+@pytest.mark.parametrize("kind", list(LENGTHS))
+def test_policy(B, kind, reduce):
+    for k, (tail, per_token, masked, old, ref, first) in enumerate(
+            ((0, False, True, True, True, 0), (5, True, True, True, False, 3), (300, False, False, True, True, 0),
+             (1, True, False, False, True, 260), (0, False, True, False, False, 0))):
+        c = policy_case(500 + k, LENGTHS[kind], tail, per_token, masked, old, ref, first=first)
+        check_policy(B, c, reduce, scale=(1.0, 0.25)[k % 2])
+
+
+@pytest.mark.parametrize("reduce", ["token", "sequence"])
+def test_policy_many_tokens(B, reduce):
+    """More segments than the GPU holds at once, so that waves walk runs of several."""
+    g = np.random.default_rng(5)
+    lengths = [int(v) for v in g.integers(0, 9000, 700)] + [300000] + [int(v) for v in g.integers(0, 5, 3000)]
+    for per_token, masked in ((False, True), (True, False)):
+        check_policy(B, policy_case(510, lengths, 77, per_token, masked), reduce)
+
+
+def test_policy_one_sequence_of_all(B):
+    c = policy_case(520, [4001])
+    for reduce in ("token", "sequence", "sum"):
+        a, da = check_policy(B, c, reduce, offsets=False)
+        b, db = check_policy(B, c, reduce)
+        assert torch.equal(a, b) and torch.equal(da, db)
+
+
+@pytest.mark.parametrize("reduce", ["token", "sequence", "sum"])
+def test_policy_nothing_counts(B, reduce):
+    """Masks that leave nothing, no sequences, no tokens: zeros, not 0 / 0."""
+    c = policy_case(530, [30, 0, 50], tail=4)
+    dev = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}
+    for mask in (torch.zeros(84, dtype=torch.bool), torch.zeros(84, dtype=torch.uint8)):
+        stats, dnll = B.poetx_policy_loss(dev["nll"], dev["adv"], dev["offsets"], nll_old=dev["old"],
+                                          nll_ref=dev["ref"], mask=mask.cuda(), beta=0.1, reduce=reduce)
+        assert not stats.any() and not dnll.any()
+    none = torch.zeros(1, dtype=torch.int64, device="cuda")
+    stats, dnll = B.poetx_policy_loss(dev["nll"], dev["adv"][:0], none, reduce=reduce)
+    assert not stats.any() and not dnll.any() and dnll.shape == (84,)
+    e = torch.empty(0, device="cuda")
+    for adv, offsets in ((e, none), (torch.ones(3, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda"))):
+        stats, dnll = B.poetx_policy_loss(e, adv, offsets, reduce=reduce)
+        assert not stats.any() and dnll.shape == (0,)
+
+
+@pytest.mark.parametrize("reduce", ["token", "sequence", "sum"])
+def test_policy_masked_tokens_hold_anything(B, reduce):
+    """Values of tokens that do not count, and those behind the last sequence, reach nothing."""
+    c = policy_case(540, [300, 41, 700, 0, 9], tail=60, first=7)
+    out = torch.ones(c["nll"].numel(), dtype=torch.bool)
+    out[7:-60] = ~c["mask"][7:-60]
+    want = check_policy(B, c, reduce)
+    for bad in (NAN, INF, -INF):
+        dirty = dict(c, **{k: torch.where(out, torch.tensor(bad), c[k]) for k in ("nll", "old", "ref")})
+        got = check_policy(B, dirty, reduce)
+        for p, q in zip(want, got):
+            assert torch.equal(p, q), bad
+        assert not got[1].cpu()[out].any()
+
+
+def test_policy_mask_bytes(B):
+    c = policy_case(550, [400, 33])
+    want = check_policy(B, c)
+    for v in (1, 2, 128, 255):
+        got = check_policy(B, dict(c, mask=c["mask"].to(torch.uint8) * v))
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_policy_borders_are_decided_in_64_bits(B):
+    """Log ratios a float32 step either side of log(1 + hi) and log(1 - lo): the gradient is there on
+    one side and gone on the other."""
+    lo, hi = 0.2, 0.28
+    nll, old, adv = [], [], []
+    for a, border in ((1.0, math.log1p(hi)), (-1.0, math.log1p(-lo))):
+        for base in (0.5, 1.0, 1.75, 3.0):
+            v = np.float32(base + border)
+            for _ in range(4):
+                v = np.nextafter(v, np.float32(-100))
+            for _ in range(9):
+                nll.append(base), old.append(float(v)), adv.append(a)
+                v = np.nextafter(v, np.float32(100))
+    t = [torch.tensor(v, dtype=F32) for v in (nll, old, adv)]
+    _, dnll = B.poetx_policy_loss(t[0].cuda(), t[2].cuda(), nll_old=t[1].cuda(), per_token=True, clip=(lo, hi),
+                                  reduce="sum")
+    r = torch.exp(t[1].double() - t[0].double())
+    held = torch.where(t[2] > 0, r > 1 + hi, r < 1 - lo)
+    assert held.any() and not held.all()
+    assert torch.equal(dnll.cpu() == 0, held)
+
+
+def test_policy_extremes(B):
+    """Ratios that over- or underflow, advantages of zero, no clipping at all."""
+    nll = torch.tensor([0.0, 200.0, 0.0, 200.0, 0.0, 200.0, 1.0, 0.0])
+    old = torch.tensor([200.0, 0.0, 200.0, 0.0, 0.0, 200.0, 1.0, 88.0])
+    adv = torch.tensor([1.0, 1.0, -1.0, -1.0, 0.0, 0.0, 2.0, -1.0])
+    stats, dnll = B.poetx_policy_loss(nll.cuda(), adv.cuda(), nll_old=old.cuda(), per_token=True, reduce="sum",
+                                      clip=(0.2, 0.2))
+    got = dnll.cpu().tolist()
+    assert got[0] == 0 and got[1] == 0 and got[2] == -INF and got[3] == 0 and got[4] == 0 and got[5] == 0
+    assert got[6] == 2 and abs(got[7] / -math.exp(88.0) - 1) < 96 * 2.0 ** -24
+    assert float(stats[1]) == INF and float(stats[3]) == 2
+    stats, dnll = B.poetx_policy_loss(nll[1:2].cuda(), adv[1:2].cuda(), nll_old=old[1:2].cuda(), clip=(INF, INF))
+    assert float(stats[3]) == 0 and float(dnll) == 0  # exp(-200) in float32
+    free = policy_case(560, [500, 20])
+    check_policy(B, free, clip=(INF, INF))
+    check_policy(B, free, clip=(1.0, 0.0))
+    check_policy(B, free, clip=(0.0, 0.0))
+
+
+def test_policy_small_kl_keeps_its_digits(B):
+    """kl = e^2 / 2 + ... and its slope at e from 2^-30 to 1, each to 2^-20 of itself."""
+    e = torch.tensor([s * 2.0 ** -k * f for k in range(1, 31) for s in (1, -1) for f in (1.0, 1.4, 1.99)])
+    zero = torch.zeros(1, device="cuda")
+    for v in e.tolist():
+        x = torch.tensor([v], dtype=F32)
+        # nll - ref = v exactly
+        stats, dnll = B.poetx_policy_loss(x.cuda(), zero, nll_ref=zero, beta=1.0)
+        z = math.expm1(float(x))
+        y = float(x)
+        kl = z - y if abs(y) > 0.01 else y * y / 2 * (1 + y / 3 * (1 + y / 4 * (1 + y / 5 * (1 + y / 6))))
+        assert abs(float(stats[2]) / kl - 1) <= 2.0 ** -20, v
+        assert abs(float(dnll) / z - 1) <= 2.0 ** -20, v
+
+
+def test_policy_outputs(B):
+    """A given dnll, no gradient, any shape of nll."""
+    c = policy_case(570, [128] * 8)
+    dev = lambda t: t.cuda()  # noqa: E731
+    args = dict(nll_old=dev(c["old"]).view(8, 128), mask=dev(c["mask"]).view(8, 128))
+    buf = torch.full((8, 128), 7.0, device="cuda")
+    stats, dnll = B.poetx_policy_loss(dev(c["nll"]).view(8, 128), dev(c["adv"]), dev(c["offsets"]), dnll=buf, **args)
+    assert dnll is buf and not (buf == 7.0).any()
+    s2, none = B.poetx_policy_loss(dev(c["nll"]).view(8, 128), dev(c["adv"]), dev(c["offsets"]), want_grad=False, **args)
+    assert none is None and torch.equal(stats, s2)
+    with pytest.raises(B.PoetxError):
+        x = dev(c["nll"])
+        B.poetx_policy_loss(x, dev(c["adv"]), dev(c["offsets"]), dnll=x)
+
+
+@pytest.mark.parametrize("offsets", [[5, 3, 900, 2, 1000], [-50, 10, 10 ** 12], [10 ** 15, 0], [0, -10 ** 15, 500],
+                                     [2000, 3000, 4000], [700, 600, 500, 400, 300, 200, 100, 0] * 40])
+def test_policy_offsets_that_are_wrong_stay_in_bounds(B, offsets):
+    """Offsets that do not ascend or lie outside: the buffers around the output are untouched."""
+    n = 1000
+    pad = torch.full((n + 512,), 3.0, device="cuda")
+    nll = rand(1, n).abs()
+    off_ = torch.tensor(offsets, dtype=torch.int64, device="cuda")
+    adv = rand(2, len(offsets) - 1)
+    mask = torch.ones(n, dtype=torch.bool, device="cuda")
+    for reduce in ("token", "sequence", "sum"):
+        for m in (None, mask):
+            B.poetx_policy_loss(nll, adv, off_, nll_old=nll, mask=m, reduce=reduce, dnll=pad[256:256 + n])
+            assert (pad[:256] == 3.0).all() and (pad[256 + n:] == 3.0).all()
+
+
+def test_policy_against_differences(B):
+    c = policy_case(580, [40, 3, 60], masked=True)
+    dev = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}
+
+    def call(x):
+        return B.poetx_policy_loss(x, dev["adv"], dev["offsets"], nll_old=dev["old"], nll_ref=dev["ref"],
+                                   mask=dev["mask"], clip=(0.9, 50.0), beta=0.3, reduce="sequence")
+
+    stats, g = call(dev["nll"])
+    direc, eps = g / g.norm(), 2.0 ** -7
+    diff = (float(call(dev["nll"] + eps * direc)[0][0]) - float(call(dev["nll"] - eps * direc)[0][0])) / (2 * eps)
+    want = float((g.double() * direc.double()).sum())
+    # each loss is off by 2^-22 of the sum of its terms' sizes (below 2); third derivative eps^2 / 6
+    assert abs(diff - want) <= 2.0 ** -22 * 2 / eps + 50 * eps ** 2 * abs(want) / 6
+
+
+# ---------------------------------------------------------- gradient norm and clipping ----
+
+def grad_ref(gs, max_norm):
+    norm = torch.sqrt(sum((g.double() ** 2).sum() for g in gs))
+    return norm, torch.where(norm <= max_norm, torch.ones_like(norm), max_norm / norm)
+
+
+def check_grads(B, gs, max_norm, in_place=False):
+    """norm and coef to a rounding; the clipped values exactly coef times the gradients, rounded."""
+    norm, coef = grad_ref(gs, max_norm)
+    before = [g.clone() for g in gs]
+    n1, c1 = B.poetx_grad_norm(gs, max_norm)
+    out = None if in_place else [torch.full_like(g, 7.0) for g in gs]
+    n2, c2 = B.poetx_grad_clip(gs, max_norm, out)
+    assert torch.equal(n1, n2) and torch.equal(c1, c2)
+    count = sum(g.numel() for g in gs)
+    within(n1.reshape(1), norm.reshape(1), (U[F32] + count * 2.0 ** -52) * norm, "norm")
+    within(c1.reshape(1), coef.reshape(1), (U[F32] + count * 2.0 ** -52) * coef, "coef")
+    for k, (g, b) in enumerate(zip(gs if in_place else out, before)):
+        assert torch.equal(g, (b.float() * c1).to(b.dtype)), k
+    if not in_place:
+        for g, b in zip(gs, before):
+            assert torch.equal(g, b)
+    return n1, c1
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("sizes", [[1], [7], [8192], [8193], [1000, 1, 0, 5000], [100000, 3, 70001], [2 ** 22 + 5],
+                                   list(range(1, 300)), [0, 0, 4], [513] * 250])
+def test_grad_clip(B, sizes, in_place):
+    for max_norm in (0.5, 1e9):
+        gs = [rand(600 + k, n, dtype=(F32, BF16)[k % 2]) for k, n in enumerate(sizes)]
+        check_grads(B, gs, max_norm, in_place)
+        if in_place and max_norm > 1:
+            assert all(torch.equal(g, rand(600 + k, g.numel(), dtype=g.dtype)) for k, g in enumerate(gs))
+
+
+def test_grad_large(B):
+    check_grads(B, [rand(1, 50_000_001, dtype=BF16), rand(2, 20_000_003)], 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_grad_views_of_any_alignment(B, dtype):
+    """Pieces of one buffer that begin at every offset from a 16-byte boundary, clipped in place and
+    into a buffer of other offsets; what lies between them stays."""
+    sizes = [1, 2, 3, 5, 9, 17, 33, 1025, 2049, 4095, 30, 8191, 8193, 7, 6, 20001]
+    whole = rand(610, sum(sizes) + 3 * len(sizes) + 8, dtype=dtype)
+    keep = whole.clone()
+    other = torch.full_like(whole, 5.0)
+    spots, at = [], 1
+    for n in sizes:
+        spots.append((at, at + n))
+        at += n + 1
+    gs = [whole[a:b] for a, b in spots]
+    norm, coef = B.poetx_grad_clip(gs, 2.0, [other[a + 2:b + 2] for a, b in spots])
+    ref, _ = grad_ref(gs, 2.0)
+    within(norm.reshape(1), ref.reshape(1), 2 * U[F32] * ref, "norm")
+    want = torch.full_like(other, 5.0)
+    for a, b in spots:
+        want[a + 2:b + 2] = (keep[a:b].float() * coef).to(dtype)
+    assert torch.equal(other, want) and torch.equal(whole, keep)
+    B.poetx_grad_clip(gs, 2.0)
+    for a, b in spots:
+        keep[a:b] = (keep[a:b].float() * coef).to(dtype)
+    assert torch.equal(whole, keep)
+
+
+def test_grad_extremes(B):
+    """Squares that float32 cannot hold, zeros, NaN, infinities, a bound of zero or infinity."""
+    big, small = rand(1, 5000) * 1e30, rand(2, 5000) * 1e-30
+    check_grads(B, [big], 1e31)
+    check_grads(B, [small], 1e-31)
+    check_grads(B, [small, torch.zeros(10, device="cuda")], 1.0)
+    n, c = check_grads(B, [torch.zeros(100, device="cuda", dtype=BF16)], 1.0)
+    assert float(n) == 0 and float(c) == 1
+    n, c = check_grads(B, [torch.zeros(100, device="cuda")], 0.0)
+    assert float(c) == 1
+    n, c = check_grads(B, [rand(3, 100)], 0.0)
+    assert float(c) == 0
+    n, c = check_grads(B, [rand(3, 100)], INF)
+    assert float(c) == 1
+    top = torch.full((4,), 3.0e38, device="cuda")  # the norm itself passes float32
+    n, c = B.poetx_grad_norm([top], 1.0)
+    assert float(n) == INF and abs(float(c) * 6.0e38 - 1) < 1e-6
+    for bad, want in ((NAN, NAN), (INF, 0.0)):
+        g = rand(4, 20000, dtype=BF16)
+        g[12345] = bad
+        o = torch.zeros_like(g)
+        n, c = B.poetx_grad_clip([rand(5, 10), g], 1.0, [torch.empty(10, device="cuda"), o])
+        assert (math.isnan(float(n)) and math.isnan(float(c))) if math.isnan(bad) else (float(n) == INF and float(c) == 0)
+        assert torch.isnan(o[12345]) and torch.isnan(o).sum() == (o.numel() if math.isnan(bad) else 1)
+
+
+def test_grad_list_is_used_again(B):
+    """A list's tensors are read anew at every call."""
+    gs = [rand(1, 3000), rand(2, 500, dtype=BF16)]
+    lst = B.GradList(gs)
+    for k in range(3):
+        for j, g in enumerate(gs):
+            g.copy_(rand(10 * k + j, *g.shape))
+        before = [g.clone() for g in gs]
+        norm, coef = B.poetx_grad_clip(lst, 1.5)
+        want, _ = grad_ref(before, 1.5)
+        within(norm.reshape(1), want.reshape(1), 2 * U[F32] * want, "norm")
+        for g, b in zip(gs, before):
+            assert torch.equal(g, (b.float() * coef).to(b.dtype))
+
+
+# ----------------------------------------------------------------- all of them together ----
+
+def chain_inputs(seed, n, dtype, d=264, f=200, v=1003):
+    t = torch.randint(0, v, (n,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32).cuda()
+    return [rand(seed, n, d, dtype=dtype)] + [rand(seed + 1 + k, f, d, dtype=dtype, scale=d ** -0.5) for k in range(2)] + [
+        rand(seed + 3, d, f, dtype=dtype, scale=f ** -0.5), rand(seed + 4, v, d, dtype=dtype, scale=d ** -0.5), t,
+        torch.tensor([0, n // 3, n // 3, n - 1], device="cuda"), rand(seed + 5, 3), rand(seed + 6, n).abs() * 5,
+        torch.rand(n, generator=torch.Generator("cuda").manual_seed(seed), device="cuda") < 0.8]
+
+
+def run_all(B, x, wg, wu, wd, head, t, offsets, adv, old, mask):
+    u, gate, up = B.poetx_glu_forward(x, wg, wu, save=True)
+    y, _ = B.poetx_linear_forward(u, wd, None, x)
+    nll, lse = B.poetx_xent_forward(y, head, t)
+    res = [u, gate, up, nll]
+    for reduce in ("token", "sequence"):
+        stats, dnll = B.poetx_policy_loss(nll, adv, offsets, nll_old=old, nll_ref=old, mask=mask, beta=0.1, reduce=reduce)
+        res += [stats, dnll]
+    top = B.poetx_xent_backward(y, head, t, lse, dnll)
+    down = B.poetx_linear_backward(u, wd, top["dh"], want_dbias=False)
+    g = B.poetx_glu_backward(x, wg, wu, down["dx"], gate, up)
+    gs = [top["dw"], down["dw"], g["dw_gate"], g["dw_up"]]
+    outs = [torch.empty_like(q) for q in gs]
+    norm, coef = B.poetx_grad_clip(gs, 0.01, outs)
+    return res + [g["dx"], *gs, *outs, norm, coef]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [9, 333])
+def test_repeated_calls_are_bitwise_equal(B, n, dtype):
+    a = chain_inputs(700, n, dtype)
+    first = [r.clone() for r in run_all(B, *a)]
+    run_all(B, *chain_inputs(800, n + 3, dtype))
+    for p, q in zip(first, run_all(B, *a)):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("n", [9, 333])
+def test_on_another_stream(B, n):
+    a = chain_inputs(710, n, BF16)
+    want = run_all(B, *a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = run_all(B, *a)
+    s.synchronize()
+    for p, q in zip(want, got):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("n", [9, 333])
+def test_captured_and_replayed(B, n):
+    """Two captured graphs of the whole chain, replayed in turns with eager calls of other sizes
+    between: every replay equals the eager result on the inputs of that moment."""
+    sets = [chain_inputs(720, n, BF16), chain_inputs(730, n, BF16)]
+    graphs = []
+    for a in sets:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            run_all(B, *a)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run_all(B, *a)
+        graphs.append((g, out))
+    big = chain_inputs(740, 2 * n + 50, BF16, v=9001)
+    for rep in range(4):
+        for (g, out), a in zip(graphs, sets):
+            a[0].copy_(rand(750 + rep, *a[0].shape, dtype=BF16))
+            g.replay()
+            torch.cuda.synchronize()
+            got = [r.clone() for r in out]
+            run_all(B, *big)
+            for p, q in zip(run_all(B, *a), got):
+                assert torch.equal(p, q), rep
+
+
+def test_two_threads_on_one_stream(B):
+    import threading
+    sets = [chain_inputs(760, 333, BF16), chain_inputs(770, 210, BF16, v=5003)]
+    want = [[r.clone() for r in run_all(B, *a)] for a in sets]
+    bad = []
+
+    def work(k):
+        for _ in range(20):
+            got = run_all(B, *sets[k])
+            torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(p, q) for p, q in zip(want[k], got)):
+                bad.append(k)
+
+    ts = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
+
+
+def policy_step_inputs(d, f, v, n):
+    p = {"gamma1": 1 + rand(1, d, scale=0.2), "beta1": rand(2, d, scale=0.2), "w_gate": rand(3, f, d, scale=d ** -0.5),
+         "w_up": rand(4, f, d, scale=d ** -0.5), "w_down": rand(5, d, f, scale=f ** -0.5),
+         "gamma2": 1 + rand(7, d, scale=0.2), "beta2": rand(8, d, scale=0.2), "head": rand(9, v, d, scale=d ** -0.5)}
+    t = torch.randint(0, v, (n,), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    t[::7] = -1
+    return p, rand(10, n, d), t
+
+
+def test_policy_step(B):
+    """A whole update in float32 against float64 autograd through the definitions: stats, clipped
+    gradients, norm, and theta after one Adam step."""
+    import torch.nn.functional as F
+    from oracle import poetx_oracle as O
+    from orthogonal_reparameterized_amd import workloads as WL
+    from orthogonal_reparameterized_amd.step import LayerStep, PolicyStep
+    d, f, v, n, b = 256, 640, 1003, 96, 64
+    wl = WL.Workload(97, "policy", n, d, d, b, "f32", "f32", "f32", 0.02, d)
+    inp = WL.make_layer_inputs(wl)
+    layer = LayerStep(wl, inp, "fast")
+    p, x0, t = policy_step_inputs(d, f, v, n)
+    step = PolicyStep(layer, p)
+    offsets = torch.tensor([0, 20, 20, 61, 90])
+    adv, mask = torch.tensor([0.7, 3.0, -1.2, 0.4]), t >= 0
+    nll = step.forward(x0, t.cuda())["nll"].cpu()
+    old = nll + 0.2 * torch.randn(n, generator=torch.Generator().manual_seed(4))
+    ref = nll + 0.3 * torch.randn(n, generator=torch.Generator().manual_seed(5))
+    before = {s: getattr(layer, s).clone() for s in ("theta_r", "theta_p")}
+    max_norm, lr = 0.02, 1e-3
+    stats, got, norm = step.step(x0, t.cuda(), adv.cuda(), offsets.cuda(), max_norm=max_norm, lr=lr,
+                                 nll_old=old.cuda(), nll_ref=ref.cuda(), mask=mask.cuda(), beta=0.1, reduce="sequence")
+
+    P = {k: q.cpu().double().requires_grad_(True) for k, q in p.items()}
+    X = x0.cpu().double().requires_grad_(True)
+    G, th = [], []
+    for side in ("theta_r", "theta_p"):
+        th.append(torch.from_numpy(inp[side].astype(np.float64)).requires_grad_(True))
+        iu = torch.triu_indices(b, b, 1)
+        Q = torch.zeros(th[-1].shape[0], b, b, dtype=torch.float64)
+        Q = Q.index_put((torch.arange(Q.shape[0])[:, None], iu[0][None], iu[1][None]), th[-1])
+        Q = Q - Q.transpose(1, 2)
+        Q2 = Q @ Q
+        G.append(torch.eye(b, dtype=torch.float64) + 2 * (Q + Q2 + Q2 @ Q) + Q2 @ Q2)
+        np.testing.assert_allclose(G[-1].detach().numpy(), O.cnp_forward(inp[side].astype(np.float64), b), rtol=0,
+                                   atol=1e-12)
+    W = torch.from_numpy(inp["w"].astype(np.float64))
+    pin, pout = (torch.from_numpy(inp[k].astype(np.int64)) for k in ("perm_in", "perm_out"))
+    a = F.layer_norm(X, (d,), P["gamma1"], P["beta1"], 1e-5)
+    blocks = lambda m, g: torch.cat([m[:, j * b:(j + 1) * b] @ g[j] for j in range(d // b)], 1)  # noqa: E731
+    zt = blocks(blocks(a[:, pin], G[0]) @ W[pout][:, pin].t(), G[1])
+    z = torch.zeros_like(zt).index_copy(1, pout, zt)
+    u = F.silu(F.linear(z, P["w_gate"])) * F.linear(z, P["w_up"])
+    h = F.layer_norm(F.linear(u, P["w_down"]) + X, (d,), P["gamma2"], P["beta2"], 1e-5)
+    nll64 = F.cross_entropy(F.linear(h, P["head"]), t.long(), ignore_index=-1, reduction="none")
+    r, e = torch.exp(old.double() - nll64), nll64 - ref.double()
+    loss = pgs = kls = 0
+    for s in range(4):
+        q = slice(int(offsets[s]), int(offsets[s + 1]))
+        m = mask[q].double()
+        pg = -torch.minimum(r[q] * adv[s], r[q].clamp(0.8, 1.2) * adv[s])
+        kl = torch.expm1(e[q]) - e[q]
+        pgs = pgs + (pg * m).sum() / m.sum().clamp(min=1) / 4
+        kls = kls + (kl * m).sum() / m.sum().clamp(min=1) / 4
+    loss = pgs + 0.1 * kls
+    leaves = dict(P, theta_r=th[0], theta_p=th[1], x0=X)
+    grads = dict(zip(leaves, torch.autograd.grad(loss, list(leaves.values()))))
+    full = torch.sqrt(sum((g ** 2).sum() for k, g in grads.items() if k != "x0"))
+    coef = min(1.0, max_norm / float(full))
+    assert coef < 1
+    # float32 throughout: nine stages, each off by about sqrt(K) 2^-24 (K <= 1003 terms of
+    # independent rounding) with condition numbers of a few: 9 * 32 * 2^-24 * 4 = 7e-5
+    want = [float(w.detach()) for w in (loss, pgs, kls)]
+    for q, w in zip(stats[:3].tolist(), want):
+        assert abs(q - w) <= 7e-5 * max(abs(want[1]), abs(want[2]), 0.1)
+    assert abs(float(norm) / float(full) - 1) <= 7e-5
+    for k, g in grads.items():
+        assert off(got[k].cpu().reshape(g.shape), g * (1 if k == "x0" else coef)) <= 7e-5, k
+    # Adam's first step is lr g / (|g| + eps) with the clipped gradient the step reports
+    for s in before:
+        g = got[s].double()
+        want = before[s].double() - lr * g / (g.abs() + 1e-8)
+        assert float((getattr(layer, s).double() - want).abs().max()) <= 2.0 ** -23 * 0.2 + lr * 2.0 ** -20
+
+
+def test_policy_step_bf16(B):
+    """The same chain in bf16, on the MFMA paths: every clipped gradient near the float32 chain's."""
+    from orthogonal_reparameterized_amd import workloads as WL
+    from orthogonal_reparameterized_amd.step import LayerStep, PolicyStep
+    d, f, v, n, b = 256, 640, 1003, 320, 128
+    p, x0, t = policy_step_inputs(d, f, v, n)
+    got = {}
+    for name, dt in (("f32", F32), ("bf16", BF16)):
+        wl = WL.Workload(96, "policy", n, d, d, b, name, name, name, 0.02, d)
+        inp = WL.make_layer_inputs(wl)
+        if name == "f32":
+            keep = inp
+        else:  # the same values, rounded
+            inp = dict(keep, w=torch.from_numpy(keep["w"]).to(BF16).view(torch.int16).numpy().view(np.uint16),
+                       x=torch.from_numpy(keep["x"]).to(BF16).view(torch.int16).numpy().view(np.uint16),
+                       dz=torch.from_numpy(keep["dz"]).to(BF16).view(torch.int16).numpy().view(np.uint16))
+        dense = ("w_gate", "w_up", "w_down", "head")
+        q = {k: w.to(BF16).to(dt) if k in dense else w for k, w in p.items()}
+        step = PolicyStep(LayerStep(wl, inp, "fast"), q)
+        got[name] = step.step(x0.to(BF16).to(dt), t.cuda(), rand(30, 4), torch.tensor([0, 100, 130, 290, 320]).cuda(),
+                              max_norm=1e-3, mask=(t >= 0).cuda())
+    for k, g in got["f32"][1].items():
+        # about a dozen stages, each rounding to bf16 (2^-8 / sqrt 3 in the mean square): sqrt(12 / 3) 2^-8,
+        # with condition numbers of a few
+        assert off(got["bf16"][1][k].float().reshape(g.shape), g.double()) <= 4 * 2 * 2.0 ** -8, k
+    assert abs(float(got["bf16"][2]) / float(got["f32"][2]) - 1) <= 8 * 2.0 ** -8
