@@ -13,6 +13,14 @@
 //     kernel puts them into LDS for the tile's rows first (`rows` points at row m0's).
 //   kStats == true: reduce() gets the whole tile's accumulators (row statistics).  A product
 //     split over k leaves its partials to the caller then (no epilogue runs).
+//
+// B may come as two operands of one shape (an epilogue's kForm):
+//   kPairRows: the rows of B and B2 side by side, in runs of kRun rows of one and the same kRun of
+//     the other (gate and up weights).  Columns of C go by these rows; fragments that belong
+//     together lie in one lane, and the epilogue takes them in pairs, put_pair(m, n, g, u, nv)
+//     (kPair), with n counted in rows of one operand, of which there are a.half.
+//   kTwoRanges: B k-major, its k from a.half64 on being B2's (a sum of two products).  Each has
+//     a.half rows; those from there to a.half64, the next multiple of 64, read as zero.
 #pragma once
 
 #include "lds_tiles.h"
@@ -32,7 +40,17 @@ struct MmArgs {
   int full = 0x7fffffff, tail_splits = 1;
   int64_t tail_kc = 0;
   float *tail_part = nullptr;
+  const void *B2 = nullptr;
+  int64_t half = 0, half64 = 0;
 };
+
+enum { kOneB = 0, kPairRows = 1, kTwoRanges = 2 };
+template <class Epi, class = void> struct FormOf { static constexpr int value = kOneB; };
+template <class Epi> struct FormOf<Epi, std::void_t<decltype(Epi::kForm)>> { static constexpr int value = Epi::kForm; };
+template <class Epi, class = void> struct PairOf { static constexpr bool value = false; };
+template <class Epi> struct PairOf<Epi, std::void_t<decltype(Epi::kPair)>> { static constexpr bool value = Epi::kPair; };
+// rows of a run: a wave's columns (64 of the bf16 kernels, 32 of the smaller float32 one) hold whole pairs of runs
+template <typename T> constexpr int kRun = sizeof(T) == 2 ? 32 : 16;
 
 namespace {
 
@@ -104,6 +122,32 @@ struct StageKC {
   }
 };
 
+// The same for kPairRows: a wave loads one run, of one of the operands (128 rows over 4 waves).
+struct StagePair {
+  static constexpr int INSTR = 4;
+  int voff[INSTR];
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ void init(const MmArgs &a, int64_t n0, int64_t kbeg) {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
+    const int64_t row0 = n0 / 2, left = a.half - row0 < 64 ? a.half - row0 : 64;
+    rs = make_rsrc((const bf16_t *)(w & 1 ? a.B2 : a.B) + row0 * a.ldb, left * a.ldb * 2);
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) {
+      const int row = (w * INSTR + i) * 8 + (l >> 3);
+      voff[i] = (int)((((w >> 1) * 32 + i * 8 + (l >> 3)) * a.ldb + kbeg) * 2) + (((l & 7) ^ kc_key<64>(row)) << 4);
+    }
+  }
+  __device__ void issue_all(int t, int64_t left, bf16_t *tile) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) {
+      int off = voff[i] + t * 128;
+      if (left < 64 && (((l & 7) ^ kc_key<64>((w * INSTR + i) * 8 + (l >> 3))) << 3) >= left) off = kPast;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * INSTR + i) * 512), 16, off, 0, 0, 0);
+    }
+  }
+};
+
 template <int R, int NW>
 struct StageKM {
   static constexpr int CH = R / 8, RPI = 64 / CH, INSTR = 64 / RPI / NW;
@@ -128,6 +172,34 @@ struct StageKM {
   __device__ void issue_all(int t, int64_t left, bf16_t *tile) const {
 #pragma unroll
     for (int i = 0; i < INSTR; ++i) issue(t, left, tile, i);
+  }
+};
+
+// The rows of a kTwoRanges operand that k steps of `step` from k read: their base, and how many
+// of them there are.
+__device__ inline const void *range_rows(const MmArgs &a, int64_t k, int step, int esize, int64_t &rows) {
+  const bool second = k >= a.half64;
+  const int64_t at = second ? k - a.half64 : k;
+  rows = a.half - at < step ? a.half - at : step;
+  return (const char *)(second ? a.B2 : a.B) + at * a.ldb * esize;
+}
+template <int R, int NW>
+struct StageRanges : StageKM<R, NW> {
+  using S = StageKM<R, NW>;
+  int64_t k0;
+  __device__ void init2(const MmArgs &a, int64_t col0, int64_t kbeg) {
+    S::init(nullptr, a.ldb, col0, 0, 0);
+    k0 = kbeg;
+  }
+  __device__ void issue_all(const MmArgs &a, int t, bf16_t *tile) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    int64_t rows;
+    const void *base = range_rows(a, k0 + (int64_t)t * 64, 64, 2, rows);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, rows * a.ldb * 2);
+#pragma unroll
+    for (int i = 0; i < S::INSTR; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * S::INSTR + i) * S::RPI * R), 16, S::voff[i],
+                                               0, 0, 0);
   }
 };
 
@@ -163,6 +235,35 @@ __device__ inline void put_rows(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t 
   }
 }
 
+// The same for kPairRows: a wave's columns are runs of RUN of one operand and of the other in turn.
+template <int FM, int FN, int RUN, class Epi>
+__device__ inline void put_pairs(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int64_t M, int64_t half, float *st,
+                                 const Epi &epi) {
+  constexpr int R = 16, LD = FN * R + 4, W = FN * R / 2, LPR = W / 8, RPP = 64 / LPR < R ? 64 / LPR : R;
+  const int l = threadIdx.x & 63, c = (l % LPR) * 8, at = c / RUN * 2 * RUN + c % RUN;
+  const int64_t n = n0 / 2 + c;
+  const int nv = half - n >= 8 ? 8 : half - n > 0 ? (int)(half - n) : 0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) *(f32x4 *)(st + (l % R) * LD + R * j + 4 * (l / R)) = acc[i][j];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < R / RPP; ++p) {
+      const int r = p * RPP + l / LPR;
+      const int64_t m = m0 + R * i + r;
+      if (l / LPR < RPP && m < M && nv) {
+        const f32x4 a = *(const f32x4 *)(st + r * LD + at), b = *(const f32x4 *)(st + r * LD + at + 4);
+        const f32x4 x = *(const f32x4 *)(st + r * LD + at + RUN), y = *(const f32x4 *)(st + r * LD + at + RUN + 4);
+        float g[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        float u[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        epi.put_pair(m, n, g, u, nv);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // The epilogue of a kernel's BM x BN tile; lds: free, at least 16 (columns + 4) floats per wave
 // and kRows BM floats more.
 template <int BM, int BN, int WGM, int WGN, int FM, int FN, class Epi>
@@ -172,6 +273,9 @@ __device__ inline void finish(const f32x4 (&acc)[FM][FN], const MmArgs &a, const
   const int64_t m0 = (int64_t)tile.tm * BM, n0 = (int64_t)tile.tn * BN;
   if constexpr (Epi::kStats) {
     epi.template reduce<BM, BN, WGM, WGN>(acc, m0, n0, a.M, a.N, tile.tn, lds);
+  } else if constexpr (PairOf<Epi>::value) {
+    const int wave = threadIdx.x >> 6, wm = (wave / WGN) * WTM, wn = (wave % WGN) * WTN;
+    put_pairs<FM, FN, Epi::RUN>(acc, m0 + wm, n0 + wn, a.M, a.half, lds + wave * R * (WTN + 4), epi);
   } else {
     const int wave = threadIdx.x >> 6, wm = (wave / WGN) * WTM, wn = (wave % WGN) * WTN;
     float *rows = lds + WGM * WGN * R * (WTN + 4);
@@ -188,9 +292,10 @@ __device__ inline void finish(const f32x4 (&acc)[FM][FN], const MmArgs &a, const
 
 // Epilogue that only writes: C[m][n] in T, split s at C + s * stride.  Tag (every epilogue
 // names one, as Tag_) keeps the kernels of two source files apart.
-template <typename T, class Tag>
+template <typename T, class Tag, int FORM = kOneB>
 struct StoreEpi {
   static constexpr bool kStats = false;
+  static constexpr int kForm = FORM;
   static constexpr int kRows = 0;
   using Tag_ = Tag;
   struct Cols {};
@@ -223,16 +328,24 @@ __device__ inline void mm_body(const MmArgs &a, const Epi &epi, int id, bf16_t *
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   using SA = typename std::conditional<AKM, StageKM<BM, NW>, StageKC<BM, NW>>::type;
-  using SB = typename std::conditional<BKM, StageKM<BN, NW>, StageKC<BN, NW>>::type;
+  constexpr int FORM = FormOf<Epi>::value;
+  static_assert(FORM != kPairRows || (!BKM && BN == 128 && NW == 4), "one run per wave");
+  static_assert(FORM != kTwoRanges || BKM, "ranges of k are ranges of rows");
+  using SB = std::conditional_t<FORM == kPairRows, StagePair,
+                                std::conditional_t<FORM == kTwoRanges, StageRanges<BN, NW>,
+                                                   std::conditional_t<BKM, StageKM<BN, NW>, StageKC<BN, NW>>>>;
   SA sa;
   SB sb;
   sa.init((const bf16_t *)a.A, a.lda, m0, a.M, kbeg);
-  sb.init((const bf16_t *)a.B, a.ldb, n0, a.N, kbeg);
+  if constexpr (FORM == kPairRows) sb.init(a, n0, kbeg);
+  else if constexpr (FORM == kTwoRanges) sb.init2(a, n0, kbeg);
+  else sb.init((const bf16_t *)a.B, a.ldb, n0, a.N, kbeg);
   const int64_t span = kend - kbeg;
   const int nk = (int)((span + BK - 1) / BK);
   auto issue = [&](int t) {
     sa.issue_all(t, span - (int64_t)t * BK, smem + (t & 1) * AE);
-    sb.issue_all(t, span - (int64_t)t * BK, smem + 2 * AE + (t & 1) * BE);
+    if constexpr (FORM == kTwoRanges) sb.issue_all(a, t, smem + 2 * AE + (t & 1) * BE);
+    else sb.issue_all(t, span - (int64_t)t * BK, smem + 2 * AE + (t & 1) * BE);
   };
   if (nk > 0) issue(0);
   for (int t = 0; t < nk; ++t) {
@@ -361,6 +474,60 @@ struct Half<RUN, true> {
   __device__ static bf16x8 frag(const bf16_t *tile, int r0, int ks) { return frag_km<128>(tile, r0, ks); }
 };
 
+// kPairRows: each half tile is 128 rows of one operand.
+struct HalfPair {
+  int voff[2];
+  int64_t span;
+  __amdgpu_buffer_rsrc_t rs[2];
+  __device__ void init(const MmArgs &a, int64_t n0, int64_t kbeg, int64_t span_) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int64_t row0 = n0 / 2, left = a.half - row0 < 128 ? a.half - row0 : 128;
+    rs[0] = make_rsrc((const bf16_t *)a.B + row0 * a.ldb, left * a.ldb * 2);
+    rs[1] = make_rsrc((const bf16_t *)a.B2 + row0 * a.ldb, left * a.ldb * 2);
+    span = span_;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (w * 2 + i) * 8 + (l >> 3);
+      voff[i] = (int)((r * a.ldb + kbeg) * 2) + (((l & 7) ^ kc_key<64>(r)) << 4);
+    }
+  }
+  __device__ void issue(int t, int h, bf16_t *tile) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
+    const int64_t left64 = span - (int64_t)t * 64;
+    const int left = left64 < 64 ? (int)left64 : 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (w * 2 + i) * 8 + (l >> 3);
+      const int off = (((l & 7) ^ kc_key<64>(r)) << 3) < left ? voff[i] + t * 128 : kPast;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs[h], (lds_void *)(tile + (w * 2 + i) * 512), 16, off, 0, 0, 0);
+    }
+  }
+  __device__ static bf16x8 frag(const bf16_t *tile, int r0, int ks) { return frag_kc<64>(tile, r0, ks); }
+};
+// kTwoRanges: a k-major half whose rows are those of one operand or the other.  Steps past the range
+// of this workgroup read what follows there (in bounds) or zeros; they are not multiplied.
+template <int RUN>
+struct HalfRanges : Half<RUN, true> {
+  using H = Half<RUN, true>;
+  MmArgs a;
+  int64_t k0;
+  __device__ void init(const MmArgs &a_, int64_t col0, int64_t kbeg) {
+    H::init(nullptr, a_.ldb, col0, 0, 0, 0);
+    a.B = a_.B; a.B2 = a_.B2; a.ldb = a_.ldb; a.half = a_.half; a.half64 = a_.half64;
+    k0 = kbeg;
+  }
+  __device__ void issue(int t, int h, bf16_t *tile) const {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    int64_t rows;
+    const void *base = range_rows(a, k0 + (int64_t)t * 64, 64, 2, rows);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, rows * a.ldb * 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * 2 + i) * 512), 16, H::voff[i] + h * RUN * 2,
+                                               0, 0, 0);
+  }
+};
+
 namespace {
 // s_waitcnt vmcnt(N) lgkmcnt(0)
 template <int N>
@@ -397,11 +564,17 @@ __global__ __launch_bounds__(512) void k_mm8(MmArgs a, Epi epi) {
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   using HA = Half<64, AKM>;
-  using HB = Half<32, BKM>;
+  constexpr int FORM = FormOf<Epi>::value;
+  static_assert(FORM != kPairRows || !(BKM || FLIP), "pairs of rows are k-contiguous");
+  static_assert(FORM != kTwoRanges || BKM, "ranges of k are ranges of rows");
+  using HB = std::conditional_t<FORM == kPairRows, HalfPair,
+                                std::conditional_t<FORM == kTwoRanges, HalfRanges<32>, Half<32, BKM>>>;
   HA ha;
   HB hb;
   ha.init((const bf16_t *)a.A, a.lda, m0, a.M, kbeg, kend - kbeg);
-  hb.init((const bf16_t *)a.B, a.ldb, n0, a.N, kbeg, kend - kbeg);
+  if constexpr (FORM == kPairRows) hb.init(a, n0, kbeg, kend - kbeg);
+  else if constexpr (FORM == kTwoRanges) hb.init(a, n0, kbeg);
+  else hb.init((const bf16_t *)a.B, a.ldb, n0, a.N, kbeg, kend - kbeg);
   const int nk = (int)((kend - kbeg + 63) / 64);
   // all of A's halves within 64 KB of one base, and all of B's: the reach of a DS offset
   auto sA = [&](int s, int h) { return smem + (2 * h + s) * HE; };
@@ -528,20 +701,28 @@ __device__ inline void mm_f32_body(const MmArgs &a, const Epi &epi, int id, floa
   // them reads as zero.  k-contiguous: the base is the tile's first row and only a last step
   // that is not whole needs its elements past k cleared; k-major: the base moves with k.
   const int64_t span = kend - kbeg;
-  auto offsets = [&](int64_t ld, bool km, int (&off)[PC]) {
+  constexpr int FORM = FormOf<Epi>::value;
+  static_assert(FORM != kPairRows || !BKM, "pairs of rows are k-contiguous");
+  static_assert(FORM != kTwoRanges || BKM, "ranges of k are ranges of rows");
+  auto offsets = [&](int64_t ld, bool km, bool pair, int (&off)[PC]) {
 #pragma unroll
     for (int i = 0; i < PC; ++i) {
-      const int e = tid + 256 * i;
+      const int e = tid + 256 * i, r = e / (BK / 4);
       off[i] = km ? (int)((e / (BT / 4) * ld + e % (BT / 4) * 4) * 4)
-                  : (int)((e / (BK / 4) * ld + e % (BK / 4) * 4) * 4);
+                  : (int)(((pair ? r / 32 * 16 + r % 16 : r) * ld + e % (BK / 4) * 4) * 4);
     }
   };
+  // kPairRows: 64 lanes load rows of one run (8 or 16 rows, whose number moves by multiples of 32)
+  const bool up = __builtin_amdgcn_readfirstlane(tid / (BK / 4) / 16 & 1);
   auto fetch = [&](const float *P, int64_t ld, int64_t r0, int64_t rows, bool km, int t, const int (&off)[PC],
-                   f32x4 (&v)[PC]) {
+                   f32x4 (&v)[PC], bool ranges = false) {
     const int64_t left = span - (int64_t)t * BK;
     const int64_t nr = rows - r0 < BT ? rows - r0 : BT;
+    int64_t rk = 0;
+    const float *two = ranges ? (const float *)range_rows(a, kbeg + (int64_t)t * BK, BK, 4, rk) + r0 : nullptr;
     const __amdgpu_buffer_rsrc_t rs =
-        km ? make_rsrc(P + (kbeg + (int64_t)t * BK) * ld + r0, ((left < BK ? left : BK) * ld - r0) * 4)
+        ranges ? make_rsrc(two, (rk * ld - r0) * 4)
+        : km ? make_rsrc(P + (kbeg + (int64_t)t * BK) * ld + r0, ((left < BK ? left : BK) * ld - r0) * 4)
            : make_rsrc(P + r0 * ld + kbeg + (int64_t)t * BK, (nr * ld - kbeg - (int64_t)t * BK) * 4);
 #pragma unroll
     for (int i = 0; i < PC; ++i)
@@ -566,15 +747,16 @@ __device__ inline void mm_f32_body(const MmArgs &a, const Epi &epi, int id, floa
       }
     }
   };
-  const float *A = (const float *)a.A, *B = (const float *)a.B;
+  const float *A = (const float *)a.A, *B = (const float *)(FORM == kPairRows && up ? a.B2 : a.B);
+  const int64_t nb = FORM == kPairRows ? n0 / 2 : n0, rows_b = FORM == kPairRows ? a.half : a.N;
   const int nk = (int)((span + BK - 1) / BK);
   f32x4 va[PC], vb[PC];
   int oa[PC], ob[PC];
-  offsets(a.lda, AKM, oa);
-  offsets(a.ldb, BKM, ob);
+  offsets(a.lda, AKM, false, oa);
+  offsets(a.ldb, BKM, FORM == kPairRows, ob);
   if (nk > 0) {
     fetch(A, a.lda, m0, a.M, AKM, 0, oa, va);
-    fetch(B, a.ldb, n0, a.N, BKM, 0, ob, vb);
+    fetch(B, a.ldb, nb, rows_b, BKM, 0, ob, vb, FORM == kTwoRanges);
   }
   for (int t = 0; t < nk; ++t) {
     float *ta = smem + (t & 1) * 2 * ST, *tb = ta + ST;
@@ -585,7 +767,7 @@ __device__ inline void mm_f32_body(const MmArgs &a, const Epi &epi, int id, floa
     __syncthreads();
     if (t + 1 < nk) {
       fetch(A, a.lda, m0, a.M, AKM, t + 1, oa, va);
-      fetch(B, a.ldb, n0, a.N, BKM, t + 1, ob, vb);
+      fetch(B, a.ldb, nb, rows_b, BKM, t + 1, ob, vb, FORM == kTwoRanges);
     }
     // the four MFMAs' elements of 16 rows from r0 in 16-deep block h
     auto frag = [&](const float *st, bool km, int r0, int h) {
@@ -625,6 +807,7 @@ __global__ __launch_bounds__(256) void k_mm_f32(MmArgs a, Epi epi) {
 template <class Epi>
 struct MaybePart {
   static constexpr bool kStats = false;
+  static constexpr int kForm = FormOf<Epi>::value;
   static constexpr int kRows = Epi::kRows;
   using Tag_ = typename Epi::Tag_;
   using Cols = typename Epi::Cols;
@@ -735,57 +918,102 @@ template <typename T, int NG, bool ODD, class Epi>
 __global__ __launch_bounds__(512) void k_mm_few(MmArgs a, Epi epi) {
   constexpr int KW = 8 / NG, U = 4, E = RowFrag<T>::E, D = 4 * E;  // U fragments of D k in flight per wave
   __shared__ __align__(16) float red[8 * 16 * 20];  // the parts (8 x 256), then the rows (8 x 320)
+  __shared__ __align__(16) float red2[PairOf<Epi>::value ? NG * 16 * 20 : 4];
   const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int ng = wave / KW, kw = wave % KW;
   const int64_t n0 = ((int64_t)blockIdx.x * NG + ng) * 16, n = n0 + (l & 15), m = l & 15;
-  const T *pb = (const T *)a.B + (n < a.N ? n : a.N - 1) * a.ldb;
+  constexpr bool PAIR = PairOf<Epi>::value;
+  const int64_t row = (n < a.N ? n : a.N - 1) * a.ldb;
+  const T *pb = (const T *)a.B + row, *pb2 = PAIR ? (const T *)a.B2 + row : nullptr;
   const T *pa = (const T *)a.A + (m < a.M ? m : a.M - 1) * a.lda;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
   const int64_t steps = cdiv(a.K, D * U);
   for (int64_t t = kw; t < steps; t += KW) {
     const int64_t k0 = t * D * U + E * (l >> 4);
-    typename RowFrag<T>::V fb[U], fa[U];
+    typename RowFrag<T>::V fb[U], fa[U], fb2[PAIR ? U : 1];
     if ((t + 1) * D * U <= a.K) {
 #pragma unroll
       for (int u = 0; u < U; ++u) fb[u] = row_frag<ODD>(pb + k0 + D * u, E);
+      if constexpr (PAIR) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) fb2[u] = row_frag<ODD>(pb2 + k0 + D * u, E);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) fa[u] = row_frag<ODD>(pa + k0 + D * u, E);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         fb[u] = row_frag<ODD>(pb + k0 + D * u, a.K - k0 - D * u);
+        if constexpr (PAIR) fb2[u] = row_frag<ODD>(pb2 + k0 + D * u, a.K - k0 - D * u);
         fa[u] = row_frag<ODD>(pa + k0 + D * u, a.K - k0 - D * u);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = mul_frag(fb[u], fa[u], acc);
+    for (int u = 0; u < U; ++u) {
+      acc = mul_frag(fb[u], fa[u], acc);
+      if constexpr (PAIR) acc2 = mul_frag(fb2[u], fa[u], acc2);
+    }
   }
   // the k parts of a group, summed in wave order by its first wave
-  if constexpr (KW > 1) {
-    *(f32x4 *)(red + (wave * 64 + l) * 4) = acc;
+  auto join = [&](f32x4 &v) {
+    *(f32x4 *)(red + (wave * 64 + l) * 4) = v;
     __syncthreads();
     if (kw == 0) {
 #pragma unroll
-      for (int w = 1; w < KW; ++w) acc += *(const f32x4 *)(red + ((wave + w) * 64 + l) * 4);
+      for (int w = 1; w < KW; ++w) v += *(const f32x4 *)(red + ((wave + w) * 64 + l) * 4);
     }
     __syncthreads();
+  };
+  if constexpr (KW > 1) {
+    join(acc);
+    if constexpr (PAIR) join(acc2);
   }
   if (kw) return;
   // lane l: row l % 16, columns 4 (l / 16) .. +3; pairs of lanes make 8 columns
   float *st = red + wave * 16 * 20;
+  [[maybe_unused]] float *st2 = red2 + ng * 16 * 20;
   *(f32x4 *)(st + (l & 15) * 20 + 4 * (l >> 4)) = acc;
+  if constexpr (PAIR) *(f32x4 *)(st2 + (l & 15) * 20 + 4 * (l >> 4)) = acc2;
   __builtin_amdgcn_wave_barrier();
   const int r = l >> 1, c = (l & 1) * 8;
   if (l < 32 && r < a.M && n0 + c < a.N) {
     const f32x4 p = *(const f32x4 *)(st + r * 20 + c), q = *(const f32x4 *)(st + r * 20 + c + 4);
     float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
     const int nv = a.N - n0 - c >= 8 ? 8 : (int)(a.N - n0 - c);
-    epi.put(epi.cols(n0 + c, nv, nullptr), r, n0 + c, v, nv);
+    if constexpr (PAIR) {
+      const f32x4 x = *(const f32x4 *)(st2 + r * 20 + c), y = *(const f32x4 *)(st2 + r * 20 + c + 4);
+      float u[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      epi.put_pair(r, n0 + c, v, u, nv);
+    } else {
+      epi.put(epi.cols(n0 + c, nv, nullptr), r, n0 + c, v, nv);
+    }
   }
 }
 
 // Sum of the float32 partials of a split product, [splits][M][N] in split order, into the
 // epilogue; one thread per 8 columns.
+// (Of kPairRows the partials have N columns, runs of each operand in turn: one thread per 8 pairs.)
+template <class Epi>
+__device__ inline void join_pairs(const float *part, int splits, int64_t M, int64_t N, const Epi &epi, uint32_t id) {
+  const int64_t half = epi.half();
+  const uint32_t cpr = (uint32_t)cdiv(half, 8), i = id * 256 + threadIdx.x;
+  if (i >= M * cpr) return;
+  const int64_t m = i / cpr, n = (int64_t)(i - (uint32_t)m * cpr) * 8;
+  const int nv = half - n >= 8 ? 8 : (int)(half - n);
+  const float *p = part + m * N + n / Epi::RUN * 2 * Epi::RUN + n % Epi::RUN;
+  float g[8], u[8];
+  load8(p, 8, g);
+  load8(p + Epi::RUN, 8, u);
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) {
+    float w[8], x[8];
+    load8(p + s * M * N, 8, w);
+    load8(p + s * M * N + Epi::RUN, 8, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { g[e] += w[e]; u[e] += x[e]; }
+  }
+  epi.put_pair(m, n, g, u, nv);
+}
 template <class Epi>
 __device__ inline void join_body(const float *part, int splits, int64_t M, int64_t N, const Epi &epi, uint32_t id) {
   // (a split product has fewer than 2^32 results)
@@ -806,7 +1034,8 @@ __device__ inline void join_body(const float *part, int splits, int64_t M, int64
 }
 template <class Epi>
 __global__ __launch_bounds__(256) void k_mm_join(const float *part, int splits, int64_t M, int64_t N, Epi epi) {
-  join_body(part, splits, M, N, epi, blockIdx.x);
+  if constexpr (PairOf<Epi>::value) join_pairs(part, splits, M, N, epi, blockIdx.x);
+  else join_body(part, splits, M, N, epi, blockIdx.x);
 }
 // both products of a pair; the first has workgroups [0, ja)
 template <class EA, class EB>
@@ -817,26 +1046,37 @@ __global__ __launch_bounds__(256) void k_mm_join_pair(const float *pa, int sa, i
   else join_body(pb, sb, Mb, Nb, eb, blockIdx.x - ja);
 }
 
-// The same for the shared tiles of k_mm8: 32 workgroups per tile, one thread per 8 columns.
+// The same for the shared tiles of k_mm8: 32 workgroups per tile, one thread per 8 columns; of
+// kPairRows, whose tiles hold 256 x 128 pairs, 16 workgroups and one thread per 8 pairs.
+template <class Epi>
+constexpr int kTailGroups = PairOf<Epi>::value ? 16 : 32;
 template <class Epi>
 __global__ __launch_bounds__(256) void k_mm_tail(MmArgs a, Epi epi) {
-  const int tail = blockIdx.x / 32, i = (int)(blockIdx.x % 32) * 256 + threadIdx.x;
+  constexpr bool PAIR = PairOf<Epi>::value;
+  constexpr int G = kTailGroups<Epi>, W = 8 * G, PER = PAIR ? 2 : 1;  // columns of a tile, operands
+  const int tail = blockIdx.x / G, i = (int)(blockIdx.x % G) * 256 + threadIdx.x;
   int tm, tn;
   tile_at(a, a.full + tail, tm, tn);
-  const int64_t m = (int64_t)tm * 256 + i / 32, n = (int64_t)tn * 256 + i % 32 * 8;
-  if (m >= a.M || n >= a.N) return;
-  const float *p = a.tail_part + (int64_t)tail * a.tail_splits * 65536 + i * 8;
-  float v[8];
-  load8(p, 8, v);
+  const int row = i / G, c = i % G * 8;
+  const int64_t m = (int64_t)tm * 256 + row, n = (int64_t)tn * W + c, N = PAIR ? a.half : a.N;
+  if (m >= a.M || n >= N) return;
+  const float *p = a.tail_part + (int64_t)tail * a.tail_splits * 65536 + row * 256 + (PAIR ? c / 32 * 64 + c % 32 : c);
+  float v[PER][8];
+#pragma unroll
+  for (int q = 0; q < PER; ++q) load8(p + 32 * q, 8, v[q]);
 #pragma unroll 2
   for (int s = 1; s < a.tail_splits; ++s) {
-    float w[8];
-    load8(p + (int64_t)s * 65536, 8, w);
+    float w[PER][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += w[e];
+    for (int q = 0; q < PER; ++q) load8(p + (int64_t)s * 65536 + 32 * q, 8, w[q]);
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[q][e] += w[q][e];
   }
-  const int nv = a.N - n >= 8 ? 8 : (int)(a.N - n);
-  epi.put(epi.cols(n, nv, nullptr), m, n, v, nv);
+  const int nv = N - n >= 8 ? 8 : (int)(N - n);
+  if constexpr (PAIR) epi.put_pair(m, n, v[0], v[PER - 1], nv);
+  else epi.put(epi.cols(n, nv, nullptr), m, n, v[0], nv);
 }
 
 // ------------------------------------------------------------------ host side ----
@@ -858,7 +1098,15 @@ struct MmDesc {
   const void *A = nullptr; int64_t lda = 0;
   const void *B = nullptr; int64_t ldb = 0;
   const char *name = "mm", *large = "mm_large";  // launch labels: of the smaller and the larger tile
+  const void *B2 = nullptr;  // kPairRows, kTwoRanges
+  int64_t half = 0, half64 = 0;
 };
+// The kernels' arguments of a product through its plan.
+inline MmArgs mm_args(const MmDesc &d, const MmPlan &p) {
+  MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, (int)p.splits, p.kc};
+  a.B2 = d.B2; a.half = d.half; a.half64 = d.half64;
+  return a;
+}
 
 // float32: the kernels are bound by the matrix cores, so a CU's time is that of the tiles dealt to
 // it: w = ceil(workgroups / CUs) of them, a 32-deep step of a 64 x 64 tile taking 0.55 us (0.83
@@ -994,22 +1242,25 @@ int mm_run_as(const MmArgs &a, const MmPlan &p, const MmDesc &d, const Epi &epi,
 template <typename T, bool AKM, bool BKM, class Epi>
 int mm_run(const MmDesc &d, const MmPlan &p, float *part, const Epi &epi, hipStream_t s) {
   if (d.M <= 0 || d.N <= 0) return POETX_OK;
-  MmArgs a{d.M, d.N, d.K, d.A, d.lda, d.B, d.ldb, (int)p.tiles_m, (int)p.tiles_n, (int)p.splits, p.kc};
+  MmArgs a = mm_args(d, p);
   const int64_t tiles = p.tiles_m * p.tiles_n;
   if (tiles * p.splits > kMaxTiles) return POETX_ERR_UNSUPPORTED;
   if constexpr (!Epi::kStats && sizeof(T) == 2) {
     if (p.full < tiles) {
       a.full = (int)p.full; a.tail_splits = (int)p.tail_splits; a.tail_kc = p.tail_kc; a.tail_part = part;
       POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d, epi, s)));
-      return launch_k("mm_tail", s, k_mm_tail<Epi>, dim3((unsigned)((tiles - p.full) * 32)), dim3(256), 0, a, epi);
+      return launch_k("mm_tail", s, k_mm_tail<Epi>, dim3((unsigned)((tiles - p.full) * kTailGroups<Epi>)), dim3(256),
+                      0, a, epi);
     }
   }
   if (p.splits == 1) return mm_run_as<T, AKM, BKM>(a, p, d, epi, s);
-  POETX_TRY((mm_run_as<T, AKM, BKM>(a, p, d, StoreEpi<float, typename Epi::Tag_>{part, d.N, d.M * d.N}, s)));
+  POETX_TRY((mm_run_as<T, AKM, BKM>(
+      a, p, d, StoreEpi<float, typename Epi::Tag_, FormOf<Epi>::value>{part, d.N, d.M * d.N}, s)));
   if constexpr (Epi::kStats) {
     return POETX_OK;
   } else {
-    return launch_k("mm_join", s, k_mm_join<Epi>, dim3((unsigned)cdiv(d.M * cdiv(d.N, 8), 256)), dim3(256), 0,
+    const int64_t cols = PairOf<Epi>::value ? d.half : d.N;
+    return launch_k("mm_join", s, k_mm_join<Epi>, dim3((unsigned)cdiv(d.M * cdiv(cols, 8), 256)), dim3(256), 0,
                     (const float *)part, (int)p.splits, d.M, d.N, epi);
   }
 }
@@ -1054,8 +1305,7 @@ int mm_run_pair(const char *name, const MmDesc &da, const MmPlan &pa, float *par
   const int64_t ga = cdiv(na, 8) * 8;
   const int64_t ns = cdiv(sum.cols, 16);
   if (ga + nb + ns > kMaxTiles) return POETX_ERR_UNSUPPORTED;
-  const MmArgs a{da.M, da.N, da.K, da.A, da.lda, da.B, da.ldb, (int)pa.tiles_m, (int)pa.tiles_n, (int)pa.splits, pa.kc};
-  const MmArgs b{db.M, db.N, db.K, db.A, db.lda, db.B, db.ldb, (int)pb.tiles_m, (int)pb.tiles_n, (int)pb.splits, pb.kc};
+  const MmArgs a = mm_args(da, pa), b = mm_args(db, pb);
   const bool sa = pa.splits > 1, sb = pb.splits > 1;
   constexpr size_t lds = sizeof(T) == 4 ? f32_lds(64, 32) * 4 : (size_t)2 * 2 * 128 * 64 * 2;
   auto kern = &k_mm_pair<T, MaybePart<EA>, MaybePart<EB>>;

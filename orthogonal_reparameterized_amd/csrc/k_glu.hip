@@ -9,31 +9,56 @@ namespace poetx {
 
 struct GluTag {};
 
-// h = act(g) u from float32 products; g and u kept where wanted.  One thread per 8 columns.
+// The two projections are one product whose B interleaves runs of w_gate's and w_up's rows
+// (kPairRows): g and u of a result lie in one lane's accumulators, and act(g) u, with g and u where
+// they are kept, is the product's epilogue.
 template <typename T>
-__global__ __launch_bounds__(256) void k_glu_join(const float *g, const float *u, int act, int64_t n, int64_t f, T *h,
-                                                  T *gate, T *up) {
-  const int64_t cpr = cdiv(f, 8), total = n * cpr;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cpr, c = (i - r * cpr) * 8, o = r * f + c;
-    const int nv = f - c >= 8 ? 8 : (int)(f - c);
-    float a[8], b[8];
-    load8(g + o, nv, a);
-    load8(u + o, nv, b);
-    if (gate) store8(gate + o, nv, a);
-    if (up) store8(up + o, nv, b);
-    act_values<T>(a, act);
+struct GluEpi {
+  static constexpr bool kStats = false, kPair = true;
+  static constexpr int kRows = 0, kForm = kPairRows, RUN = kRun<T>;
+  using Tag_ = GluTag;
+  T *h, *gate, *up;
+  int act;
+  int64_t f;
+  __device__ int64_t half() const { return f; }
+  __device__ void put_pair(int64_t m, int64_t n, float (&g)[8], float (&u)[8], int nv) const {
+    const int64_t o = m * f + n;
+    if (gate) {
+      store8(gate + o, nv, g);
+      store8(up + o, nv, u);
+    }
+    act_values<T>(g, act);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] *= b[e];
-    store8(h + o, nv, a);
+    for (int e = 0; e < 8; ++e) g[e] *= u[e];
+    store8(h + o, nv, g);
   }
-}
+};
 
-// dg and du in T, rows of ld >= f elements (the rest zero).
+// Rows [0, f) of a product go to dw_gate, rows [f64, f64 + f) to dw_up.
+template <typename T>
+struct GluWeightEpi {
+  static constexpr bool kStats = false;
+  static constexpr int kRows = 0;
+  using Tag_ = GluTag;
+  struct Cols {};
+  T *wg, *wu;
+  int64_t f, f64, ld;
+  __device__ Cols cols(int64_t, int, const float *) const { return {}; }
+  __device__ const GluWeightEpi &at(int) const { return *this; }
+  __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const {
+    const bool second = m >= f64;
+    const int64_t r = second ? m - f64 : m;
+    if (r < f) store8((second ? wu : wg) + r * ld + n, nv, v);
+  }
+};
+
+// dg and du in T, side by side: rows [dg, zeros up to f64, du, zeros].  The rounding is the
+// precision in which the products read them (an operand's half step, independent from element to
+// element).
 template <typename T>
 __global__ __launch_bounds__(256) void k_glu_grad(const T *dh, const T *gate, const T *up, int act, int64_t n, int64_t f,
-                                                  T *dg, T *du, int64_t ld) {
-  const int64_t cpr = cdiv(ld, 8), total = n * cpr;
+                                                  int64_t f64, T *dgu) {
+  const int64_t cpr = f64 / 8, total = n * cpr;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / cpr, c = (i - r * cpr) * 8, left = f - c;
     const int nv = left >= 8 ? 8 : left > 0 ? (int)left : 0;
@@ -47,69 +72,61 @@ __global__ __launch_bounds__(256) void k_glu_grad(const T *dh, const T *gate, co
     act_values<T>(a, act);
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] *= a[e];
-    const int nw = ld - c >= 8 ? 8 : (int)(ld - c);
-    store8(dg + r * ld + c, nw, s);
-    store8(du + r * ld + c, nw, d);
+    T *out = dgu + r * 2 * f64 + c;
+    store8(out, 8, s);
+    store8(out + f64, 8, d);
   }
 }
 
-// out = a + b, rounded to T
-template <typename T>
-__global__ __launch_bounds__(256) void k_glu_add(const float *a, const float *b, int64_t n, T *out) {
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
-    const int nv = n - i >= 8 ? 8 : (int)(n - i);
-    float v[8], w[8];
-    load8(a + i, nv, v);
-    load8(b + i, nv, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += w[e];
-    store8(out + i, nv, v);
-  }
-}
+// (Named here because hipcc 7.2 leaves one of these out where only mm_launch asks for them, and the
+// library then lacks the symbol.)
+template __global__ void k_mm8<false, true, false, StoreEpi<float, GluTag, kTwoRanges>>(
+    MmArgs, StoreEpi<float, GluTag, kTwoRanges>);
+template __global__ void k_mm8<false, true, false, StoreEpi<bf16_t, GluTag, kTwoRanges>>(
+    MmArgs, StoreEpi<bf16_t, GluTag, kTwoRanges>);
 
 namespace {
 
-int64_t round8(int64_t v) { return (v + 7) & ~(int64_t)7; }
-dim3 stride_grid(int64_t n) {
-  const int64_t g = cdiv(n, 256);
-  return dim3((unsigned)(g < 65536 ? g : 65536));
-}
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // A bf16 operand whose rows are not a multiple of 16 bytes is copied to padded rows.
 const void *packed(const void *in, int64_t rows, int64_t cols, int dt, Arena &ar, PackList &l) {
   if (dt == POETX_F32 || cols % 8 == 0) return in;
-  void *q = ar.take((size_t)rows * round8(cols) * 2);
-  l.add({in, rows, cols, q, round8(cols), nullptr, 0});
+  void *q = ar.take((size_t)rows * round_up(cols, 8) * 2);
+  l.add({in, rows, cols, q, round_up(cols, 8), nullptr, 0});
   return q;
-}
-
-template <typename T, bool AKM, bool BKM, typename C>
-int product(const MmDesc &m, int dt, C *out, Arena &ar, bool measure, PackList *l, hipStream_t s) {
-  const MmPlan p = mm_plan(m.M, m.N, m.K, dt);
-  float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
-  if (measure) return POETX_OK;
-  if (l) POETX_TRY(pack_rows(*l, dt, s));
-  return mm_run<T, AKM, BKM>(m, p, part, StoreEpi<C, GluTag>{out, m.N, 0}, s);
 }
 
 template <typename T>
 int fwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
-  PackList l;
-  const int64_t k = d.dt == POETX_BF16 ? round8(d.d) : d.d;
-  float *g = (float *)ar.take((size_t)d.n * d.f * 4), *u = (float *)ar.take((size_t)d.n * d.f * 4);
+  const GluEpi<T> epi{(T *)d.h, (T *)d.gate, (T *)d.up, d.act, d.f};
   MmDesc m;
-  m.M = d.n; m.N = d.f; m.K = k; m.lda = m.ldb = k; m.name = "glu_fwd"; m.large = "glu_fwd_large";
+  m.M = d.n; m.N = 2 * round_up(d.f, kRun<T>); m.K = d.d; m.half = d.f; m.name = "glu_fwd"; m.large = "glu_fwd_large";
+  m.A = d.x; m.lda = d.d; m.B = d.wg; m.B2 = d.wu; m.ldb = d.d;
+  if (d.n <= 16) {  // reading the weights bounds these: no LDS tiles, any alignment
+    if (measure) return POETX_OK;
+    MmArgs a{m.M, d.f, m.K, m.A, m.lda, m.B, m.ldb, 1, 1, 1, m.K};
+    a.B2 = m.B2;
+    const int64_t groups = cdiv(d.f, 16), two = groups >= 1024;
+    constexpr bool B16 = sizeof(T) == 2;
+    auto kern = two ? k_mm_few<T, 2, false, GluEpi<T>> : k_mm_few<T, 1, false, GluEpi<T>>;
+    if (B16 && d.d % 2) kern = two ? k_mm_few<T, 2, B16, GluEpi<T>> : k_mm_few<T, 1, B16, GluEpi<T>>;
+    return launch_k("glu_fwd", s, kern, dim3((unsigned)(two ? cdiv(groups, 2) : groups)), dim3(512), 0, a, epi);
+  }
+  PackList l;
+  if (sizeof(T) == 2) m.K = m.lda = m.ldb = round_up(d.d, 8);  // the padding is zero
   m.A = packed(d.x, d.n, d.d, d.dt, ar, l);
-  const void *wg = packed(d.wg, d.f, d.d, d.dt, ar, l), *wu = packed(d.wu, d.f, d.d, d.dt, ar, l);
-  m.B = wg;
-  POETX_TRY((product<T, false, false>(m, d.dt, g, ar, measure, &l, s)));
-  m.B = wu;
-  POETX_TRY((product<T, false, false>(m, d.dt, u, ar, measure, nullptr, s)));
+  m.B = packed(d.wg, d.f, d.d, d.dt, ar, l);
+  m.B2 = packed(d.wu, d.f, d.d, d.dt, ar, l);
+  const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
+  float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
   if (measure) return POETX_OK;
-  return launch_k("glu_join", s, k_glu_join<T>, stride_grid(d.n * cdiv(d.f, 8)), dim3(256), 0, (const float *)g,
-                  (const float *)u, d.act, d.n, d.f, (T *)d.h, (T *)d.gate, (T *)d.up);
+  POETX_TRY(pack_rows(l, d.dt, s));
+  return mm_run<T, false, false>(m, p, part, epi, s);
 }
 
+// dx = [dg du] [Wg; Wu]: one product over 2 f64, dg du k-contiguous, the weights k-major and one
+// after the other (kTwoRanges);  [dWg; dWu] = [dg du]^T x: both k-major
 template <typename T>
 int bwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
   if (d.n == 0) {
@@ -117,34 +134,46 @@ int bwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
     POETX_TRY(fill_zero(d.dwg, d.f * d.d, d.dt, s));
     return fill_zero(d.dwu, d.f * d.d, d.dt, s);
   }
+  const int64_t f64 = round_up(d.f, 64), ld = sizeof(T) == 2 ? round_up(d.d, 8) : d.d;
+  T *dgu = (T *)ar.take((size_t)d.n * 2 * f64 * sizeof(T));
+  const StoreEpi<T, GluTag, kTwoRanges> ex{(T *)d.dx, d.d, 0};
+  const GluWeightEpi<T> ew{(T *)d.dwg, (T *)d.dwu, d.f, f64, d.d};
+  MmDesc mx, mw;
   PackList l;
-  const bool b16 = d.dt == POETX_BF16;
-  const int64_t lf = b16 ? round8(d.f) : d.f, ld = b16 ? round8(d.d) : d.d;
-  T *dg = (T *)ar.take((size_t)d.n * lf * sizeof(T)), *du = (T *)ar.take((size_t)d.n * lf * sizeof(T));
-  if (!measure)
-    POETX_TRY(launch_k("glu_grad", s, k_glu_grad<T>, stride_grid(d.n * cdiv(lf, 8)), dim3(256), 0, (const T *)d.dh,
-                       (const T *)d.gate_in, (const T *)d.up_in, d.act, d.n, d.f, dg, du, lf));
   if (d.dx) {
-    float *a = (float *)ar.take((size_t)d.n * d.d * 4), *b = (float *)ar.take((size_t)d.n * d.d * 4);
-    MmDesc m;
-    m.M = d.n; m.N = d.d; m.K = d.f; m.lda = lf; m.ldb = ld; m.name = "glu_dx"; m.large = "glu_dx_large";
-    const void *wg = packed(d.wg, d.f, d.d, d.dt, ar, l), *wu = packed(d.wu, d.f, d.d, d.dt, ar, l);
-    m.A = dg; m.B = wg;
-    POETX_TRY((product<T, false, true>(m, d.dt, a, ar, measure, &l, s)));
-    m.A = du; m.B = wu;
-    POETX_TRY((product<T, false, true>(m, d.dt, b, ar, measure, nullptr, s)));
-    if (!measure)
-      POETX_TRY(launch_k("glu_add", s, k_glu_add<T>, stride_grid(cdiv(d.n * d.d, 8)), dim3(256), 0, (const float *)a,
-                         (const float *)b, d.n * d.d, (T *)d.dx));
+    mx.M = d.n; mx.N = d.d; mx.K = 2 * f64; mx.half = d.f; mx.half64 = f64; mx.name = "glu_dx"; mx.large = "glu_dx_large";
+    mx.A = dgu; mx.lda = 2 * f64; mx.ldb = ld;
+    mx.B = packed(d.wg, d.f, d.d, d.dt, ar, l);
+    mx.B2 = packed(d.wu, d.f, d.d, d.dt, ar, l);
   }
-  if (d.dwg) {
-    MmDesc m;
-    m.M = d.f; m.N = d.d; m.K = d.n; m.lda = lf; m.ldb = ld; m.name = "glu_dw"; m.large = "glu_dw_large";
-    m.B = packed(d.x, d.n, d.d, d.dt, ar, l);
-    m.A = dg;
-    POETX_TRY((product<T, true, true>(m, d.dt, (T *)d.dwg, ar, measure, &l, s)));
-    m.A = du;
-    POETX_TRY((product<T, true, true>(m, d.dt, (T *)d.dwu, ar, measure, nullptr, s)));
+  const bool flip = d.dwg && dw_flips(2 * f64, d.d, d.n, d.dt);
+  if (d.dwg && !flip) {
+    mw.M = 2 * f64; mw.N = d.d; mw.K = d.n; mw.name = "glu_dw"; mw.large = "glu_dw_large";
+    mw.A = dgu; mw.lda = 2 * f64; mw.ldb = ld;
+    mw.B = packed(d.x, d.n, d.d, d.dt, ar, l);
+  }
+  const MmTwo two = mm_two(mx.M, mx.N, mx.K, mw.M, mw.N, mw.K, d.dt);
+  const MmPlan &px = two.a, &pw = two.b;
+  float *part_x = px.part_bytes ? (float *)ar.take(px.part_bytes) : nullptr;
+  float *part_w = pw.part_bytes ? (float *)ar.take(pw.part_bytes) : nullptr;
+  const int64_t ldt = round_up(d.n, 8);
+  void *xt = flip ? ar.take((size_t)d.d * ldt * 2) : nullptr;
+  if (measure) return POETX_OK;
+  const int64_t groups = cdiv(d.n * (f64 / 8), 256);
+  POETX_TRY(launch_k("glu_grad", s, k_glu_grad<T>, dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256), 0,
+                     (const T *)d.dh, (const T *)d.gate_in, (const T *)d.up_in, d.act, d.n, d.f, f64, dgu));
+  POETX_TRY(pack_rows(l, d.dt, s));
+  if (two.pair) return mm_run_pair<T>("glu_dx_dw", mx, px, part_x, ex, mw, pw, part_w, ew, SumArgs{}, s);
+  POETX_TRY((mm_run<T, false, true>(mx, px, part_x, ex, s)));
+  POETX_TRY((mm_run<T, true, true>(mw, pw, part_w, ew, s)));
+  if constexpr (sizeof(T) == 2) {
+    if (flip) {
+      POETX_TRY(pack_rows_t(d.x, d.n, d.d, xt, ldt, nullptr, 0, s));
+      MmDesc m;
+      m.M = d.d; m.N = 2 * f64; m.K = d.n; m.large = "glu_dw_large";
+      m.A = xt; m.lda = ldt; m.B = dgu; m.ldb = 2 * f64;
+      return mm_run_flipped(m, ew, s);
+    }
   }
   return POETX_OK;
 }
