@@ -4,9 +4,9 @@
 // and the sum of any number of them keeps every digit that a float32 norm shows.  (64-bit
 // multiply-adds run at a tenth of their rate beside loads from memory.)
 //
-// The list of gradients comes with the launch, in its arguments: 120 of them at a time.  Each
-// launch deals equal spans of elements to its workgroups; a workgroup's sum goes to one partial,
-// and the partials are joined in their order.
+// The elements are cut into spans, one workgroup each; a workgroup's sum goes to one partial, and
+// the partials are joined in their order.  A short list of gradients comes with each launch, in its
+// arguments; a longer one is written into the workspace first, as a table of the spans.
 #include "kernels.h"
 #include "vec.h"
 
@@ -14,137 +14,245 @@ namespace poetx {
 
 namespace {
 
-constexpr int kGradList = 120;
-constexpr int64_t kGradBlocks = 2048;  // workgroups over all gradients (and one more per gradient)
+constexpr int kGradList = 140;        // gradients in a launch's arguments (4 KB)
+constexpr int64_t kGradSpans = 8192;  // spans of much data
+constexpr int64_t kGradLeast = 4096;  // elements of a span of little data
+constexpr int64_t kGradFew = 512;     // partials that every workgroup joins for itself
 
-struct GradItem {
+struct GradSpan {
   const void *g;
   void *out;
-  int64_t n;
-  uint32_t first;  // its first workgroup in the launch
-  uint32_t bf16;
+  uint32_t n, bf16;
 };
 struct GradArgs {
-  GradItem t[kGradList];
+  const void *g[kGradList];
+  void *out[kGradList];
+  int64_t n[kGradList];         // negative: bf16
+  uint32_t first[kGradList];    // the gradient's first span in this launch
   int count;
-  int64_t span;    // elements per workgroup, a multiple of 2048
-  double *part;    // this launch's partials
-  const float *coef;
+  uint32_t spans;               // of this launch
+  int64_t span;                 // elements, a multiple of 2048
+  GradSpan *table;
 };
 
-// the gradient of this workgroup
-__device__ inline int item_of(const GradArgs &a) {
+// span s of the list in the arguments
+__device__ inline GradSpan span_of(const GradArgs &a, uint32_t s) {
   int lo = 0, hi = a.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.t[mid].first <= blockIdx.x) lo = mid;
+    if (a.first[mid] <= s) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  const bool bf16 = a.n[lo] < 0;
+  const int64_t n = bf16 ? -a.n[lo] : a.n[lo], at = (int64_t)(s - a.first[lo]) * a.span;
+  const int64_t left = n - at < a.span ? n - at : a.span, byte = at * (bf16 ? 2 : 4);
+  return {(const char *)a.g[lo] + byte, (char *)a.out[lo] + byte, (uint32_t)left, bf16 ? 1u : 0u};
 }
 
-// Elements of [begin, end) from p, 8 at a time from its first 16-byte boundary on:
-// visit(index, count) with count <= 8.
-template <typename T, class F>
-__device__ inline void walk(const T *p, int64_t begin, int64_t end, const F &visit) {
-  const int64_t head = ((16 - (int64_t)((uintptr_t)(p + begin) & 15)) & 15) / (int64_t)sizeof(T);
-  const int64_t first = begin + head < end ? begin + head : end;
-  if ((int64_t)threadIdx.x < first - begin) visit(begin + threadIdx.x, 1);
-  for (int64_t i = first + 8 * (int64_t)threadIdx.x; i < end; i += 2048) visit(i, end - i >= 8 ? 8 : (int)(end - i));
+// Elements [0, n) at p, 8 at a time from its first 16-byte boundary on, four such groups of a
+// thread loaded before the first is used: visit(index, elements, values), zeros past the end.
+// go() is asked after the first groups' loads are on their way; all threads come to it.
+template <typename T, class Go, class F>
+__device__ inline void walk(const T *p, uint32_t n, const Go &go, const F &visit) {
+  const uint32_t head = (uint32_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)), first = head < n ? head : n;
+  uint32_t i = first + 8 * threadIdx.x;
+  Raw8<T> r[4];
+  auto load = [&] {
+    if ((int64_t)i + 3 * 2048 + 8 <= n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load_raw(p + i + k * 2048, 8, r[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t left = (int64_t)n - i - k * 2048;
+        load_raw(p + i + k * 2048, left >= 8 ? 8 : left > 0 ? (int)left : 0, r[k]);
+      }
+    }
+  };
+  load();
+  if (!go()) return;
+  if (threadIdx.x < first) {
+    float v[8];
+    load8(p + threadIdx.x, 1, v);
+    visit(threadIdx.x, 1, v);
+  }
+  while (i < n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t left = (int64_t)n - i - k * 2048;
+      if (left > 0) {
+        float v[8];
+        widen(r[k], v);
+        visit(i + k * 2048, left >= 8 ? 8 : (int)left, v);
+      }
+    }
+    i += 4 * 2048;
+    load();
+  }
 }
 
+template <int WAVES>
 __device__ inline double block_sum(double v, double *red) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  return ((red[0] + red[1]) + red[2]) + red[3];
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) v += red[w];
+  return v;
 }
 
 template <typename T>
-__device__ inline double squares(const T *p, int64_t begin, int64_t end) {
-  double s = 0;
-  walk(p, begin, end, [&](int64_t i, int nv) {
-    float v[8];
-    load8(p + i, nv, v);
+__device__ inline double squares(const GradSpan &t) {
+  double s[2] = {0, 0};
+  walk((const T *)t.g, t.n, [] { return true; }, [&](uint32_t, int, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fma((double)v[e], (double)v[e], s);
+    for (int e = 0; e < 8; ++e) s[e & 1] = fma((double)v[e], (double)v[e], s[e & 1]);
   });
-  return s;
+  return s[0] + s[1];
 }
 
-template <typename T>
-__device__ inline void scale(const T *p, T *out, int64_t begin, int64_t end, float c) {
-  walk(p, begin, end, [&](int64_t i, int nv) {
-    float v[8];
-    load8(p + i, nv, v);
+// Stores that are not to stay in the caches, where they would push out what is still to be read (and
+// be written back under the next reads): 352 million values, norm and scaling 404 -> 379 us.
+__device__ inline void store_past(bf16_t *p, int nv, const float (&v)[8]) {
+  if (nv == 8 && !((uintptr_t)p & 15))
+    __builtin_nontemporal_store(
+        u32v4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, (u32v4 *)p);
+  else
+    store8(p, nv, v);
+}
+__device__ inline void store_past(float *p, int nv, const float (&v)[8]) {
+  if (nv == 8 && !((uintptr_t)p & 15)) {
+    __builtin_nontemporal_store(f32v4{v[0], v[1], v[2], v[3]}, (f32v4 *)p);
+    __builtin_nontemporal_store(f32v4{v[4], v[5], v[6], v[7]}, (f32v4 *)p + 1);
+  } else {
+    store8(p, nv, v);
+  }
+}
+
+template <typename T, class Coef>
+__device__ inline void scale(const GradSpan &t, const Coef &coef) {
+  float c = 0.f;
+  walk((const T *)t.g, t.n,
+       [&] {
+         c = coef();
+         return c != 1.f || t.out != t.g;
+       },
+       [&](uint32_t i, int nv, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= c;
-    store8(out + i, nv, v);
-  });
+         for (int e = 0; e < 8; ++e) v[e] *= c;
+         store_past((T *)t.out + i, nv, v);
+       });
+}
+
+__device__ inline float coef_of(double norm, float max_norm) {
+  return norm <= (double)max_norm ? 1.f : (float)((double)max_norm / norm);
 }
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void k_grad_squares(GradArgs a) {
-  __shared__ double red[4];
-  const GradItem &t = a.t[item_of(a)];
-  const int64_t begin = (int64_t)(blockIdx.x - t.first) * a.span, end = begin + a.span < t.n ? begin + a.span : t.n;
-  const double s = block_sum(t.bf16 ? squares((const bf16_t *)t.g, begin, end) : squares((const float *)t.g, begin, end),
-                             red);
-  if (threadIdx.x == 0) a.part[blockIdx.x] = s;
+__global__ __launch_bounds__(256) void k_grad_table(GradArgs a) {
+  const uint32_t s = blockIdx.x * 256 + threadIdx.x;
+  if (s < a.spans) a.table[s] = span_of(a, s);
 }
 
-__global__ __launch_bounds__(256) void k_grad_join(const double *part, int64_t parts, float max_norm, float *norm,
-                                                   float *coef) {
+template <bool TABLE>
+__global__ __launch_bounds__(256) void k_grad_squares(GradArgs a, double *part) {
   __shared__ double red[4];
+  const GradSpan t = TABLE ? a.table[blockIdx.x] : span_of(a, blockIdx.x);
+  const double s = block_sum<4>(t.bf16 ? squares<bf16_t>(t) : squares<float>(t), red);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(1024) void k_grad_join(const double *part, uint32_t parts, float max_norm, float *norm,
+                                                    float *coef) {
+  __shared__ double red[16];
   double s = 0;
-  for (int64_t i = threadIdx.x; i < parts; i += 256) s += part[i];
-  s = sqrt(block_sum(s, red));
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < parts; i += 1024) s += part[i];
+  s = sqrt(block_sum<16>(s, red));
   if (threadIdx.x) return;
   *norm = (float)s;
-  *coef = s <= (double)max_norm ? 1.f : (float)((double)max_norm / s);
+  *coef = coef_of(s, max_norm);
 }
 
-__global__ __launch_bounds__(256) void k_grad_scale(GradArgs a) {
-  const GradItem &t = a.t[item_of(a)];
-  const float c = *a.coef;
-  if (c == 1.f && t.out == t.g) return;
-  const int64_t begin = (int64_t)(blockIdx.x - t.first) * a.span, end = begin + a.span < t.n ? begin + a.span : t.n;
-  if (t.bf16) scale((const bf16_t *)t.g, (bf16_t *)t.out, begin, end, c);
-  else scale((const float *)t.g, (float *)t.out, begin, end, c);
+// The last spans first: they were read last before, and some are still in the caches.  JOIN: the
+// few partials of a small list are joined by every workgroup for itself, while its first loads are
+// under way, which costs less than a launch between.
+template <bool TABLE, bool JOIN>
+__global__ __launch_bounds__(256) void k_grad_scale(GradArgs a, const double *part, float max_norm, float *norm,
+                                                    float *coef) {
+  __shared__ double red[4];
+  const uint32_t k = gridDim.x - 1 - blockIdx.x;
+  const GradSpan t = TABLE ? a.table[k] : span_of(a, k);
+  const float given = JOIN ? 0.f : *coef;
+  if (given == 1.f && t.out == t.g) return;
+  auto get = [&] {
+    if (!JOIN) return given;
+    double s = 0;
+    for (uint32_t i = threadIdx.x; i < a.spans; i += 256) s += part[i];
+    s = sqrt(block_sum<4>(s, red));
+    const float c = coef_of(s, max_norm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      *norm = (float)s;
+      *coef = c;
+    }
+    return c;
+  };
+  if (t.bf16) scale<bf16_t>(t, get);
+  else scale<float>(t, get);
 }
 
 int grad_norm(const GradDesc &d, Arena &ar, bool measure, hipStream_t s) {
-  int64_t total = 0, blocks = 0;
-  for (int64_t k = 0; k < d.n; ++k) total += d.g[k].n;
-  int64_t span = cdiv(cdiv(total, kGradBlocks), 2048) * 2048;
-  if (span < 8192) span = 8192;
-  for (int64_t k = 0; k < d.n; ++k) blocks += cdiv(d.g[k].n, span);
-  double *part = (double *)ar.take((size_t)(blocks > 0 ? blocks : 1) * 8);
-  if (measure) return POETX_OK;
-  for (int pass = 0; pass < (d.clip ? 2 : 1); ++pass) {
-    GradArgs a;
-    a.span = span; a.part = part; a.coef = d.coef; a.count = 0;
-    int64_t grid = 0;
-    for (int64_t k = 0; k <= d.n; ++k) {
-      if (k < d.n && d.g[k].n > 0) {
-        a.t[a.count++] = {d.g[k].g, d.g[k].out, d.g[k].n, (uint32_t)grid, d.g[k].dtype == POETX_BF16 ? 1u : 0u};
-        grid += cdiv(d.g[k].n, span);
-      }
-      if (a.count == kGradList || (k == d.n && a.count)) {
-        if (pass == 0) POETX_TRY(launch_k("grad_squares", s, k_grad_squares, dim3((unsigned)grid), dim3(256), 0, a));
-        else POETX_TRY(launch_k("grad_scale", s, k_grad_scale, dim3((unsigned)grid), dim3(256), 0, a));
-        a.part += grid;
-        a.count = 0;
-        grid = 0;
-      }
-    }
-    if (pass == 0)
-      POETX_TRY(launch_k("grad_join", s, k_grad_join, dim3(1), dim3(256), 0, (const double *)part, blocks, d.max_norm,
-                         d.norm, d.coef));
+  int64_t total = 0, items = 0, spans = 0;
+  for (int64_t k = 0; k < d.n; ++k) {
+    total += d.g[k].n;
+    items += d.g[k].n > 0;
   }
-  return POETX_OK;
+  int64_t span = cdiv(cdiv(total, kGradSpans), 2048) * 2048;
+  if (span < kGradLeast) span = kGradLeast;
+  if (span > (int64_t)1 << 31) span = (int64_t)1 << 31;
+  for (int64_t k = 0; k < d.n; ++k) spans += cdiv(d.g[k].n, span);
+  const bool table = items > kGradList, join = !table && spans <= kGradFew;
+  double *part = (double *)ar.take((size_t)(spans > 0 ? spans : 1) * 8);
+  GradArgs a;
+  a.span = span;
+  a.table = table ? (GradSpan *)ar.take((size_t)spans * sizeof(GradSpan)) : nullptr;
+  if (measure) return POETX_OK;
+  a.count = 0;
+  a.spans = 0;
+  GradSpan *const rows = a.table;
+  for (int64_t k = 0; k < d.n; ++k) {
+    const poetx_grad &g = d.g[k];
+    if (g.n > 0) {
+      a.g[a.count] = g.g;
+      a.out[a.count] = d.clip ? g.out : nullptr;
+      a.n[a.count] = g.dtype == POETX_BF16 ? -g.n : g.n;
+      a.first[a.count++] = a.spans;
+      a.spans += (uint32_t)cdiv(g.n, span);
+    }
+    if (table && a.count && (a.count == kGradList || k == d.n - 1)) {
+      POETX_TRY(launch_k("grad_table", s, k_grad_table, dim3((unsigned)cdiv(a.spans, 256)), dim3(256), 0, a));
+      a.table += a.spans;
+      a.count = 0;
+      a.spans = 0;
+    }
+  }
+  if (table) {
+    a.table = rows;
+    a.spans = (uint32_t)spans;
+  }
+  const dim3 grid((unsigned)spans), block(256);
+  if (spans > 0)
+    POETX_TRY(launch_k("grad_squares", s, table ? k_grad_squares<true> : k_grad_squares<false>, grid, block, 0, a, part));
+  if (!d.clip || !join || spans == 0)
+    POETX_TRY(launch_k("grad_join", s, k_grad_join, dim3(1), dim3(1024), 0, (const double *)part, (uint32_t)spans, d.max_norm,
+                       d.norm, d.coef));
+  if (!d.clip || spans == 0) return POETX_OK;
+  const auto kern = table ? k_grad_scale<true, false> : join ? k_grad_scale<false, true> : k_grad_scale<false, false>;
+  return launch_k("grad_scale", s, kern, grid, block, 0, a,
+                  (const double *)part, d.max_norm, d.norm, d.coef);
 }
 
 }  // namespace poetx

@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kSeg = 256;         // tokens of a wave's segment
 constexpr int64_t kCountParts = 1024;
+constexpr int64_t kFewTokens = 8192, kFewSeqs = 4096;  // up to these one workgroup does it all
 
 struct PolicyArgs {
   int64_t n, seqs;
@@ -356,6 +357,51 @@ __global__ __launch_bounds__(256) void k_policy_stats(PolicyArgs a, int blocks) 
   write_stats(a, s);
 }
 
+// Few tokens: one launch.  The counts stay in LDS.
+__global__ __launch_bounds__(1024) void k_policy_few(PolicyArgs a, int64_t segs) {
+  __shared__ int cnt[kFewSeqs];
+  __shared__ double red[16][3];
+  const int wave = threadIdx.x >> 6;
+  const bool by_seq = a.reduce == POETX_REDUCE_SEQUENCE;
+  const int64_t s0 = wave * a.run, s1 = s0 + a.run < segs ? s0 + a.run : segs;
+  float whole = 0.f;
+  if (by_seq && a.mask) {
+    for (int i = threadIdx.x; i < a.seqs; i += 1024) cnt[i] = 0;
+    __syncthreads();
+    count_run(a, s0, s1, [&](int64_t q, int c) { atomicAdd(&cnt[q], c); });
+    __syncthreads();
+  } else if (!by_seq) {
+    int64_t lo, hi;
+    bounds(a, lo, hi);
+    int64_t count = hi - lo;
+    if (a.mask && a.reduce == POETX_REDUCE_TOKEN) {
+      const int c = wave_sum_i(count_all(a, lo, hi, threadIdx.x, 1024));
+      if ((threadIdx.x & 63) == 0) cnt[wave] = c;
+      __syncthreads();
+      count = 0;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) count += cnt[w];
+    }
+    whole = shared_weight(a, count);
+  }
+  double sum[3] = {0, 0, 0};
+  policy_run(a, s0, s1, whole, [&](int64_t q) { return a.mask ? (cnt[q] > 1 ? cnt[q] : 1) : length_of(a, q); }, sum);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const double v = wave_sum_d(sum[k]);
+    if ((threadIdx.x & 63) == 0) red[wave][k] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    sum[k] = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) sum[k] += red[w][k];
+  }
+  write_stats(a, sum);
+}
+
 int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s) {
   PolicyArgs a{};
   a.n = d.n; a.seqs = d.seqs; a.offsets = d.offsets;
@@ -364,6 +410,11 @@ int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s) {
   a.low = d.low; a.high = d.high; a.r_low = d.r_low; a.r_high = d.r_high; a.beta = d.beta; a.scale = (float)d.scale;
   a.stats = d.stats; a.dnll = d.dnll;
   const int64_t segs = cdiv(d.n, kSeg), cus = device_cus() > 0 ? device_cus() : 256;
+  if (d.n <= kFewTokens && d.seqs <= kFewSeqs) {
+    if (measure) return POETX_OK;
+    a.run = cdiv(segs, 16);
+    return launch_k("policy_few", s, k_policy_few, dim3(1), dim3(1024), 0, a, segs);
+  }
   a.run = cdiv(segs, 4 * 8 * cus);
   if (a.run < 1) a.run = 1;
   const int64_t blocks = segs > 0 ? cdiv(segs, 4 * a.run) : 1;

@@ -86,7 +86,7 @@ def test_policy_refusals(B):
     for kw in (dict(n=1 << 31), dict(s=1 << 31)):
         assert policy(B, **kw) == B.POETX_ERR_UNSUPPORTED, kw
     for kw in (dict(), dict(reduce=1), dict(reduce=2), dict(low=inf, high=inf)):
-        assert policy(B, nb=16, **kw) == B.POETX_ERR_WORKSPACE, kw
+        assert policy(B, n=10000, nb=16, **kw) == B.POETX_ERR_WORKSPACE, kw
         assert policy(B, ws=None, nb=0, **kw) == B.POETX_OK, kw
     q = B.PoetxPolicyC(0.2, 0.2, 0.0, 1.0, 0, 0)
     assert B.raw.poetx_policy_loss(10, 2, *A[:6], ctypes.byref(q), A[6], A[7], A[8], None, None) == bad
