@@ -470,7 +470,7 @@ typedef struct {
  * out of bounds.  Workspace: query with ws == NULL.  Errors: NULL p, nll, adv or stats, offsets NULL
  * with n_seqs != 1, beta without nll_ref, negative or NaN bounds, beta or scale not finite, bad
  * reduce, n_tokens or n_seqs < 0, misaligned pointer, an output that equals an input or the other
- * output -> INVALID_ARG; more than 2^31 - 1 tokens or sequences -> UNSUPPORTED.
+ * output -> INVALID_ARG; more than 2^31 - 1 tokens or 2^31 - 2 sequences -> UNSUPPORTED.
  */
 int poetx_policy_loss(int64_t n_tokens, int64_t n_seqs, const int64_t *offsets, const float *nll,
                       const float *nll_old, const float *nll_ref, const float *adv, const uint8_t *mask,
@@ -486,18 +486,32 @@ typedef struct {
 } poetx_grad;
 
 /*
+ * poetx_grad_plan -- the device form of a list of gradients, for poetx_grad_norm and
+ * poetx_grad_clip calls on a list that stays the same (its buffers and lengths, not their values): a
+ * list of more than 140 gradients is dealt out from a table in device memory, which those calls
+ * otherwise write anew each time.  plan: device buffer of *plan_bytes (query with plan == NULL: the
+ * bytes needed, 0 for a list that needs no plan), 16-byte aligned; it holds the list's addresses and
+ * is read by every call that is given it.  Errors: as poetx_grad_norm; *plan_bytes too small ->
+ * POETX_ERR_WORKSPACE.
+ */
+int poetx_grad_plan(int64_t n_grads, const poetx_grad *grads /*[host]*/, void *plan, size_t *plan_bytes,
+                    void *stream);
+
+/*
  * poetx_grad_norm -- norm of all gradients of a list together, and the factor that clips it:
  *     norm = sqrt(sum_k sum_i g_k[i]^2),  coef = 1 if norm <= max_norm, else max_norm / norm
  * grads [host]: read during the call.  Its device pointers need only be aligned to their elements;
  * gradients with n == 0 are passed over (their pointers may be NULL), `out` is not used.  Types may
  * be mixed.  max_norm >= 0, infinity for the norm alone.  norm, coef: float32 device outputs, 4-byte
- * aligned.  Squares and their sum are taken in 64 bits.  A NaN anywhere makes both NaN; an infinity
- * makes norm infinite and coef 0.  n_grads == 0: norm 0, coef 1.  Workspace: query with ws == NULL
- * (the same lengths).  Errors: NULL grads, g, norm or coef, a length < 0, bad dtype, misaligned
- * pointer, max_norm < 0 or NaN -> INVALID_ARG; more than 2^20 gradients or 2^48 elements -> UNSUPPORTED.
+ * aligned.  plan (nullable): what poetx_grad_plan wrote for this very list.  Squares and their sum
+ * are taken in 64 bits.  A NaN anywhere makes both NaN; an infinity makes norm infinite and coef 0
+ * (where max_norm is finite).  n_grads == 0: norm 0, coef 1.  Workspace: query with ws == NULL (the
+ * same lengths, plan NULL or not).  Errors: NULL grads, g, norm or coef, a length < 0, bad dtype,
+ * misaligned pointer, max_norm < 0 or NaN -> INVALID_ARG; more than 2^20 gradients or 2^48 elements
+ * -> UNSUPPORTED.
  */
 int poetx_grad_norm(int64_t n_grads, const poetx_grad *grads /*[host]*/, float max_norm, float *norm, float *coef,
-                    void *ws, size_t *ws_bytes, void *stream);
+                    const void *plan, void *ws, size_t *ws_bytes, void *stream);
 
 /*
  * poetx_grad_clip -- poetx_grad_norm, then out_k = coef g_k (rounded to its dtype) for every gradient.
@@ -505,7 +519,7 @@ int poetx_grad_norm(int64_t n_grads, const poetx_grad *grads /*[host]*/, float m
  * the same elements twice as out.  Errors: as poetx_grad_norm; NULL out -> INVALID_ARG.
  */
 int poetx_grad_clip(int64_t n_grads, const poetx_grad *grads /*[host]*/, float max_norm, float *norm, float *coef,
-                    void *ws, size_t *ws_bytes, void *stream);
+                    const void *plan, void *ws, size_t *ws_bytes, void *stream);
 
 /* Human-readable name of a poetx_status code (static string). */
 const char *poetx_status_string(int status);

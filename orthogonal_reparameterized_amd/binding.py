@@ -100,8 +100,9 @@ _lib.poetx_glu_forward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _i32, 
 _lib.poetx_glu_backward.argtypes = [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp,
                                     _szp, _vp]
 _lib.poetx_policy_loss.argtypes = [_i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp]
-_lib.poetx_grad_norm.argtypes = [_i64, _vp, ctypes.c_float, _vp, _vp, _vp, _szp, _vp]
-_lib.poetx_grad_clip.argtypes = [_i64, _vp, ctypes.c_float, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_grad_plan.argtypes = [_i64, _vp, _vp, _szp, _vp]
+_lib.poetx_grad_norm.argtypes = [_i64, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _szp, _vp]
+_lib.poetx_grad_clip.argtypes = [_i64, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _szp, _vp]
 _lib.poetx_status_string.argtypes = [ctypes.c_int]
 _lib.poetx_status_string.restype = ctypes.c_char_p
 _lib.poetx_version.restype = ctypes.c_char_p
@@ -111,14 +112,14 @@ _lib.poetx_prof_only.argtypes = [ctypes.c_char_p]
 for _f in ("poetx_merge_perm", "poetx_cnp", "poetx_cnp_noalloc", "poetx_forward", "poetx_backward", "poetx_backward_adam", "poetx_fold",
            "poetx_adam_step", "poetx_layernorm_forward", "poetx_layernorm_backward", "poetx_linear_forward",
            "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward", "poetx_glu_forward",
-           "poetx_glu_backward", "poetx_policy_loss", "poetx_grad_norm", "poetx_grad_clip",
+           "poetx_glu_backward", "poetx_policy_loss", "poetx_grad_plan", "poetx_grad_norm", "poetx_grad_clip",
            "poetx_prof_enable", "poetx_prof_only", "poetx_prof_read"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("poetx_merge_perm", "poetx_cnp", "poetx_cnp_noalloc", "poetx_forward", "poetx_backward", "poetx_backward_adam", "poetx_fold",
             "poetx_adam_step", "poetx_layernorm_forward", "poetx_layernorm_backward", "poetx_linear_forward",
             "poetx_linear_backward", "poetx_xent_forward", "poetx_xent_backward", "poetx_glu_forward",
-            "poetx_glu_backward", "poetx_policy_loss", "poetx_grad_norm", "poetx_grad_clip",
+            "poetx_glu_backward", "poetx_policy_loss", "poetx_grad_plan", "poetx_grad_norm", "poetx_grad_clip",
             "poetx_status_string", "poetx_version", "poetx_prof_enable", "poetx_prof_only", "poetx_prof_read")
 
 
@@ -828,8 +829,10 @@ def poetx_policy_loss(nll: torch.Tensor, adv: torch.Tensor, offsets: Optional[to
 class GradList:
     """The gradients of a training step, for poetx_grad_norm and poetx_grad_clip: contiguous float32
     or bf16 tensors on one device, of any shapes.  out: where the clipped gradients go, tensors like
-    them that share no memory with them; None: in place.  The list keeps its tensors; a program
-    whose gradients stay where they are makes it once."""
+    them that share no memory with them; None: in place.  The list keeps its tensors (their memory
+    must stay theirs: no resizing, no setting of .data); a program whose gradients stay where they are
+    makes it once.  A list of more than 140 gradients keeps its device form (poetx_grad_plan) for each
+    stream that it is used on."""
 
     def __init__(self, grads, out=None):
         self.grads = tuple(grads)
@@ -859,10 +862,30 @@ class GradList:
         for (_, end), (begin, _) in zip(spans, spans[1:]):
             if begin < end:
                 raise ValueError("gradients" + ("" if self.out is None else " and out") + " share memory")
-        need = _sz(0)
-        _check(_lib.poetx_grad_norm(len(self.grads), self.array, 0.0, None, None, None, _byref(need), None),
+        need, n = _sz(0), len(self.grads)
+        _check(_lib.poetx_grad_plan(n, self.array, None, _byref(need), None), "poetx_grad_plan(size)")
+        self._plan_bytes, self._plans = need.value, {}
+        # with a plan where one is needed
+        _check(_lib.poetx_grad_norm(n, self.array, 0.0, None, None, _SOME, None, _byref(need), None),
                "poetx_grad_norm(size)")
         self.workspace_bytes = need.value
+
+    def plan(self) -> Optional[torch.Tensor]:
+        """The list's device form for the current stream of its device, which is the current device
+        (None: it needs none).  A call under graph capture makes its own, in the graph, from the
+        graph's memory pool.  The caller holds the tensor until its kernels are launched, so that
+        nothing it allocates before then takes the same memory."""
+        if not self._plan_bytes:
+            return None
+        key, capturing = _raw_stream(self.device.index), _capturing()
+        p = None if capturing else self._plans.get(key)
+        if p is None:
+            p = torch.empty(self._plan_bytes, dtype=torch.uint8, device=self.device)
+            _check(_lib.poetx_grad_plan(len(self.grads), self.array, p.data_ptr(), _byref(_sz(self._plan_bytes)), key),
+                   "poetx_grad_plan")
+            if not capturing:
+                self._plans[key] = p
+        return p
 
 
 def _grad_call(fn, grads, max_norm: float, out=None):
@@ -870,9 +893,17 @@ def _grad_call(fn, grads, max_norm: float, out=None):
         grads = GradList(grads, out)
     elif out is not None:
         raise ValueError("out is the list's own")
-    r = torch.empty(2, dtype=torch.float32, device=grads.device)
-    p = r.data_ptr()
-    _run(fn, grads.device, (len(grads.grads), grads.array, max_norm, p, p + 4), grads.workspace_bytes)
+    dev = grads.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _grad_call(fn, grads, max_norm)
+    r = torch.empty(2, dtype=torch.float32, device=dev)
+    p, plan = r.data_ptr(), grads.plan()
+    _run(fn, dev, (len(grads.grads), grads.array, max_norm, p, p + 4, None if plan is None else plan.data_ptr()),
+         grads.workspace_bytes)
+    del plan  # held until here
     return r[0], r[1]
 
 

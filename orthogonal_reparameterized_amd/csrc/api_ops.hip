@@ -246,7 +246,7 @@ extern "C" int poetx_policy_loss(int64_t n_tokens, int64_t n_seqs, const int64_t
   if (p->reduce < POETX_REDUCE_TOKEN || p->reduce > POETX_REDUCE_SUM) return POETX_ERR_INVALID_ARG;
   if (!(p->clip_low >= 0) || !(p->clip_high >= 0)) return POETX_ERR_INVALID_ARG;
   if (!std::isfinite(p->beta) || !std::isfinite(p->scale)) return POETX_ERR_INVALID_ARG;
-  if (n_tokens > kPolicyMaxTokens || n_seqs > kPolicyMaxTokens) return POETX_ERR_UNSUPPORTED;
+  if (n_tokens > kPolicyMaxTokens || n_seqs >= kPolicyMaxTokens) return POETX_ERR_UNSUPPORTED;
   PolicyDesc d;
   d.n = n_tokens; d.seqs = n_seqs; d.offsets = offsets;
   d.nll = nll; d.old = nll_old; d.ref = nll_ref; d.adv = adv; d.mask = mask;
@@ -269,9 +269,8 @@ extern "C" int poetx_policy_loss(int64_t n_tokens, int64_t n_seqs, const int64_t
 }
 
 namespace {
-int grad_call(int64_t n, const poetx_grad *g, float max_norm, float *norm, float *coef, bool clip, void *ws,
-              size_t *ws_bytes, void *stream) {
-  if (n < 0 || (n > 0 && !g) || !ws_bytes || !(max_norm >= 0.f)) return POETX_ERR_INVALID_ARG;
+int grad_list(int64_t n, const poetx_grad *g) {
+  if (n < 0 || (n > 0 && !g)) return POETX_ERR_INVALID_ARG;
   if (n > kGradMaxList) return POETX_ERR_UNSUPPORTED;
   int64_t total = 0;
   for (int64_t k = 0; k < n; ++k) {
@@ -279,31 +278,56 @@ int grad_call(int64_t n, const poetx_grad *g, float max_norm, float *norm, float
     if (g[k].n > kGradMaxTotal - total) return POETX_ERR_UNSUPPORTED;
     total += g[k].n;
   }
+  return POETX_OK;
+}
+// the list's buffers; `out` where it is wanted, or wherever it is set
+int grad_buffers(int64_t n, const poetx_grad *g, bool out) {
+  for (int64_t k = 0; k < n; ++k) {
+    if (g[k].n == 0) continue;
+    const uintptr_t e = dtype_size(g[k].dtype) - 1;
+    if (!g[k].g || ((uintptr_t)g[k].g & e) || ((uintptr_t)g[k].out & e) || (out && !g[k].out))
+      return POETX_ERR_INVALID_ARG;
+  }
+  return POETX_OK;
+}
+int grad_call(int64_t n, const poetx_grad *g, float max_norm, float *norm, float *coef, const void *plan, bool clip,
+              void *ws, size_t *ws_bytes, void *stream) {
+  if (!ws_bytes || !(max_norm >= 0.f)) return POETX_ERR_INVALID_ARG;
+  POETX_TRY(grad_list(n, g));
   GradDesc d;
-  d.n = n; d.g = g; d.max_norm = max_norm; d.clip = clip; d.norm = norm; d.coef = coef;
+  d.n = n; d.g = g; d.max_norm = max_norm; d.clip = clip; d.norm = norm; d.coef = coef; d.plan = plan;
   Arena need(nullptr), ar(ws);
   POETX_TRY(grad_norm(d, need, true, nullptr));
   bool query;
   POETX_TRY(ws_check(ws, ws_bytes, need.used, &query));
   if (query) return POETX_OK;
-  for (int64_t k = 0; k < n; ++k) {
-    if (g[k].n == 0) continue;
-    const uintptr_t e = dtype_size(g[k].dtype) - 1;
-    if (!g[k].g || ((uintptr_t)g[k].g & e) || (clip && (!g[k].out || ((uintptr_t)g[k].out & e))))
-      return POETX_ERR_INVALID_ARG;
-  }
-  if (!norm || !coef || norm == coef || (((uintptr_t)norm | (uintptr_t)coef) & 3) || !aligned({ws}))
+  POETX_TRY(grad_buffers(n, g, clip));
+  if (!norm || !coef || norm == coef || (((uintptr_t)norm | (uintptr_t)coef) & 3) || !aligned({plan, ws}))
     return POETX_ERR_INVALID_ARG;
   return grad_norm(d, ar, false, (hipStream_t)stream);
 }
 }  // namespace
 
+extern "C" int poetx_grad_plan(int64_t n_grads, const poetx_grad *grads, void *plan, size_t *plan_bytes,
+                               void *stream) {
+  if (!plan_bytes) return POETX_ERR_INVALID_ARG;
+  POETX_TRY(grad_list(n_grads, grads));
+  GradDesc d;
+  d.n = n_grads; d.g = grads;
+  bool query;
+  POETX_TRY(ws_check(plan, plan_bytes, grad_plan_bytes(d), &query));
+  if (query) return POETX_OK;
+  POETX_TRY(grad_buffers(n_grads, grads, false));
+  if (!aligned({plan})) return POETX_ERR_INVALID_ARG;
+  return grad_plan(d, plan, (hipStream_t)stream);
+}
+
 extern "C" int poetx_grad_norm(int64_t n_grads, const poetx_grad *grads, float max_norm, float *norm, float *coef,
-                               void *ws, size_t *ws_bytes, void *stream) {
-  return grad_call(n_grads, grads, max_norm, norm, coef, false, ws, ws_bytes, stream);
+                               const void *plan, void *ws, size_t *ws_bytes, void *stream) {
+  return grad_call(n_grads, grads, max_norm, norm, coef, plan, false, ws, ws_bytes, stream);
 }
 
 extern "C" int poetx_grad_clip(int64_t n_grads, const poetx_grad *grads, float max_norm, float *norm, float *coef,
-                               void *ws, size_t *ws_bytes, void *stream) {
-  return grad_call(n_grads, grads, max_norm, norm, coef, true, ws, ws_bytes, stream);
+                               const void *plan, void *ws, size_t *ws_bytes, void *stream) {
+  return grad_call(n_grads, grads, max_norm, norm, coef, plan, true, ws, ws_bytes, stream);
 }

@@ -6,7 +6,8 @@
 //
 // The elements are cut into spans, one workgroup each; a workgroup's sum goes to one partial, and
 // the partials are joined in their order.  A short list of gradients comes with each launch, in its
-// arguments; a longer one is written into the workspace first, as a table of the spans.
+// arguments; a longer one goes into memory first, as a table of the spans (140 gradients a launch),
+// which a caller whose list stays the same keeps as its plan.
 #include "kernels.h"
 #include "vec.h"
 
@@ -17,7 +18,7 @@ namespace {
 constexpr int kGradList = 140;        // gradients in a launch's arguments (4 KB)
 constexpr int64_t kGradSpans = 8192;  // spans of much data
 constexpr int64_t kGradLeast = 4096;  // elements of a span of little data
-constexpr int64_t kGradFew = 512;     // partials that every workgroup joins for itself
+constexpr int64_t kGradFew = 2048;    // partials that every workgroup joins for itself
 
 struct GradSpan {
   const void *g;
@@ -204,55 +205,93 @@ __global__ __launch_bounds__(256) void k_grad_scale(GradArgs a, const double *pa
   else scale<float>(t, get);
 }
 
-int grad_norm(const GradDesc &d, Arena &ar, bool measure, hipStream_t s) {
-  int64_t total = 0, items = 0, spans = 0;
+namespace {
+
+struct GradDeal {
+  int64_t items = 0, spans = 0, span = 0;
+  bool listed() const { return items <= kGradList; }
+};
+GradDeal deal(const GradDesc &d) {
+  GradDeal r;
+  int64_t total = 0;
   for (int64_t k = 0; k < d.n; ++k) {
     total += d.g[k].n;
-    items += d.g[k].n > 0;
+    r.items += d.g[k].n > 0;
   }
-  int64_t span = cdiv(cdiv(total, kGradSpans), 2048) * 2048;
-  if (span < kGradLeast) span = kGradLeast;
-  if (span > (int64_t)1 << 31) span = (int64_t)1 << 31;
-  for (int64_t k = 0; k < d.n; ++k) spans += cdiv(d.g[k].n, span);
-  const bool table = items > kGradList, join = !table && spans <= kGradFew;
-  double *part = (double *)ar.take((size_t)(spans > 0 ? spans : 1) * 8);
-  GradArgs a;
-  a.span = span;
-  a.table = table ? (GradSpan *)ar.take((size_t)spans * sizeof(GradSpan)) : nullptr;
-  if (measure) return POETX_OK;
+  r.span = cdiv(cdiv(total, kGradSpans), 2048) * 2048;
+  if (r.span < kGradLeast) r.span = kGradLeast;
+  if (r.span > (int64_t)1 << 31) r.span = (int64_t)1 << 31;
+  for (int64_t k = 0; k < d.n; ++k) r.spans += cdiv(d.g[k].n, r.span);
+  return r;
+}
+
+// The list in `a`, kGradList gradients at a time: full(a) after each such part.
+template <class F>
+int parts_of(const GradDesc &d, GradArgs &a, const F &full) {
   a.count = 0;
   a.spans = 0;
-  GradSpan *const rows = a.table;
   for (int64_t k = 0; k < d.n; ++k) {
     const poetx_grad &g = d.g[k];
-    if (g.n > 0) {
-      a.g[a.count] = g.g;
-      a.out[a.count] = d.clip ? g.out : nullptr;
-      a.n[a.count] = g.dtype == POETX_BF16 ? -g.n : g.n;
-      a.first[a.count++] = a.spans;
-      a.spans += (uint32_t)cdiv(g.n, span);
-    }
-    if (table && a.count && (a.count == kGradList || k == d.n - 1)) {
-      POETX_TRY(launch_k("grad_table", s, k_grad_table, dim3((unsigned)cdiv(a.spans, 256)), dim3(256), 0, a));
-      a.table += a.spans;
+    if (g.n == 0) continue;
+    if (a.count == kGradList) {
+      POETX_TRY(full());
       a.count = 0;
       a.spans = 0;
     }
+    a.g[a.count] = g.g;
+    a.out[a.count] = g.out;
+    a.n[a.count] = g.dtype == POETX_BF16 ? -g.n : g.n;
+    a.first[a.count++] = a.spans;
+    a.spans += (uint32_t)cdiv(g.n, a.span);
   }
-  if (table) {
-    a.table = rows;
-    a.spans = (uint32_t)spans;
-  }
-  const dim3 grid((unsigned)spans), block(256);
-  if (spans > 0)
+  return a.count ? full() : (int)POETX_OK;
+}
+
+int write_table(const GradDesc &d, int64_t span, GradSpan *table, hipStream_t s) {
+  GradArgs a;
+  a.span = span;
+  a.table = table;
+  return parts_of(d, a, [&] {
+    POETX_TRY(launch_k("grad_table", s, k_grad_table, dim3((unsigned)cdiv(a.spans, 256)), dim3(256), 0, a));
+    a.table += a.spans;
+    return (int)POETX_OK;
+  });
+}
+
+}  // namespace
+
+size_t grad_plan_bytes(const GradDesc &d) {
+  const GradDeal r = deal(d);
+  return r.listed() ? 0 : (size_t)r.spans * sizeof(GradSpan);
+}
+int grad_plan(const GradDesc &d, void *plan, hipStream_t s) {
+  const GradDeal r = deal(d);
+  return r.listed() ? (int)POETX_OK : write_table(d, r.span, (GradSpan *)plan, s);
+}
+
+int grad_norm(const GradDesc &d, Arena &ar, bool measure, hipStream_t s) {
+  const GradDeal r = deal(d);
+  const bool table = !r.listed(), join = r.spans <= kGradFew;
+  double *part = (double *)ar.take((size_t)(r.spans > 0 ? r.spans : 1) * 8);
+  GradSpan *rows = nullptr;
+  if (table) rows = d.plan ? (GradSpan *)d.plan : (GradSpan *)ar.take((size_t)r.spans * sizeof(GradSpan));
+  if (measure) return POETX_OK;
+  GradArgs a;
+  a.span = r.span;
+  a.table = rows;
+  if (!table) POETX_TRY(parts_of(d, a, [] { return (int)POETX_OK; }));
+  else if (!d.plan) POETX_TRY(write_table(d, r.span, rows, s));
+  a.spans = (uint32_t)r.spans;
+  const dim3 grid((unsigned)r.spans), block(256);
+  if (r.spans > 0)
     POETX_TRY(launch_k("grad_squares", s, table ? k_grad_squares<true> : k_grad_squares<false>, grid, block, 0, a, part));
-  if (!d.clip || !join || spans == 0)
-    POETX_TRY(launch_k("grad_join", s, k_grad_join, dim3(1), dim3(1024), 0, (const double *)part, (uint32_t)spans, d.max_norm,
+  if (!d.clip || !join || r.spans == 0)
+    POETX_TRY(launch_k("grad_join", s, k_grad_join, dim3(1), dim3(1024), 0, (const double *)part, a.spans, d.max_norm,
                        d.norm, d.coef));
-  if (!d.clip || spans == 0) return POETX_OK;
-  const auto kern = table ? k_grad_scale<true, false> : join ? k_grad_scale<false, true> : k_grad_scale<false, false>;
-  return launch_k("grad_scale", s, kern, grid, block, 0, a,
-                  (const double *)part, d.max_norm, d.norm, d.coef);
+  if (!d.clip || r.spans == 0) return POETX_OK;
+  const auto kern = table ? join ? k_grad_scale<true, true> : k_grad_scale<true, false>
+                          : join ? k_grad_scale<false, true> : k_grad_scale<false, false>;
+  return launch_k("grad_scale", s, kern, grid, block, 0, a, (const double *)part, d.max_norm, d.norm, d.coef);
 }
 
 }  // namespace poetx

@@ -34,11 +34,21 @@ struct PolicyArgs {
   double low, high;
   float r_low, r_high, beta, scale;
   float *stats, *dnll;
-  int *cnt;        // [seqs] tokens that count, of a masked call's sequences
   int *parts;      // [nparts] tokens that count, over all sequences
   int nparts;
   double *sums;    // [gridDim.x][3] partials of pg, kl, clipped
   int64_t run;     // segments per wave
+};
+
+// Tokens that count, of a masked call's sequences.  Each wave counts the tokens of its run and
+// writes what it knows for certain, so nothing is added up in memory: a sequence that begins and ends
+// in the run has its count in cnt; one that crosses runs has the tail of the run it begins in, all
+// of those between, and the head of the one it ends in.
+struct Counts {
+  int *cnt;                   // [seqs]
+  int *head, *tail, *all;     // [runs]
+  int *open;                  // [runs] offsets before the run's first token
+  int64_t runs, tokens;       // tokens of a run
 };
 
 __device__ inline int64_t offset_at(const PolicyArgs &a, int64_t j) {
@@ -64,18 +74,16 @@ __device__ inline int64_t offsets_up_to(const PolicyArgs &a, int64_t i) {
   return lo;
 }
 
+// 0x80 in the bytes of u that are not 0
+__device__ inline uint32_t set_bytes(uint32_t u) { return (((u & 0x7f7f7f7fu) + 0x7f7f7f7fu) | u) & 0x80808080u; }
 // The mask bytes of tokens i .. i + 3 as bits; tokens past the last are off.
 __device__ inline uint32_t mask4(const PolicyArgs &a, int64_t i) {
   if (!a.mask) return i + 4 <= a.n ? 15u : i >= a.n ? 0u : (1u << (a.n - i)) - 1;
+  if (i + 4 <= a.n)  // the four bits side by side at bit 24
+    return (set_bytes(*(const uint32_t *)(a.mask + i)) >> 7) * ((1u << 24) + (1u << 17) + (1u << 10) + (1u << 3)) >> 24 & 15u;
   uint32_t m = 0;
-  if (i + 4 <= a.n) {
-    const uint32_t u = *(const uint32_t *)(a.mask + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m |= (u >> (8 * k) & 255u ? 1u : 0u) << k;
-  } else {
-    for (int k = 0; k < 4; ++k)
-      if (i + k < a.n && a.mask[i + k]) m |= 1u << k;
-  }
+  for (int k = 0; k < 4; ++k)
+    if (i + k < a.n && a.mask[i + k]) m |= 1u << k;
   return m;
 }
 
@@ -90,60 +98,85 @@ __device__ inline double wave_sum_d(double v) {
   return v;
 }
 
-// Adds the counted tokens of segments [s0, s1) to cnt (int sums: any order gives the same).
-template <class Add>
-__device__ inline void count_run(const PolicyArgs &a, int64_t s0, int64_t s1, const Add &add) {
+// The counts of run r.
+__device__ inline void count_run(const PolicyArgs &a, int64_t segs, int64_t r, const Counts &c) {
   const int l = threadIdx.x & 63;
+  const int64_t s0 = r * a.run, s1 = s0 + a.run < segs ? s0 + a.run : segs;
   if (s0 >= s1) return;
   int64_t open = offsets_up_to(a, s0 * kSeg - 1);  // offsets passed; the open sequence is open - 1
-  int acc = 0;                                     // its tokens so far
+  int64_t next = offset_at(a, open);
+  if (l == 0) c.open[r] = (int)open;
+  int mine = 0;       // this lane's tokens of the open sequence
+  bool head = true;   // no offset in the run yet
   for (int64_t s = s0; s < s1; ++s) {
-    const int64_t t0 = s * kSeg, i = t0 + 4 * l;
-    const uint32_t m = mask4(a, i);
-    int before = __popc(m);  // becomes the tokens of the lanes before this one
+    const int64_t t0 = s * kSeg;
+    const uint32_t m = mask4(a, t0 + 4 * l);
+    if (next >= t0 + kSeg) {
+      mine += __popc(m);
+      continue;
+    }
+    int acc = wave_sum_i(mine);  // the open sequence's tokens before this segment
+    int before = __popc(m);      // becomes the tokens of the lanes before this one
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(before, o);
       if (l >= o) before += v;
     }
-    const int total = __shfl(before, 63);
     before -= __popc(m);
     int done = 0;  // tokens of this segment already given to a sequence
     while (true) {
       const int64_t b = offset_at(a, open + l);
-      const bool in = b < t0 + kSeg;
-      const int c = __popcll(__ballot(in));
-      if (c == 0) break;
+      const int k = __popcll(__ballot(b < t0 + kSeg));
+      if (k == 0) break;
       // tokens of the segment before this lane's offset
       const int rel = b <= t0 ? 0 : b < t0 + kSeg ? (int)(b - t0) : kSeg - 1;
-      int pre = __shfl(before, rel >> 2) + __popc(__shfl(m, rel >> 2) & ((1u << (rel & 3)) - 1));
-      if (pre < done) pre = done;  // (offsets that do not ascend: nothing is counted twice)
+      const int pre = __shfl(before, rel >> 2) + __popc(__shfl(m, rel >> 2) & ((1u << (rel & 3)) - 1));
       int prev = __shfl_up(pre, 1);
       if (l == 0) prev = done;
       const int give = pre - prev + (l == 0 ? acc : 0);
       const int64_t q = open - 1 + l;
-      if (l < c && give > 0 && q >= 0 && q < a.seqs) add(q, give);
+      if (l == 0 && head) c.head[r] = give;
+      else if (l < k && q >= 0 && q < a.seqs) c.cnt[q] = give;
+      head = false;
       acc = 0;
-      done = __shfl(pre, c - 1);
-      open += c;
-      if (c < 64) break;
+      done = __shfl(pre, k - 1);
+      open += k;
+      if (k < 64) break;
     }
-    acc += total - done;
+    next = offset_at(a, open);
+    const int at = done - before;  // of this lane's tokens, those before the last offset
+    mine = __popc(m) - (at < 0 ? 0 : at < (int)__popc(m) ? at : (int)__popc(m));
   }
-  if (l == 0 && acc > 0 && open >= 1 && open <= a.seqs) add(open - 1, acc);
+  const int rest = wave_sum_i(mine);
+  if (l == 0) (head ? c.all : c.tail)[r] = rest;
+}
+
+// Tokens that count in sequence q (0 <= q < seqs, the same for all lanes), at least 1.
+__device__ inline int count_of(const PolicyArgs &a, const Counts &c, int64_t q) {
+  const int64_t b = offset_at(a, q), e = offset_at(a, q + 1), end = c.runs * c.tokens;
+  const int64_t rb = b < 0 ? -1 : b < end ? b / c.tokens : c.runs, re = e < 0 ? 0 : e < end ? e / c.tokens : c.runs;
+  int n;
+  if (rb == re) {
+    n = c.cnt[q];
+  } else {
+    int v = 0;
+    for (int64_t r = rb + 1 + (threadIdx.x & 63); r < re; r += 64) v += c.all[r];
+    n = wave_sum_i(v) + (rb >= 0 && rb < c.runs ? c.tail[rb] : 0) + (re < c.runs ? c.head[re] : 0);
+  }
+  return n > 1 ? n : 1;
 }
 
 // Tokens that count among [lo, hi) for this thread of `threads`.
 __device__ inline int count_all(const PolicyArgs &a, int64_t lo, int64_t hi, int64_t thread, int64_t threads) {
   int c = 0;
+#pragma unroll 4
   for (int64_t i = (lo & ~(int64_t)15) + 16 * thread; i < hi; i += 16 * threads) {
+    if (i >= lo && i + 16 <= hi) {
+      const u32v4 u = *(const u32v4 *)(a.mask + i);
 #pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-      uint32_t m = mask4(a, i + k);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (i + k + q < lo || i + k + q >= hi) m &= ~(1u << q);
-      c += __popc(m);
+      for (int k = 0; k < 4; ++k) c += __popc(set_bytes(u[k]));
+    } else {
+      for (int k = 0; k < 16; ++k) c += i + k >= lo && i + k < hi && a.mask[i + k] ? 1 : 0;
     }
   }
   return c;
@@ -157,21 +190,24 @@ __device__ inline void bounds(const PolicyArgs &a, int64_t &lo, int64_t &hi) {
 }
 
 // The tokens of segments [s0, s1): their gradients, and this lane's share of the sums.
-// whole: the weight of a token where it is the same for all (0: by sequence, from tokens_of).
-template <class Count>
-__device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, float whole, const Count &tokens_of,
-                                  double (&sum)[3]) {
+// whole: the weight of a token where it is the same for all (0: by sequence).  count: the tokens of
+// a sequence, the same for all lanes; inside: of one that lies in this run, lane by lane.
+// start: the offsets before the run's first token.
+template <class Start, class Count, class Inside>
+__device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, float whole, const Start &start,
+                                  const Count &count, const Inside &inside, double (&sum)[3]) {
   const int l = threadIdx.x & 63;
   if (s0 >= s1) return;
-  const bool by_seq = whole == 0.f, lookup = by_seq || !a.per_token;
-  int64_t lo, hi;
-  bounds(a, lo, hi);
-  int64_t open = lookup ? offsets_up_to(a, s0 * kSeg - 1) : 0;
-  for (int64_t s = s0; s < s1; ++s) {
-    const int64_t t0 = s * kSeg, i = t0 + 4 * l;
-    uint32_t m = mask4(a, i);
+  // a lane's four tokens, loaded a segment ahead (and before the run's first lookups)
+  struct Four {
+    uint32_t m;
+    f32v4 x, o, r, A;
+  };
+  auto load = [&](int64_t s) {
+    const int64_t i = s * kSeg + 4 * l;
     const int nv = a.n - i >= 4 ? 4 : a.n - i > 0 ? (int)(a.n - i) : 0;
-    f32v4 x = {0.f, 0.f, 0.f, 0.f}, o = x, r = x, A = x;
+    Four f = {};
+    f.m = mask4(a, i);
     auto get = [&](const float *p, f32v4 &v) {
       if (nv == 4) {
         v = *(const f32v4 *)(p + i);
@@ -181,41 +217,80 @@ __device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, f
           if (k < nv) v[k] = p[i + k];
       }
     };
-    get(a.nll, x);
-    if (a.old) get(a.old, o);
-    if (a.ref) get(a.ref, r);
-    if (a.per_token) get(a.adv, A);
-    f32v4 w = {whole, whole, whole, whole};
-    if (lookup) {
-      int past[4] = {0, 0, 0, 0};  // offsets at or before each token, beyond `open`
-      int64_t next = open;
-      while (true) {
-        const int64_t b = offset_at(a, next + l);
-        const int c = __popcll(__ballot(b < t0 + kSeg));
-        for (int j = 0; j < c; ++j) {
-          const int64_t bj = __shfl(b, j);
-          const int rel = bj <= t0 ? 0 : (int)(bj - t0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) past[k] += rel <= 4 * l + k ? 1 : 0;
-        }
-        next += c;
-        if (c < 64) break;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t q = open - 1 + past[k];
-        if (q < 0 || q >= a.seqs || i + k >= a.n) {
-          m &= ~(1u << k);
-        } else {
-          if (!a.per_token) A[k] = a.adv[q];
-          if (by_seq) w[k] = 1.f / ((float)tokens_of(q) * (float)a.seqs);
-        }
-      }
-      open = next;
-    } else {
+    get(a.nll, f.x);
+    if (a.old) get(a.old, f.o);
+    if (a.ref) get(a.ref, f.r);
+    if (a.per_token) get(a.adv, f.A);
+    return f;
+  };
+  Four ahead = load(s0);
+  const bool by_seq = whole == 0.f, lookup = by_seq || !a.per_token;
+  int64_t lo = 0, hi = 0;
+  if (!lookup) bounds(a, lo, hi);
+  int64_t open = 0, next = INT64_MAX;  // offsets passed, the offset to come
+  bool in = true;                      // the open sequence is one
+  float A0 = 0.f, w0 = whole;          // its advantage, its tokens' weight
+  auto weight = [&](int n) { return 1.f / ((float)n * (float)a.seqs); };
+  auto enter = [&] {
+    next = offset_at(a, open);
+    in = open >= 1 && open <= a.seqs;
+    if (in && !a.per_token) A0 = a.adv[open - 1];
+    if (in && by_seq) w0 = weight(count(open - 1));
+  };
+  if (lookup) {
+    open = start();
+    enter();
+  }
+  for (int64_t s = s0; s < s1; ++s) {
+    const int64_t t0 = s * kSeg, i = t0 + 4 * l;
+    const int nv = a.n - i >= 4 ? 4 : a.n - i > 0 ? (int)(a.n - i) : 0;
+    uint32_t m = ahead.m;
+    const f32v4 x = ahead.x, o = ahead.o, r = ahead.r;
+    f32v4 A = ahead.A;
+    if (s + 1 < s1) ahead = load(s + 1);
+    f32v4 w = {w0, w0, w0, w0};
+    if (!lookup) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (i + k < lo || i + k >= hi) m &= ~(1u << k);
+    } else {
+      if (!a.per_token) A = f32v4{A0, A0, A0, A0};
+      const bool was_in = in;
+      if (next >= t0 + kSeg) {
+        if (!in) m = 0;
+      } else {
+        int past[4] = {0, 0, 0, 0};  // offsets at or before each token, beyond `open`
+        const int64_t from = open;
+        while (true) {
+          const int64_t b = offset_at(a, open + l);
+          const int c = __popcll(__ballot(b < t0 + kSeg));
+          for (int j = 0; j < c; ++j) {
+            const int64_t bj = __shfl(b, j);
+            const int rel = bj <= t0 ? 0 : bj < t0 + kSeg ? (int)(bj - t0) : kSeg;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) past[k] += rel <= 4 * l + k ? 1 : 0;
+          }
+          open += c;
+          if (c < 64) break;
+        }
+        enter();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t q = from - 1 + past[k];
+          if (past[k] == 0) {
+            if (!was_in) m &= ~(1u << k);
+          } else if (q == open - 1) {
+            if (!in) m &= ~(1u << k);
+            if (!a.per_token) A[k] = A0;
+            w[k] = w0;
+          } else if (q >= 0 && q < a.seqs) {  // began and ended in this segment
+            if (!a.per_token) A[k] = a.adv[q];
+            if (by_seq) w[k] = weight(inside(q));
+          } else {
+            m &= ~(1u << k);
+          }
+        }
+      }
     }
     f32v4 g;
     float part[3] = {0.f, 0.f, 0.f};
@@ -276,21 +351,16 @@ __device__ inline int length_of(const PolicyArgs &a, int64_t q) {
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void k_policy_zero(int *p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
-}
-
-__global__ __launch_bounds__(256) void k_policy_count(PolicyArgs a, int64_t segs) {
+__global__ __launch_bounds__(256) void k_policy_count(PolicyArgs a, int64_t segs, Counts c) {
   if (a.reduce == POETX_REDUCE_SEQUENCE) {
-    const int64_t s0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * a.run;
-    count_run(a, s0, s0 + a.run < segs ? s0 + a.run : segs, [&](int64_t q, int c) { atomicAdd(a.cnt + q, c); });
+    count_run(a, segs, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), c);
     return;
   }
   __shared__ int red[4];
   int64_t lo, hi;
   bounds(a, lo, hi);
-  const int c = wave_sum_i(count_all(a, lo, hi, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
+  const int n = wave_sum_i(count_all(a, lo, hi, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = n;
   __syncthreads();
   if (threadIdx.x == 0) a.parts[blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
@@ -300,7 +370,7 @@ __device__ inline float shared_weight(const PolicyArgs &a, int64_t count) {
   return a.reduce == POETX_REDUCE_TOKEN ? (float)(1.0 / (double)(count > 1 ? count : 1)) : 1.f;
 }
 
-__global__ __launch_bounds__(256) void k_policy_tokens(PolicyArgs a, int64_t segs) {
+__global__ __launch_bounds__(256) void k_policy_tokens(PolicyArgs a, int64_t segs, Counts c) {
   __shared__ int64_t redi[4];
   __shared__ double red[4][3];
   const int wave = threadIdx.x >> 6;
@@ -325,8 +395,11 @@ __global__ __launch_bounds__(256) void k_policy_tokens(PolicyArgs a, int64_t seg
   }
   double sum[3] = {0, 0, 0};
   const int64_t s0 = ((int64_t)blockIdx.x * 4 + wave) * a.run;
+  const bool counted = a.mask && a.reduce == POETX_REDUCE_SEQUENCE;
   policy_run(a, s0, s0 + a.run < segs ? s0 + a.run : segs, whole,
-             [&](int64_t q) { return a.mask ? (a.cnt[q] > 1 ? a.cnt[q] : 1) : length_of(a, q); }, sum);
+             [&] { return counted ? c.open[s0 / a.run] : offsets_up_to(a, s0 * kSeg - 1); },
+             [&](int64_t q) { return a.mask ? count_of(a, c, q) : length_of(a, q); },
+             [&](int64_t q) { return a.mask ? (c.cnt[q] > 1 ? c.cnt[q] : 1) : length_of(a, q); }, sum);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const double v = wave_sum_d(sum[k]);
@@ -359,24 +432,23 @@ __global__ __launch_bounds__(256) void k_policy_stats(PolicyArgs a, int blocks) 
 
 // Few tokens: one launch.  The counts stay in LDS.
 __global__ __launch_bounds__(1024) void k_policy_few(PolicyArgs a, int64_t segs) {
-  __shared__ int cnt[kFewSeqs];
+  __shared__ int cnt[kFewSeqs], parts[4][16];
   __shared__ double red[16][3];
   const int wave = threadIdx.x >> 6;
   const bool by_seq = a.reduce == POETX_REDUCE_SEQUENCE;
+  const Counts c{cnt, parts[0], parts[1], parts[2], parts[3], cdiv(segs, a.run), a.run * kSeg};
   const int64_t s0 = wave * a.run, s1 = s0 + a.run < segs ? s0 + a.run : segs;
   float whole = 0.f;
   if (by_seq && a.mask) {
-    for (int i = threadIdx.x; i < a.seqs; i += 1024) cnt[i] = 0;
-    __syncthreads();
-    count_run(a, s0, s1, [&](int64_t q, int c) { atomicAdd(&cnt[q], c); });
+    count_run(a, segs, wave, c);
     __syncthreads();
   } else if (!by_seq) {
     int64_t lo, hi;
     bounds(a, lo, hi);
     int64_t count = hi - lo;
     if (a.mask && a.reduce == POETX_REDUCE_TOKEN) {
-      const int c = wave_sum_i(count_all(a, lo, hi, threadIdx.x, 1024));
-      if ((threadIdx.x & 63) == 0) cnt[wave] = c;
+      const int n = wave_sum_i(count_all(a, lo, hi, threadIdx.x, 1024));
+      if ((threadIdx.x & 63) == 0) cnt[wave] = n;
       __syncthreads();
       count = 0;
 #pragma unroll
@@ -385,7 +457,10 @@ __global__ __launch_bounds__(1024) void k_policy_few(PolicyArgs a, int64_t segs)
     whole = shared_weight(a, count);
   }
   double sum[3] = {0, 0, 0};
-  policy_run(a, s0, s1, whole, [&](int64_t q) { return a.mask ? (cnt[q] > 1 ? cnt[q] : 1) : length_of(a, q); }, sum);
+  const bool counted = a.mask && by_seq;
+  policy_run(a, s0, s1, whole, [&] { return counted ? c.open[wave] : offsets_up_to(a, s0 * kSeg - 1); },
+             [&](int64_t q) { return a.mask ? count_of(a, c, q) : length_of(a, q); },
+             [&](int64_t q) { return a.mask ? (cnt[q] > 1 ? cnt[q] : 1) : length_of(a, q); }, sum);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const double v = wave_sum_d(sum[k]);
@@ -412,29 +487,33 @@ int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const int64_t segs = cdiv(d.n, kSeg), cus = device_cus() > 0 ? device_cus() : 256;
   if (d.n <= kFewTokens && d.seqs <= kFewSeqs) {
     if (measure) return POETX_OK;
-    a.run = cdiv(segs, 16);
+    a.run = segs > 16 ? cdiv(segs, 16) : 1;
     return launch_k("policy_few", s, k_policy_few, dim3(1), dim3(1024), 0, a, segs);
   }
-  a.run = cdiv(segs, 4 * 8 * cus);
+  // as many waves as are at work at once (4 on a SIMD): 2^24 tokens 72 us with twice as many, 68 so
+  // as many waves as are at work at once, 4 on a SIMD (2^24 tokens: 72 us with twice as many, 68 so)
+  a.run = cdiv(segs, 4 * 4 * cus);
   if (a.run < 1) a.run = 1;
   const int64_t blocks = segs > 0 ? cdiv(segs, 4 * a.run) : 1;
   const bool by_seq = d.reduce == POETX_REDUCE_SEQUENCE;
   a.sums = (double *)ar.take((size_t)blocks * 3 * 8);
-  if (by_seq) a.cnt = (int *)ar.take((size_t)d.seqs * 4);
-  int64_t parts = cdiv(d.n, 4096);
+  Counts c{};
+  c.runs = cdiv(segs, a.run);
+  c.tokens = a.run * kSeg;
+  const int64_t parts = cdiv(d.n, 4096);
   a.nparts = (int)(parts < 1 ? 1 : parts < kCountParts ? parts : kCountParts);
-  if (!by_seq) a.parts = (int *)ar.take((size_t)a.nparts * 4);
-  if (measure) return POETX_OK;
-  if (d.mask && d.reduce != POETX_REDUCE_SUM) {
-    if (by_seq && d.seqs > 0) {
-      const int64_t z = cdiv(d.seqs, 256);
-      POETX_TRY(launch_k("policy_zero", s, k_policy_zero, dim3((unsigned)(z < 1024 ? z : 1024)), dim3(256), 0, a.cnt,
-                         d.seqs));
-    }
-    POETX_TRY(launch_k("policy_count", s, k_policy_count, dim3((unsigned)(by_seq ? blocks : a.nparts)), dim3(256), 0,
-                       a, segs));
+  if (by_seq) {
+    c.cnt = (int *)ar.take((size_t)d.seqs * 4);
+    int *q = (int *)ar.take((size_t)c.runs * 4 * 4);
+    c.head = q; c.tail = q + c.runs; c.all = q + 2 * c.runs; c.open = q + 3 * c.runs;
+  } else {
+    a.parts = (int *)ar.take((size_t)a.nparts * 4);
   }
-  POETX_TRY(launch_k("policy_tokens", s, k_policy_tokens, dim3((unsigned)blocks), dim3(256), 0, a, segs));
+  if (measure) return POETX_OK;
+  if (d.mask && d.reduce != POETX_REDUCE_SUM)
+    POETX_TRY(launch_k("policy_count", s, k_policy_count, dim3((unsigned)(by_seq ? blocks : a.nparts)), dim3(256), 0,
+                       a, segs, c));
+  POETX_TRY(launch_k("policy_tokens", s, k_policy_tokens, dim3((unsigned)blocks), dim3(256), 0, a, segs, c));
   return launch_k("policy_stats", s, k_policy_stats, dim3(1), dim3(256), 0, a, (int)blocks);
 }
 

@@ -314,7 +314,10 @@ struct GradDesc {
   float max_norm = 0.f;
   bool clip = false;
   float *norm = nullptr, *coef = nullptr;
+  const void *plan = nullptr;  // the list's table, where it is kept (grad_plan_bytes > 0)
 };
+size_t grad_plan_bytes(const GradDesc &d);
+int grad_plan(const GradDesc &d, void *plan, hipStream_t s);
 int grad_norm(const GradDesc &d, Arena &ar, bool measure, hipStream_t s);
 
 }  // namespace poetx

@@ -45,10 +45,11 @@ def grads(B, *items):
     return a
 
 
-def clip(B, *items, n=None, a=True, max_norm=1.0, norm=A[8], coef=A[9], ws=A[10], nb=BIG, f="poetx_grad_clip"):
+def clip(B, *items, n=None, a=True, max_norm=1.0, norm=A[8], coef=A[9], plan=None, ws=A[10], nb=BIG,
+         f="poetx_grad_clip"):
     arr = grads(B, *items)
-    return getattr(B.raw, f)(len(items) if n is None else n, arr if a else None, max_norm, norm, coef, ws, size(nb),
-                             None)
+    return getattr(B.raw, f)(len(items) if n is None else n, arr if a else None, max_norm, norm, coef, plan, ws,
+                             size(nb), None)
 
 
 def test_glu_refusals(B):
@@ -83,7 +84,7 @@ def test_policy_refusals(B):
                dict(nll=A[1] + 4), dict(off=A[0] + 8), dict(mask=A[5] + 1), dict(dnll=A[1]), dict(dnll=A[2]),
                dict(stats=A[7]), dict(stats=A[4]), dict(ws=A[8] + 8)):
         assert policy(B, **kw) == bad, kw
-    for kw in (dict(n=1 << 31), dict(s=1 << 31)):
+    for kw in (dict(n=1 << 31), dict(s=(1 << 31) - 1)):
         assert policy(B, **kw) == B.POETX_ERR_UNSUPPORTED, kw
     for kw in (dict(), dict(reduce=1), dict(reduce=2), dict(low=inf, high=inf)):
         assert policy(B, n=10000, nb=16, **kw) == B.POETX_ERR_WORKSPACE, kw
@@ -107,9 +108,17 @@ def test_grad_refusals(B):
         assert clip(B, *[(A[0], A[1], 1 << 47, 1)] * 3, f=f) == B.POETX_ERR_UNSUPPORTED
         assert clip(B, ok, f=f, ws=None) == B.POETX_OK
         assert clip(B, f=f, a=False, ws=None) == B.POETX_OK
-        assert getattr(B.raw, f)(1, grads(B, ok), 1.0, A[8], A[9], A[10], None, None) == bad
+        assert getattr(B.raw, f)(1, grads(B, ok), 1.0, A[8], A[9], None, A[10], None, None) == bad
+        assert clip(B, *[ok] * 200, f=f, plan=A[11] + 8) == bad
+        assert clip(B, *[ok] * 200, f=f, nb=4000) == B.POETX_ERR_WORKSPACE
     assert clip(B, (A[0], None, 100, 0)) == bad
     assert clip(B, (A[0], A[1] + 2, 100, 0)) == bad
+    f, many = B.raw.poetx_grad_plan, grads(B, *[ok] * 200)
+    assert f(200, many, A[2], None, None) == bad and f(-1, many, A[2], size(BIG), None) == bad
+    assert f(200, None, A[2], size(BIG), None) == bad and f(200, many, A[2] + 8, size(BIG), None) == bad
+    assert f(200, many, A[2], size(100), None) == B.POETX_ERR_WORKSPACE
+    assert f(200, grads(B, *[(A[0] + 2, A[1], 100, 0)] * 200), A[2], size(BIG), None) == bad
+    assert f(1, grads(B, ok), A[2], size(0), None) == B.POETX_OK  # nothing to write
 
 
 def query(f, *args):
@@ -128,7 +137,14 @@ def test_workspace_queries(B):
     big = query(r.poetx_policy_loss, 1 << 24, 1 << 20, *[None] * 6, ctypes.byref(p), None, None)
     assert 4 << 20 <= big < 8 << 20  # one count per sequence, nothing per token
     assert query(r.poetx_policy_loss, 0, 0, *[None] * 6, ctypes.byref(p), None, None) < 4096
-    assert query(r.poetx_grad_norm, 1, grads(B, (A[0], None, 1 << 40, 0)), 1.0, None, None) <= 1 << 16
+    one = grads(B, (A[0], None, 1 << 40, 0))
+    assert query(r.poetx_grad_norm, 1, one, 1.0, None, None, None) <= 1 << 17
+    # a long list's plan takes its table out of the workspace; a short one needs none
+    many = grads(B, *[(A[0], A[1], 5000, 0)] * 200)
+    plan = query(r.poetx_grad_plan, 200, many)
+    assert plan >= 200 * 24 and query(r.poetx_grad_plan, 1, one) == query(r.poetx_grad_plan, 0, None) == 0
+    without, kept = (query(r.poetx_grad_clip, 200, many, 1.0, None, None, p) for p in (None, A[2]))
+    assert without >= kept + plan
 
 
 def test_binding_refusals(B):

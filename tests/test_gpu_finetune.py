@@ -666,6 +666,45 @@ def test_grad_list_is_used_again(B):
             assert torch.equal(g, (b.float() * coef).to(b.dtype))
 
 
+def test_grad_long_list_on_streams_and_in_graphs(B):
+    """A list that keeps its device form: on two streams, captured twice, dropped and made anew."""
+    gs = [rand(620 + k, 1 + (k * 977) % 9000, dtype=(F32, BF16)[k % 2]) for k in range(333)]
+    outs = [torch.zeros_like(g) for g in gs]
+    lst = B.GradList(gs, outs)
+    want, _ = grad_ref(gs, 1.0)
+
+    def same(norm, coef):
+        within(norm.reshape(1), want.reshape(1), 2 * U[F32] * want, "norm")
+        for g, o in zip(gs, outs):
+            assert torch.equal(o, (g.float() * coef).to(g.dtype))
+            o.zero_()
+
+    same(*B.poetx_grad_clip(lst, 1.0))
+    _, ran = labelled(B, lambda: B.poetx_grad_clip(lst, 1.0))
+    assert "grad_table" not in ran
+    _, ran = labelled(B, lambda: B.poetx_grad_clip(gs, 1.0, outs))
+    assert "grad_table" in ran
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = B.poetx_grad_clip(lst, 1.0)
+    s.synchronize()
+    same(*got)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = B.poetx_grad_clip(lst, 1.0)
+        graphs.append((g, got))
+    del lst
+    for _ in range(3):
+        for g, got in graphs:
+            g.replay()
+            torch.cuda.synchronize()
+            same(*(t.clone() for t in got))
+            same(*B.poetx_grad_clip(gs, 1.0, outs))
+
+
 # ----------------------------------------------------------------- all of them together ----
 
 def chain_inputs(seed, n, dtype, d=264, f=200, v=1003):
