@@ -48,7 +48,8 @@ struct Counts {
   int *cnt;                   // [seqs]
   int *head, *tail, *all;     // [runs]
   int *open;                  // [runs] offsets before the run's first token
-  int64_t runs, tokens;       // tokens of a run
+  int64_t runs;
+  uint32_t segs;              // segments of a run
 };
 
 __device__ inline int64_t offset_at(const PolicyArgs &a, int64_t j) {
@@ -151,10 +152,11 @@ __device__ inline void count_run(const PolicyArgs &a, int64_t segs, int64_t r, c
   if (l == 0) (head ? c.all : c.tail)[r] = rest;
 }
 
-// Tokens that count in sequence q (0 <= q < seqs, the same for all lanes), at least 1.
-__device__ inline int count_of(const PolicyArgs &a, const Counts &c, int64_t q) {
-  const int64_t b = offset_at(a, q), e = offset_at(a, q + 1), end = c.runs * c.tokens;
-  const int64_t rb = b < 0 ? -1 : b < end ? b / c.tokens : c.runs, re = e < 0 ? 0 : e < end ? e / c.tokens : c.runs;
+// Tokens that count in sequence q from b to e (0 <= q < seqs, the same for all lanes), at least 1.
+__device__ inline int count_of(const Counts &c, int64_t q, int64_t b, int64_t e) {
+  const int64_t end = c.runs * c.segs * kSeg;  // (at most 2^31 tokens and their last run)
+  auto run_of = [&](int64_t t) { return t < end ? (int64_t)((uint32_t)(t / kSeg) / c.segs) : c.runs; };
+  const int64_t rb = b < 0 ? -1 : run_of(b), re = e < 0 ? 0 : run_of(e);
   int n;
   if (rb == re) {
     n = c.cnt[q];
@@ -227,18 +229,26 @@ __device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, f
   const bool by_seq = whole == 0.f, lookup = by_seq || !a.per_token;
   int64_t lo = 0, hi = 0;
   if (!lookup) bounds(a, lo, hi);
+  // offsets wbase + lane, read together (each lookup alone would wait for memory)
+  int64_t wbase = 0, win = 0;
+  auto fill = [&](int64_t j) {
+    wbase = j;
+    win = offset_at(a, j + l);
+  };
   int64_t open = 0, next = INT64_MAX;  // offsets passed, the offset to come
   bool in = true;                      // the open sequence is one
   float A0 = 0.f, w0 = whole;          // its advantage, its tokens' weight
   auto weight = [&](int n) { return 1.f / ((float)n * (float)a.seqs); };
   auto enter = [&] {
-    next = offset_at(a, open);
+    if (open > wbase + 63) fill(open - 1);  // (open - 1 is never before the window)
+    next = __shfl(win, (int)(open - wbase));
     in = open >= 1 && open <= a.seqs;
     if (in && !a.per_token) A0 = a.adv[open - 1];
-    if (in && by_seq) w0 = weight(count(open - 1));
+    if (in && by_seq) w0 = weight(count(open - 1, __shfl(win, (int)(open - 1 - wbase)), next));
   };
   if (lookup) {
     open = start();
+    fill(open - 1);
     enter();
   }
   for (int64_t s = s0; s < s1; ++s) {
@@ -262,16 +272,17 @@ __device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, f
         int past[4] = {0, 0, 0, 0};  // offsets at or before each token, beyond `open`
         const int64_t from = open;
         while (true) {
-          const int64_t b = offset_at(a, open + l);
-          const int c = __popcll(__ballot(b < t0 + kSeg));
+          const int first = (int)(open - wbase);  // the lane of the next offset
+          const int c = __popcll(__ballot(l >= first && win < t0 + kSeg));
           for (int j = 0; j < c; ++j) {
-            const int64_t bj = __shfl(b, j);
+            const int64_t bj = __shfl(win, first + j);
             const int rel = bj <= t0 ? 0 : bj < t0 + kSeg ? (int)(bj - t0) : kSeg;
 #pragma unroll
             for (int k = 0; k < 4; ++k) past[k] += rel <= 4 * l + k ? 1 : 0;
           }
           open += c;
-          if (c < 64) break;
+          if (first + c < 64) break;
+          fill(open - 1);
         }
         enter();
 #pragma unroll
@@ -341,9 +352,8 @@ __device__ inline void write_stats(const PolicyArgs &a, const double (&s)[3]) {
   for (int k = 0; k < 3; ++k) a.stats[1 + k] = (float)s[k];
 }
 
-// tokens of sequence q by its offsets alone
-__device__ inline int length_of(const PolicyArgs &a, int64_t q) {
-  int64_t b = offset_at(a, q), e = offset_at(a, q + 1);
+// tokens of a sequence by its offsets alone
+__device__ inline int length_of(const PolicyArgs &a, int64_t b, int64_t e) {
   b = b < 0 ? 0 : b;
   e = e < a.n ? e : a.n;
   return e - b > 1 ? (int)(e - b) : 1;
@@ -397,9 +407,10 @@ __global__ __launch_bounds__(256) void k_policy_tokens(PolicyArgs a, int64_t seg
   const int64_t s0 = ((int64_t)blockIdx.x * 4 + wave) * a.run;
   const bool counted = a.mask && a.reduce == POETX_REDUCE_SEQUENCE;
   policy_run(a, s0, s0 + a.run < segs ? s0 + a.run : segs, whole,
-             [&] { return counted ? c.open[s0 / a.run] : offsets_up_to(a, s0 * kSeg - 1); },
-             [&](int64_t q) { return a.mask ? count_of(a, c, q) : length_of(a, q); },
-             [&](int64_t q) { return a.mask ? (c.cnt[q] > 1 ? c.cnt[q] : 1) : length_of(a, q); }, sum);
+             [&] { return counted ? c.open[(int64_t)blockIdx.x * 4 + wave] : offsets_up_to(a, s0 * kSeg - 1); },
+             [&](int64_t q, int64_t b, int64_t e) { return a.mask ? count_of(c, q, b, e) : length_of(a, b, e); },
+             [&](int64_t q) { return a.mask ? (c.cnt[q] > 1 ? c.cnt[q] : 1)
+                                              : length_of(a, offset_at(a, q), offset_at(a, q + 1)); }, sum);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const double v = wave_sum_d(sum[k]);
@@ -436,7 +447,7 @@ __global__ __launch_bounds__(1024) void k_policy_few(PolicyArgs a, int64_t segs)
   __shared__ double red[16][3];
   const int wave = threadIdx.x >> 6;
   const bool by_seq = a.reduce == POETX_REDUCE_SEQUENCE;
-  const Counts c{cnt, parts[0], parts[1], parts[2], parts[3], cdiv(segs, a.run), a.run * kSeg};
+  const Counts c{cnt, parts[0], parts[1], parts[2], parts[3], cdiv(segs, a.run), (uint32_t)a.run};
   const int64_t s0 = wave * a.run, s1 = s0 + a.run < segs ? s0 + a.run : segs;
   float whole = 0.f;
   if (by_seq && a.mask) {
@@ -459,8 +470,9 @@ __global__ __launch_bounds__(1024) void k_policy_few(PolicyArgs a, int64_t segs)
   double sum[3] = {0, 0, 0};
   const bool counted = a.mask && by_seq;
   policy_run(a, s0, s1, whole, [&] { return counted ? c.open[wave] : offsets_up_to(a, s0 * kSeg - 1); },
-             [&](int64_t q) { return a.mask ? count_of(a, c, q) : length_of(a, q); },
-             [&](int64_t q) { return a.mask ? (cnt[q] > 1 ? cnt[q] : 1) : length_of(a, q); }, sum);
+             [&](int64_t q, int64_t b, int64_t e) { return a.mask ? count_of(c, q, b, e) : length_of(a, b, e); },
+             [&](int64_t q) { return a.mask ? (cnt[q] > 1 ? cnt[q] : 1)
+                                              : length_of(a, offset_at(a, q), offset_at(a, q + 1)); }, sum);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const double v = wave_sum_d(sum[k]);
@@ -499,7 +511,7 @@ int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s) {
   a.sums = (double *)ar.take((size_t)blocks * 3 * 8);
   Counts c{};
   c.runs = cdiv(segs, a.run);
-  c.tokens = a.run * kSeg;
+  c.segs = (uint32_t)a.run;
   const int64_t parts = cdiv(d.n, 4096);
   a.nparts = (int)(parts < 1 ? 1 : parts < kCountParts ? parts : kCountParts);
   if (by_seq) {

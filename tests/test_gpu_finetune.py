@@ -384,6 +384,9 @@ LENGTHS = {
     "one token": [1], "one": [1000], "few": [5, 0, 17, 256, 1], "edges": [255, 1, 256, 257, 511, 0, 0, 4],
     "ragged": [1 + (k * 7919) % 613 for k in range(200)], "tiny": [k % 4 for k in range(5000)],
     "empty ones": [0] * 300 + [700] + [0] * 900 + [3], "long": [40000, 3, 90001], "singles": [1] * 2000,
+    # either side of what one workgroup does alone, by tokens and by sequences
+    "8192 tokens": [8192 - 4095] + [1] * 4095, "4097 sequences": [1] * 4096 + [9], "8193 tokens": [5000, 3193],
+    "window": [1] * 62 + [300] + [0] * 63 + [2, 255] + [0] * 64 + [1, 511, 1] + [4] * 128 + [256] * 3 + [9000],
 }
 
 
@@ -404,6 +407,33 @@ def test_policy_many_tokens(B, reduce):
     lengths = [int(v) for v in g.integers(0, 9000, 700)] + [300000] + [int(v) for v in g.integers(0, 5, 3000)]
     for per_token, masked in ((False, True), (True, False)):
         check_policy(B, policy_case(510, lengths, 77, per_token, masked), reduce)
+
+
+def test_policy_of_more_than_2_28_tokens(B):
+    """The last tokens' gradients, and the sums over all, against float64 on the device."""
+    n = (1 << 28) + 77
+    nll, old = rand(1, n).abs_(), rand(2, n).abs_()
+    offsets = torch.tensor([0, 1000, n - 300, n - 5], device="cuda")
+    adv = torch.tensor([0.5, -1.0, 2.0], device="cuda")
+    mask = torch.ones(n, dtype=torch.uint8, device="cuda")
+    mask[::3] = 0
+    stats, dnll = B.poetx_policy_loss(nll, adv, offsets, nll_old=old, mask=mask, reduce="sequence", clip=(0.2, 0.2))
+    want = 0.0
+    for s in range(3):
+        q = slice(int(offsets[s]), int(offsets[s + 1]))
+        m, a = mask[q].double(), float(adv[s])
+        r = torch.exp(old[q].double() - nll[q].double())
+        w = 1.0 / (float(m.sum()) * 3)
+        pg = -torch.minimum(r * a, r.clamp(0.8, 1.2) * a)
+        want += float((pg * m).sum()) * w
+        held = (r > 1.2) if a > 0 else (r < 0.8)
+        g = torch.where(held, 0.0, r * a) * m * w
+        # |d| below 12 here: (12 + 8 + 8) float32 roundings of each gradient
+        within(dnll[q][-2000:], g[-2000:], 28 * U[F32] * g[-2000:].abs(), f"dnll {s}")
+        del m, r, pg, held, g
+    assert not dnll[-5:].any()
+    # the terms of one sign each: a term is off by 28 roundings at most
+    assert abs(float(stats[1]) - want) <= 28 * U[F32] * 3 * (0.5 * 1.2 + 60 + 2 * 1.2)
 
 
 def test_policy_one_sequence_of_all(B):
@@ -599,6 +629,20 @@ def test_grad_large(B):
     check_grads(B, [rand(1, 50_000_001, dtype=BF16), rand(2, 20_000_003)], 1.0)
 
 
+def test_grad_of_more_than_2_31_elements(B):
+    """Known values in a buffer whose offsets pass 32 bits, out of place and in place."""
+    n = (1 << 31) + 12345
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 5, n // 2, n - 9, n - 1], device="cuda")
+    g[at] = torch.tensor([1.0, 2.0, 4.0, 2.0, 0.0], dtype=BF16, device="cuda")
+    out = torch.empty_like(g)
+    norm, coef = B.poetx_grad_clip([g], 1.0, [out])
+    assert float(norm) == 5.0 and abs(float(coef) / 0.2 - 1) <= U[F32]
+    assert torch.equal(out[at], (g[at].float() * coef).to(BF16)) and int(torch.count_nonzero(out)) == 4
+    norm, coef = B.poetx_grad_clip([g], 2.5)
+    assert torch.equal(g[at].float(), torch.tensor([0.5, 1.0, 2.0, 1.0, 0.0], device="cuda"))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_grad_views_of_any_alignment(B, dtype):
     """Pieces of one buffer that begin at every offset from a 16-byte boundary, clipped in place and
@@ -753,6 +797,24 @@ def test_on_another_stream(B, n):
     s.synchronize()
     for p, q in zip(want, got):
         assert torch.equal(p, q)
+
+
+def test_two_streams_at_once(B):
+    """Chains of two streams, launched in turns without waiting, each with its own workspaces."""
+    sets = [chain_inputs(780, 333, BF16), chain_inputs(790, 210, F32, v=5003)]
+    want = [[r.clone() for r in run_all(B, *a)] for a in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(run_all(B, *sets[k]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for g in runs:
+            for p, q in zip(w, g):
+                assert torch.equal(p, q)
 
 
 @pytest.mark.parametrize("n", [9, 333])
