@@ -13,7 +13,12 @@
 //
 // A wave walks a run of consecutive tokens in segments of 256, four per lane, and knows the
 // sequence of each from the boundaries that the segment holds, 64 offsets at a time: one search
-// per run, no per-token search and no per-token index in memory.
+// per run, no per-token search and no per-token index in memory.  Where the mean needs counts, a
+// pass over the mask (a byte a token) comes first; the sums' partials are joined by a last launch.
+//
+// Bound by HBM for many tokens: 2^24 of 21 bytes, 68 us for the pass over the tokens (5.2 TB/s, a
+// large copy's rate), 5 for the count and 4 for the join; for fewer by the three launches (2^20
+// tokens: 5, 10 and 4 us).
 #include "kernels.h"
 #include "vec.h"
 
@@ -23,7 +28,10 @@ namespace {
 
 constexpr int kSeg = 256;         // tokens of a wave's segment
 constexpr int64_t kCountParts = 1024;
-constexpr int64_t kFewTokens = 8192, kFewSeqs = 4096;  // up to these one workgroup does it all
+// Up to these one workgroup of 16 waves does it all in one launch, counts in LDS: 2000 tokens 11.6
+// us a call (the host's time) against 17.8, 8192 tokens 11.2-14 against 17.5; replayed from a graph 7.3
+// against 10.8, and 11-14 against 10.5-12.5.  16384 tokens would take 19-25 us so, 17 by the launches.
+constexpr int64_t kFewTokens = 8192, kFewSeqs = 4096;
 
 struct PolicyArgs {
   int64_t n, seqs;
@@ -274,11 +282,24 @@ __device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, f
         while (true) {
           const int first = (int)(open - wbase);  // the lane of the next offset
           const int c = __popcll(__ballot(l >= first && win < t0 + kSeg));
-          for (int j = 0; j < c; ++j) {
-            const int64_t bj = __shfl(win, first + j);
-            const int rel = bj <= t0 ? 0 : bj < t0 + kSeg ? (int)(bj - t0) : kSeg;
+          const int rel = win <= t0 ? 0 : win < t0 + kSeg ? (int)(win - t0) : kSeg;
+          if (c <= 8) {
+            for (int j = 0; j < c; ++j) {
+              const int at = __shfl(rel, first + j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) past[k] += rel <= 4 * l + k ? 1 : 0;
+              for (int k = 0; k < 4; ++k) past[k] += at <= 4 * l + k ? 1 : 0;
+            }
+          } else {  // many (at most 63): a search for each token (8192 tokens, 2000 sequences 29 -> 16 us)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              int n = 0;
+#pragma unroll
+              for (int step = 32; step; step >>= 1) {
+                const int at = __shfl(rel, first + n + step - 1);
+                if (n + step <= c && at <= 4 * l + k) n += step;
+              }
+              past[k] += n;
+            }
           }
           open += c;
           if (first + c < 64) break;
