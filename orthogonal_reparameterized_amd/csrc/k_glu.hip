@@ -103,11 +103,15 @@ int fwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
   MmDesc m;
   m.M = d.n; m.N = 2 * round_up(d.f, kRun<T>); m.K = d.d; m.half = d.f; m.name = "glu_fwd"; m.large = "glu_fwd_large";
   m.A = d.x; m.lda = d.d; m.B = d.wg; m.B2 = d.wu; m.ldb = d.d;
-  if (d.n <= 16) {  // reading the weights bounds these: no LDS tiles, any alignment
+  // Few tokens: reading the weights bounds these (one token, 4096 -> 14336 bf16: 41-46 us, 5.1-5.7
+  // TB/s); no LDS tiles, any alignment.  Eight waves share the k of 16 rows of each weight; of short
+  // rows, where there are many, four do (512 -> 30000: 14.3 us, 15.8 with eight; 8192 -> 28672: 184
+  // and 170).
+  if (d.n <= 16) {
     if (measure) return POETX_OK;
     MmArgs a{m.M, d.f, m.K, m.A, m.lda, m.B, m.ldb, 1, 1, 1, m.K};
     a.B2 = m.B2;
-    const int64_t groups = cdiv(d.f, 16), two = groups >= 1024;
+    const int64_t groups = cdiv(d.f, 16), two = groups >= 1024 && d.d <= 1024;
     constexpr bool B16 = sizeof(T) == 2;
     auto kern = two ? k_mm_few<T, 2, false, GluEpi<T>> : k_mm_few<T, 1, false, GluEpi<T>>;
     if (B16 && d.d % 2) kern = two ? k_mm_few<T, 2, B16, GluEpi<T>> : k_mm_few<T, 1, B16, GluEpi<T>>;
@@ -123,6 +127,37 @@ int fwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
   if (measure) return POETX_OK;
   POETX_TRY(pack_rows(l, d.dt, s));
   return mm_run<T, false, false>(m, p, part, epi, s);
+}
+
+// How many ranges the k of a pair's first product (bf16, 128 x 128 tiles) is best cut into, the second
+// being whole: the launch's workgroups, two per CU, taken in their order, each as long as its steps of 64
+// k and six more for its first loads and its results (0.94 us a step); partials cost their join.  Half
+// the GPU for each product, which the dense layer's pair assumes, may leave a second round: 509 tokens,
+// 1024 -> 2819 37.1 us with 8 ranges, 34.9 with 5; 256 tokens 29.5 with 16, 26.3 with 8; 600 tokens,
+// 1500 -> 1500 47.9 and 40.8.
+int pair_ranges(int tiles, int steps_a, double part_us, int wgs, int steps_b, int slots) {
+  const int b = steps_b + 6;
+  int best = 1;
+  double least = 1e30;
+  for (int sp = 1; sp <= 32 && 4 * (sp - 1) < steps_a; ++sp) {
+    const int kc = (steps_a + sp - 1) / sp, a = kc + 6, na = tiles * sp;
+    if (kc * (sp - 1) >= steps_a) continue;  // fewer ranges come out
+    // after the first product `late` slots are free at t + a, the others at t
+    const int t = na / slots * a, late = na % slots;
+    int at[2] = {t, t + a}, free[2] = {slots - late, late}, end = late ? t + a : t;
+    for (int left = wgs; left > 0;) {
+      const int k = free[1] == 0 || (free[0] && at[0] <= at[1]) ? 0 : 1;
+      at[k] += b;
+      left -= free[k];
+      if (at[k] > end) end = at[k];
+    }
+    const double us = 0.94 * end + (sp > 1 ? 6 + sp * part_us : 0);
+    if (us < least) {
+      least = us;
+      best = sp;
+    }
+  }
+  return best;
 }
 
 // dx = [dg du] [Wg; Wu]: one product over 2 f64, dg du k-contiguous, the weights k-major and one
@@ -152,7 +187,18 @@ int bwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
     mw.A = dgu; mw.lda = 2 * f64; mw.ldb = ld;
     mw.B = packed(d.x, d.n, d.d, d.dt, ar, l);
   }
-  const MmTwo two = mm_two(mx.M, mx.N, mx.K, mw.M, mw.N, mw.K, d.dt);
+  MmTwo two = mm_two(mx.M, mx.N, mx.K, mw.M, mw.N, mw.K, d.dt);
+  if (two.pair && sizeof(T) == 2 && two.b.splits == 1) {
+    MmPlan &p = two.a;
+    const int64_t slots = 2 * (device_cus() > 0 ? device_cus() : 256), tiles = p.tiles_m * p.tiles_n;
+    const int64_t wgs = two.b.tiles_m * two.b.tiles_n;
+    if (tiles * p.splits + wgs > slots && tiles + wgs <= 64 * slots) {
+      const double part_us = (double)mx.M * mx.N * 4 / 5e6;
+      p.splits = pair_ranges((int)tiles, (int)(mx.K / 64), part_us, (int)wgs, (int)cdiv(mw.K, 64), (int)slots);
+      p.kc = p.splits > 1 ? cdiv(cdiv(mx.K, p.splits), 64) * 64 : mx.K;
+      p.part_bytes = p.splits > 1 ? (size_t)p.splits * mx.M * mx.N * 4 : 0;
+    }
+  }
   const MmPlan &px = two.a, &pw = two.b;
   float *part_x = px.part_bytes ? (float *)ar.take(px.part_bytes) : nullptr;
   float *part_w = pw.part_bytes ? (float *)ar.take(pw.part_bytes) : nullptr;
