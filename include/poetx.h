@@ -440,7 +440,7 @@ typedef enum { POETX_REDUCE_TOKEN = 0, POETX_REDUCE_SEQUENCE = 1, POETX_REDUCE_S
 typedef struct {
   double clip_low, clip_high;  /* lo and hi: the ratio is clipped to [1 - lo, 1 + hi]; both >= 0,
                                   infinity for no bound (a lo of 1 or more is none either)   */
-  double beta;                 /* weight of the KL term                                       */
+  double beta;                 /* weight of the KL term (0: the KL is reported and has no other part) */
   double scale;                /* factor of dnll (1 / accumulation steps), not of stats       */
   int32_t reduce;              /* a poetx_reduce                                              */
   int32_t adv_per_token;       /* 0: adv is [n_seqs], else [n_tokens]                         */

@@ -345,7 +345,7 @@ __device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, f
         const float z = expf(e) - 1.f;
         const bool near = fabsf(e) < 0.5f;
         kl = near ? p : z - e;
-        slope += a.beta * (near ? e + p : z);
+        if (a.beta != 0.f) slope += a.beta * (near ? e + p : z);  // (0: an infinite KL is only reported)
       }
       const bool on = m >> k & 1;
       g[k] = on ? slope * w[k] * a.scale : 0.f;
@@ -368,7 +368,7 @@ __device__ inline void policy_run(const PolicyArgs &a, int64_t s0, int64_t s1, f
 }
 
 __device__ inline void write_stats(const PolicyArgs &a, const double (&s)[3]) {
-  a.stats[0] = (float)(s[0] + (double)a.beta * s[1]);
+  a.stats[0] = (float)(a.beta != 0.f ? s[0] + (double)a.beta * s[1] : s[0]);
 #pragma unroll
   for (int k = 0; k < 3; ++k) a.stats[1 + k] = (float)s[k];
 }

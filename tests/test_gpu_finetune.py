@@ -526,6 +526,17 @@ def test_policy_extremes(B):
     check_policy(B, free, clip=(0.0, 0.0))
 
 
+def test_policy_kl_that_is_only_reported(B):
+    """beta 0: a KL that overflows shows in its own place and nowhere else."""
+    nll = torch.tensor([300.0, 1.0, 2.0], device="cuda")
+    ref, adv = torch.tensor([1.0, 1.0, 2.5], device="cuda"), torch.tensor([2.0], device="cuda")
+    stats, dnll = B.poetx_policy_loss(nll, adv, nll_ref=ref, reduce="sum")
+    want, plain = B.poetx_policy_loss(nll, adv, reduce="sum")
+    assert torch.equal(dnll, plain) and torch.equal(stats[:2], want[:2]) and float(stats[2]) == INF
+    stats, dnll = B.poetx_policy_loss(nll, adv, nll_ref=ref, reduce="sum", beta=0.5)
+    assert float(stats[0]) == INF and float(dnll[0]) == INF and torch.isfinite(dnll[1:]).all()
+
+
 def test_policy_small_kl_keeps_its_digits(B):
     """kl = e^2 / 2 + ... and its slope at e from 2^-30 to 1, each to 2^-20 of itself."""
     e = torch.tensor([s * 2.0 ** -k * f for k in range(1, 31) for s in (1, -1) for f in (1.0, 1.4, 1.99)])
@@ -693,6 +704,12 @@ def test_grad_extremes(B):
         n, c = B.poetx_grad_clip([rand(5, 10), g], 1.0, [torch.empty(10, device="cuda"), o])
         assert (math.isnan(float(n)) and math.isnan(float(c))) if math.isnan(bad) else (float(n) == INF and float(c) == 0)
         assert torch.isnan(o[12345]) and torch.isnan(o).sum() == (o.numel() if math.isnan(bad) else 1)
+
+
+def test_grad_nothing_but_empty_ones(B):
+    for gs in ([torch.empty(0, device="cuda")], [torch.empty(0, 3, device="cuda", dtype=BF16)] * 200):
+        for norm, coef in (B.poetx_grad_norm(gs, 0.0), B.poetx_grad_clip(gs, 1.0)):
+            assert float(norm) == 0 and float(coef) == 1
 
 
 def test_grad_list_is_used_again(B):
