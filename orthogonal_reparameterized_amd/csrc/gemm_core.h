@@ -47,6 +47,8 @@ struct MmArgs {
 enum { kOneB = 0, kPairRows = 1, kTwoRanges = 2 };
 template <class Epi, class = void> struct FormOf { static constexpr int value = kOneB; };
 template <class Epi> struct FormOf<Epi, std::void_t<decltype(Epi::kForm)>> { static constexpr int value = Epi::kForm; };
+template <class Tag, class = void> struct DeepOf { static constexpr bool value = false; };
+template <class Tag> struct DeepOf<Tag, std::void_t<decltype(Tag::kDeep)>> { static constexpr bool value = true; };
 template <class Epi, class = void> struct PairOf { static constexpr bool value = false; };
 template <class Epi> struct PairOf<Epi, std::void_t<decltype(Epi::kPair)>> { static constexpr bool value = Epi::kPair; };
 // rows of a run: a wave's columns (64 of the bf16 kernels, 32 of the smaller float32 one) hold whole pairs of runs
@@ -137,14 +139,15 @@ struct StagePair {
       voff[i] = (int)((((w >> 1) * 32 + i * 8 + (l >> 3)) * a.ldb + kbeg) * 2) + (((l & 7) ^ kc_key<64>(row)) << 4);
     }
   }
-  __device__ void issue_all(int t, int64_t left, bf16_t *tile) const {
+  __device__ void issue(int t, int64_t left, bf16_t *tile, int i) const {
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = threadIdx.x & 63;
+    int off = voff[i] + t * 128;
+    if (left < 64 && (((l & 7) ^ kc_key<64>((w * INSTR + i) * 8 + (l >> 3))) << 3) >= left) off = kPast;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * INSTR + i) * 512), 16, off, 0, 0, 0);
+  }
+  __device__ void issue_all(int t, int64_t left, bf16_t *tile) const {
 #pragma unroll
-    for (int i = 0; i < INSTR; ++i) {
-      int off = voff[i] + t * 128;
-      if (left < 64 && (((l & 7) ^ kc_key<64>((w * INSTR + i) * 8 + (l >> 3))) << 3) >= left) off = kPast;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * INSTR + i) * 512), 16, off, 0, 0, 0);
-    }
+    for (int i = 0; i < INSTR; ++i) issue(t, left, tile, i);
   }
 };
 
@@ -191,15 +194,17 @@ struct StageRanges : StageKM<R, NW> {
     S::init(nullptr, a.ldb, col0, 0, 0);
     k0 = kbeg;
   }
-  __device__ void issue_all(const MmArgs &a, int t, bf16_t *tile) const {
+  __device__ void issue(const MmArgs &a, int t, bf16_t *tile, int i) const {
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     int64_t rows;
     const void *base = range_rows(a, k0 + (int64_t)t * 64, 64, 2, rows);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, rows * a.ldb * 2);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * S::INSTR + i) * S::RPI * R), 16, S::voff[i],
+                                             0, 0, 0);
+  }
+  __device__ void issue_all(const MmArgs &a, int t, bf16_t *tile) const {
 #pragma unroll
-    for (int i = 0; i < S::INSTR; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(tile + (w * S::INSTR + i) * S::RPI * R), 16, S::voff[i],
-                                               0, 0, 0);
+    for (int i = 0; i < S::INSTR; ++i) issue(a, t, tile, i);
   }
 };
 
@@ -305,11 +310,36 @@ struct StoreEpi {
   __device__ void put(const Cols &, int64_t m, int64_t n, float (&v)[8], int nv) const { store8(C + m * ld + n, nv, v); }
 };
 
+namespace {
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ inline void wait_vm_lds() {
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (((N >> 4) & 3) << 14));
+}
+// s_waitcnt lgkmcnt(0)
+__device__ inline void wait_lds() { __builtin_amdgcn_s_waitcnt(0xF | (0x7 << 4) | (3 << 14)); }
+// a barrier that nothing is moved across and that waits for no memory operation by itself
+__device__ inline void phase_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+}  // namespace
+
 // bf16 kernel of the smaller products: 128 x 128 tile over 2 x 2 waves (64 x 64 each), 64-deep k
 // steps, two LDS stages filled by direct global -> LDS loads, one barrier per step, two
 // workgroups per CU that fill each other's waits.  2048^3: 27-30 us, 0.6 PFLOP/s (the vendor
 // library 21-27 us); a handful of tokens or columns is bound by the load latency of its k range.
-template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, class Epi>
+//
+// NS == 4: four LDS stages (128 KB, one workgroup per CU), for products that leave no CU a second
+// workgroup: three stages are in flight while a step is multiplied, and fragments of the half step
+// ahead are read between the products, one instruction after each.  A step of a lone workgroup takes 0.5
+// us instead of 0.65, or 0.94 with weights that are not in the caches (the loads' latency over what
+// LDS holds in flight); two workgroups per CU take 0.75-1.05 for a step of both, four stages 1.0.
+// The waits count a wave's loads, 8 a stage, so steps past the range are loaded too, as zeros.
+template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, int NS = 2, class Epi>
 __device__ inline void mm_body(const MmArgs &a, const Epi &epi, int id, bf16_t *smem) {
   constexpr int NW = WGM * WGN, BK = 64;
   constexpr int WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 16, FN = WTN / 16;
@@ -343,36 +373,86 @@ __device__ inline void mm_body(const MmArgs &a, const Epi &epi, int id, bf16_t *
   const int64_t span = kend - kbeg;
   const int nk = (int)((span + BK - 1) / BK);
   auto issue = [&](int t) {
-    sa.issue_all(t, span - (int64_t)t * BK, smem + (t & 1) * AE);
-    if constexpr (FORM == kTwoRanges) sb.issue_all(a, t, smem + 2 * AE + (t & 1) * BE);
-    else sb.issue_all(t, span - (int64_t)t * BK, smem + 2 * AE + (t & 1) * BE);
+    const int st = t & (NS - 1);
+    sa.issue_all(t, span - (int64_t)t * BK, smem + st * AE);
+    if constexpr (FORM == kTwoRanges) sb.issue_all(a, t, smem + NS * AE + st * BE);
+    else sb.issue_all(t, span - (int64_t)t * BK, smem + NS * AE + st * BE);
   };
-  if (nk > 0) issue(0);
-  for (int t = 0; t < nk; ++t) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();  // stage t is in LDS for every wave; the other stage is no longer read
-    const bf16_t *ta = smem + (t & 1) * AE, *tb = smem + 2 * AE + (t & 1) * BE;
-    bf16x8 fa[2][FM], fb[2][FN];
+  static_assert((NS & (NS - 1)) == 0 && SA::INSTR + SB::INSTR == 8, "stages, loads of a wave and stage");
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+  for (int s = 0; s < NS - 1; ++s)
+    if (NS > 2 || nk > 0) issue(s);
+  bf16x8 fa[2][FM], fb[2][FN];
+  auto read = [&](int h, int t) {
+    const bf16_t *ta = smem + (t & (NS - 1)) * AE, *tb = smem + NS * AE + (t & (NS - 1)) * BE;
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        fa[h][i] = AKM ? frag_km<BM>(ta, wm + 16 * i, 32 * h) : frag_kc<BK>(ta, wm + 16 * i, 32 * h);
+    for (int i = 0; i < FM; ++i)
+      fa[h][i] = AKM ? frag_km<BM>(ta, wm + 16 * i, 32 * h) : frag_kc<BK>(ta, wm + 16 * i, 32 * h);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      fb[h][j] = BKM ? frag_km<BN>(tb, wn + 16 * j, 32 * h) : frag_kc<BK>(tb, wn + 16 * j, 32 * h);
+  };
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        fb[h][j] = BKM ? frag_km<BN>(tb, wn + 16 * j, 32 * h) : frag_kc<BK>(tb, wn + 16 * j, 32 * h);
+        // operands swapped: lane l then holds C[m = l % 16][n = 4 (l / 16) + 0..3]
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+  };
+  if constexpr (NS == 2) {
+    for (int t = 0; t < nk; ++t) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();  // stage t is in LDS for every wave; the other stage is no longer read
+      read(0, t);
+      read(1, t);
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + 1 < nk) issue(t + 1);
+      multiply(0);
+      multiply(1);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (t + 1 < nk) issue(t + 1);
+  } else {
+    // one fragment, one load
+    auto read1 = [&](int h, int t, int q) {
+      const bf16_t *ta = smem + (t & (NS - 1)) * AE, *tb = smem + NS * AE + (t & (NS - 1)) * BE;
+      if (q < FM) fa[h][q] = AKM ? frag_km<BM>(ta, wm + 16 * q, 32 * h) : frag_kc<BK>(ta, wm + 16 * q, 32 * h);
+      else fb[h][q - FM] = BKM ? frag_km<BN>(tb, wn + 16 * (q - FM), 32 * h) : frag_kc<BK>(tb, wn + 16 * (q - FM), 32 * h);
+    };
+    auto issue1 = [&](int t, int q) {
+      const int st = t & (NS - 1);
+      const int64_t left = span - (int64_t)t * BK;
+      if (q < 4) sa.issue(t, left, smem + st * AE, q);
+      else if constexpr (FORM == kTwoRanges) sb.issue(a, t, smem + NS * AE + st * BE, q - 4);
+      else sb.issue(t, left, smem + NS * AE + st * BE, q - 4);
+    };
+    // the products of half a step, each followed by one other instruction
+    auto multiply_and = [&](int h, auto &&other) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          // operands swapped: lane l then holds C[m = l % 16][n = 4 (l / 16) + 0..3]
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+      for (int q = 0; q < FM * FN; ++q) {
+        const int i = q / FN, j = q % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+        other(q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    wait_vmcnt<8 * (NS - 2)>();
+    phase_barrier();
+    read(0, 0);
+    for (int t = 0; t < nk; ++t) {
+      wait_lds();
+      __builtin_amdgcn_sched_barrier(0);
+      multiply_and(0, [&](int q) {
+        if (q < FM + FN) read1(1, t, q);
+        else issue1(t + NS - 1, q - FM - FN);  // into the stage before t, which every wave has read
+      });
+      wait_vm_lds<8 * (NS - 2)>();
+      phase_barrier();  // stage t is read, stage t + 1 has landed
+      multiply_and(1, [&](int q) {
+        if (q < FM + FN) read1(0, t + 1, q);
+      });
+    }
   }
+  if constexpr (NS > 2) __builtin_amdgcn_s_waitcnt(0);  // the loads past the range have written their zeros
   __syncthreads();  // every wave is done with the last stage: the epilogue reuses the LDS
   finish<BM, BN, WGM, WGN>(acc, a, tile, (float *)smem, epi);
 }
@@ -380,6 +460,13 @@ template <int BM, int BN, int WGM, int WGN, bool AKM, bool BKM, class Epi>
 __global__ __launch_bounds__(64 * WGM * WGN) void k_mm(MmArgs a, Epi epi) {
   extern __shared__ __align__(16) bf16_t smem[];
   mm_body<BM, BN, WGM, WGN, AKM, BKM>(a, epi, blockIdx.x, smem);
+}
+// (Registers as for two workgroups per CU: with more the compiler keeps the accumulators in the
+// accumulation registers and moves them around.)
+template <bool AKM, bool BKM, class Epi>
+__global__ __launch_bounds__(256, 2) void k_mm_deep(MmArgs a, Epi epi) {
+  extern __shared__ __align__(16) bf16_t smem[];
+  mm_body<128, 128, 2, 2, AKM, BKM, 4>(a, epi, blockIdx.x, smem);
 }
 
 // 256 x 256 tile, 8 waves (2 x 4, 128 x 64 each), 64-deep k steps: the large products.
@@ -528,21 +615,6 @@ struct HalfRanges : Half<RUN, true> {
   }
 };
 
-namespace {
-// s_waitcnt vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ inline void wait_vm_lds() {
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (((N >> 4) & 3) << 14));
-}
-// a barrier that nothing is moved across and that waits for no memory operation by itself
-__device__ inline void phase_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-}  // namespace
 
 // FLIP: the results leave as C^T, rows n and columns m: the roles of the operands (128 rows of
 // A and 64 of B per wave) are then the caller's choice.
@@ -1091,6 +1163,7 @@ struct MmPlan {
   int64_t tiles_m = 0, tiles_n = 0;
   int64_t full = 0, tail_splits = 1, tail_kc = 0;  // 256 x 256 tiles from `full` on share their k
   size_t part_bytes = 0;  // workspace of a split product
+  bool deep = false;      // 128 x 128 tiles with four stages in LDS, one workgroup per CU
 };
 
 struct MmDesc {
@@ -1209,7 +1282,7 @@ inline MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int dt, bool may_split = 
 }
 
 template <bool AKM, bool BKM, class Epi>
-int mm_launch(const MmArgs &a, int64_t bt, const MmDesc &d, const Epi &epi, hipStream_t s) {
+int mm_launch(const MmArgs &a, int64_t bt, bool deep, const MmDesc &d, const Epi &epi, hipStream_t s) {
   const int tiles = a.tiles_m * a.tiles_n;
   const dim3 grid((unsigned)(a.full < tiles ? a.full + (tiles - a.full) * a.tail_splits : tiles * a.splits));
   if (bt == 256) {
@@ -1218,6 +1291,15 @@ int mm_launch(const MmArgs &a, int64_t bt, const MmDesc &d, const Epi &epi, hipS
     static std::atomic<uint64_t> attr{0};  // dynamic-LDS limit, per device
     POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
     return launch_k(d.large, s, kern, grid, dim3(512), lds, a, epi);
+  }
+  if constexpr (DeepOf<typename Epi::Tag_>::value) {
+    if (deep) {
+      constexpr size_t lds = (size_t)4 * 2 * 128 * 64 * 2;
+      auto kern = &k_mm_deep<AKM, BKM, Epi>;
+      static std::atomic<uint64_t> attr{0};
+      POETX_TRY(lds_limit(reinterpret_cast<const void *>(kern), lds, attr));
+      return launch_k(d.name, s, kern, grid, dim3(256), lds, a, epi);
+    }
   }
   constexpr size_t lds = (size_t)2 * 2 * 128 * 64 * 2;
   auto kern = &k_mm<128, 128, 2, 2, AKM, BKM, Epi>;
@@ -1233,7 +1315,7 @@ int mm_run_as(const MmArgs &a, const MmPlan &p, const MmDesc &d, const Epi &epi,
     if (p.bt == 128) return launch_k(d.large, s, k_mm_f32<128, 16, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
     return launch_k(d.name, s, k_mm_f32<64, 32, AKM, BKM, Epi>, grid, dim3(256), 0, a, epi);
   } else {
-    return mm_launch<AKM, BKM>(a, p.bt, d, epi, s);
+    return mm_launch<AKM, BKM>(a, p.bt, p.deep, d, epi, s);
   }
 }
 

@@ -7,7 +7,7 @@
 
 namespace poetx {
 
-struct GluTag {};
+struct GluTag { static constexpr bool kDeep = true; };  // its products may take four LDS stages
 
 // The two projections are one product whose B interleaves runs of w_gate's and w_up's rows
 // (kPairRows): g and u of a result lie in one lane's accumulators, and act(g) u, with g and u where
@@ -97,6 +97,31 @@ const void *packed(const void *in, int64_t rows, int64_t cols, int dt, Arena &ar
   return q;
 }
 
+// The forward's plan.  bf16 on 128 x 128 tiles: k in as many ranges, with four stages where every CU
+// has one workgroup at most, as makes the time shortest by 0.5 us a step with four stages, with two
+// 0.95 for up to two workgroups per CU and 0.47 for each of more; 5 us for the first loads and the
+// results; partials 4 us, written and read at 5 TB/s; the weights at 5.2 TB/s.
+MmPlan fwd_plan(const MmDesc &m, int dt) {
+  MmPlan p = mm_plan(m.M, m.N, m.K, dt);
+  if (dt == POETX_F32 || p.bt != 128) return p;
+  const int64_t cus = device_cus() > 0 ? device_cus() : 256, tiles = p.tiles_m * p.tiles_n;
+  const double weights = (double)m.N * m.K * 2 / 5.2e6, part = (double)m.M * m.N * 8 / 5e6;
+  double least = 0;
+  for (int64_t sp = 1; sp <= 16 && (sp == 1 || (m.K >= 128 * sp && tiles * sp <= 4 * cus)); ++sp) {
+    const int64_t kc = cdiv(cdiv(m.K, sp), 64) * 64, w = cdiv(tiles * sp, cus);
+    if (cdiv(m.K, kc) != sp) continue;
+    double us = cdiv(kc, 64) * (w == 1 ? 0.5 : w == 2 ? 0.95 : 0.47 * w) + 5;
+    us = (us > weights ? us : weights) + (sp > 1 ? 4 + sp * part : 0);
+    if (sp > 1 && us >= least) continue;
+    least = us;
+    p.splits = sp;
+    p.kc = sp > 1 ? kc : m.K;
+    p.part_bytes = sp > 1 ? (size_t)sp * m.M * m.N * 4 : 0;
+    p.deep = w == 1;
+  }
+  return p;
+}
+
 template <typename T>
 int fwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
   const GluEpi<T> epi{(T *)d.h, (T *)d.gate, (T *)d.up, d.act, d.f};
@@ -122,7 +147,7 @@ int fwd_t(const GluDesc &d, Arena &ar, bool measure, hipStream_t s) {
   m.A = packed(d.x, d.n, d.d, d.dt, ar, l);
   m.B = packed(d.wg, d.f, d.d, d.dt, ar, l);
   m.B2 = packed(d.wu, d.f, d.d, d.dt, ar, l);
-  const MmPlan p = mm_plan(m.M, m.N, m.K, d.dt);
+  const MmPlan p = fwd_plan(m, d.dt);
   float *part = p.part_bytes ? (float *)ar.take(p.part_bytes) : nullptr;
   if (measure) return POETX_OK;
   POETX_TRY(pack_rows(l, d.dt, s));

@@ -994,3 +994,14 @@ def test_policy_step_bf16(B):
         # with condition numbers of a few
         assert off(got["bf16"][1][k].float().reshape(g.shape), g.double()) <= 4 * 2 * 2.0 ** -8, k
     assert abs(float(got["bf16"][2]) / float(got["f32"][2]) - 1) <= 8 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("n,d,f,split", [(128, 4096, 7000, True), (128, 4096, 14300, False), (40, 2000, 1000, True),
+                                         (130, 72, 1001, False), (300, 1003, 2100, False), (200, 8000, 1000, True),
+                                         (17, 64, 64, False), (64, 520, 9000, False)])
+def test_glu_forward_with_four_stages(B, n, d, f, split):
+    """Products that leave a CU one workgroup, whole and split over k, with k that ends inside a step
+    and with fewer steps than stages."""
+    for k, act in enumerate(("silu", "none")):
+        ran = check_glu_fwd(B, n, d, f, BF16, act, save=k == 0, seed=150 + k)
+        assert ("mm_join" in ran) == split and "glu_fwd_large" not in ran, ran
