@@ -2,6 +2,11 @@
 //   forward   g = x Wg^T,  u = x Wu^T,  h = act(g) u
 //   backward  dg = dh u act'(g),  du = dh act(g),
 //             dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+// Each line is one launch of the product kernels of gemm_core.h (a pass for dg and du before the
+// backward's).  Bound by the chip's power where there are many tokens: 8192 tokens, 4096 -> 14336 bf16,
+// forward with g and u kept 1326 us (1.45 PFLOP/s), as two products of their own and a pass that joins
+// them 1722; backward 3030 us, of which dg and du 200 us (5.8 TB/s), dx 1405 (1.37 PFLOP/s), dW 1390,
+// x transposed 26; with dx as two products, dW as two and a sum 3256.
 #include "act.h"
 #include "gemm_core.h"
 

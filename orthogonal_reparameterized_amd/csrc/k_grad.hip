@@ -22,8 +22,9 @@ constexpr int kGradList = 140;  // gradients in a launch's arguments (4 KB); of 
 // us, of 4096 14.7, of 16384 12.6; 1 million 9.0, 9.3 and 10.1).
 constexpr int64_t kGradSpans = 8192, kGradLeast = 8192;
 // Partials that every workgroup of the scaling pass joins for itself, instead of a launch between: 2
-// x 522240 values 9.6 us against 10.7, 977 partials 14.7 against 15.4, 1954 27.4 against 26.0.
-constexpr int64_t kGradFew = 1024;
+// x 522240 values 9.6 us against 10.7, 977 partials 14.7 against 15.4, 1072 (of 1000 vectors) 17.8 against
+// 18.8, 1954 27.4 against 26.0.
+constexpr int64_t kGradFew = 1280;
 
 struct GradSpan {
   const void *g;
