@@ -503,7 +503,7 @@ int poetx_grad_plan(int64_t n_grads, const poetx_grad *grads /*[host]*/, void *p
  * grads [host]: read during the call.  Its device pointers need only be aligned to their elements;
  * gradients with n == 0 are passed over (their pointers may be NULL), `out` is not used.  Types may
  * be mixed.  max_norm >= 0, infinity for the norm alone.  norm, coef: float32 device outputs, 4-byte
- * aligned.  plan (nullable): what poetx_grad_plan wrote for this very list.  Squares and their sum
+ * aligned, outside every gradient.  plan (nullable): what poetx_grad_plan wrote for this very list.  Squares and their sum
  * are taken in 64 bits.  A NaN anywhere makes both NaN; an infinity makes norm infinite and coef 0
  * (where max_norm is finite).  n_grads == 0: norm 0, coef 1.  Workspace: query with ws == NULL (the
  * same lengths, plan NULL or not).  Errors: NULL grads, g, norm or coef, a length < 0, bad dtype,

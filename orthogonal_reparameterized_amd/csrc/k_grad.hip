@@ -5,10 +5,10 @@
 // 748 MB of bf16 take 123 us with sums of either width.
 //
 // The elements are cut into spans, one workgroup each; a workgroup's sum goes to one partial, and
-// the partials are joined in their order.  Bound by HBM: 352 million values, mostly bf16, take 113 us for
-// the squares (6.3 TB/s) and 255 for the scaling (5.6 TB/s read and written).  A short list of gradients comes with each launch, in its
-// arguments; a longer one goes into memory first, as a table of the spans (140 gradients a launch),
-// which a caller whose list stays the same keeps as its plan.
+// the partials are joined in their order.  Bound by HBM: 352 million values, mostly bf16, take 113 us
+// for the squares (6.3 TB/s) and 255 for the scaling (5.6 TB/s read and written).  A short list of
+// gradients comes with each launch, in its arguments; a longer one goes into memory first, as a table
+// of the spans (140 gradients a launch), which a caller whose list stays the same keeps as its plan.
 #include "kernels.h"
 #include "vec.h"
 

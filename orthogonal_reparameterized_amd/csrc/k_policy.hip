@@ -523,7 +523,6 @@ int policy_loss(const PolicyDesc &d, Arena &ar, bool measure, hipStream_t s) {
     a.run = segs > 16 ? cdiv(segs, 16) : 1;
     return launch_k("policy_few", s, k_policy_few, dim3(1), dim3(1024), 0, a, segs);
   }
-  // as many waves as are at work at once (4 on a SIMD): 2^24 tokens 72 us with twice as many, 68 so
   // as many waves as are at work at once, 4 on a SIMD (2^24 tokens: 72 us with twice as many, 68 so)
   a.run = cdiv(segs, 4 * 4 * cus);
   if (a.run < 1) a.run = 1;
